@@ -38,7 +38,8 @@ STATUS_NAMES = {
 # every symbol include/attn.h declares
 EXPORTED = ("attn_fwd", "attn_fwd_fp8", "attn_bwd", "attn_bwd_noalloc", "attn_bwd_deterministic", "attn_bwd_workspace_size",
             "attn_decode",
-            "attn_decode_workspace_size", "attn_status", "attn_last_error",
+            "attn_decode_workspace_size", "attn_paged", "attn_paged_workspace_size", "attn_pages_write",
+            "attn_pages_plan", "attn_pages_release", "attn_status", "attn_last_error",
             "attn_set_wait_timeout_ns", "attn_debug_set_producer_stall", "attn_debug_set_bwd_events",
             "attn_debug_launch_count", "attn_debug_launch_name", "attn_version")
 

@@ -401,6 +401,14 @@ attn_status_t bwd_check_inputs(const attn_bwd_params* p, bool* empty) {
     return check_tensor("dv", p->dv, p->dv_stride, 2, false);
 }
 
+attn_status_t launch_setup(LaunchCommon* lc) { return device_setup(lc); }
+
+attn_status_t map_encoder(PFN_cuTensorMapEncodeTiled_v12000* encode) {
+    const attn_status_t st = get_encoder();
+    *encode = g_encode;
+    return st;
+}
+
 attn_status_t build_dq_acc_map(const attn_fwd_params& p, float* dq_acc, CUtensorMap* m) {
     return encode_dq_acc_map(p, dq_acc, m);
 }
@@ -573,6 +581,8 @@ attn_status_t attn_status(void* stream) {
         e = cudaMemcpyToSymbol(g_error_word, &zero, sizeof(int));
         if (e != cudaSuccess) return cuda_fail(e, "clearing the device error word");
         if (word == ATTN_ERR_TIMEOUT) return fail(ATTN_ERR_TIMEOUT, "a kernel's bounded wait ran out");
+        if (word == ATTN_ERR_INVALID)
+            return fail(ATTN_ERR_INVALID, "a paged-cache kernel met a length, page or slot out of range");
         if (word == -7) return fail(ATTN_ERR_CUDA, "a kernel skipped a misaligned access or buffer");
         return fail(ATTN_ERR_CUDA, "device error word %d", word);
     }

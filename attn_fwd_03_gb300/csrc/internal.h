@@ -2,6 +2,7 @@
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <cstddef>
 #include <cstdint>
@@ -85,6 +86,8 @@ attn_status_t report_error(attn_status_t st, const char* fmt, ...);
 attn_status_t bwd_check_inputs(const attn_bwd_params* p, bool* empty);  // all but the workspace
 BwdWorkspace bwd_workspace_at(void* base, const attn_fwd_params& f);
 attn_status_t bwd_launch_with(const attn_bwd_params& p, const BwdWorkspace& ws, void* stream);
+attn_status_t launch_setup(LaunchCommon* lc);  // error word, SM count and time limit of the current device
+attn_status_t map_encoder(PFN_cuTensorMapEncodeTiled_v12000* encode);
 attn_status_t build_dq_acc_map(const attn_fwd_params& p, float* dq_acc, CUtensorMap* m);
 
 // attn_decode.cu — split-KV decode. The plan (key ranges per (b, h) and their
@@ -135,6 +138,15 @@ cudaError_t launch_bwd256(const attn_bwd_params& p, const Bwd256Maps& maps, cons
 // in the dtype of Q from the row statistics in ws.stats.
 cudaError_t launch_bwd_dq(const attn_bwd_params& p, const BwdMaps& maps, const BwdWorkspace& ws,
                           const LaunchCommon& lc, cudaStream_t s);
+
+// attn_paged.cu — attention over a paged cache.
+size_t paged_workspace_bytes(const attn_paged_params& p, int num_sms);
+cudaError_t launch_paged(const attn_paged_params& p, const LaunchCommon& lc, cudaStream_t s);
+
+// attn_pages.cu — the paged cache's tables and writes.
+cudaError_t launch_pages_write(const attn_pages_write_params& p, const LaunchCommon& lc, cudaStream_t s);
+cudaError_t launch_pages_plan(const attn_pages_plan_params& p, const LaunchCommon& lc, cudaStream_t s);
+cudaError_t launch_pages_release(const attn_pages_release_params& p, const LaunchCommon& lc, cudaStream_t s);
 
 // attn_simt.cu — CUDA-core kernels.
 cudaError_t launch_fwd_simt(const attn_fwd_params& p, cudaStream_t s);  // fp32 inputs

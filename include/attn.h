@@ -248,9 +248,166 @@ ATTN_API size_t attn_decode_workspace_size(const attn_decode_params *p);
  * attn_fwd; nq outside 1 .. 128 returns ATTN_ERR_UNSUPPORTED. */
 ATTN_API attn_status_t attn_decode(const attn_decode_params *p, void *stream);
 
+/*
+ * Paged key/value cache. Serving keeps the keys and values of many sequences
+ * in pages of `page_size` tokens; a block table names each sequence's pages in
+ * order, so key j of sequence b is slot j % page_size of page
+ * block_table[b][j / page_size]. Four entry points work on it: attn_paged
+ * attends to it, attn_pages_write stores new keys and values in it,
+ * attn_pages_plan takes pages for a step's new tokens and says where each token
+ * goes, attn_pages_release gives the pages of ended sequences back. A step is
+ * plan, then (per layer) write and paged.
+ *
+ * Lengths, tables and slots are int32 arrays in DEVICE memory that the kernels
+ * read when they run: nothing is copied to the host, and a captured graph of
+ * these calls follows the lengths it finds at each replay. The kernels check
+ * what they read (lengths against the table, pages against num_pages, slots
+ * against the cache): an entry out of range is skipped or read as zeros, never
+ * followed, and the next attn_status() reports ATTN_ERR_INVALID. Results of
+ * such a call are unspecified for the sequence concerned.
+ *
+ * The cache tensors are logically [num_pages, num_kv_heads, page_size, d] with
+ * element strides for (page, head, slot) and d contiguous, so pages may hold
+ * [page_size, heads, d] or [heads, page_size, d]. page_size is a power of two,
+ * 16 or more. Strides over an extent of 1 are ignored; the others must be
+ * positive. bf16 and fp16, head dims 64 and 128.
+ */
+
+/*
+ * Attention of new tokens over a paged cache. Sequence b of num_seqs brings
+ * n = cu_q[b + 1] - cu_q[b] query rows, rows cu_q[b] .. cu_q[b + 1] - 1 of q, and
+ * has L = kv_len[b] keys (the new tokens' own among them). Query head h attends
+ * with key/value head h / (num_q_heads / num_kv_heads):
+ *   O = softmax(scale * Q K^T + causal) V, LSE = log(sum exp(s)), per row.
+ * causal = 1: the rows are the LAST n positions; row i sees keys
+ * j <= L - n + i. causal = 0: every row sees all L keys (a decoder's rows
+ * against an encoder's states of another length, kept in the same pages).
+ * A row that sees no key (L = 0, or i < n - L) gets O = 0 and LSE = -inf.
+ * n = 0 is allowed. Rows of q from cu_q[num_seqs] to total_q (padding) are not
+ * read, and their O and LSE are left as they were. cu_q[0] must be 0 and cu_q
+ * must not decrease. Slots of the last page beyond L are not used: they may
+ * hold anything, NaN too.
+ *
+ * Results depend on a call's lengths only through the order of fp32 sums, and
+ * are the same bits for the same inputs on a given GPU model.
+ */
+typedef struct attn_paged_params {
+    int32_t num_seqs;
+    int32_t num_q_heads;     /* a multiple of num_kv_heads, at most 128 times as many */
+    int32_t num_kv_heads;
+    int32_t d;               /* 64 or 128 */
+    int32_t total_q;         /* rows of q and o, columns of lse */
+    int32_t max_q;           /* the most query rows a sequence is expected to bring, >= 1: chooses
+                                the tile shape. More rows than this are still right, only slower */
+    int32_t num_pages, page_size;
+    int32_t max_pages;       /* columns of the block table, >= 1; max_pages * page_size < 2^31 */
+    int32_t dtype;           /* ATTN_BF16 or ATTN_F16 (q, caches and o alike) */
+    int32_t causal;          /* 0 or 1 */
+    float scale;             /* > 0 */
+    int32_t reserved0[2];    /* must be 0 */
+    const void *q;           /* [total_q, num_q_heads, d] */
+    const void *k_cache, *v_cache;
+    void *o;                 /* [total_q, num_q_heads, d] */
+    float *lse;              /* [num_q_heads, total_q] fp32, contiguous */
+    const int32_t *cu_q;     /* [num_seqs + 1] */
+    const int32_t *kv_len;   /* [num_seqs] */
+    const int32_t *block_table; /* [num_seqs, max_pages]; entries beyond a sequence's pages are not read */
+    int64_t table_stride;    /* elements from one sequence's row to the next; 0 = one row for all */
+    int64_t q_stride[2], o_stride[2];  /* elements, (row, head) */
+    int64_t k_stride[3], v_stride[3];  /* elements, (page, head, slot) */
+    void *workspace;         /* >= attn_paged_workspace_size(p) bytes, 256-byte aligned; scratch after the
+                                call. Calls that may overlap on the GPU need one each */
+    size_t workspace_bytes;
+} attn_paged_params;
+
+/* Bytes of workspace attn_paged needs: a bound that depends on the head dim, the
+ * head group, max_q and the GPU, not on the lengths. 0 for a call it would refuse. */
+ATTN_API size_t attn_paged_workspace_size(const attn_paged_params *p);
+
+ATTN_API attn_status_t attn_paged(const attn_paged_params *p, void *stream);
+
+/*
+ * Stores keys and values of new tokens: row t of k and v goes to slot
+ * slots[t] % page_size of page slots[t] / page_size, for every head. Rows whose
+ * slot is negative are skipped. Slots named twice in one call end up holding
+ * either row's values, piece by piece: name each once.
+ */
+typedef struct attn_pages_write_params {
+    int32_t rows;            /* rows of k and v */
+    int32_t num_kv_heads;
+    int32_t d;               /* 64 or 128 */
+    int32_t num_pages, page_size;  /* num_pages * page_size < 2^31 */
+    int32_t dtype;           /* ATTN_BF16 or ATTN_F16 */
+    int32_t reserved0[2];    /* must be 0 */
+    const void *k, *v;       /* [rows, num_kv_heads, d] */
+    const int32_t *slots;    /* [rows] */
+    void *k_cache, *v_cache;
+    int64_t k_row_stride[2], v_row_stride[2];  /* elements, (row, head) */
+    int64_t k_stride[3], v_stride[3];          /* elements, (page, head, slot) */
+} attn_pages_write_params;
+
+ATTN_API attn_status_t attn_pages_write(const attn_pages_write_params *p, void *stream);
+
+/*
+ * Block tables and slot map of one step. Sequence b has kv_len[b] tokens in the
+ * cache and brings q_len[b] more. Pages for the blocks that the new tokens open
+ * are popped from the stack free_pages[0 .. free_count): sequence by sequence, in
+ * order of position, the k-th page taken is free_pages[free_count - 1 - k].
+ * Written: the new entries of block_table; cu_q (exclusive prefix sums of q_len);
+ * new_len = kv_len + q_len; for each new token, in order, its slot
+ * (page * page_size + offset) and its position in its sequence; free_left =
+ * free_count less the pages taken. Rows from cu_q[num_seqs] to total_q get slot
+ * and position -1. The inputs other than the table stay as they are, so the same
+ * call again gives the same answer; a step is taken by using new_len and
+ * free_left as the next kv_len and free_count.
+ * When the stack runs out free_left is negative by the pages that were missing,
+ * and the table entries and slots that got none are -1.
+ */
+typedef struct attn_pages_plan_params {
+    int32_t num_seqs;
+    int32_t total_q;         /* entries of slots and positions, >= the sum of q_len */
+    int32_t page_size;
+    int32_t max_pages;       /* columns of the block table, >= 1; max_pages * page_size < 2^31 */
+    int32_t free_capacity;   /* entries of free_pages */
+    int32_t reserved0;       /* must be 0 */
+    const int32_t *q_len, *kv_len;   /* [num_seqs] */
+    int32_t *block_table;    /* [num_seqs, max_pages], updated */
+    int64_t table_stride;    /* elements, >= max_pages */
+    const int32_t *free_pages, *free_count;  /* [free_capacity], [1] */
+    int32_t *cu_q;           /* [num_seqs + 1] */
+    int32_t *new_len;        /* [num_seqs]; not kv_len itself */
+    int32_t *slots, *positions;  /* [total_q] */
+    int32_t *free_left;      /* [1]; not free_count itself */
+} attn_pages_plan_params;
+
+ATTN_API attn_status_t attn_pages_plan(const attn_pages_plan_params *p, void *stream);
+
+/*
+ * Gives the pages of ended sequences back: for each b with done[b] != 0, in order,
+ * the pages of its kv_len[b] tokens are pushed onto free_pages, the first of them
+ * at free_pages[free_count]; new_len[b] becomes 0 (kv_len[b] for the others), and
+ * free_left = free_count plus the pages given back. The block table is only read.
+ */
+typedef struct attn_pages_release_params {
+    int32_t num_seqs;
+    int32_t page_size;
+    int32_t max_pages;       /* columns of the block table, >= 1; max_pages * page_size < 2^31 */
+    int32_t free_capacity;   /* entries of free_pages */
+    const int32_t *done, *kv_len;    /* [num_seqs] */
+    const int32_t *block_table;      /* [num_seqs, max_pages] */
+    int64_t table_stride;    /* elements, >= max_pages */
+    int32_t *free_pages;     /* [free_capacity], updated from free_count on */
+    const int32_t *free_count;       /* [1] */
+    int32_t *new_len;        /* [num_seqs]; not kv_len itself */
+    int32_t *free_left;      /* [1]; not free_count itself */
+} attn_pages_release_params;
+
+ATTN_API attn_status_t attn_pages_release(const attn_pages_release_params *p, void *stream);
+
 /* Synchronizes `stream`, then reports (and clears) the current device's
  * error word: ATTN_ERR_TIMEOUT if a kernel gave up on a bounded wait since
- * the last call, ATTN_ERR_CUDA for an asynchronous CUDA error, else ATTN_OK. */
+ * the last call, ATTN_ERR_INVALID if a paged-cache kernel met a length, page or
+ * slot out of range, ATTN_ERR_CUDA for an asynchronous CUDA error, else ATTN_OK. */
 ATTN_API attn_status_t attn_status(void *stream);
 
 /* Message for the last non-OK status returned on this host thread ("" if none). */

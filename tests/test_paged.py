@@ -1,0 +1,507 @@
+"""The paged cache on the GPU: attention, writes and tables against the fp64 oracle (oracle/paged.py).
+
+Attention outputs are held to the bounds of the other forward kernels (parity_util): the arithmetic is
+the same, 16-bit operands with fp32 accumulation and P rounded to the operand type. Everything of a
+cache that a sequence does not hold is NaN (free pages, slots of the last page beyond its length), and
+block-table entries beyond its pages are far out of range, so anything read by mistake shows.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import workloads as W
+from oracle import paged, ref
+from parity_util import assert_close_bf16, assert_lse, assert_masked_rows_zero, to64
+
+pytestmark = pytest.mark.gpu
+
+UNUSED = 0x7FFFFF00  # a block-table entry that must not be followed
+
+
+@pytest.fixture(scope="module")
+def A():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import attn_fwd_03_gb300 as m
+    assert m.attn_status() == m.ATTN_OK
+    return m
+
+
+class Case:
+    """Random q, caches and tables of a ragged batch."""
+
+    def __init__(self, n, kv, hkv, group, d, page, dtype, seed, pad=0, heads_first=False, mult=1.0, columns=0):
+        rng = np.random.default_rng(seed)
+        self.n, self.kv, self.page, self.dtype = list(n), list(kv), page, dtype
+        self.cu = np.concatenate([[0], np.cumsum(n)]).astype(int)
+        rows = int(self.cu[-1]) + pad
+        need = [(k + page - 1) // page for k in kv]
+        pages = sum(need) + 3
+        order = rng.permutation(pages).tolist()
+        cols = max(max(need), 1) + columns
+        self.table = np.full((len(n), cols), UNUSED, dtype=np.int64)
+        self.q = W.random_tensor((rows, hkv * group, d), seed, dtype) * mult
+        shape = (pages, hkv, page, d) if heads_first else (pages, page, hkv, d)
+        self.k, self.v = (torch.full(shape, float("nan"), dtype=dtype) for _ in range(2))
+        ks, vs = (W.random_tensor(shape, seed + i, dtype) for i in (1, 2))
+        for b, m in enumerate(need):
+            for i in range(m):
+                at, held = order.pop(), min(page, kv[b] - i * page)
+                self.table[b, i] = at
+                for cache, src in ((self.k, ks), (self.v, vs)):
+                    if heads_first:
+                        cache[at, :, :held] = src[at, :, :held]
+                    else:
+                        cache[at, :held] = src[at, :held]
+        if not heads_first:
+            self.k, self.v = self.k.transpose(1, 2), self.v.transpose(1, 2)
+        self.k = self.k * mult if mult != 1.0 else self.k
+
+    def device(self):
+        i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")  # noqa: E731
+        dev = lambda t: t.cuda() if t.is_contiguous() else t.transpose(1, 2).cuda().transpose(1, 2)  # noqa: E731
+        return dev(self.q), dev(self.k), dev(self.v), i32(self.table), i32(self.cu), i32(self.kv)
+
+    def oracle(self, causal, scale=None):
+        scale = 1 / math.sqrt(self.q.shape[2]) if scale is None else scale
+        return paged.paged_forward(to64(self.q), to64(self.k), to64(self.v), self.table, self.cu, self.kv, scale, causal)
+
+    def check(self, o, lse, causal, scale=None):
+        rows = int(self.cu[-1])
+        O, L = self.oracle(causal, scale)
+        assert_close_bf16("O", o[:rows], O[:rows])
+        assert_lse(lse[:, :rows], L[:, :rows])
+        assert_masked_rows_zero(o[:rows].transpose(0, 1), L[:, :rows])
+
+
+def _ok(A):
+    torch.cuda.synchronize()
+    assert A.attn_status() == A.ATTN_OK, A.last_error()
+
+
+SHAPES = {
+    "one key": ([1], [1], 1, 1, 64, 16),
+    "page and tile ends": ([1] * 9, [1, 15, 16, 17, 127, 128, 129, 255, 256], 2, 4, 128, 16),
+    "ragged chunks with empty ones": ([3, 0, 7, 1, 0], [3, 5, 130, 257, 0], 2, 3, 64, 32),
+    "one head to a group": ([5, 130, 1], [260, 130, 400], 3, 1, 128, 64),
+    "two-tile units": ([300, 70], [700, 70], 2, 4, 128, 64),
+    "two-tile units, small head dim": ([300, 70], [700, 333], 2, 4, 64, 128),
+    "more rows than keys": ([4, 2, 200], [2, 0, 90], 2, 2, 64, 16),
+    "odd group": ([129, 1, 64], [500, 1000, 64], 1, 7, 128, 32),
+    "group of 128": ([3, 1], [40, 200], 1, 128, 64, 16),
+    "group of 80": ([5, 2], [150, 20], 1, 80, 128, 64),
+    "long pages": ([1, 40], [600, 1100], 2, 5, 64, 512),
+    "long rows": ([2, 1], [2500, 1900], 1, 8, 128, 256),
+}
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_paged_matches_oracle(A, shape, causal, dtype):
+    c = Case(*SHAPES[shape], dtype, 40)
+    o, lse = A.attn_paged(*c.device(), causal=causal, max_q=max(max(c.n), 1))
+    _ok(A)
+    c.check(o, lse, causal)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("max_q", [None, 1, 3, 17, 40, 5000])
+def test_max_q_is_only_a_hint(A, max_q, d):
+    c = Case([1, 45, 0, 9, 1], [300, 77, 12, 513, 5], 2, 4, d, 32, torch.bfloat16, 50)
+    o, lse = A.attn_paged(*c.device(), causal=True, max_q=max_q)
+    _ok(A)
+    c.check(o, lse, True)
+
+
+@pytest.mark.parametrize("n", [1, 60])
+def test_heads_first_pages_and_strided_rows(A, n):
+    # pages hold [heads, slots, d]; q is part of a wider row, O is written into one
+    c = Case([n, n], [200, 129], 2, 4, 64, 32, torch.bfloat16, 60, heads_first=True, columns=3)
+    q, k, v, table, cu, kv = c.device()
+    wide = torch.zeros(q.shape[0], 12, 64, dtype=q.dtype, device="cuda")
+    wide[:, :8] = q
+    out = torch.zeros_like(wide)
+    o, lse = A.attn_paged(wide[:, :8], k, v, table[:, :max(1, table.shape[1] - 1)], cu, kv, causal=True, out=out[:, 2:10], max_q=n)
+    _ok(A)
+    c.check(o, lse, True)
+    assert torch.all(out[:, :2] == 0) and torch.all(out[:, 10:] == 0)
+
+
+def test_keys_and_values_interleaved_in_one_tensor(A):
+    c = Case([1, 2], [70, 100], 3, 2, 128, 16, torch.float16, 65)
+    q, k, v, table, cu, kv = c.device()
+    both = torch.stack([k.transpose(1, 2), v.transpose(1, 2)], dim=1).contiguous()  # [pages, 2, slot, head, d]
+    o, lse = A.attn_paged(q, both[:, 0].transpose(1, 2), both[:, 1].transpose(1, 2), table, cu, kv, causal=True)
+    _ok(A)
+    c.check(o, lse, True)
+
+
+@pytest.mark.parametrize("n", [1, 150])
+def test_padding_rows_stay_as_they_were(A, n):
+    c = Case([n, 2], [n + 30, 90], 2, 2, 64, 16, torch.bfloat16, 70, pad=9)
+    rows = int(c.cu[-1])
+    c.q[rows:] = float("nan")
+    out = torch.full(c.q.shape, 7.0, dtype=c.dtype, device="cuda")
+    lse = torch.full((4, rows + 9), 3.0, device="cuda")
+    A.attn_paged(*c.device(), causal=True, out=out, lse=lse, max_q=n)
+    _ok(A)
+    c.check(out, lse, True)
+    assert torch.all(out[rows:] == 7.0) and torch.all(lse[:, rows:] == 3.0)
+
+
+def test_one_table_for_every_sequence(A):
+    # a table stride of 0: all sequences attend to the same pages (an encoder's states)
+    c = Case([3, 1, 6], [90, 0, 0], 2, 2, 64, 32, torch.bfloat16, 75)
+    c.kv, c.table = [90, 90, 41], np.repeat(c.table[:1], 3, 0)
+    q, k, v, table, cu, kv = c.device()
+    o, lse = A.attn_paged(q, k, v, table[:1].expand(3, -1), cu, kv)
+    _ok(A)
+    c.check(o, lse, False)
+
+
+@pytest.mark.parametrize("n", [2, 140])
+def test_large_scores(A, n):
+    # q and k times sqrt(30): raw scores reach about +-90, where an unshifted fp32 exp overflows
+    c = Case([n, 1], [600, 300], 2, 4, 128, 64, torch.bfloat16, 80, mult=math.sqrt(30.0))
+    o, lse = A.attn_paged(*c.device(), causal=True, max_q=n)
+    _ok(A)
+    c.check(o, lse, True)
+
+
+def test_explicit_scale(A):
+    c = Case([2], [50], 1, 2, 64, 16, torch.float16, 85)
+    o, lse = A.attn_paged(*c.device(), causal=True, scale=0.31)
+    _ok(A)
+    c.check(o, lse, True, 0.31)
+
+
+def test_many_sequences(A):
+    rng = np.random.default_rng(3)
+    n, kv = rng.integers(0, 3, 700), rng.integers(0, 70, 700)
+    c = Case(n.tolist(), kv.tolist(), 1, 2, 64, 16, torch.bfloat16, 90)
+    o, lse = A.attn_paged(*c.device(), causal=True, max_q=2)
+    _ok(A)
+    c.check(o, lse, True)
+
+
+@pytest.mark.parametrize("n,kv", [([1] * 8, [4000, 10, 900, 1, 128, 2048, 77, 1500]), ([600, 1, 90], [1900, 2500, 90])])
+def test_same_bits_on_every_call_and_stream(A, n, kv):
+    c = Case(n, kv, 2, 4, 128, 64, torch.bfloat16, 95)
+    args = c.device()
+    o, lse = A.attn_paged(*args, causal=True, max_q=max(n))
+    _ok(A)
+    c.check(o, lse, True)
+    side = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for s in side:
+        s.wait_stream(torch.cuda.current_stream())
+    for i in range(6):  # two streams at once, a workspace to each call
+        got.append(A.attn_paged(*args, causal=True, max_q=max(n), stream=side[i % 2]))
+    _ok(A)
+    for o2, lse2 in got:
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_against_attn_fwd_and_decode(A):
+    # a whole prompt is the causal forward, its last rows are the causal decode
+    B, H, N, d, page = 1, 3, 384, 64, 128
+    q, k, v = (W.random_tensor((B, H, N, d), 100 + i, torch.bfloat16).cuda() for i in range(3))
+    want, want_lse = A.attn_fwd(q, k, v, causal=True)
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32, device="cuda")
+    kc, vc = (torch.empty(3, H, page, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for i, at in enumerate([2, 0, 1]):
+        kc[at], vc[at] = k[0, :, i * page:(i + 1) * page], v[0, :, i * page:(i + 1) * page]
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    o, lse = A.attn_paged(q[0].transpose(0, 1), kc, vc, table, i32(0, N), i32(N), causal=True)
+    od, lsed = A.attn_decode(q[:, :, -5:], k, v, causal=True)
+    o5, lse5 = A.attn_paged(q[0, :, -5:].transpose(0, 1), kc, vc, table, i32(0, 5), i32(N), causal=True)
+    _ok(A)
+    assert_close_bf16("O", o, to64(want[0].transpose(0, 1)))
+    assert_lse(lse, want_lse[0])
+    assert_close_bf16("O of the last rows", o5, to64(od[0].transpose(0, 1)))
+    assert_lse(lse5, lsed[0])
+
+
+def test_cache_beyond_32_bit_offsets(A):
+    # more than 2^32 elements a cache; the pages in use lie at both ends
+    hkv, page, d = 8, 256, 128
+    pages = (1 << 32) // (hkv * page * d) + 40
+    kv, table = [700, 300], np.array([[pages - 1, 3, pages - 2], [pages - 3, 0, UNUSED]])
+    k, v = (torch.empty(pages, page, hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    slots, rows = [], []
+    for b in range(2):
+        slots += [int(table[b, j // page]) * page + j % page for j in range(kv[b])]
+    rows = [W.random_tensor((len(slots), hkv, d), 110 + i, torch.bfloat16) for i in range(2)]
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")  # noqa: E731
+    A.attn_pages_write(rows[0].cuda(), rows[1].cuda(), i32(slots), k.transpose(1, 2), v.transpose(1, 2))
+    q = W.random_tensor((4, hkv * 2, d), 112, torch.bfloat16)
+    o, lse = A.attn_paged(q.cuda(), k.transpose(1, 2), v.transpose(1, 2), i32(table), i32([0, 1, 4]), i32(kv), causal=True)
+    _ok(A)
+    ks, vs = to64(rows[0]).transpose(1, 0, 2), to64(rows[1]).transpose(1, 0, 2)
+    for b, (r0, r1, k0, k1) in enumerate([(0, 1, 0, 700), (1, 4, 700, 1000)]):
+        qs = to64(q[r0:r1]).transpose(1, 0, 2)
+        O, L = ref.decode_forward(qs[None], np.repeat(ks[:, k0:k1], 2, 0)[None], np.repeat(vs[:, k0:k1], 2, 0)[None],
+                                  1 / math.sqrt(d), True)
+        assert_close_bf16("O", o[r0:r1], O[0].transpose(1, 0, 2))
+        assert_lse(lse[:, r0:r1], L[0])
+
+
+def test_captured_call_follows_the_lengths(A):
+    c = Case([1, 1, 1], [500, 40, 129], 2, 4, 64, 16, torch.bfloat16, 120)
+    q, k, v, table, cu, kv = c.device()
+    out, lse = torch.empty_like(q), torch.empty(8, 3, device="cuda")
+    ws = torch.empty(A.paged_workspace_size(q, k, v, table, cu, kv, max_q=1), dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=s):
+        A.attn_paged(q, k, v, table, cu, kv, causal=True, max_q=1, out=out, lse=lse, workspace=ws)
+    for lengths in ([500, 40, 129], [1, 33, 0], [16, 17, 128]):
+        c.kv = lengths
+        kv.copy_(torch.tensor(lengths, dtype=torch.int32))
+        g.replay()
+        _ok(A)
+        c.check(out, lse, True)
+
+
+@pytest.mark.parametrize("n", [1, 200])
+def test_bad_lengths_and_pages_are_reported(A, n):
+    # a page out of range, a length that the table cannot hold: no access follows them, attn_status
+    # tells, and the other sequences are right
+    c = Case([n, 1, n], [300, 90, 210], 2, 2, 64, 32, torch.bfloat16, 130)
+    q, k, v, table, cu, kv = c.device()
+    for spoil in ("page", "negative page", "length", "negative length"):
+        t2, kv2 = table.clone(), kv.clone()
+        if "page" in spoil:
+            t2[0, 2] = -5 if "negative" in spoil else k.shape[0]
+        else:
+            kv2[0] = -3 if "negative" in spoil else table.shape[1] * 32 + 1
+        o, lse = A.attn_paged(q, k, v, t2, cu, kv2, causal=True, max_q=n)
+        torch.cuda.synchronize()
+        assert A.attn_status() == A.ATTN_ERR_INVALID and "out of range" in A.last_error()
+        assert A.attn_status() == A.ATTN_OK
+        O, L = c.oracle(True)
+        rest = slice(int(c.cu[1]), int(c.cu[3]))
+        assert_close_bf16("O", o[rest], O[rest])
+        assert_lse(lse[:, rest], L[:, rest])
+
+
+# ---------------------------------------------------------------- writes
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows,hkv,d,page,heads_first", [(1, 1, 64, 16, False), (7, 1, 128, 32, True), (300, 3, 64, 16, True),
+                                                         (1000, 8, 128, 64, False), (65, 5, 128, 128, False), (9, 16, 128, 16, True)])
+def test_write_stores_rows_in_their_slots(A, rows, hkv, d, page, heads_first, dtype):
+    pages = rows // page + 5
+    shape = (pages, hkv, page, d) if heads_first else (pages, page, hkv, d)
+    fused = W.random_tensor((rows, hkv + 2, 2 * d), 200, dtype).cuda()  # k and v as parts of wider rows
+    k, v = fused[:, 1:hkv + 1, :d], fused[:, :hkv, d:]
+    k[0, 0, 0] = float("nan")
+    g = torch.Generator().manual_seed(rows)
+    slots = torch.randperm(pages * page, generator=g)[:rows].to(torch.int32)
+    slots[rows // 2::5] = -1
+    caches = [torch.full(shape, 9.0, dtype=dtype, device="cuda") for _ in range(2)]
+    views = [c if heads_first else c.transpose(1, 2) for c in caches]
+    A.attn_pages_write(k, v, slots.cuda(), *views)
+    _ok(A)
+    for src, got in ((k, views[0]), (v, views[1])):
+        want = torch.full((pages * page, hkv, d), 9.0, dtype=dtype)
+        keep = slots >= 0
+        want[slots[keep].long()] = src.cpu()[keep]
+        want = want.view(pages, page, hkv, d).transpose(1, 2)
+        assert torch.equal(got.cpu().contiguous().view(torch.int16), want.contiguous().view(torch.int16))
+
+
+def test_write_skips_and_reports_slots_beyond_the_cache(A):
+    k, v = (W.random_tensor((3, 2, 64), 210 + i, torch.bfloat16).cuda() for i in range(2))
+    caches = [torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    A.attn_pages_write(k, v, torch.tensor([5, 64, 2 ** 31 - 1], dtype=torch.int32, device="cuda"), *caches)
+    torch.cuda.synchronize()
+    assert A.attn_status() == A.ATTN_ERR_INVALID
+    assert torch.equal(caches[0][0, :, 5], k[0]) and torch.equal(caches[1][0, :, 5], v[0])
+    assert int((caches[0] != 0).any(-1).sum()) == 2
+
+
+# ---------------------------------------------------------------- tables
+def _i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def _filled_table(rng, lengths, page, cols, spare):
+    need = [(n + page - 1) // page for n in lengths]
+    order = rng.permutation(sum(need) + spare)
+    table, at = np.full((len(lengths), cols), -1, dtype=np.int64), 0
+    for b, m in enumerate(need):
+        table[b, :m] = order[at:at + m]
+        at += m
+    return table, order[at:].tolist()
+
+
+@pytest.mark.parametrize("seqs,most,page,pad", [(1, 1, 16, 0), (5, 3, 16, 4), (64, 40, 32, 0), (257, 9, 16, 300),
+                                                (600, 30, 64, 1), (3, 5000, 128, 17)])
+def test_plan_matches_oracle(A, seqs, most, page, pad):
+    rng = np.random.default_rng(seqs)
+    q_len, old = rng.integers(0, most + 1, seqs), rng.integers(0, 500, seqs)
+    old[rng.random(seqs) < 0.3] //= page
+    cols = int(max((old + q_len).max() + page - 1, page) // page) + 1
+    table, free = _filled_table(rng, old, page, cols, int(((q_len + page - 1) // page + 1).sum()))
+    total = int(q_len.sum()) + pad
+    want = paged.plan(q_len.tolist(), old.tolist(), table, free, len(free), page, total)
+    args = [_i32(q_len), _i32(old), _i32(table), _i32(free + [77, 78]), _i32([len(free)])]
+    for _ in range(2):  # the inputs stay as they are, so a second call gives the same
+        got = A.attn_pages_plan(*args, page, total)
+        _ok(A)
+        for name, g, w in zip(("cu_q", "new_len", "slots", "positions", "free_left"), got, want):
+            assert g.cpu().tolist() == (w if isinstance(w, list) else [w]), name
+        assert args[2].cpu().tolist() == [[int(x) for x in r] for r in want[5]]
+
+
+def test_plan_without_sequences_or_rows(A):
+    empty = _i32([]).view(-1)
+    cu, new, slots, pos, left = A.attn_pages_plan(empty, empty, _i32(np.zeros((0, 3))), _i32([4, 5]), _i32([2]), 16, 3)
+    _ok(A)
+    assert cu.tolist() == [0] and new.numel() == 0 and slots.tolist() == [-1] * 3 and pos.tolist() == [-1] * 3
+    assert left.tolist() == [2]
+    cu, new, slots, pos, left = A.attn_pages_plan(_i32([0, 0]), _i32([3, 0]), _i32([[1], [-1]]), empty, _i32([0]), 16, 0)
+    _ok(A)
+    assert cu.tolist() == [0, 0, 0] and new.tolist() == [3, 0] and slots.numel() == 0 and left.tolist() == [0]
+
+
+def test_plan_that_runs_out_of_pages(A):
+    args = ([20, 40, 1], [10, 0, 5], [[2, -1, -1], [-1, -1, -1], [0, -1, -1]], [8, 6])
+    want = paged.plan(*args, 2, 16, 61)
+    table = _i32(args[2])
+    got = A.attn_pages_plan(_i32(args[0]), _i32(args[1]), table, _i32(args[3]), _i32([2]), 16, 61)
+    _ok(A)
+    assert want[4] == -2 and got[4].tolist() == [-2]
+    assert got[2].tolist() == want[2] and table.tolist() == want[5]
+
+
+def test_plan_reports_lengths_out_of_range(A):
+    table, free = [[0, 1]], _i32([2, 3])
+    for q_len, old, total in ([40], [0], 40), ([-1], [4], 4), ([1], [-2], 4), ([5], [0], 3), ([2 ** 31 - 1], [2 ** 31 - 1], 8):
+        t = _i32(table)
+        A.attn_pages_plan(_i32(q_len), _i32(old), t, free, _i32([2]), 16, total)
+        torch.cuda.synchronize()
+        assert A.attn_status() == A.ATTN_ERR_INVALID
+    # a stack pointer beyond the stack, a page that the table does not name
+    for count, t, old in (9, [[0, 1]], 3), (2, [[-1, 1]], 3):
+        A.attn_pages_plan(_i32([14]), _i32([old]), _i32(t), free, _i32([count]), 16, 14)
+        torch.cuda.synchronize()
+        assert A.attn_status() == A.ATTN_ERR_INVALID
+
+
+@pytest.mark.parametrize("seqs,page,every", [(1, 16, 1), (9, 32, 2), (777, 16, 3), (5000, 16, 7), (40, 256, 1), (6, 16, 99)])
+def test_release_matches_oracle(A, seqs, page, every):
+    rng = np.random.default_rng(seqs + 1)
+    lengths = rng.integers(0, 900 if seqs < 1000 else 60, seqs)
+    cols = int(max(lengths.max() + page - 1, page) // page)
+    table, free = _filled_table(rng, lengths, page, cols, 11)
+    done = (np.arange(seqs) % every == every - 1).astype(int) * 3
+    room = int((table >= 0).sum())
+    want = paged.release(done, lengths, table, free + [0] * room, len(free), page)
+    stack = _i32(free + [0] * room)
+    new, left = A.attn_pages_release(_i32(done), _i32(lengths), _i32(table), stack, _i32([len(free)]), page)
+    _ok(A)
+    assert new.tolist() == want[0] and left.tolist() == [want[1]] and stack.tolist() == want[2]
+
+
+def test_release_reports_a_stack_that_cannot_hold_the_pages(A):
+    stack = _i32([5, 0, 0])
+    A.attn_pages_release(_i32([1]), _i32([64]), _i32([[1, 2, 3, 4]]), stack, _i32([1]), 16)
+    torch.cuda.synchronize()
+    assert A.attn_status() == A.ATTN_ERR_INVALID and stack.tolist() == [5, 1, 2]
+    empty = _i32([]).view(-1)
+    new, left = A.attn_pages_release(empty, empty, _i32(np.zeros((0, 2))), stack, _i32([3]), 16)
+    _ok(A)
+    assert new.numel() == 0 and left.tolist() == [3]
+
+
+# ---------------------------------------------------------------- all of it, as a server runs it
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64)])
+def test_serving_steps_match_attention_over_the_whole_sequences(A, d, page):
+    """Prompts come in chunks, sequences decode, end, and give their pages to new ones; after each
+    step every sequence's rows are checked against attention over all of its keys."""
+    hkv, group, columns, pages = 2, 3, 400 // page, 40 * 16 // page
+    dev = "cuda"
+    rng = np.random.default_rng(d)
+    k_cache, v_cache = (torch.full((pages, page, hkv, d), float("nan"), dtype=torch.bfloat16, device=dev).transpose(1, 2)
+                        for _ in range(2))
+    table, lens = _i32(np.full((3, columns), -1)), _i32([0, 0, 0])
+    free, count = _i32(rng.permutation(pages)), _i32([pages])
+    keys = [[np.zeros((hkv, 0, d))] * 2 for _ in range(3)]
+    for step, (q_len, done) in enumerate([([130, 0, 3], None), ([50, 20, 1], None), ([1, 1, 1], [0, 0, 1]), ([1, 1, 60], None),
+                                          ([1, 0, 1], [1, 0, 0]), ([90, 5, 1], None), ([1, 1, 1], None)]):
+        rows = sum(q_len) + step % 3
+        cu, lens, slots, pos, count = A.attn_pages_plan(_i32(q_len), lens, table, free, count, page, rows)
+        q, k, v = (W.random_tensor((rows, hkv * (group if i == 0 else 1), d), 300 + 10 * step + i, torch.bfloat16) for i in range(3))
+        A.attn_pages_write(k.to(dev), v.to(dev), slots, k_cache, v_cache)
+        o, lse = A.attn_paged(q.to(dev), k_cache, v_cache, table, cu, lens, causal=True, max_q=max(q_len))
+        _ok(A)
+        r0 = 0
+        for b, n in enumerate(q_len):
+            keys[b] = [np.concatenate([old, to64(x[r0:r0 + n]).transpose(1, 0, 2)], 1) for old, x in zip(keys[b], (k, v))]
+            if n:
+                O, L = ref.decode_forward(to64(q[r0:r0 + n]).transpose(1, 0, 2)[None], np.repeat(keys[b][0], group, 0)[None],
+                                          np.repeat(keys[b][1], group, 0)[None], 1 / math.sqrt(d), True)
+                assert_close_bf16(f"O step {step}", o[r0:r0 + n], O[0].transpose(1, 0, 2))
+                assert_lse(lse[:, r0:r0 + n], L[0])
+            r0 += n
+        assert lens.tolist() == [x[0].shape[1] for x in keys]
+        if done is not None:
+            lens, count = A.attn_pages_release(_i32(done), lens, table, free, count, page)
+            for b in range(3):
+                if done[b]:
+                    keys[b] = [x[:, :0] for x in keys[b]]
+        held = sum((x[0].shape[1] + page - 1) // page for x in keys)
+        _ok(A)
+        assert count.tolist() == [pages - held]
+
+
+def test_captured_decode_loop(A):
+    """One captured step (plan, write, attend, take the step) replayed across page ends."""
+    hkv, group, d, page, seqs = 1, 2, 64, 16, 3
+    rng = np.random.default_rng(8)
+    pages, start, steps = 30, [14, 31, 0], 20
+    k_cache, v_cache = (torch.full((pages, hkv, page, d), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table, lens = _i32(np.full((seqs, 8), -1)), _i32([0] * seqs)
+    free, count = _i32(rng.permutation(pages)), _i32([pages])
+    fill = [W.random_tensor((sum(start), hkv, d), 400 + i, torch.bfloat16) for i in range(2)]
+    _, lens2, slots, _, count2 = A.attn_pages_plan(_i32(start), lens, table, free, count, page, sum(start))
+    A.attn_pages_write(fill[0].cuda(), fill[1].cuda(), slots, k_cache, v_cache)
+    lens.copy_(lens2)
+    count.copy_(count2)
+    ones = _i32([1] * seqs)
+    q, k, v = (torch.zeros(seqs, hkv * (group if i == 0 else 1), d, dtype=torch.bfloat16, device="cuda") for i in range(3))
+
+    def one_step():
+        cu, new, slots, _, left = A.attn_pages_plan(ones, lens, table, free, count, page, seqs)
+        A.attn_pages_write(k, v, slots, k_cache, v_cache)
+        o, lse = A.attn_paged(q, k_cache, v_cache, table, cu, new, causal=True, max_q=1)
+        lens.copy_(new)
+        count.copy_(left)
+        return o, lse
+
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, lse = one_step()
+    at, keys = 0, []
+    for b in range(seqs):
+        keys.append([to64(x[at:at + start[b]]).transpose(1, 0, 2) for x in fill])
+        at += start[b]
+    for step in range(steps):
+        new = [W.random_tensor(t.shape, 410 + 3 * step + i, torch.bfloat16) for i, t in enumerate((q, k, v))]
+        for t, x in zip((q, k, v), new):
+            t.copy_(x)
+        g.replay()
+        _ok(A)
+        for b in range(seqs):
+            keys[b] = [np.concatenate([old, to64(x[b:b + 1]).transpose(1, 0, 2)], 1) for old, x in zip(keys[b], new[1:])]
+            O, L = ref.decode_forward(to64(new[0][b:b + 1]).transpose(1, 0, 2)[None], np.repeat(keys[b][0], group, 0)[None],
+                                      np.repeat(keys[b][1], group, 0)[None], 1 / math.sqrt(d), True)
+            assert_close_bf16("O", o[b:b + 1], O[0].transpose(1, 0, 2))
+            assert_lse(lse[:, b:b + 1], L[0])
+    assert lens.tolist() == [s + steps for s in start]
