@@ -1,7 +1,42 @@
-// attn_paged.cu — attention of a ragged batch of new tokens over a paged cache.
+// attn_paged.cu — attention of a ragged batch of new tokens over a paged cache, on
+// the tensor cores.
 //
-// One warp to a (query row, head): it walks the row's keys with the online softmax's
-// running max, sum and accumulator in fp32 registers.
+// Mathematics: per (sequence, key/value head) the G query heads of the group and a
+// run of new tokens are packed as rows of a 128-row M tile (row = token * G + head
+// in the group), so grouped heads share every key/value tile they read. A unit of
+// work is NT such tiles (1 when a whole sequence's rows fit one tile, as in decode;
+// 2 for prompt chunks, so that one tile's softmax overlaps the other's products)
+// against the sequence's key tiles of 128. The loop over key tiles is the online
+// softmax of the other forward kernels: S = Q K^T in tensor memory, P = 2^(S - m)
+// rounded to the 16-bit type, O += P V, with a reference max that moves only when
+// a tile's max exceeds it by more than 8 (log2 units).
+//
+// Work split: lengths are known on the device only, and ragged, so units are not
+// dealt out whole. All units lie one after another on a line, each as long as its
+// visible keys plus a constant for its start and end; CTA i of the grid takes the
+// i-th equal piece of the line, cut at key-tile borders. A CTA then holds part of
+// at most two units that others share (its first and its last) and writes their
+// partial states (m, l, divisor of o, o) to the workspace, at most two per CTA
+// whatever the problem; paged_combine_kernel merges them in the order of the
+// keys. Decode of a few long sequences, a single short one and a long prompt
+// chunk all fill the GPU the same way, and the order of every sum is fixed.
+//
+// A tile's keys are copied page by page with TMA (one box per page and 64
+// columns; the lanes of the producer warp each look one page up). The last tile's
+// rows beyond the sequence's length are not copied: scores there are masked by
+// selection, and a helper warp zeroes those rows of V in shared memory before the
+// P V product, since 0 * NaN from an unwritten slot would reach O.
+//
+// Warp roles, NT = 2 (12 warps): 0-3 and 4-7 softmax of tile 0 and 1 (one thread
+// per row), 8 producer, 9 MMA issuer (d = 64: of tile 0), 10 V tail, 11 MMA issuer of tile 1
+// (d = 64). NT = 1 (7 warps): 0-3 softmax (only those that hold rows work), 4
+// producer, 5 MMA issuer, 6 V tail.
+// Tensor memory (lane = row): S_t [128 t, +128), O_t [256 + d t, +d), and P_t in
+// columns of its own [384 + 64 t, +64) except for NT = 2 at d = 128, where the
+// columns run out and P_t overwrites S_t ("split P" in attn_fwd_sm103.cu has the
+// reasons for either order of products).
+#include <cuda_bf16.h>
+
 #include <cmath>
 #include <cstdint>
 
@@ -11,85 +46,963 @@
 namespace attn {
 namespace {
 
+using namespace ptx;
+
+constexpr int BM = 128;  // query rows per tile
+constexpr int BN = 128;  // keys per tile
+constexpr float kRescaleThreshold = 8.0f;
+constexpr int kUnitCost = 64;  // what a unit costs beyond its key tiles, in keys
 constexpr unsigned kFull = 0xffffffffu;
 
-struct PagedArgs {
-    attn_paged_params p;
-    int shift;
-    int* err;
+template <int D, int NT>
+struct Cfg {
+    static constexpr int kBoxes = D / 64;
+    static constexpr int kTileBytes = BM * D * 2;
+    static constexpr bool kSplit = D == 64 || NT == 1;  // P in tensor-memory columns of its own
+    static constexpr int kIssuers = kSplit ? NT : 1;
+    static constexpr int kStages = D == 64 ? 12 : (NT == 1 ? 6 : 4);  // K and V tiles in flight
+    static constexpr int kWarps = NT == 1 ? 7 : 12;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kProducer = 4 * NT, kIssuer = 4 * NT + 1, kTail = 4 * NT + 2;  // warps
+    // NT = 2: registers per thread after the rebalance, 2 x 128 x softmax + 128 x other = 384 x 168
+    static constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+    static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= 384 * 168, "register split");
+    static constexpr int kQOff = 0;
+    static constexpr int kKVOff = kQOff + NT * kTileBytes;
+    static constexpr int kBarOff = kKVOff + kStages * kTileBytes;
+    static constexpr int kSmemBytes = kBarOff + 1024 + 1024;  // barriers and schedule + alignment slack
+    static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(256) paged_simple_kernel(const PagedArgs a) {
-    ptx::grid_dep_launch();
-    ptx::grid_dep_wait();
-    constexpr int PER = D / 32;
-    const attn_paged_params& p = a.p;
-    const int lane = threadIdx.x & 31, h = blockIdx.y;
-    const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (t >= p.total_q || t >= p.cu_q[p.num_seqs]) return;
-    int lo = 0, hi = p.num_seqs;  // the last sequence that starts at or before t
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (p.cu_q[mid] <= t) lo = mid; else hi = mid;
+struct PagedDev {
+    int B, G, Hkv, T;
+    int tok_tile;     // tokens of a tile: its rows are tok_tile * G
+    int n_sm_warps;   // softmax warps that hold rows
+    int num_pages, page_size, shift, max_pages;
+    int causal;
+    float c;          // scale * log2(e)
+    const int32_t *cu_q, *kv_len, *table;
+    long long table_stride;
+    uint8_t* o;
+    float* lse;
+    long long o_sr, o_sh;  // elements
+    float* part;      // [grid][2][NT][tok_tile * G][D + 4]
+    int4* meta;       // [grid][2]: see Meta
+    int* err;
+    unsigned long long timeout_ns;
+};
+
+// What the combine kernel reads about a CTA's slot: x = 0 nothing, 1 a part, 2 the unit's last part;
+// y = first query row of the unit, z = its tokens, w = key/value head.
+enum : int { kNone = 0, kPart = 1, kLast = 2 };
+
+struct __align__(8) Shared {
+    uint64_t q_full, q_empty;
+    uint64_t kv_full[12], kv_empty[12], v_tail[12];
+    uint64_t s_full[2], p_full[2], o_full[2], s_free[2], pv_done[2];
+    uint64_t drain[2];
+    long long x0, x1, u0;  // this CTA's piece of the line, and where the unit that holds x0 starts
+    long long scan[12], total;
+    int b, h, blk;         // that unit
+    uint32_t tmem_base;
+    int abort_flag;
+};
+static_assert(sizeof(Shared) <= 1024, "barrier area");
+
+// ---------------------------------------------------------------- the line of units
+struct Seq {
+    int row0, n, len;  // first row of q, rows, keys; within the arrays whatever the lengths say
+};
+
+__device__ __forceinline__ Seq seq_of(const PagedDev& p, int b, bool* bad) {
+    const int c0 = p.cu_q[b], c1 = p.cu_q[b + 1], len = p.kv_len[b];
+    const long long most = (long long)p.max_pages << p.shift;
+    Seq s;
+    s.row0 = min(max(c0, 0), p.T);
+    s.n = min(max(c1, s.row0), p.T) - s.row0;
+    s.len = (int)min((long long)max(len, 0), most);
+    if (bad) *bad |= c0 < 0 || c1 < c0 || c1 > p.T || len < 0 || len > most || (b == 0 && c0 != 0);
+    return s;
+}
+
+// Keys that the last of a sequence's first `tok` rows sees.
+__device__ __forceinline__ int visible(const PagedDev& p, const Seq& s, int tok) {
+    return p.causal ? max(0, s.len - s.n + tok) : s.len;
+}
+
+// Cost of the first i units of one head (all but the sequence's last unit are full, so their visible
+// keys grow by `step` rows each, from where they are positive on).
+__device__ __forceinline__ long long cost_before(const PagedDev& p, const Seq& s, int step, long long i) {
+    if (!p.causal) return i * (s.len + kUnitCost);
+    const long long base = s.len - s.n;
+    const long long m = base >= 0 ? 1 : -base / step + 1;  // the first unit (from 1) with a visible key
+    long long sum = i * kUnitCost;
+    if (i >= m) sum += (i - m + 1) * base + step * (i * (i + 1) / 2 - m * (m - 1) / 2);
+    return sum;
+}
+
+__device__ __forceinline__ long long head_cost(const PagedDev& p, const Seq& s, int step) {
+    if (s.n == 0) return 0;
+    const int units = (s.n + step - 1) / step;
+    return cost_before(p, s, step, units - 1) + visible(p, s, s.n) + kUnitCost;
+}
+
+// Finds this CTA's piece of the line. All threads take part.
+template <int THREADS>
+__device__ __forceinline__ void locate(const PagedDev& p, int step, Shared& sh) {
+    constexpr int WARPS = THREADS / 32;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    bool bad = false;
+    long long mine = 0, sum = 0;
+    for (int b = tid; b < p.B; b += THREADS) {
+        mine = head_cost(p, seq_of(p, b, &bad), step) * p.Hkv;
+        sum += mine;
     }
-    const int start = p.cu_q[lo], n = p.cu_q[lo + 1] - start;
-    long long len = p.kv_len[lo];
-    const long long most = (long long)p.max_pages << a.shift;
-    bool bad = len < 0 || len > most;
-    len = len < 0 ? 0 : len > most ? most : len;
-    const long long end = p.causal ? min(len, len - n + (t - start) + 1) : len;
-    const int hk = h / (p.num_q_heads / p.num_kv_heads);
-    const uint16_t* q = static_cast<const uint16_t*>(p.q) + t * p.q_stride[0] + h * p.q_stride[1] + lane * PER;
-    float qv[PER], o[PER];
+    if (bad && blockIdx.x == 0) atomicCAS(p.err, 0, ATTN_ERR_INVALID);
 #pragma unroll
-    for (int e = 0; e < PER; ++e) {
-        qv[e] = ptx::h16_to_float<F16>(q[e]) * p.scale * kLog2e;
-        o[e] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    for (long long j = 0; j < end; ++j) {
-        const int page = p.block_table[lo * p.table_stride + (j >> a.shift)];
-        if (page < 0 || page >= p.num_pages) {
-            bad = true;
-            continue;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    if (lane == 0) sh.scan[warp] = sum;
+    if (tid == 0) sh.u0 = -1;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) total += sh.scan[w];
+    const long long each = total / gridDim.x, rest = total % gridDim.x, i = blockIdx.x;
+    const long long x0 = each * i + min(i, rest), x1 = each * (i + 1) + min(i + 1, rest);
+    long long before = 0;  // cost of the chunks of sequences before this one
+    for (int b0 = 0; b0 < p.B && x0 < x1; b0 += THREADS) {
+        const int b = b0 + tid;
+        if (p.B > THREADS) mine = b < p.B ? head_cost(p, seq_of(p, b, nullptr), step) * p.Hkv : 0;
+        if (b >= p.B) mine = 0;
+        long long x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(kFull, x, o);
+            if (lane >= o) x += u;
         }
-        const long long slot = j & (p.page_size - 1);
-        const uint16_t* k = static_cast<const uint16_t*>(p.k_cache) + page * p.k_stride[0] + hk * p.k_stride[1] + slot * p.k_stride[2] + lane * PER;
-        const uint16_t* v = static_cast<const uint16_t*>(p.v_cache) + page * p.v_stride[0] + hk * p.v_stride[1] + slot * p.v_stride[2] + lane * PER;
-        float s = 0.f;
+        __syncthreads();  // the last use of scan
+        if (lane == 31) sh.scan[warp] = x;
+        __syncthreads();
+        long long chunk = 0;
+        x += before;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) s = fmaf(qv[e], ptx::h16_to_float<F16>(k[e]), s);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
-        const float mn = fmaxf(m, s), alpha = ptx::ex2(m - mn), w = ptx::ex2(s - mn);
-        l = l * alpha + w;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) o[e] = fmaf(w, ptx::h16_to_float<F16>(v[e]), o[e] * alpha);
-        m = mn;
+        for (int w = 0; w < WARPS; ++w) {
+            if (w < warp) x += sh.scan[w];
+            chunk += sh.scan[w];
+        }
+        if (x - mine <= x0 && x0 < x) {
+            const Seq s = seq_of(p, b, nullptr);
+            const long long per_head = mine / p.Hkv, at = x0 - (x - mine);
+            const int h = (int)(at / per_head);
+            const long long in_head = at - h * per_head;
+            int lo = 0, hi = (s.n + step - 1) / step;  // the last unit that starts at or before in_head
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (cost_before(p, s, step, mid) <= in_head)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            sh.b = b;
+            sh.h = h;
+            sh.blk = lo;
+            sh.u0 = x - mine + h * per_head + cost_before(p, s, step, lo);
+        }
+        before += chunk;
+        if (before > x0) break;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + t * p.o_stride[0] + h * p.o_stride[1] + lane * PER);
+    if (tid == 0) {
+        sh.x0 = x0;
+        sh.x1 = x1;
+    }
+    __syncthreads();
+}
+
+struct Unit {
+    int h, row0, ntok;  // key/value head, first row of q, tokens
+    int base;           // position of the first token (causal), or the last key for all rows
+    int len;            // keys of the sequence
+    int b;
+    int k0, cnt0, cnt1, cnt_max;  // first key tile of this part, key tiles of either tile in it
+    bool first, last;   // this part holds the unit's first / last key tile
+    __device__ __forceinline__ int cnt(int t) const { return t == 0 ? cnt0 : cnt1; }
+};
+
+// Walks this CTA's units in order. Every warp role walks for itself and finds the same units.
+template <int NT>
+struct Walk {
+    const PagedDev& p;
+    long long u0, x0, x1;
+    int b, h, blk;
+    Seq s;
+
+    __device__ __forceinline__ Walk(const PagedDev& p_, const Shared& sh) : p(p_), x0(sh.x0), x1(sh.x1) {
+        b = sh.b;
+        h = sh.h;
+        blk = sh.blk;
+        u0 = sh.u0 < 0 ? x1 : sh.u0;
+        if (u0 < x1) s = seq_of(p, b, nullptr);
+    }
+    __device__ __forceinline__ bool next(Unit& w) {
+        const int step = NT * p.tok_tile;
+        while (u0 < x1) {
+            const int tok0 = blk * step;
+            w.ntok = min(step, s.n - tok0);
+            const int keys = visible(p, s, tok0 + w.ntok);
+            const int tiles = (keys + BN - 1) / BN;
+            const long long end = u0 + keys + kUnitCost;
+            const int k0 = x0 <= u0 ? 0 : min(tiles, (int)((x0 - u0 + BN / 2) / BN));
+            const int k1 = x1 >= end ? tiles : min(tiles, (int)((x1 - u0 + BN / 2) / BN));
+            const bool mine = k0 < k1 || (tiles == 0 && u0 >= x0);
+            if (mine) {
+                w.b = b;
+                w.h = h;
+                w.row0 = s.row0 + tok0;
+                w.len = s.len;
+                w.base = p.causal ? s.len - s.n + tok0 : s.len - 1;
+                w.k0 = k0;
+                w.first = k0 == 0;
+                w.last = k1 == tiles;
+                w.cnt_max = k1 - k0;
+                w.cnt0 = w.cnt_max;
+                w.cnt1 = 0;
+                if (NT == 2 && w.ntok > p.tok_tile) {  // causal: tile 0's rows may see fewer tiles
+                    w.cnt1 = w.cnt_max;
+                    w.cnt0 = max(0, min(k1, (visible(p, s, tok0 + p.tok_tile) + BN - 1) / BN) - k0);
+                }
+            }
+            u0 = end;
+            if (tok0 + step < s.n) {
+                ++blk;
+            } else {
+                blk = 0;
+                if (++h == p.Hkv) {
+                    h = 0;
+                    do {
+                        if (++b >= p.B) {
+                            u0 = x1;
+                            break;
+                        }
+                        s = seq_of(p, b, nullptr);
+                    } while (s.n == 0);
+                }
+            }
+            if (mine) return true;
+        }
+        return false;
+    }
+};
+
+// ---------------------------------------------------------------- helpers of the roles
+__device__ __forceinline__ uint64_t kmajor_desc(uint32_t tile, int kk) {
+    return sdesc_sw128(tile + (kk >> 2) * (BM * 128) + (kk & 3) * 32, 16, 1024);
+}
+__device__ __forceinline__ uint64_t vmajor_desc(uint32_t tile, int kk) {
+    return sdesc_sw128(tile + kk * (16 * 128), BN * 128, 1024);
+}
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
+    const uint32_t a = smem_u32(bar);
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait(a, parity))
+        if (globaltimer() - t0 > timeout_ns) break;
+}
+
+// The page that holds key `key` for this lane: its number, or num_pages (a row of zeros to TMA) for
+// one that the cache does not have.
+__device__ __forceinline__ int page_at(const PagedDev& p, int b, int key, bool* bad) {
+    const int page = p.table[b * p.table_stride + (key >> p.shift)];
+    if (page >= 0 && page < p.num_pages) return page;
+    *bad = true;
+    return p.num_pages;
+}
+
+template <int D, bool F16, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const PagedDev p) {
+    using C = Cfg<D, NT>;
+    constexpr uint32_t kIdescS = idesc_h16(BM, BN, false, false, F16);
+    constexpr uint32_t kIdescO = idesc_h16(BM, D, false, true, F16);
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Shared& bar = *reinterpret_cast<Shared*>(smem + C::kBarOff);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    WaitCtl wc{p.err, &bar.abort_flag, p.timeout_ns};
+
+    if (threadIdx.x == 0) {
+        bar.abort_flag = 0;
+        const uint32_t rows = 32u * (uint32_t)p.n_sm_warps;  // softmax threads of a tile
+        mbar_init(&bar.q_full, 1);
+        mbar_init(&bar.q_empty, C::kIssuers);
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&bar.kv_full[s], 1);
+            mbar_init(&bar.kv_empty[s], C::kIssuers);
+            mbar_init(&bar.v_tail[s], 1);
+        }
+        for (int t = 0; t < NT; ++t) {
+            mbar_init(&bar.s_full[t], 1);
+            mbar_init(&bar.p_full[t], rows);
+            mbar_init(&bar.o_full[t], 1);
+            mbar_init(&bar.s_free[t], rows);
+            mbar_init(&bar.pv_done[t], 1);
+            mbar_init(&bar.drain[t], 1);
+        }
+        fence_mbar_init();
+    }
+    if (warp == C::kIssuer) {
+        tmem_alloc(&bar.tmem_base, 512);
+        tmem_relinquish();
+    }
+    if (warp == C::kProducer && elect_one()) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
+    tc_fence_before();
+    // No global memory is touched above: from here on the previous kernel must be complete.
+    grid_dep_launch();
+    grid_dep_wait();
+    locate<C::kThreads>(p, NT * p.tok_tile, bar);  // ends in a block barrier
+    tc_fence_after();
+    const uint32_t tmem = bar.tmem_base;
+    const uint32_t sQ = smem_u32(smem + C::kQOff);
+    const uint32_t sKV = smem_u32(smem + C::kKVOff);
+
+    if (warp >= 4 * NT) {
+        if constexpr (NT == 2) regs_decrease<C::kOtherRegs>();
+        Walk<NT> walk(p, bar);
+        Unit w;
+        if (warp == C::kProducer) {
+            // ------------------------------------------------ Q / K / V producer
+            const int box_rows = min(p.page_size, BN);   // keys a box holds
+            const uint32_t box_bytes = (uint32_t)box_rows * 128;
+            const uint32_t q_bytes = (uint32_t)(p.tok_tile * p.G) * 128 * C::kBoxes;
+            const int my_key = lane * box_rows;          // of a tile, where this lane has a box
+            uint32_t it = 0, n_units = 0;
+            bool ok = true, bad = false;
+            while (ok && walk.next(w)) {
+                if (w.cnt_max == 0) continue;
+                int page = 0;  // this lane's page of the current tile
+                if (my_key < BN && w.k0 * BN + my_key < w.len) page = page_at(p, w.b, w.k0 * BN + my_key, &bad);
+                ok = mbar_wait_warp(&bar.q_empty, (n_units & 1) ^ 1, wc);
+                if (!ok) break;
+                ++n_units;
+                if (elect_one()) {
+                    const int nt = NT == 2 && w.ntok > p.tok_tile ? 2 : 1;
+                    mbar_arrive_expect_tx(&bar.q_full, nt * q_bytes);
+                    for (int t = 0; t < nt; ++t)
+                        for (int bx = 0; bx < C::kBoxes; ++bx)
+                            tma_load_4d(smem + C::kQOff + t * C::kTileBytes + bx * BM * 128, &tm_q, &bar.q_full, bx * 64,
+                                        0, w.row0 + t * p.tok_tile, w.h);
+                }
+                __syncwarp();
+                for (int j = w.k0; j < w.k0 + w.cnt_max && ok; ++j) {
+                    const int key0 = j * BN;
+                    const bool active = my_key < BN && key0 + my_key < w.len;
+                    const uint32_t boxes = __popc(__ballot_sync(kFull, active));
+                    const int slot_row = (key0 + my_key) & (p.page_size - 1);
+                    const int my_page = page;
+                    // the next tile's page, looked up while this one's copies are issued
+                    if (j + 1 < w.k0 + w.cnt_max && my_key < BN && key0 + BN + my_key < w.len)
+                        page = page_at(p, w.b, key0 + BN + my_key, &bad);
+                    const bool tail = key0 + BN > w.len;
 #pragma unroll
-    for (int e = 0; e < PER / 2; ++e) out[e] = ptx::pack_h16<F16>(o[2 * e] * inv, o[2 * e + 1] * inv);
-    if (lane == 0) p.lse[(long long)h * p.total_q + t] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
-    if (bad) atomicCAS(a.err, 0, ATTN_ERR_INVALID);
+                    for (int kv = 0; kv < 2; ++kv, ++it) {
+                        const uint32_t s = it % C::kStages;
+                        ok = mbar_wait_warp(&bar.kv_empty[s], ((it / C::kStages) & 1) ^ 1, wc);
+                        if (!ok) break;
+                        uint64_t* full = kv == 1 && tail ? &bar.v_tail[s] : &bar.kv_full[s];
+                        if (elect_one()) mbar_arrive_expect_tx(full, boxes * box_bytes * C::kBoxes);
+                        __syncwarp();
+                        if (active) {
+                            uint8_t* dst = smem + C::kKVOff + s * C::kTileBytes + my_key * 128;
+                            for (int bx = 0; bx < C::kBoxes; ++bx)
+                                tma_load_4d(dst + bx * BN * 128, kv == 0 ? &tm_k : &tm_v, full, bx * 64, slot_row, w.h,
+                                            my_page);
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            if (bad) atomicCAS(p.err, 0, ATTN_ERR_INVALID);
+            // every copy issued must land before the CTA exits
+            if (lane == 0) {
+                const uint32_t last = it < (uint32_t)C::kStages ? it : (uint32_t)C::kStages;
+                for (uint32_t i = it - last; i < it; ++i)
+                    drain_wait(&bar.kv_full[i % C::kStages], (i / C::kStages) & 1, p.timeout_ns);
+                if (n_units > 0) drain_wait(&bar.q_full, (n_units - 1) & 1, p.timeout_ns);
+            }
+        } else if (warp == C::kTail) {
+            // ------------------------------------------------ rows of V beyond the sequence, and the CTA's slots
+            uint32_t it = 0, phases = 0;  // phase of v_tail[s] in bit s
+            int4 slot0 = make_int4(kNone, 0, 0, 0), slot1 = slot0;
+            bool ok = true;
+            while (walk.next(w)) {
+                if (!(w.first && w.last)) {
+                    const int4 m = make_int4(w.last ? kLast : kPart, w.row0, w.ntok, w.h);
+                    if (w.first)
+                        slot1 = m;
+                    else
+                        slot0 = m;
+                }
+                it += 2 * w.cnt_max;
+                const int left = w.len - (w.k0 + w.cnt_max - 1) * BN;  // keys in the part's last tile
+                if (w.cnt_max == 0 || left >= BN || !ok) continue;
+                const uint32_t s = (it - 1) % C::kStages;  // the part's last V
+                ok = mbar_wait_warp(&bar.v_tail[s], (phases >> s) & 1, wc);
+                if (!ok) continue;  // the slots are still written
+                phases ^= 1u << s;
+                uint8_t* tile = smem + C::kKVOff + s * C::kTileBytes;
+                for (int bx = 0; bx < C::kBoxes; ++bx)
+                    for (int at = left * 128 + lane * 16; at < BN * 128; at += 32 * 16)
+                        *reinterpret_cast<uint4*>(tile + bx * BN * 128 + at) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (elect_one()) mbar_arrive(&bar.kv_full[s]);
+                __syncwarp();
+            }
+            if (lane < 2) p.meta[blockIdx.x * 2 + lane] = lane == 0 ? slot0 : slot1;
+        } else if (C::kSplit && (warp == C::kIssuer || (NT == 2 && warp == C::kIssuer + 2))) {
+            // ------------------------------------------------ MMA issuers, one per query tile
+            // S_t^{j+1} runs as soon as the softmax warps have read S_t^j. Each issuer walks every
+            // ring slot and releases it once, used or not.
+            const int t = warp == C::kIssuer ? 0 : 1;
+            const uint32_t tS = tmem + t * BN, tO = tmem + 256 + t * D, tP = tmem + 384 + t * 64;
+            uint32_t it = 0, n_units = 0, n_s = 0, n_p = 0;
+            bool ok = true;
+            while (ok && walk.next(w)) {
+                if (w.cnt_max == 0) continue;
+                const int cnt = w.cnt(t);
+                ok = mbar_wait_warp(&bar.q_full, n_units & 1, wc);
+                if (!ok) break;
+                ++n_units;
+                tc_fence_after();
+                if (cnt == 0) {  // nothing for this tile: release Q at once
+                    if (elect_one()) mbar_arrive(&bar.q_empty);
+                    __syncwarp();
+                }
+                for (int j = 0; j <= w.cnt_max && ok; ++j) {
+                    const uint32_t itK = it;  // ring slot of K_j; V_j follows it
+                    const uint32_t sK = itK % C::kStages, sV_prev = (itK + C::kStages - 1) % C::kStages;
+                    if (j < w.cnt_max) {
+                        ok = mbar_wait_warp(&bar.kv_full[sK], (itK / C::kStages) & 1, wc);
+                        if (!ok) break;
+                        if (j < cnt) {
+                            if (n_s > 0) {
+                                ok = mbar_wait_warp(&bar.s_free[t], (n_s - 1) & 1, wc);
+                                if (!ok) break;
+                            }
+                            tc_fence_after();
+                            const uint32_t qt = sQ + t * C::kTileBytes, kt = sKV + sK * C::kTileBytes;
+                            if (elect_one()) {
+#pragma unroll
+                                for (int kk = 0; kk < D / 16; ++kk)
+                                    mma_ss(tS, kmajor_desc(qt, kk), kmajor_desc(kt, kk), kIdescS, kk > 0 ? 1u : 0u);
+                                mma_commit(&bar.s_full[t]);
+                                if (j == cnt - 1) mma_commit(&bar.q_empty);  // last read of Q_t
+                            }
+                            __syncwarp();
+                            ++n_s;
+                        }
+                        if (elect_one()) mma_commit(&bar.kv_empty[sK]);
+                        __syncwarp();
+                    }
+                    if (j > 0) {  // V_{j-1} lives in the slot before K_j
+                        ok = mbar_wait_warp(&bar.kv_full[sV_prev], ((itK - 1) / C::kStages) & 1, wc);
+                        if (!ok) break;
+                        if (j <= cnt) {
+                            ok = mbar_wait_warp(&bar.p_full[t], n_p & 1, wc);
+                            if (!ok) break;
+                            ++n_p;
+                            tc_fence_after();
+                            const uint32_t vt = sKV + sV_prev * C::kTileBytes;
+                            if (elect_one()) {
+#pragma unroll
+                                for (int kk = 0; kk < BN / 16; ++kk)
+                                    mma_ts(tO, tP + kk * 8, vmajor_desc(vt, kk), kIdescO, (j > 1 || kk > 0) ? 1u : 0u);
+                                mma_commit(&bar.pv_done[t]);
+                            }
+                            __syncwarp();
+                        }
+                        if (elect_one()) mma_commit(&bar.kv_empty[sV_prev]);
+                        __syncwarp();
+                    }
+                    if (j < w.cnt_max) it += 2;
+                }
+            }
+            // every MMA this warp issued completes before TMEM is released
+            if (elect_one()) {
+                mma_commit(&bar.drain[t]);
+                drain_wait(&bar.drain[t], 0, p.timeout_ns);
+            }
+            __syncwarp();
+        } else if (!C::kSplit && warp == C::kIssuer) {
+            // ------------------------------------------------ MMA issuer of both tiles
+            uint32_t it = 0, n_units = 0, pcnt0 = 0, pcnt1 = 0;
+            bool ok = true;
+            while (ok && walk.next(w)) {
+                if (w.cnt_max == 0) continue;
+                ok = mbar_wait_warp(&bar.q_full, n_units & 1, wc);
+                if (!ok) break;
+                ++n_units;
+                tc_fence_after();
+                for (int j = 0; j <= w.cnt_max && ok; ++j) {
+                    const uint32_t itK = it;  // ring slot of K_j; V_j follows it
+                    const uint32_t sK = itK % C::kStages, sV_prev = (itK + C::kStages - 1) % C::kStages;
+                    if (j < w.cnt_max) {
+                        ok = mbar_wait_warp(&bar.kv_full[sK], (itK / C::kStages) & 1, wc);
+                        if (!ok) break;
+                    }
+                    if (j > 0) {  // V_{j-1} lives in the slot before K_j
+                        ok = mbar_wait_warp(&bar.kv_full[sV_prev], ((itK - 1) / C::kStages) & 1, wc);
+                        if (!ok) break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        if (!ok || w.cnt(t) == 0 || j > w.cnt(t)) continue;
+                        const uint32_t tS = tmem + t * BN, tO = tmem + 256 + t * D;
+                        if (j > 0) {
+                            // O_t += P_t^{j-1} V_{j-1}; the epilogue has read O_t before its threads
+                            // arrive on p_full for a new unit
+                            uint32_t& pcnt = t == 0 ? pcnt0 : pcnt1;
+                            ok = mbar_wait_warp(&bar.p_full[t], pcnt & 1, wc);
+                            if (!ok) continue;
+                            ++pcnt;
+                            tc_fence_after();
+                            const uint32_t vt = sKV + sV_prev * C::kTileBytes;
+                            if (elect_one()) {
+#pragma unroll
+                                for (int kk = 0; kk < BN / 16; ++kk)
+                                    mma_ts(tO, tS + kk * 8, vmajor_desc(vt, kk), kIdescO, (j > 1 || kk > 0) ? 1u : 0u);
+                            }
+                            __syncwarp();
+                        }
+                        if (j < w.cnt(t)) {
+                            const uint32_t qt = sQ + t * C::kTileBytes, kt = sKV + sK * C::kTileBytes;
+                            if (elect_one()) {
+#pragma unroll
+                                for (int kk = 0; kk < D / 16; ++kk)
+                                    mma_ss(tS, kmajor_desc(qt, kk), kmajor_desc(kt, kk), kIdescS, kk > 0 ? 1u : 0u);
+                                mma_commit(&bar.s_full[t]);
+                            }
+                            __syncwarp();
+                        } else {
+                            if (elect_one()) mma_commit(&bar.o_full[t]);  // last product of this tile issued
+                            __syncwarp();
+                        }
+                    }
+                    if (!ok) break;
+                    if (elect_one()) {
+                        if (j == w.cnt_max - 1) mma_commit(&bar.q_empty);  // last S of the part issued
+                        if (j < w.cnt_max) mma_commit(&bar.kv_empty[sK]);
+                        if (j > 0) mma_commit(&bar.kv_empty[sV_prev]);
+                    }
+                    __syncwarp();
+                    if (j < w.cnt_max) it += 2;
+                }
+            }
+            if (elect_one()) {
+                mma_commit(&bar.drain[0]);
+                drain_wait(&bar.drain[0], 0, p.timeout_ns);
+            }
+            __syncwarp();
+        }
+    } else {
+        if constexpr (NT == 2) regs_increase<C::kSoftmaxRegs>();
+        // ------------------------------------------------ softmax (thread = query row)
+        const int t = NT == 2 ? warp >> 2 : 0;
+        if ((warp & 3) < p.n_sm_warps) {
+            const int r = (warp & 3) * 32 + lane;
+            const int rows = p.tok_tile * p.G;
+            const int my_tok = t * p.tok_tile + r / p.G, my_head = r % p.G;
+            const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t tS = tmem + lane_off + t * BN;
+            const uint32_t tO = tmem + lane_off + 256 + t * D;
+            const uint32_t tP = C::kSplit ? tmem + lane_off + 384 + t * 64 : tS;
+            uint32_t scnt = 0, ocnt = 0;  // ocnt: phases of pv_done (split) or o_full
+            bool ok = true;
+            Walk<NT> walk(p, bar);
+            Unit w;
+            while (ok && walk.next(w)) {
+                const int cnt = w.cnt(t);
+                // keys this row sees, and those that the tile's first row sees
+                const int lim = p.causal ? min(w.len, w.base + my_tok + 1) : w.len;
+                const int lim_first = p.causal ? min(w.len, w.base + t * p.tok_tile + 1) : w.len;
+                float m_ref = -INFINITY, m_row = -INFINITY, l = 0.f;
+                for (int j = 0; j < cnt; ++j) {
+                    ok = mbar_wait(&bar.s_full[t], scnt & 1, wc);
+                    ok = __all_sync(kFull, ok);
+                    if (!ok) break;
+                    ++scnt;
+                    tc_fence_after();
+                    uint32_t su[BN];
+                    tmem_ld32_at<0>(tS + 0, su);
+                    tmem_ld32_at<32>(tS + 32, su);
+                    tmem_ld32_at<64>(tS + 64, su);
+                    tmem_ld32_at<96>(tS + 96, su);
+                    tmem_wait_ld();
+                    if (C::kSplit) {  // S_t is in registers: the next S_t may overwrite it
+                        tc_fence_before();
+                        mbar_arrive(&bar.s_free[t]);
+                    }
+                    const int key0 = (w.k0 + j) * BN;
+                    if (key0 + BN > lim_first) {
+                        const int out = lim - key0;  // first column this row does not see
+#pragma unroll
+                        for (int col = 0; col < BN; ++col)
+                            if (col >= out) su[col] = __float_as_uint(-INFINITY);
+                    }
+                    float mx[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        float m = fmaxf(__uint_as_float(su[16 * c]), __uint_as_float(su[16 * c + 1]));
+#pragma unroll
+                        for (int e = 2; e < 16; e += 2)
+                            m = fmax3(m, __uint_as_float(su[16 * c + e]), __uint_as_float(su[16 * c + e + 1]));
+                        mx[c] = m;
+                    }
+                    const float m_tile =
+                        fmaxf(fmax3(fmax3(mx[0], mx[1], mx[2]), mx[3], mx[4]), fmax3(mx[5], mx[6], mx[7])) * p.c;
+                    m_row = fmaxf(m_row, m_tile);
+                    float m_new = m_ref;
+                    if (m_tile > m_ref + kRescaleThreshold) m_new = m_tile;
+                    const bool moved = m_new != m_ref;
+                    const float alpha = moved ? ex2(m_ref - m_new) : 1.f;  // 0 when m_ref = -inf
+                    const bool rescale = j > 0 && __any_sync(kFull, moved && m_ref != -INFINITY);
+                    auto rescale_o = [&]() {
+#pragma unroll
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t ov[32];
+                            tmem_ld32(tO + c0, ov);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                const float2 r2 = fmul2(make_float2(__uint_as_float(ov[i]), __uint_as_float(ov[i + 1])),
+                                                        make_float2(alpha, alpha));
+                                ov[i] = __float_as_uint(r2.x);
+                                ov[i + 1] = __float_as_uint(r2.y);
+                            }
+                            tmem_st32(tO + c0, ov);
+                        }
+                    };
+                    // without split P the previous P V precedes this S in the MMA stream
+                    if (!C::kSplit && rescale) rescale_o();
+                    m_ref = m_new;
+                    const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
+                    const float2 cc2 = make_float2(p.c, p.c), nm2 = make_float2(neg_m, neg_m);
+                    float2 suma = make_float2(0.f, 0.f), sumb = make_float2(0.f, 0.f);
+                    if (C::kSplit) {
+#pragma unroll
+                        for (int i = 0; i < BN / 2; ++i) {
+                            const float2 x = ffma2(make_float2(__uint_as_float(su[2 * i]), __uint_as_float(su[2 * i + 1])),
+                                                   cc2, nm2);
+                            const float2 pp = make_float2(ex2(x.x), ex2(x.y));
+                            if (i & 1)
+                                sumb = fadd2(sumb, pp);
+                            else
+                                suma = fadd2(suma, pp);
+                            su[i] = pack_h16<F16>(pp.x, pp.y);
+                        }
+                        if (j > 0) {  // the product of tile j-1 has read P_t and written O_t
+                            ok = mbar_wait(&bar.pv_done[t], ocnt & 1, wc);
+                            ok = __all_sync(kFull, ok);
+                            if (!ok) break;
+                            ++ocnt;
+                            tc_fence_after();
+                            if (rescale) rescale_o();
+                        }
+                        tmem_st32_at<0>(tP + 0, su);
+                        tmem_st32_at<32>(tP + 32, su);
+                    } else {
+#pragma unroll
+                        for (int c0 = 0; c0 < BN; c0 += 32) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 x = ffma2(
+                                    make_float2(__uint_as_float(su[c0 + 2 * i]), __uint_as_float(su[c0 + 2 * i + 1])), cc2,
+                                    nm2);
+                                const float2 pp = make_float2(ex2(x.x), ex2(x.y));
+                                if (i & 1)
+                                    sumb = fadd2(sumb, pp);
+                                else
+                                    suma = fadd2(suma, pp);
+                                pk[i] = pack_h16<F16>(pp.x, pp.y);
+                            }
+                            tmem_st16(tS + c0 / 2, pk);
+                        }
+                    }
+                    l = l * alpha + ((suma.x + suma.y) + (sumb.x + sumb.y));
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(&bar.p_full[t]);
+                }
+                if (!ok) break;
+                if (cnt > 0) {
+                    ok = mbar_wait(C::kSplit ? &bar.pv_done[t] : &bar.o_full[t], ocnt & 1, wc);
+                    ok = __all_sync(kFull, ok);
+                    if (!ok) break;
+                    ++ocnt;
+                    tc_fence_after();
+                }
+                const bool held = r < rows && my_tok < w.ntok;
+                const float den = o_divisor<F16>(l, m_row, m_ref);
+                if (w.first && w.last) {
+                    const float inv = den > 0.f ? 1.f / den : 0.f;
+                    const long long row = w.row0 + my_tok, head = w.h * p.G + my_head;
+                    uint16_t* orow = reinterpret_cast<uint16_t*>(p.o) + row * p.o_sr + head * p.o_sh;
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t ov[32];
+                        if (cnt > 0) {
+                            tmem_ld32(tO + c0, ov);
+                            tmem_wait_ld();
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) ov[i] = 0;
+                        }
+                        if (held) {
+                            uint4* dst = reinterpret_cast<uint4*>(orow + c0);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                uint4 v;
+                                v.x = pack_h16<F16>(__uint_as_float(ov[8 * q + 0]) * inv, __uint_as_float(ov[8 * q + 1]) * inv);
+                                v.y = pack_h16<F16>(__uint_as_float(ov[8 * q + 2]) * inv, __uint_as_float(ov[8 * q + 3]) * inv);
+                                v.z = pack_h16<F16>(__uint_as_float(ov[8 * q + 4]) * inv, __uint_as_float(ov[8 * q + 5]) * inv);
+                                v.w = pack_h16<F16>(__uint_as_float(ov[8 * q + 6]) * inv, __uint_as_float(ov[8 * q + 7]) * inv);
+                                dst[q] = v;
+                            }
+                        }
+                    }
+                    if (held) p.lse[head * p.T + row] = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
+                } else {
+                    // the part's state of this row; a row without keys in it is m = -inf, and its o is not read
+                    float* rec = p.part + (((long long)(blockIdx.x * 2 + (w.first ? 1 : 0)) * NT + t) * rows + r) * (D + 4);
+                    if (held)
+                        *reinterpret_cast<float4*>(rec) = make_float4(l > 0.f ? m_ref : -INFINITY, l, den, 0.f);
+                    if (cnt > 0) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t ov[32];
+                            tmem_ld32(tO + c0, ov);
+                            tmem_wait_ld();
+                            if (held) {
+                                float4* dst = reinterpret_cast<float4*>(rec + 4 + c0);
+#pragma unroll
+                                for (int q = 0; q < 8; ++q)
+                                    dst[q] = make_float4(__uint_as_float(ov[4 * q]), __uint_as_float(ov[4 * q + 1]),
+                                                         __uint_as_float(ov[4 * q + 2]), __uint_as_float(ov[4 * q + 3]));
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == C::kIssuer) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- merging parts
+struct CombineArgs {
+    const float* part;
+    const int4* meta;
+    int ctas;            // of the split pass
+    int tiles, rows;     // tiles of a unit, rows of a tile
+    int tok_tile, G, T;
+    uint8_t* o;
+    float* lse;
+    long long o_sr, o_sh;
+    int rows_per_block;
+};
+
+constexpr int kCombineThreads = 256;
+
+// Block (e, y) merges rows [y * rows_per_block, ...) of the unit whose last part CTA e wrote, if there
+// is one: its first part is in slot 1 of the nearest CTA before e that has one, the parts between in
+// the slots 0. A warp takes a row; w_s = 2^(m_s - M) as in the merge of tiles, in the order of the keys.
+template <int D, bool F16>
+__global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const CombineArgs a) {
+    grid_dep_launch();
+    grid_dep_wait();
+    constexpr int PER = D / 32;
+    const int e = blockIdx.x;
+    const int4 unit = a.meta[e * 2];
+    if (unit.x != kLast) return;
+    __shared__ int s_first;
+    extern __shared__ uint8_t s_has[];  // CTA c's slot 0 holds a part
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) s_first = 0;
+    __syncthreads();
+    for (int c = tid; c < e; c += kCombineThreads) {
+        s_has[c] = a.meta[c * 2].x != kNone;
+        if (a.meta[c * 2 + 1].x != kNone) atomicMax(&s_first, c);
+    }
+    if (tid == 0) s_has[e] = 1;
+    __syncthreads();
+    const int first = s_first;
+    const long long slot = (long long)a.tiles * a.rows * (D + 4);  // floats of a slot
+    const int row_end = min(a.tiles * a.rows, (int)(blockIdx.y + 1) * a.rows_per_block);
+    for (int row = blockIdx.y * a.rows_per_block + warp; row < row_end; row += kCombineThreads / 32) {
+        const int t = row / a.rows, r = row % a.rows;
+        const int tok = t * a.tok_tile + r / a.G;
+        if (tok >= unit.z) continue;
+        const float* base = a.part + (long long)row * (D + 4);
+        auto rec = [&](int c) { return base + (c * 2 + (c == first ? 1 : 0)) * slot; };
+        float M = -INFINITY;
+        for (int c = first + lane; c <= e; c += 32)
+            if (c == first || s_has[c]) M = fmaxf(M, rec(c)[0]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+        float L = 0.f, Lo = 0.f, out[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) out[i] = 0.f;
+        if (M != -INFINITY) {
+            for (int c = first; c <= e; ++c) {
+                if (c != first && !s_has[c]) continue;
+                const float* x = rec(c);
+                const float m = x[0];
+                if (m == -INFINITY) continue;  // no key of this row: its o was not written
+                const float w = ex2(m - M);
+                L += w * x[1];
+                Lo += w * x[2];
+#pragma unroll
+                for (int i = 0; i < PER; ++i) out[i] = fmaf(w, x[4 + lane * PER + i], out[i]);
+            }
+        }
+        const float inv = Lo > 0.f ? 1.f / Lo : 0.f;
+        const long long q_row = unit.y + tok, head = unit.w * a.G + r % a.G;
+        uint16_t* orow = reinterpret_cast<uint16_t*>(a.o) + q_row * a.o_sr + head * a.o_sh;
+        if constexpr (PER == 2) {
+            *reinterpret_cast<uint32_t*>(orow + lane * 2) = pack_h16<F16>(out[0] * inv, out[1] * inv);
+        } else {
+            *reinterpret_cast<uint2*>(orow + lane * 4) =
+                make_uint2(pack_h16<F16>(out[0] * inv, out[1] * inv), pack_h16<F16>(out[2] * inv, out[3] * inv));
+        }
+        if (lane == 0) a.lse[head * a.T + q_row] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+    }
+}
+
+// ---------------------------------------------------------------- host side
+// The tile shape of a call. One tile per unit while the rows that a sequence is expected to bring fit
+// it, so that decode does not carry an empty second tile; two beyond.
+struct Plan {
+    int tiles, tok_tile, rows;
+    size_t meta_bytes, bytes;
+};
+
+Plan plan_of(const attn_paged_params& p, int num_sms) {
+    const int G = p.num_q_heads / p.num_kv_heads;
+    Plan pl;
+    pl.tiles = (long long)p.max_q * G > BM ? 2 : 1;
+    pl.tok_tile = BM / G;
+    if (pl.tiles == 1 && p.max_q < pl.tok_tile) pl.tok_tile = p.max_q;
+    pl.rows = pl.tok_tile * G;
+    pl.meta_bytes = ((size_t)num_sms * 2 * sizeof(int4) + 255) / 256 * 256;
+    pl.bytes = pl.meta_bytes + (size_t)num_sms * 2 * pl.tiles * pl.rows * (p.d + 4) * sizeof(float);
+    return pl;
+}
+
+// 4-D map of 16-bit elements over the given extents, dimension 0 contiguous, 64-column boxes.
+CUresult encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, int32_t dtype, const void* base,
+                const cuuint64_t (&dims)[4], const int64_t (&st)[3], cuuint32_t box1, cuuint32_t box2) {
+    cuuint64_t strides[3];
+    for (int i = 0; i < 3; ++i) strides[i] = dims[i + 1] > 1 ? (cuuint64_t)st[i] * 2 : 16;  // unread over an extent of 1
+    const cuuint32_t box[4] = {64, box1, box2, 1}, es[4] = {1, 1, 1, 1};
+    return enc(m, dtype == ATTN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+               const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+template <int D, bool F16, int NT>
+cudaError_t launch_tc(const CUtensorMap (&maps)[3], const PagedDev& p, int grid, cudaStream_t s) {
+    using C = Cfg<D, NT>;
+    const cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D, F16, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(paged_tc_kernel<D, F16, NT>, dim3(grid), dim3(C::kThreads), C::kSmemBytes, s, maps[0], maps[1],
+                      maps[2], p);
+}
+
+template <int D, bool F16>
+cudaError_t launch_both(const CUtensorMap (&maps)[3], const PagedDev& p, const Plan& pl, int grid, cudaStream_t s) {
+    const cudaError_t e = pl.tiles == 1 ? launch_tc<D, F16, 1>(maps, p, grid, s) : launch_tc<D, F16, 2>(maps, p, grid, s);
+    if (e != cudaSuccess) return e;
+    CombineArgs a{};
+    a.part = p.part;
+    a.meta = p.meta;
+    a.ctas = grid;
+    a.tiles = pl.tiles;
+    a.rows = pl.rows;
+    a.tok_tile = p.tok_tile;
+    a.G = p.G;
+    a.T = p.T;
+    a.o = p.o;
+    a.lse = p.lse;
+    a.o_sr = p.o_sr;
+    a.o_sh = p.o_sh;
+    a.rows_per_block = pl.tiles == 1 ? kCombineThreads / 32 : kCombineThreads / 8;
+    const int chunks = (pl.tiles * pl.rows + a.rows_per_block - 1) / a.rows_per_block;
+    return launch_pdl(paged_combine_kernel<D, F16>, dim3(grid, chunks), dim3(kCombineThreads), (size_t)grid, s, a);
 }
 
 }  // namespace
 
-size_t paged_workspace_bytes(const attn_paged_params&, int) { return 256; }
+size_t paged_workspace_bytes(const attn_paged_params& p, int num_sms) { return plan_of(p, num_sms).bytes; }
 
-cudaError_t launch_paged(const attn_paged_params& p, const LaunchCommon& lc, cudaStream_t s) {
-    PagedArgs a{};
-    a.p = p;
+attn_status_t launch_paged(const attn_paged_params& p, const LaunchCommon& lc, cudaStream_t s) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc;
+    const attn_status_t st = map_encoder(&enc);
+    if (st != ATTN_OK) return st;
+    const Plan pl = plan_of(p, lc.num_sms);
+    const int G = p.num_q_heads / p.num_kv_heads;
+    CUtensorMap maps[3];
+    // q as (column, head in the group, row, key/value head); the caches as (column, slot, head, page)
+    const cuuint64_t qd[4] = {(cuuint64_t)p.d, (cuuint64_t)G, (cuuint64_t)p.total_q, (cuuint64_t)p.num_kv_heads};
+    const int64_t qs[3] = {p.q_stride[1], p.q_stride[0], p.q_stride[1] * G};
+    const cuuint64_t cd[4] = {(cuuint64_t)p.d, (cuuint64_t)p.page_size, (cuuint64_t)p.num_kv_heads, (cuuint64_t)p.num_pages};
+    const int64_t ks[3] = {p.k_stride[2], p.k_stride[1], p.k_stride[0]}, vs[3] = {p.v_stride[2], p.v_stride[1], p.v_stride[0]};
+    const cuuint32_t box_rows = (cuuint32_t)(p.page_size < BN ? p.page_size : BN);
+    CUresult r = encode(enc, &maps[0], p.dtype, p.q, qd, qs, (cuuint32_t)G, (cuuint32_t)pl.tok_tile);
+    if (r == CUDA_SUCCESS) r = encode(enc, &maps[1], p.dtype, p.k_cache, cd, ks, box_rows, 1);
+    if (r == CUDA_SUCCESS) r = encode(enc, &maps[2], p.dtype, p.v_cache, cd, vs, box_rows, 1);
+    if (r != CUDA_SUCCESS) return report_error(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled(attn_paged) failed with %d", (int)r);
+    PagedDev a{};
+    a.B = p.num_seqs;
+    a.G = G;
+    a.Hkv = p.num_kv_heads;
+    a.T = p.total_q;
+    a.tok_tile = pl.tok_tile;
+    a.n_sm_warps = (pl.rows + 31) / 32;
+    a.num_pages = p.num_pages;
+    a.page_size = p.page_size;
     while ((1 << a.shift) < p.page_size) ++a.shift;
+    a.max_pages = p.max_pages;
+    a.causal = p.causal;
+    a.c = p.scale * kLog2e;
+    a.cu_q = p.cu_q;
+    a.kv_len = p.kv_len;
+    a.table = p.block_table;
+    a.table_stride = p.table_stride;
+    a.o = static_cast<uint8_t*>(p.o);
+    a.lse = p.lse;
+    a.o_sr = p.o_stride[0];
+    a.o_sh = p.o_stride[1];
+    a.meta = static_cast<int4*>(p.workspace);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + pl.meta_bytes);
     a.err = lc.err;
+    a.timeout_ns = lc.timeout_ns;
     const bool f16 = p.dtype == ATTN_F16;
-    const dim3 grid((p.total_q + 7) / 8, p.num_q_heads);
-    auto k = p.d == 64 ? (f16 ? paged_simple_kernel<64, true> : paged_simple_kernel<64, false>)
-                       : (f16 ? paged_simple_kernel<128, true> : paged_simple_kernel<128, false>);
-    return launch_pdl(k, grid, dim3(256), 0, s, a);
+    const cudaError_t e =
+        p.d == 64 ? (f16 ? launch_both<64, true>(maps, a, pl, lc.num_sms, s) : launch_both<64, false>(maps, a, pl, lc.num_sms, s))
+                  : (f16 ? launch_both<128, true>(maps, a, pl, lc.num_sms, s)
+                         : launch_both<128, false>(maps, a, pl, lc.num_sms, s));
+    return e == cudaSuccess ? ATTN_OK : report_error(ATTN_ERR_CUDA, "attn_paged launch: %s", cudaGetErrorString(e));
 }
 
 }  // namespace attn

@@ -131,7 +131,7 @@ attn_status_t attn_paged(const attn_paged_params* p, void* stream) {
     if (!p->workspace || p->workspace_bytes < need)
         return report_error(ATTN_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", p->workspace_bytes, need);
     if (misaligned(p->workspace, 256)) return report_error(ATTN_ERR_ALIGN, "workspace is not 256-byte aligned");
-    return launched(launch_paged(*p, lc, static_cast<cudaStream_t>(stream)), "attn_paged");
+    return launch_paged(*p, lc, static_cast<cudaStream_t>(stream));
 }
 
 attn_status_t attn_pages_write(const attn_pages_write_params* p, void* stream) {

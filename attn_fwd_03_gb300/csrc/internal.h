@@ -141,7 +141,7 @@ cudaError_t launch_bwd_dq(const attn_bwd_params& p, const BwdMaps& maps, const B
 
 // attn_paged.cu — attention over a paged cache.
 size_t paged_workspace_bytes(const attn_paged_params& p, int num_sms);
-cudaError_t launch_paged(const attn_paged_params& p, const LaunchCommon& lc, cudaStream_t s);
+attn_status_t launch_paged(const attn_paged_params& p, const LaunchCommon& lc, cudaStream_t s);
 
 // attn_pages.cu — the paged cache's tables and writes.
 cudaError_t launch_pages_write(const attn_pages_write_params& p, const LaunchCommon& lc, cudaStream_t s);
