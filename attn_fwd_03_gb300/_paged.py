@@ -8,7 +8,8 @@ from __future__ import annotations
 
 import ctypes
 import math
-from typing import Optional, Tuple
+import struct
+from typing import Dict, Optional, Tuple
 
 import torch
 
@@ -64,98 +65,92 @@ class PagesReleaseParams(ctypes.Structure):
     ]
 
 
-for _name, _params in (("attn_paged", PagedParams), ("attn_pages_write", PagesWriteParams),
-                       ("attn_pages_plan", PagesPlanParams), ("attn_pages_release", PagesReleaseParams)):
-    _entry = getattr(lib, _name)
-    _entry.argtypes = [ctypes.POINTER(_params), ctypes.c_void_p]
+def _packer(params) -> struct.Struct:
+    """Packs a parameter struct from plain numbers, its array fields spelled out (NULL is 0). One pack
+    call costs about a tenth of filling the ctypes struct, and a decode step is paced by the host."""
+    codes = {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_void_p: "P", ctypes.c_size_t: "N"}
+    fmt = "".join(codes[kind] if kind in codes else codes[kind._type_] * kind._length_ for _, kind in params._fields_)
+    packer = struct.Struct("@" + fmt + "0q")
+    assert packer.size == ctypes.sizeof(params)
+    return packer
+
+
+_PAGED, _WRITE, _PLAN, _RELEASE = map(_packer, (PagedParams, PagesWriteParams, PagesPlanParams, PagesReleaseParams))
+
+# the struct is passed as packed bytes or by reference
+for _entry in (lib.attn_paged, lib.attn_pages_write, lib.attn_pages_plan, lib.attn_pages_release):
+    _entry.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     _entry.restype = ctypes.c_int
-lib.attn_paged_workspace_size.argtypes = [ctypes.POINTER(PagedParams)]
+lib.attn_paged_workspace_size.argtypes = [ctypes.c_void_p]
 lib.attn_paged_workspace_size.restype = ctypes.c_size_t
 
-
-def _shape(name: str, t: torch.Tensor, *want: int) -> None:
-    """want: one extent per dimension, -1 for any."""
-    if t.dim() != len(want) or any(w >= 0 and s != w for s, w in zip(t.shape, want)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
-                         f"[{', '.join('any' if w < 0 else str(w) for w in want)}]")
+_INT32 = torch.int32
+_TYPES = {torch.bfloat16: _dtype_code(torch.bfloat16), torch.float16: _dtype_code(torch.float16)}
 
 
-def _ints(name: str, t: torch.Tensor, *want: int) -> None:
-    if t.dtype != torch.int32:
-        raise TypeError(f"{name} must be int32, got {t.dtype}")
-    _shape(name, t, *want)
-    if t.numel() > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must be contiguous along its last dimension")
+def _is_ints(t: torch.Tensor, shape: tuple) -> bool:
+    return t.dtype is _INT32 and t.shape == shape and (t.is_contiguous() or t.stride(-1) == 1)
 
 
-def _vectors(name: str, t: torch.Tensor, dtype: torch.dtype, *want: int) -> None:
+def _is_rows(t: torch.Tensor, dtype: torch.dtype, shape: tuple) -> bool:
+    return t.dtype is dtype and t.shape == shape and (t.stride()[-1] == 1 or t.numel() == 0)
+
+
+def _refuse(name: str, t: torch.Tensor, dtype: torch.dtype, shape) -> None:
+    """Says what is wrong with a tensor that one of the checks above turned down."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    _shape(name, t, *want)
-    if t.stride(-1) != 1:
-        raise ValueError(f"{name} must be contiguous along its last dimension")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous along its last dimension")
 
 
-def _device(first: torch.Tensor, *others: torch.Tensor) -> torch.device:
-    dev = first.device
-    for t in others:
-        if t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device} in one call")
-    if dev.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device, got {dev}")
+def _need_dims(name: str, t: torch.Tensor, dims: int) -> None:
+    if t.dim() != dims:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {dims} dimensions")
+
+
+def _type_code(name: str, t: torch.Tensor) -> int:
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def _device(*tensors: torch.Tensor) -> int:
+    """The index of the CUDA device that all tensors are on."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev or not t.is_cuda:
+            raise ValueError(f"tensors must be on one CUDA device, got {sorted({str(x.device) for x in tensors})}")
     return dev
 
 
-def _caches(k_cache: torch.Tensor, v_cache: torch.Tensor, dtype: torch.dtype, heads: int, d: int) -> None:
-    _vectors("k_cache", k_cache, dtype, -1, heads, -1, d)
-    _vectors("v_cache", v_cache, dtype, k_cache.shape[0], heads, k_cache.shape[2], d)
+def _guard(dev: int, stream):
+    """What to enter for a call on `stream` (default: the current stream of the tensors' device): that
+    stream and its device made current, so that what the call allocates belongs to the stream that uses
+    it. None where they are current already."""
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"stream of {stream.device} given for tensors on cuda:{dev}")
+        return torch.cuda.stream(stream)
+    if dev != torch._C._cuda_getDevice():
+        return torch.cuda.device(dev)
+    return None
 
 
-class _Launch:
-    """Runs a call on `stream` (default: the current stream of the tensors' device) with that stream
-    and its device current, so that what the call allocates belongs to the stream that uses it."""
-
-    def __init__(self, dev: torch.device, stream):
-        self.dev, self.stream = dev, stream
-        if stream is not None:
-            if stream.device != dev:
-                raise ValueError(f"stream of {stream.device} given for tensors on {dev}")
-            self.guard = torch.cuda.stream(stream)
-        elif dev.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(dev)
-        else:
-            self.guard = None
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        if self.stream is None:
-            self.stream = torch.cuda.current_stream()
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def empty(self, shape, dtype: torch.dtype) -> torch.Tensor:
-        return torch.empty(shape, dtype=dtype, device=self.dev)
-
-    def call(self, entry, params) -> None:
-        _check(entry(ctypes.byref(params), ctypes.c_void_p(self.stream.cuda_stream)))
+def _guarded(call, dev: int, stream, *args):
+    guard = _guard(dev, stream)
+    if guard is None:
+        return call(dev, *args)
+    with guard:
+        return call(dev, *args)
 
 
-def paged_params(q, k_cache, v_cache, block_table, cu_q, kv_len, out, lse, scale: float, causal: bool,
-                 max_q: int) -> PagedParams:
-    """Fill attn_paged_params; out and lse may be None (attn_paged_workspace_size reads sizes only)."""
-    total_q, hq, d = q.shape
-    o = q if out is None else out
-    qs, os_, ks, vs = q.stride(), o.stride(), k_cache.stride(), v_cache.stride()
-    return PagedParams(
-        block_table.shape[0], hq, k_cache.shape[1], d, total_q, max_q, k_cache.shape[0], k_cache.shape[2],
-        block_table.shape[1], _dtype_code(q.dtype), 1 if causal else 0, scale, _i32x2(0, 0),
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), q.data_ptr() if lse is None else lse.data_ptr(),
-        cu_q.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(), block_table.stride(0) if block_table.shape[0] > 1 else 0,
-        _i64x2(qs[0], qs[1]), _i64x2(os_[0], os_[1]), _i64x3(*ks[:3]), _i64x3(*vs[:3]), None, 0)
+def _launch(entry, dev: int, packed: bytes) -> None:
+    status = entry(packed, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        _check(status)
 
 
 def _default_max_q(total_q: int, num_seqs: int) -> int:
@@ -163,12 +158,52 @@ def _default_max_q(total_q: int, num_seqs: int) -> int:
     return max(1, total_q - num_seqs + 1)
 
 
+def _pack_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, out, lse, scale, causal, max_q, workspace, nbytes) -> bytes:
+    total_q, hq, d = q.shape
+    num_seqs, columns = block_table.shape
+    pages, hkv, page_size, _ = k_cache.shape
+    qr, qh, _ = q.stride()
+    orow, oh, _ = out.stride()
+    kp, kh, ks, _ = k_cache.stride()
+    vp, vh, vs, _ = v_cache.stride()
+    return _PAGED.pack(num_seqs, hq, hkv, d, total_q, max_q, pages, page_size, columns, _TYPES[q.dtype],
+                       1 if causal else 0, scale, 0, 0, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                       out.data_ptr(), lse.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(),
+                       block_table.stride(0), qr, qh, orow, oh, kp, kh, ks, vp, vh, vs, workspace, nbytes)
+
+
 def paged_workspace_size(q, k_cache, v_cache, block_table, cu_q, kv_len, *, max_q: Optional[int] = None) -> int:
     """Bytes of workspace attn_paged needs for these shapes."""
     if max_q is None:
         max_q = _default_max_q(q.shape[0], block_table.shape[0])
-    return int(lib.attn_paged_workspace_size(ctypes.byref(
-        paged_params(q, k_cache, v_cache, block_table, cu_q, kv_len, None, None, 1.0, False, max_q))))
+    # out and lse are not read: q stands in for both
+    return int(lib.attn_paged_workspace_size(
+        _pack_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, q, q, 1.0, False, max_q, 0, 0)))
+
+
+# (device, d, heads, key/value heads, max_q) -> bytes; all that the size depends on
+_workspace_bytes: Dict[tuple, int] = {}
+
+
+def _attn_paged(dev, q, k_cache, v_cache, block_table, cu_q, kv_len, out, lse, scale, causal, max_q, workspace):
+    total_q, hq, d = q.shape
+    if out is None:
+        out = torch.empty((total_q, hq, d), dtype=q.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((hq, total_q), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        key = (dev, d, hq, k_cache.shape[1], max_q)
+        nbytes = _workspace_bytes.get(key)
+        if nbytes is None:
+            nbytes = paged_workspace_size(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q=max_q)
+            if nbytes > 0:  # 0: nothing to do, or a call that will be refused
+                _workspace_bytes[key] = nbytes
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    _launch(lib.attn_paged, dev, _pack_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, out, lse, scale, causal,
+                                             max_q, workspace.data_ptr(), nbytes))
+    return out, lse
 
 
 def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -184,65 +219,104 @@ def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
     last sequence are left as they are in out and lse (unset in tensors allocated here).
 
     max_q, the most rows that a sequence is expected to bring, only chooses the tile shape."""
-    _vectors("q", q, q.dtype, -1, -1, -1)
+    dtype = q.dtype
+    _type_code("q", q)
+    _need_dims("q", q, 3)
+    _need_dims("k_cache", k_cache, 4)
+    _need_dims("block_table", block_table, 2)
     total_q, hq, d = q.shape
-    _dtype_code(q.dtype)
-    _caches(k_cache, v_cache, q.dtype, -1, d)
-    if v_cache.shape[1] != k_cache.shape[1]:
-        raise ValueError(f"k_cache has {k_cache.shape[1]} heads, v_cache {v_cache.shape[1]}")
-    _ints("block_table", block_table, -1, -1)
+    pages, hkv, page_size, _ = k_cache.shape
     num_seqs = block_table.shape[0]
-    _ints("cu_q", cu_q, num_seqs + 1)
-    _ints("kv_len", kv_len, num_seqs)
+    if q.stride()[2] != 1 and q.numel() > 0:
+        _refuse("q", q, dtype, q.shape)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not _is_rows(t, dtype, (pages, hkv, page_size, d)):
+            _refuse(name, t, dtype, (pages, hkv, page_size, d))
+    if not _is_ints(block_table, block_table.shape):
+        _refuse("block_table", block_table, _INT32, block_table.shape)
+    if not _is_ints(cu_q, (num_seqs + 1,)):
+        _refuse("cu_q", cu_q, _INT32, (num_seqs + 1,))
+    if not _is_ints(kv_len, (num_seqs,)):
+        _refuse("kv_len", kv_len, _INT32, (num_seqs,))
+    tensors = [q, k_cache, v_cache, block_table, cu_q, kv_len]
     if out is not None:
-        _vectors("out", out, q.dtype, total_q, hq, d)
+        if not _is_rows(out, dtype, (total_q, hq, d)):
+            _refuse("out", out, dtype, (total_q, hq, d))
+        tensors.append(out)
     if lse is not None:
-        _vectors("lse", lse, torch.float32, hq, total_q)
+        if lse.dtype is not torch.float32 or lse.shape != (hq, total_q):
+            _refuse("lse", lse, torch.float32, (hq, total_q))
         if not lse.is_contiguous():
             raise ValueError("lse must be contiguous")
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    dev = _device(q, k_cache, v_cache, block_table, cu_q, kv_len, *(t for t in (out, lse, workspace) if t is not None))
-    if max_q is None:
-        max_q = _default_max_q(total_q, num_seqs)
-    with _Launch(dev, stream) as at:
-        if out is None:
-            out = at.empty((total_q, hq, d), q.dtype)
-        if lse is None:
-            lse = at.empty((hq, total_q), torch.float32)
-        p = paged_params(q, k_cache, v_cache, block_table, cu_q, kv_len, out, lse,
-                         1.0 / math.sqrt(d) if scale is None else float(scale), causal, int(max_q))
-        if workspace is None:
-            workspace = at.empty((max(int(lib.attn_paged_workspace_size(ctypes.byref(p))), 1),), torch.uint8)
-        p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        at.call(lib.attn_paged, p)
-    return out, lse
+        tensors.append(lse)
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        tensors.append(workspace)
+    return _guarded(_attn_paged, _device(*tensors), stream, q, k_cache, v_cache, block_table, cu_q, kv_len, out, lse,
+                    1.0 / math.sqrt(d) if scale is None else float(scale), causal,
+                    _default_max_q(total_q, num_seqs) if max_q is None else int(max_q), workspace)
+
+
+def _attn_pages_write(dev, packed):
+    _launch(lib.attn_pages_write, dev, packed)
 
 
 def attn_pages_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
                      v_cache: torch.Tensor, *, stream=None) -> None:
     """Store k, v [rows, Hkv, d] in the caches [pages, Hkv, page_size, d]: row t goes to slot
     slots[t] % page_size of page slots[t] // page_size; rows with a negative slot are skipped."""
-    _vectors("k", k, k.dtype, -1, -1, -1)
+    dtype, code = k.dtype, _type_code("k", k)
+    _need_dims("k", k, 3)
+    _need_dims("k_cache", k_cache, 4)
     rows, heads, d = k.shape
-    dtype = _dtype_code(k.dtype)
-    _vectors("v", v, k.dtype, rows, heads, d)
-    _ints("slots", slots, rows)
-    _caches(k_cache, v_cache, k.dtype, heads, d)
-    dev = _device(k, v, slots, k_cache, v_cache)
-    ks, vs = k.stride(), v.stride()
-    p = PagesWriteParams(rows, heads, d, k_cache.shape[0], k_cache.shape[2], dtype, _i32x2(0, 0),
-                         k.data_ptr(), v.data_ptr(), slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                         _i64x2(ks[0], ks[1]), _i64x2(vs[0], vs[1]), _i64x3(*k_cache.stride()[:3]),
-                         _i64x3(*v_cache.stride()[:3]))
-    with _Launch(dev, stream) as at:
-        at.call(lib.attn_pages_write, p)
+    pages, _, page_size, _ = k_cache.shape
+    if k.stride()[2] != 1 and k.numel() > 0:
+        _refuse("k", k, dtype, k.shape)
+    if not _is_rows(v, dtype, (rows, heads, d)):
+        _refuse("v", v, dtype, (rows, heads, d))
+    if not _is_ints(slots, (rows,)):
+        _refuse("slots", slots, _INT32, (rows,))
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not _is_rows(t, dtype, (pages, heads, page_size, d)):
+            _refuse(name, t, dtype, (pages, heads, page_size, d))
+    kr, kh, _ = k.stride()
+    vr, vh, _ = v.stride()
+    kp, kch, ks, _ = k_cache.stride()
+    vp, vch, vs, _ = v_cache.stride()
+    _guarded(_attn_pages_write, _device(k, v, slots, k_cache, v_cache), stream, _WRITE.pack(
+        rows, heads, d, pages, page_size, code, 0, 0, k.data_ptr(), v.data_ptr(), slots.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), kr, kh, vr, vh, kp, kch, ks, vp, vch, vs))
 
 
-def _table(block_table: torch.Tensor, num_seqs: int) -> int:
-    """Checks the block table and returns its row stride."""
-    _ints("block_table", block_table, num_seqs, -1)
-    return block_table.stride(0) if num_seqs > 1 else block_table.shape[1]
+def _check_tables(name: str, first: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor,
+                  free_pages: torch.Tensor, free_count: torch.Tensor) -> int:
+    """The checks that plan and release share; `first` has an entry per sequence. Returns the number of
+    sequences."""
+    _need_dims(name, first, 1)
+    _need_dims("block_table", block_table, 2)
+    n = first.shape[0]
+    if not (_is_ints(first, (n,)) and _is_ints(kv_len, (n,)) and _is_ints(block_table, (n, block_table.shape[1]))
+            and _is_ints(free_pages, (free_pages.numel(),)) and _is_ints(free_count, (1,))):
+        for what, t, shape in ((name, first, (n,)), ("kv_len", kv_len, (n,)), ("block_table", block_table, (n, block_table.shape[1])),
+                               ("free_pages", free_pages, (free_pages.numel(),)), ("free_count", free_count, (1,))):
+            if not _is_ints(t, shape):
+                _refuse(what, t, _INT32, shape)
+    return n
+
+
+def _attn_pages_plan(dev, q_len, kv_len, block_table, free_pages, free_count, page_size, total_q, outs):
+    n, columns = block_table.shape
+    where = q_len.device
+    outs = cu_q, new_len, slots, positions, free_left = [
+        torch.empty(m, dtype=_INT32, device=where) if t is None else t
+        for t, m in zip(outs, (n + 1, n, total_q, total_q, 1))]
+    _launch(lib.attn_pages_plan, dev, _PLAN.pack(
+        n, total_q, page_size, columns, free_pages.shape[0], 0, q_len.data_ptr(), kv_len.data_ptr(),
+        block_table.data_ptr(), block_table.stride(0) if n > 1 else columns, free_pages.data_ptr(),
+        free_count.data_ptr(), cu_q.data_ptr(), new_len.data_ptr(), slots.data_ptr(), positions.data_ptr(),
+        free_left.data_ptr()))
+    return tuple(outs)
 
 
 def attn_pages_plan(q_len: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -257,32 +331,30 @@ def attn_pages_plan(q_len: torch.Tensor, kv_len: torch.Tensor, block_table: torc
     [total_q], positions [total_q], free_left [1]); total_q is the number of query rows, padding
     included, whose slots and positions are -1. All int32 on the GPU. new_len and free_left are the
     next call's kv_len and free_count. free_left < 0: pages were missing."""
-    num_seqs = q_len.shape[0] if q_len.dim() == 1 else -1
-    _ints("q_len", q_len, -1)
-    _ints("kv_len", kv_len, num_seqs)
-    table_stride = _table(block_table, num_seqs)
-    _ints("free_pages", free_pages, -1)
-    _ints("free_count", free_count, 1)
-    outs = {"cu_q": (cu_q, num_seqs + 1), "new_len": (new_len, num_seqs), "slots": (slots, total_q),
-            "positions": (positions, total_q), "free_left": (free_left, 1)}
-    given = []
-    for name, (t, n) in outs.items():
+    n = _check_tables("q_len", q_len, kv_len, block_table, free_pages, free_count)
+    if total_q < 0:
+        raise ValueError(f"total_q must not be negative, got {total_q}")
+    outs, given = (cu_q, new_len, slots, positions, free_left), []
+    for name, t, m in zip(("cu_q", "new_len", "slots", "positions", "free_left"), outs, (n + 1, n, total_q, total_q, 1)):
         if t is not None:
-            _ints(name, t, n)
+            if not _is_ints(t, (m,)):
+                _refuse(name, t, _INT32, (m,))
             given.append(t)
-    dev = _device(q_len, kv_len, block_table, free_pages, free_count, *given)
-    with _Launch(dev, stream) as at:
-        if not given:  # one allocation for all: a step's tables are small
-            whole = at.empty((2 * num_seqs + 2 + 2 * total_q,), torch.int32)
-            outs = whole.split((num_seqs + 1, num_seqs, total_q, total_q, 1))
-        else:
-            outs = tuple(at.empty((n,), torch.int32) if t is None else t for t, n in outs.values())
-        cu_q, new_len, slots, positions, free_left = outs
-        at.call(lib.attn_pages_plan, PagesPlanParams(
-            num_seqs, total_q, page_size, block_table.shape[1], free_pages.shape[0], 0, q_len.data_ptr(),
-            kv_len.data_ptr(), block_table.data_ptr(), table_stride, free_pages.data_ptr(), free_count.data_ptr(),
-            cu_q.data_ptr(), new_len.data_ptr(), slots.data_ptr(), positions.data_ptr(), free_left.data_ptr()))
-    return outs
+    return _guarded(_attn_pages_plan, _device(q_len, kv_len, block_table, free_pages, free_count, *given), stream, q_len,
+                    kv_len, block_table, free_pages, free_count, page_size, total_q, outs)
+
+
+def _attn_pages_release(dev, done, kv_len, block_table, free_pages, free_count, page_size, new_len, free_left):
+    n, columns = block_table.shape
+    if new_len is None:
+        new_len = torch.empty(n, dtype=_INT32, device=done.device)
+    if free_left is None:
+        free_left = torch.empty(1, dtype=_INT32, device=done.device)
+    _launch(lib.attn_pages_release, dev, _RELEASE.pack(
+        n, page_size, columns, free_pages.shape[0], done.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(),
+        block_table.stride(0) if n > 1 else columns, free_pages.data_ptr(), free_count.data_ptr(), new_len.data_ptr(),
+        free_left.data_ptr()))
+    return new_len, free_left
 
 
 def attn_pages_release(done: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -291,22 +363,12 @@ def attn_pages_release(done: torch.Tensor, kv_len: torch.Tensor, block_table: to
     """Push the pages of the sequences with done[b] != 0 onto the stack free_pages, in place from
     free_count[0] on. Returns (new_len [B], free_left [1]): new_len is 0 for those sequences and kv_len
     for the others. All int32 on the GPU."""
-    num_seqs = done.shape[0] if done.dim() == 1 else -1
-    _ints("done", done, -1)
-    _ints("kv_len", kv_len, num_seqs)
-    table_stride = _table(block_table, num_seqs)
-    _ints("free_pages", free_pages, -1)
-    _ints("free_count", free_count, 1)
-    if new_len is not None:
-        _ints("new_len", new_len, num_seqs)
-    if free_left is not None:
-        _ints("free_left", free_left, 1)
-    dev = _device(done, kv_len, block_table, free_pages, free_count, *(t for t in (new_len, free_left) if t is not None))
-    with _Launch(dev, stream) as at:
-        new_len = at.empty((num_seqs,), torch.int32) if new_len is None else new_len
-        free_left = at.empty((1,), torch.int32) if free_left is None else free_left
-        at.call(lib.attn_pages_release, PagesReleaseParams(
-            num_seqs, page_size, block_table.shape[1], free_pages.shape[0], done.data_ptr(), kv_len.data_ptr(),
-            block_table.data_ptr(), table_stride, free_pages.data_ptr(), free_count.data_ptr(), new_len.data_ptr(),
-            free_left.data_ptr()))
-    return new_len, free_left
+    n = _check_tables("done", done, kv_len, block_table, free_pages, free_count)
+    given = []
+    for name, t, m in (("new_len", new_len, n), ("free_left", free_left, 1)):
+        if t is not None:
+            if not _is_ints(t, (m,)):
+                _refuse(name, t, _INT32, (m,))
+            given.append(t)
+    return _guarded(_attn_pages_release, _device(done, kv_len, block_table, free_pages, free_count, *given), stream, done,
+                    kv_len, block_table, free_pages, free_count, page_size, new_len, free_left)

@@ -37,6 +37,7 @@
 // reasons for either order of products).
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -922,9 +923,18 @@ CUresult encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, int32_t d
 template <int D, bool F16, int NT>
 cudaError_t launch_tc(const CUtensorMap (&maps)[3], const PagedDev& p, int grid, cudaStream_t s) {
     using C = Cfg<D, NT>;
-    const cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D, F16, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               C::kSmemBytes);
+    // The attribute stays with the function on a device: one call instead of one a launch (decode is paced
+    // by the host). Threads that come at the same time both set it, to the same value.
+    static std::atomic<uint64_t> set{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(set.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(paged_tc_kernel<D, F16, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+        if (e != cudaSuccess) return e;
+        set.fetch_or(bit, std::memory_order_relaxed);
+    }
     return launch_pdl(paged_tc_kernel<D, F16, NT>, dim3(grid), dim3(C::kThreads), C::kSmemBytes, s, maps[0], maps[1],
                       maps[2], p);
 }
