@@ -53,32 +53,39 @@ constexpr int BM = 128;  // query rows per tile
 constexpr int BN = 128;  // keys per tile
 constexpr float kRescaleThreshold = 8.0f;
 constexpr int kUnitCost = 64;  // what a unit costs beyond its key tiles, in keys
+constexpr float kPairCost = 1.5f;  // a key tile of a two-tile unit against one of a one-tile unit
+constexpr int kTilesBytes = 224 * 1024;  // shared memory for Q, K and V tiles
 constexpr unsigned kFull = 0xffffffffu;
 
-template <int D, int NT>
+// A CTA that works on units of NT tiles; the warps of its roles begin at FIRST, behind the softmax warps.
+template <int D, int NT, int FIRST>
 struct Cfg {
     static constexpr int kBoxes = D / 64;
     static constexpr int kTileBytes = BM * D * 2;
     static constexpr bool kSplit = D == 64 || NT == 1;  // P in tensor-memory columns of its own
     static constexpr int kIssuers = kSplit ? NT : 1;
-    static constexpr int kStages = D == 64 ? 12 : (NT == 1 ? 6 : 4);  // K and V tiles in flight
-    static constexpr int kWarps = NT == 1 ? 7 : 12;
-    static constexpr int kThreads = kWarps * 32;
-    static constexpr int kProducer = 4 * NT, kIssuer = 4 * NT + 1, kTail = 4 * NT + 2;  // warps
-    // NT = 2: registers per thread after the rebalance, 2 x 128 x softmax + 128 x other = 384 x 168
-    static constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
-    static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= 384 * 168, "register split");
     static constexpr int kQOff = 0;
     static constexpr int kKVOff = kQOff + NT * kTileBytes;
-    static constexpr int kBarOff = kKVOff + kStages * kTileBytes;
-    static constexpr int kSmemBytes = kBarOff + 1024 + 1024;  // barriers and schedule + alignment slack
-    static_assert(kSmemBytes <= 232448, "shared memory");
+    static constexpr int kStages = (kTilesBytes - kKVOff) / kTileBytes;  // K and V tiles in flight
+    static constexpr int kProducer = FIRST, kIssuer = FIRST + 1, kTail = FIRST + 2, kIssuer1 = FIRST + 3;  // warps
 };
+
+// The kernel for batches whose sequences all fit one tile (NT = 1), and the one that also takes longer
+// chunks (NT = 2): there each CTA works either on the former or on the latter.
+template <int NT>
+struct Shape {
+    static constexpr int kFirst = 4 * NT;
+    static constexpr int kThreads = NT == 1 ? 224 : 384;
+    // NT = 2: registers per thread after the rebalance, 2 x 128 x softmax + 128 x other = 384 x 168
+    static constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
+    static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= 384 * 168, "register split");
+};
+constexpr int kSmemBytes = kTilesBytes + 2048 + 1024;  // barriers and schedule + alignment slack
+static_assert(kSmemBytes <= 232448, "shared memory");
 
 struct PagedDev {
     int B, G, Hkv, T;
     int tok_tile;     // tokens of a tile: its rows are tok_tile * G
-    int n_sm_warps;   // softmax warps that hold rows
     int num_pages, page_size, shift, max_pages;
     int causal;
     float c;          // scale * log2(e)
@@ -87,7 +94,7 @@ struct PagedDev {
     uint8_t* o;
     float* lse;
     long long o_sr, o_sh;  // elements
-    float* part;      // [grid][2][NT][tok_tile * G][D + 4]
+    float* part;      // [grid][2][NT] records of tok_tile * G rows: see Record
     int4* meta;       // [grid][2]: see Meta
     int* err;
     unsigned long long timeout_ns;
@@ -97,24 +104,36 @@ struct PagedDev {
 // y = first query row of the unit, z = its tokens, w = key/value head.
 enum : int { kNone = 0, kPart = 1, kLast = 2 };
 
-struct __align__(8) Shared {
-    uint64_t q_full, q_empty;
-    uint64_t kv_full[12], kv_empty[12], v_tail[12];
-    uint64_t s_full[2], p_full[2], o_full[2], s_free[2], pv_done[2];
-    uint64_t drain[2];
-    long long x0, x1, u0;  // this CTA's piece of the line, and where the unit that holds x0 starts
-    long long scan[12], total;
-    int b, h, blk;         // that unit
-    uint32_t tmem_base;
-    int abort_flag;
-};
-static_assert(sizeof(Shared) <= 1024, "barrier area");
-
-// ---------------------------------------------------------------- the line of units
 struct Seq {
     int row0, n, len;  // first row of q, rows, keys; within the arrays whatever the lengths say
 };
 
+// Where a warp's walk over its CTA's units stands: the unit to come.
+struct Place {
+    long long u0;    // where it starts on the line
+    int b, h, blk;   // sequence, key/value head, number of the unit in them
+    Seq seq;
+};
+
+struct __align__(16) Shared {
+    uint64_t q_full, q_empty;
+    uint64_t kv_full[13], kv_empty[13], v_tail[13];
+    uint64_t s_full[2], p_full[2], o_full[2], s_free[2], pv_done[2];
+    uint64_t drain[2];
+    long long x0, x1;      // this CTA's piece of the line
+    Place first;           // the unit that holds x0; u0 = -1 if there is none
+    Place place[12];       // of each warp
+    int4 unit[12];         // of each softmax warp, the unit it is in: first row of q, tokens, key/value
+                           // head, 1 if it holds the first key tile + 2 if the last
+    long long scan[3][12]; // per warp: sums of either class, running sum
+    int pair;              // whether this CTA works on two-tile units
+    int widest[12], sm_warps;  // most rows of a one-tile unit; softmax warps of a tile that hold rows
+    uint32_t tmem_base;
+    int abort_flag;
+};
+static_assert(sizeof(Shared) <= 2048, "barrier area");
+
+// ---------------------------------------------------------------- the line of units
 __device__ __forceinline__ Seq seq_of(const PagedDev& p, int b, bool* bad) {
     const int c0 = p.cu_q[b], c1 = p.cu_q[b + 1], len = p.kv_len[b];
     const long long most = (long long)p.max_pages << p.shift;
@@ -148,52 +167,96 @@ __device__ __forceinline__ long long head_cost(const PagedDev& p, const Seq& s, 
     return cost_before(p, s, step, units - 1) + visible(p, s, s.n) + kUnitCost;
 }
 
-// Finds this CTA's piece of the line. All threads take part.
-template <int THREADS>
-__device__ __forceinline__ void locate(const PagedDev& p, int step, Shared& sh) {
-    constexpr int WARPS = THREADS / 32;
+// Whether a sequence is worked on in two-tile units: in the kernel that has them, if one tile does not
+// hold its rows.
+template <int NT>
+__device__ __forceinline__ bool is_pair(const PagedDev& p, const Seq& s) {
+    return NT == 2 && s.n > p.tok_tile;
+}
+
+// Finds this CTA's piece of the line. All threads take part. In the NT = 2 kernel there are two lines, of
+// one-tile and of two-tile units, and the CTAs are shared out between them by their costs: the former are
+// bound by reading keys and values, the latter by the tensor cores, so they run side by side.
+template <int NT>
+__device__ __forceinline__ void locate(const PagedDev& p, Shared& sh) {
+    constexpr int THREADS = Shape<NT>::kThreads, WARPS = THREADS / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     bool bad = false;
-    long long mine = 0, sum = 0;
+    Seq s{0, 0, 0};
+    long long per_head = 0, sum0 = 0, sum1 = 0;
+    int rows = 0;
     for (int b = tid; b < p.B; b += THREADS) {
-        mine = head_cost(p, seq_of(p, b, &bad), step) * p.Hkv;
-        sum += mine;
+        s = seq_of(p, b, &bad);
+        if (is_pair<NT>(p, s)) {
+            per_head = head_cost(p, s, 2 * p.tok_tile);
+            sum1 += per_head * p.Hkv;
+        } else {
+            per_head = head_cost(p, s, p.tok_tile);
+            sum0 += per_head * p.Hkv;
+            rows = max(rows, min(s.n, p.tok_tile) * p.G);
+        }
     }
     if (bad && blockIdx.x == 0) atomicCAS(p.err, 0, ATTN_ERR_INVALID);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    if (lane == 0) sh.scan[warp] = sum;
-    if (tid == 0) sh.u0 = -1;
+    for (int o = 16; o > 0; o >>= 1) {
+        sum0 += __shfl_xor_sync(kFull, sum0, o);
+        if (NT == 2) sum1 += __shfl_xor_sync(kFull, sum1, o);
+    }
+    rows = __reduce_max_sync(kFull, rows);
+    if (lane == 0) {
+        sh.scan[0][warp] = sum0;
+        sh.scan[1][warp] = sum1;
+        sh.widest[warp] = rows;
+    }
+    if (tid == 0) sh.first.u0 = -1;
     __syncthreads();
-    long long total = 0;
+    long long total0 = 0, total1 = 0;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) total += sh.scan[w];
-    const long long each = total / gridDim.x, rest = total % gridDim.x, i = blockIdx.x;
-    const long long x0 = each * i + min(i, rest), x1 = each * (i + 1) + min(i + 1, rest);
+    for (int w = 0; w < WARPS; ++w) {
+        total0 += sh.scan[0][w];
+        if (NT == 2) total1 += sh.scan[1][w];
+        rows = max(rows, sh.widest[w]);
+    }
+    int i = blockIdx.x, n = gridDim.x;
+    bool pair = false;
+    if (NT == 2) {
+        const float c0 = (float)total0, c1 = (float)total1 * kPairCost;
+        int n0 = total0 == 0 ? 0 : max(1, (int)(n * (c0 / (c0 + c1)) + 0.5f));
+        if (total1 > 0) n0 = min(n0, n - 1);
+        pair = i >= n0;
+        i = pair ? i - n0 : i;
+        n = pair ? n - n0 : n0;
+    }
+    const long long total = pair ? total1 : total0;
+    const long long each = total / max(n, 1), rest = total - each * n;
+    const long long x0 = each * i + min((long long)i, rest), x1 = x0 + each + (i < rest ? 1 : 0);
     long long before = 0;  // cost of the chunks of sequences before this one
     for (int b0 = 0; b0 < p.B && x0 < x1; b0 += THREADS) {
         const int b = b0 + tid;
-        if (p.B > THREADS) mine = b < p.B ? head_cost(p, seq_of(p, b, nullptr), step) * p.Hkv : 0;
-        if (b >= p.B) mine = 0;
+        if (p.B > THREADS) {
+            s = b < p.B ? seq_of(p, b, nullptr) : Seq{0, 0, 0};
+            per_head = head_cost(p, s, is_pair<NT>(p, s) ? 2 * p.tok_tile : p.tok_tile);
+        }
+        const long long mine = is_pair<NT>(p, s) == pair ? per_head * p.Hkv : 0;
         long long x = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long u = __shfl_up_sync(kFull, x, o);
             if (lane >= o) x += u;
         }
-        __syncthreads();  // the last use of scan
-        if (lane == 31) sh.scan[warp] = x;
+        if (b0 > 0) __syncthreads();  // the last use of scan
+        if (lane == 31) sh.scan[2][warp] = x;
         __syncthreads();
         long long chunk = 0;
         x += before;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
-            if (w < warp) x += sh.scan[w];
-            chunk += sh.scan[w];
+            if (w < warp) x += sh.scan[2][w];
+            chunk += sh.scan[2][w];
         }
         if (x - mine <= x0 && x0 < x) {
-            const Seq s = seq_of(p, b, nullptr);
-            const long long per_head = mine / p.Hkv, at = x0 - (x - mine);
+            const int step = pair ? 2 * p.tok_tile : p.tok_tile;
+            const long long at = x0 - (x - mine);
             const int h = (int)(at / per_head);
             const long long in_head = at - h * per_head;
             int lo = 0, hi = (s.n + step - 1) / step;  // the last unit that starts at or before in_head
@@ -204,10 +267,7 @@ __device__ __forceinline__ void locate(const PagedDev& p, int step, Shared& sh) 
                 else
                     hi = mid;
             }
-            sh.b = b;
-            sh.h = h;
-            sh.blk = lo;
-            sh.u0 = x - mine + h * per_head + cost_before(p, s, step, lo);
+            sh.first = Place{x - mine + h * per_head + cost_before(p, s, step, lo), b, h, lo, s};
         }
         before += chunk;
         if (before > x0) break;
@@ -215,8 +275,9 @@ __device__ __forceinline__ void locate(const PagedDev& p, int step, Shared& sh) 
     if (tid == 0) {
         sh.x0 = x0;
         sh.x1 = x1;
+        sh.pair = pair;
+        sh.sm_warps = pair ? (p.tok_tile * p.G + 31) / 32 : (rows + 31) / 32;
     }
-    __syncthreads();
 }
 
 struct Unit {
@@ -229,70 +290,82 @@ struct Unit {
     __device__ __forceinline__ int cnt(int t) const { return t == 0 ? cnt0 : cnt1; }
 };
 
-// Walks this CTA's units in order. Every warp role walks for itself and finds the same units.
-template <int NT>
+// Walks this CTA's units of NT tiles in order. Every warp role walks for itself and finds the same units;
+// its place is kept in shared memory, since the softmax warps need their registers for a row of scores.
+// KERNEL is the NT of the kernel: where it is 2, sequences of the other kind are passed over.
+template <int NT, int KERNEL>
 struct Walk {
     const PagedDev& p;
-    long long u0, x0, x1;
-    int b, h, blk;
-    Seq s;
+    const Shared& sh;
+    Place& place;
 
-    __device__ __forceinline__ Walk(const PagedDev& p_, const Shared& sh) : p(p_), x0(sh.x0), x1(sh.x1) {
-        b = sh.b;
-        h = sh.h;
-        blk = sh.blk;
-        u0 = sh.u0 < 0 ? x1 : sh.u0;
-        if (u0 < x1) s = seq_of(p, b, nullptr);
+    __device__ __forceinline__ Walk(const PagedDev& p_, Shared& sh_)
+        : p(p_), sh(sh_), place(sh_.place[threadIdx.x >> 5]) {
+        if ((threadIdx.x & 31) == 0) {
+            place = sh.first;
+            if (place.u0 < 0) place.u0 = sh.x1;
+        }
     }
+    // All lanes of a warp, converged.
     __device__ __forceinline__ bool next(Unit& w) {
         const int step = NT * p.tok_tile;
-        while (u0 < x1) {
-            const int tok0 = blk * step;
+        const long long x0 = sh.x0, x1 = sh.x1;
+        __syncwarp();
+        Place at = place;
+        bool mine = false;
+        while (!mine && at.u0 < x1) {
+            const Seq s = at.seq;
+            const int tok0 = at.blk * step;
             w.ntok = min(step, s.n - tok0);
             const int keys = visible(p, s, tok0 + w.ntok);
             const int tiles = (keys + BN - 1) / BN;
-            const long long end = u0 + keys + kUnitCost;
-            const int k0 = x0 <= u0 ? 0 : min(tiles, (int)((x0 - u0 + BN / 2) / BN));
-            const int k1 = x1 >= end ? tiles : min(tiles, (int)((x1 - u0 + BN / 2) / BN));
-            const bool mine = k0 < k1 || (tiles == 0 && u0 >= x0);
-            if (mine) {
-                w.b = b;
-                w.h = h;
-                w.row0 = s.row0 + tok0;
-                w.len = s.len;
-                w.base = p.causal ? s.len - s.n + tok0 : s.len - 1;
-                w.k0 = k0;
-                w.first = k0 == 0;
-                w.last = k1 == tiles;
-                w.cnt_max = k1 - k0;
-                w.cnt0 = w.cnt_max;
-                w.cnt1 = 0;
-                if (NT == 2 && w.ntok > p.tok_tile) {  // causal: tile 0's rows may see fewer tiles
-                    w.cnt1 = w.cnt_max;
-                    w.cnt0 = max(0, min(k1, (visible(p, s, tok0 + p.tok_tile) + BN - 1) / BN) - k0);
-                }
+            const long long end = at.u0 + keys + kUnitCost;
+            const int k0 = x0 <= at.u0 ? 0 : min(tiles, (int)((x0 - at.u0 + BN / 2) / BN));
+            const int k1 = x1 >= end ? tiles : min(tiles, (int)((x1 - at.u0 + BN / 2) / BN));
+            mine = k0 < k1 || (tiles == 0 && at.u0 >= x0);
+            w.b = at.b;
+            w.h = at.h;
+            w.row0 = s.row0 + tok0;
+            w.len = s.len;
+            w.base = p.causal ? s.len - s.n + tok0 : s.len - 1;
+            w.k0 = k0;
+            w.first = k0 == 0;
+            w.last = k1 == tiles;
+            w.cnt_max = k1 - k0;
+            w.cnt0 = w.cnt_max;
+            w.cnt1 = 0;
+            if (NT == 2 && w.ntok > p.tok_tile) {  // causal: tile 0's rows may see fewer tiles
+                w.cnt1 = w.cnt_max;
+                w.cnt0 = max(0, min(k1, (visible(p, s, tok0 + p.tok_tile) + BN - 1) / BN) - k0);
             }
-            u0 = end;
+            at.u0 = end;
             if (tok0 + step < s.n) {
-                ++blk;
+                ++at.blk;
             } else {
-                blk = 0;
-                if (++h == p.Hkv) {
-                    h = 0;
+                at.blk = 0;
+                if (++at.h == p.Hkv) {
+                    at.h = 0;
                     do {
-                        if (++b >= p.B) {
-                            u0 = x1;
+                        if (++at.b >= p.B) {
+                            at.u0 = x1;
                             break;
                         }
-                        s = seq_of(p, b, nullptr);
-                    } while (s.n == 0);
+                        at.seq = seq_of(p, at.b, nullptr);
+                    } while (at.seq.n == 0 || (KERNEL == 2 && is_pair<2>(p, at.seq) != (NT == 2)));
                 }
             }
-            if (mine) return true;
         }
-        return false;
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) place = at;
+        return mine;
     }
 };
+
+// The record of tile t of a CTA's slot: per row (m, l, divisor of o, unused), then o by groups of four
+// columns, each group's rows side by side, so that neighbouring threads (rows) write neighbouring 16 bytes.
+__device__ __forceinline__ float4* record(float* part, int slot, int tiles, int t, int rows, int d) {
+    return reinterpret_cast<float4*>(part) + ((long long)slot * tiles + t) * rows * (1 + d / 4);
+}
 
 // ---------------------------------------------------------------- helpers of the roles
 __device__ __forceinline__ uint64_t kmajor_desc(uint32_t tile, int kk) {
@@ -317,22 +390,17 @@ __device__ __forceinline__ int page_at(const PagedDev& p, int b, int key, bool* 
     return p.num_pages;
 }
 
-template <int D, bool F16, int NT>
-__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
-    paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                    const __grid_constant__ CUtensorMap tm_v, const PagedDev p) {
-    using C = Cfg<D, NT>;
+// The work of a CTA on units of NT tiles, from the located piece of the line to its end.
+template <int D, bool F16, int NT, int KERNEL>
+__device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                     const PagedDev& p, uint8_t* smem, Shared& bar) {
+    using C = Cfg<D, NT, Shape<KERNEL>::kFirst>;
     constexpr uint32_t kIdescS = idesc_h16(BM, BN, false, false, F16);
     constexpr uint32_t kIdescO = idesc_h16(BM, D, false, true, F16);
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Shared& bar = *reinterpret_cast<Shared*>(smem + C::kBarOff);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    WaitCtl wc{p.err, &bar.abort_flag, p.timeout_ns};
-
+    const WaitCtl wc{p.err, &bar.abort_flag, p.timeout_ns};
     if (threadIdx.x == 0) {
-        bar.abort_flag = 0;
-        const uint32_t rows = 32u * (uint32_t)p.n_sm_warps;  // softmax threads of a tile
+        const uint32_t rows = 32u * (uint32_t)bar.sm_warps;  // softmax threads of a tile
         mbar_init(&bar.q_full, 1);
         mbar_init(&bar.q_empty, C::kIssuers);
         for (int s = 0; s < C::kStages; ++s) {
@@ -350,28 +418,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
         fence_mbar_init();
     }
-    if (warp == C::kIssuer) {
-        tmem_alloc(&bar.tmem_base, 512);
-        tmem_relinquish();
-    }
-    if (warp == C::kProducer && elect_one()) {
-        prefetch_tmap(&tm_q);
-        prefetch_tmap(&tm_k);
-        prefetch_tmap(&tm_v);
-    }
-    tc_fence_before();
-    // No global memory is touched above: from here on the previous kernel must be complete.
-    grid_dep_launch();
-    grid_dep_wait();
-    locate<C::kThreads>(p, NT * p.tok_tile, bar);  // ends in a block barrier
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar.tmem_base;
     const uint32_t sQ = smem_u32(smem + C::kQOff);
     const uint32_t sKV = smem_u32(smem + C::kKVOff);
 
-    if (warp >= 4 * NT) {
-        if constexpr (NT == 2) regs_decrease<C::kOtherRegs>();
-        Walk<NT> walk(p, bar);
+    if (warp >= C::kProducer) {
+        if constexpr (KERNEL == 2) regs_decrease<Shape<2>::kOtherRegs>();
+        Walk<NT, KERNEL> walk(p, bar);
         Unit w;
         if (warp == C::kProducer) {
             // ------------------------------------------------ Q / K / V producer
@@ -463,7 +518,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 __syncwarp();
             }
             if (lane < 2) p.meta[blockIdx.x * 2 + lane] = lane == 0 ? slot0 : slot1;
-        } else if (C::kSplit && (warp == C::kIssuer || (NT == 2 && warp == C::kIssuer + 2))) {
+        } else if (C::kSplit && (warp == C::kIssuer || (NT == 2 && warp == C::kIssuer1))) {
             // ------------------------------------------------ MMA issuers, one per query tile
             // S_t^{j+1} runs as soon as the softmax warps have read S_t^j. Each issuer walks every
             // ring slot and releases it once, used or not.
@@ -610,10 +665,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             __syncwarp();
         }
     } else {
-        if constexpr (NT == 2) regs_increase<C::kSoftmaxRegs>();
+        if constexpr (KERNEL == 2) regs_increase<Shape<2>::kSoftmaxRegs>();
         // ------------------------------------------------ softmax (thread = query row)
         const int t = NT == 2 ? warp >> 2 : 0;
-        if ((warp & 3) < p.n_sm_warps) {
+        if (warp < 4 * NT && (warp & 3) < bar.sm_warps) {
             const int r = (warp & 3) * 32 + lane;
             const int rows = p.tok_tile * p.G;
             const int my_tok = t * p.tok_tile + r / p.G, my_head = r % p.G;
@@ -623,10 +678,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             const uint32_t tP = C::kSplit ? tmem + lane_off + 384 + t * 64 : tS;
             uint32_t scnt = 0, ocnt = 0;  // ocnt: phases of pv_done (split) or o_full
             bool ok = true;
-            Walk<NT> walk(p, bar);
-            Unit w;
-            while (ok && walk.next(w)) {
-                const int cnt = w.cnt(t);
+            Walk<NT, KERNEL> walk(p, bar);
+            while (ok) {
+                Unit w;
+                if (!walk.next(w)) break;
+                if (lane == 0) bar.unit[warp] = make_int4(w.row0, w.ntok, w.h, (w.first ? 1 : 0) + (w.last ? 2 : 0));
+                const int cnt = w.cnt(t), k0 = w.k0;
                 // keys this row sees, and those that the tile's first row sees
                 const int lim = p.causal ? min(w.len, w.base + my_tok + 1) : w.len;
                 const int lim_first = p.causal ? min(w.len, w.base + t * p.tok_tile + 1) : w.len;
@@ -647,7 +704,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                         tc_fence_before();
                         mbar_arrive(&bar.s_free[t]);
                     }
-                    const int key0 = (w.k0 + j) * BN;
+                    const int key0 = (k0 + j) * BN;
                     if (key0 + BN > lim_first) {
                         const int out = lim - key0;  // first column this row does not see
 #pragma unroll
@@ -672,7 +729,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                     const float alpha = moved ? ex2(m_ref - m_new) : 1.f;  // 0 when m_ref = -inf
                     const bool rescale = j > 0 && __any_sync(kFull, moved && m_ref != -INFINITY);
                     auto rescale_o = [&]() {
-#pragma unroll
+#pragma unroll 1  // rare, and unrolled it costs the key loop its registers
                         for (int c0 = 0; c0 < D; c0 += 32) {
                             uint32_t ov[32];
                             tmem_ld32(tO + c0, ov);
@@ -747,11 +804,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                     ++ocnt;
                     tc_fence_after();
                 }
-                const bool held = r < rows && my_tok < w.ntok;
+                __syncwarp();
+                const int4 u = bar.unit[warp];
+                const bool held = r < rows && my_tok < u.y, first = u.w & 1, last = u.w & 2;
                 const float den = o_divisor<F16>(l, m_row, m_ref);
-                if (w.first && w.last) {
+                if (first && last) {
                     const float inv = den > 0.f ? 1.f / den : 0.f;
-                    const long long row = w.row0 + my_tok, head = w.h * p.G + my_head;
+                    const long long row = u.x + my_tok, head = u.z * p.G + my_head;
                     uint16_t* orow = reinterpret_cast<uint16_t*>(p.o) + row * p.o_sr + head * p.o_sh;
 #pragma unroll
                     for (int c0 = 0; c0 < D; c0 += 32) {
@@ -779,9 +838,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                     if (held) p.lse[head * p.T + row] = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
                 } else {
                     // the part's state of this row; a row without keys in it is m = -inf, and its o is not read
-                    float* rec = p.part + (((long long)(blockIdx.x * 2 + (w.first ? 1 : 0)) * NT + t) * rows + r) * (D + 4);
-                    if (held)
-                        *reinterpret_cast<float4*>(rec) = make_float4(l > 0.f ? m_ref : -INFINITY, l, den, 0.f);
+                    float4* rec = record(p.part, blockIdx.x * 2 + (first ? 1 : 0), KERNEL, t, rows, D);
+                    if (held) rec[r] = make_float4(l > 0.f ? m_ref : -INFINITY, l, den, 0.f);
                     if (cnt > 0) {
 #pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -789,11 +847,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                             tmem_ld32(tO + c0, ov);
                             tmem_wait_ld();
                             if (held) {
-                                float4* dst = reinterpret_cast<float4*>(rec + 4 + c0);
+                                float4* dst = rec + (1 + c0 / 4) * rows + r;
 #pragma unroll
                                 for (int q = 0; q < 8; ++q)
-                                    dst[q] = make_float4(__uint_as_float(ov[4 * q]), __uint_as_float(ov[4 * q + 1]),
-                                                         __uint_as_float(ov[4 * q + 2]), __uint_as_float(ov[4 * q + 3]));
+                                    dst[q * rows] = make_float4(__uint_as_float(ov[4 * q]), __uint_as_float(ov[4 * q + 1]),
+                                                                __uint_as_float(ov[4 * q + 2]), __uint_as_float(ov[4 * q + 3]));
                             }
                         }
                     }
@@ -802,91 +860,139 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             }
         }
     }
+}
 
+template <int D, bool F16, int NT>
+__global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const PagedDev p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Shared& bar = *reinterpret_cast<Shared*>(smem + kTilesBytes);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) bar.abort_flag = 0;
+    if (warp == 0) {
+        tmem_alloc(&bar.tmem_base, 512);
+        tmem_relinquish();
+        if (elect_one()) {
+            prefetch_tmap(&tm_q);
+            prefetch_tmap(&tm_k);
+            prefetch_tmap(&tm_v);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    // No global memory is touched above: from here on the previous kernel must be complete.
+    grid_dep_launch();
+    grid_dep_wait();
+    locate<NT>(p, bar);
+    __syncthreads();
+    if constexpr (NT == 2) {
+        if (bar.pair)
+            work<D, F16, 2, 2>(tm_q, tm_k, tm_v, p, smem, bar);
+        else
+            work<D, F16, 1, 2>(tm_q, tm_k, tm_v, p, smem, bar);
+    } else {
+        work<D, F16, 1, 1>(tm_q, tm_k, tm_v, p, smem, bar);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == C::kIssuer) tmem_dealloc(tmem, 512);
+    if (warp == 0) tmem_dealloc(bar.tmem_base, 512);
 }
 
 // ---------------------------------------------------------------- merging parts
 struct CombineArgs {
-    const float* part;
+    float* part;
     const int4* meta;
-    int ctas;            // of the split pass
-    int tiles, rows;     // tiles of a unit, rows of a tile
+    int tiles, rows;     // tiles of a slot, rows of a tile
     int tok_tile, G, T;
     uint8_t* o;
     float* lse;
     long long o_sr, o_sh;
-    int rows_per_block;
 };
 
 constexpr int kCombineThreads = 256;
 
-// Block (e, y) merges rows [y * rows_per_block, ...) of the unit whose last part CTA e wrote, if there
-// is one: its first part is in slot 1 of the nearest CTA before e that has one, the parts between in
-// the slots 0. A warp takes a row; w_s = 2^(m_s - M) as in the merge of tiles, in the order of the keys.
+// Blocks (e, y) merge the unit whose last part CTA e wrote, if there is one: its first part is in slot 1
+// of the nearest CTA before e that has one, the parts between in the slots 0. A thread takes 16 columns of
+// a row, threads side by side the rows; the parts are merged as tiles are, in the order of the keys.
 template <int D, bool F16>
 __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const CombineArgs a) {
     grid_dep_launch();
     grid_dep_wait();
-    constexpr int PER = D / 32;
-    const int e = blockIdx.x;
+    const int e = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int4 unit = a.meta[e * 2];
     if (unit.x != kLast) return;
-    __shared__ int s_first;
-    extern __shared__ uint8_t s_has[];  // CTA c's slot 0 holds a part
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) s_first = 0;
-    __syncthreads();
-    for (int c = tid; c < e; c += kCombineThreads) {
-        s_has[c] = a.meta[c * 2].x != kNone;
-        if (a.meta[c * 2 + 1].x != kNone) atomicMax(&s_first, c);
-    }
-    if (tid == 0) s_has[e] = 1;
-    __syncthreads();
-    const int first = s_first;
-    const long long slot = (long long)a.tiles * a.rows * (D + 4);  // floats of a slot
-    const int row_end = min(a.tiles * a.rows, (int)(blockIdx.y + 1) * a.rows_per_block);
-    for (int row = blockIdx.y * a.rows_per_block + warp; row < row_end; row += kCombineThreads / 32) {
-        const int t = row / a.rows, r = row % a.rows;
-        const int tok = t * a.tok_tile + r / a.G;
-        if (tok >= unit.z) continue;
-        const float* base = a.part + (long long)row * (D + 4);
-        auto rec = [&](int c) { return base + (c * 2 + (c == first ? 1 : 0)) * slot; };
-        float M = -INFINITY;
-        for (int c = first + lane; c <= e; c += 32)
-            if (c == first || s_has[c]) M = fmaxf(M, rec(c)[0]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-        float L = 0.f, Lo = 0.f, out[PER];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) out[i] = 0.f;
-        if (M != -INFINITY) {
-            for (int c = first; c <= e; ++c) {
-                if (c != first && !s_has[c]) continue;
-                const float* x = rec(c);
-                const float m = x[0];
-                if (m == -INFINITY) continue;  // no key of this row: its o was not written
-                const float w = ex2(m - M);
-                L += w * x[1];
-                Lo += w * x[2];
-#pragma unroll
-                for (int i = 0; i < PER; ++i) out[i] = fmaf(w, x[4 + lane * PER + i], out[i]);
-            }
+    // bit c of has[0] / has[1]: CTA c's slot 0 / 1 holds a part (c <= e)
+    extern __shared__ unsigned s_mem[];
+    const int words = (gridDim.x + 31) / 32;
+    unsigned *has0 = s_mem, *has1 = s_mem + words;
+    int* slots = reinterpret_cast<int*>(s_mem + 2 * words);  // the unit's, in the order of the keys
+    for (int w = warp; w < words; w += kCombineThreads / 32) {
+        const int c = w * 32 + lane;
+        const unsigned m0 = __ballot_sync(kFull, c <= e && a.meta[min(c, e) * 2].x != kNone);
+        const unsigned m1 = __ballot_sync(kFull, c < e && a.meta[min(c, e) * 2 + 1].x != kNone);
+        if (lane == 0) {
+            has0[w] = m0;
+            has1[w] = m1;
         }
-        const float inv = Lo > 0.f ? 1.f / Lo : 0.f;
-        const long long q_row = unit.y + tok, head = unit.w * a.G + r % a.G;
-        uint16_t* orow = reinterpret_cast<uint16_t*>(a.o) + q_row * a.o_sr + head * a.o_sh;
-        if constexpr (PER == 2) {
-            *reinterpret_cast<uint32_t*>(orow + lane * 2) = pack_h16<F16>(out[0] * inv, out[1] * inv);
-        } else {
-            *reinterpret_cast<uint2*>(orow + lane * 4) =
-                make_uint2(pack_h16<F16>(out[0] * inv, out[1] * inv), pack_h16<F16>(out[2] * inv, out[3] * inv));
-        }
-        if (lane == 0) a.lse[head * a.T + q_row] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
     }
+    __syncthreads();
+    int first = 0;
+    for (int w = 0; w < words; ++w)
+        if (has1[w]) first = w * 32 + 31 - __clz(has1[w]);
+    int parts = 1;  // the first, then every slot 0 behind it
+    for (int w = first / 32; w < words; ++w) {
+        const unsigned m = w == first / 32 ? has0[w] & ~(0xffffffffu >> (31 - (first & 31))) : has0[w];
+        if (w % (kCombineThreads / 32) == warp && (m >> lane & 1)) slots[parts + __popc(m & ((1u << lane) - 1))] = (w * 32 + lane) * 2;
+        parts += __popc(m);
+    }
+    if (tid == 0) slots[0] = first * 2 + 1;
+    __syncthreads();
+    const int i = blockIdx.y * kCombineThreads + tid;
+    const int r = i % a.rows, group = i / a.rows % (D / 16), t = i / a.rows / (D / 16);
+    const int tok = t * a.tok_tile + r / a.G;
+    if (t >= a.tiles || tok >= unit.z) return;
+    float M = -INFINITY, L = 0.f, Lo = 0.f, out[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) out[c] = 0.f;
+    // one pass with a running maximum, so that the loads of several parts are in flight at once
+#pragma unroll 3
+    for (int k = 0; k < parts; ++k) {
+        const float4* rec = record(a.part, slots[k], a.tiles, t, a.rows, D) + r;
+        const float4 head = rec[0];
+        float4 o[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[c] = rec[(1 + group * 4 + c) * a.rows];
+        const float m = fmaxf(M, head.x);
+        // a part without a key of this row: its o was not written
+        const float was = M == -INFINITY ? 0.f : ex2(M - m), w = head.x == -INFINITY ? 0.f : ex2(head.x - m);
+        M = m;
+        L = L * was + w * head.y;
+        Lo = Lo * was + w * head.z;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float4 v = w > 0.f ? o[c] : make_float4(0.f, 0.f, 0.f, 0.f);
+            out[4 * c] = fmaf(w, v.x, out[4 * c] * was);
+            out[4 * c + 1] = fmaf(w, v.y, out[4 * c + 1] * was);
+            out[4 * c + 2] = fmaf(w, v.z, out[4 * c + 2] * was);
+            out[4 * c + 3] = fmaf(w, v.w, out[4 * c + 3] * was);
+        }
+    }
+    const float inv = Lo > 0.f ? 1.f / Lo : 0.f;
+    const long long row = unit.y + tok, head = unit.w * a.G + r % a.G;
+    uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.o) + row * a.o_sr + head * a.o_sh + group * 16);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        uint4 v;
+        v.x = pack_h16<F16>(out[8 * q + 0] * inv, out[8 * q + 1] * inv);
+        v.y = pack_h16<F16>(out[8 * q + 2] * inv, out[8 * q + 3] * inv);
+        v.z = pack_h16<F16>(out[8 * q + 4] * inv, out[8 * q + 5] * inv);
+        v.w = pack_h16<F16>(out[8 * q + 6] * inv, out[8 * q + 7] * inv);
+        dst[q] = v;
+    }
+    if (group == 0) a.lse[head * a.T + row] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
 }
 
 // ---------------------------------------------------------------- host side
@@ -922,7 +1028,6 @@ CUresult encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, int32_t d
 
 template <int D, bool F16, int NT>
 cudaError_t launch_tc(const CUtensorMap (&maps)[3], const PagedDev& p, int grid, cudaStream_t s) {
-    using C = Cfg<D, NT>;
     // The attribute stays with the function on a device: one call instead of one a launch (decode is paced
     // by the host). Threads that come at the same time both set it, to the same value.
     static std::atomic<uint64_t> set{0};
@@ -931,11 +1036,11 @@ cudaError_t launch_tc(const CUtensorMap (&maps)[3], const PagedDev& p, int grid,
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(set.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(paged_tc_kernel<D, F16, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+        e = cudaFuncSetAttribute(paged_tc_kernel<D, F16, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (e != cudaSuccess) return e;
         set.fetch_or(bit, std::memory_order_relaxed);
     }
-    return launch_pdl(paged_tc_kernel<D, F16, NT>, dim3(grid), dim3(C::kThreads), C::kSmemBytes, s, maps[0], maps[1],
+    return launch_pdl(paged_tc_kernel<D, F16, NT>, dim3(grid), dim3(Shape<NT>::kThreads), kSmemBytes, s, maps[0], maps[1],
                       maps[2], p);
 }
 
@@ -946,7 +1051,6 @@ cudaError_t launch_both(const CUtensorMap (&maps)[3], const PagedDev& p, const P
     CombineArgs a{};
     a.part = p.part;
     a.meta = p.meta;
-    a.ctas = grid;
     a.tiles = pl.tiles;
     a.rows = pl.rows;
     a.tok_tile = p.tok_tile;
@@ -956,9 +1060,8 @@ cudaError_t launch_both(const CUtensorMap (&maps)[3], const PagedDev& p, const P
     a.lse = p.lse;
     a.o_sr = p.o_sr;
     a.o_sh = p.o_sh;
-    a.rows_per_block = pl.tiles == 1 ? kCombineThreads / 32 : kCombineThreads / 8;
-    const int chunks = (pl.tiles * pl.rows + a.rows_per_block - 1) / a.rows_per_block;
-    return launch_pdl(paged_combine_kernel<D, F16>, dim3(grid, chunks), dim3(kCombineThreads), (size_t)grid, s, a);
+    const int chunks = (pl.tiles * pl.rows * (D / 16) + kCombineThreads - 1) / kCombineThreads;
+    return launch_pdl(paged_combine_kernel<D, F16>, dim3(grid, chunks), dim3(kCombineThreads), (2 * ((grid + 31) / 32) + grid) * sizeof(int), s, a);
 }
 
 }  // namespace
@@ -988,7 +1091,6 @@ attn_status_t launch_paged(const attn_paged_params& p, const LaunchCommon& lc, c
     a.Hkv = p.num_kv_heads;
     a.T = p.total_q;
     a.tok_tile = pl.tok_tile;
-    a.n_sm_warps = (pl.rows + 31) / 32;
     a.num_pages = p.num_pages;
     a.page_size = p.page_size;
     while ((1 << a.shift) < p.page_size) ++a.shift;
