@@ -117,13 +117,8 @@ def _type_code(name: str, t: torch.Tensor) -> int:
     return code
 
 
-def _device(*tensors: torch.Tensor) -> int:
-    """The index of the CUDA device that all tensors are on."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t.get_device() != dev or not t.is_cuda:
-            raise ValueError(f"tensors must be on one CUDA device, got {sorted({str(x.device) for x in tensors})}")
-    return dev
+def _refuse_devices(*tensors: torch.Tensor) -> None:
+    raise ValueError(f"tensors must be on one CUDA device, got {sorted({str(t.device) for t in tensors})}")
 
 
 def _guard(dev: int, stream):
@@ -139,19 +134,14 @@ def _guard(dev: int, stream):
     return None
 
 
-def _guarded(call, dev: int, stream, *args):
-    guard = _guard(dev, stream)
-    if guard is None:
-        return call(dev, *args)
-    with guard:
-        return call(dev, *args)
-
-
 def _launch(entry, dev: int, packed: bytes) -> None:
     status = entry(packed, torch._C._cuda_getCurrentRawStream(dev))
     if status:
         _check(status)
 
+
+# The entry points below are written for the host time of a call that is all right: one condition over plain
+# reads of the tensors, and a slower function that finds out what is wrong where it does not hold.
 
 def _default_max_q(total_q: int, num_seqs: int) -> int:
     # the longest chunk if every sequence brings at least one row
@@ -185,25 +175,25 @@ def paged_workspace_size(q, k_cache, v_cache, block_table, cu_q, kv_len, *, max_
 _workspace_bytes: Dict[tuple, int] = {}
 
 
-def _attn_paged(dev, q, k_cache, v_cache, block_table, cu_q, kv_len, out, lse, scale, causal, max_q, workspace):
-    total_q, hq, d = q.shape
-    if out is None:
-        out = torch.empty((total_q, hq, d), dtype=q.dtype, device=q.device)
-    if lse is None:
-        lse = torch.empty((hq, total_q), dtype=torch.float32, device=q.device)
-    if workspace is None:
-        key = (dev, d, hq, k_cache.shape[1], max_q)
-        nbytes = _workspace_bytes.get(key)
-        if nbytes is None:
-            nbytes = paged_workspace_size(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q=max_q)
-            if nbytes > 0:  # 0: nothing to do, or a call that will be refused
-                _workspace_bytes[key] = nbytes
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
-    else:
-        nbytes = workspace.numel() * workspace.element_size()
-    _launch(lib.attn_paged, dev, _pack_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, out, lse, scale, causal,
-                                             max_q, workspace.data_ptr(), nbytes))
-    return out, lse
+def _check_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, out, lse) -> None:
+    _type_code("q", q)
+    _need_dims("q", q, 3)
+    _need_dims("k_cache", k_cache, 4)
+    _need_dims("block_table", block_table, 2)
+    (total_q, hq, d), (pages, hkv, page_size, _), num_seqs = q.shape, k_cache.shape, block_table.shape[0]
+    for name, t, shape in (("q", q, (total_q, hq, d)), ("k_cache", k_cache, (pages, hkv, page_size, d)),
+                           ("v_cache", v_cache, (pages, hkv, page_size, d)), ("out", out, (total_q, hq, d))):
+        if t is not None and not _is_rows(t, q.dtype, shape):
+            _refuse(name, t, q.dtype, shape)
+    for name, t, shape in (("block_table", block_table, block_table.shape), ("cu_q", cu_q, (num_seqs + 1,)),
+                           ("kv_len", kv_len, (num_seqs,))):
+        if not _is_ints(t, shape):
+            _refuse(name, t, _INT32, shape)
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.shape != (hq, total_q):
+            _refuse("lse", lse, torch.float32, (hq, total_q))
+        if not lse.is_contiguous():
+            raise ValueError("lse must be contiguous")
 
 
 def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -220,103 +210,139 @@ def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
 
     max_q, the most rows that a sequence is expected to bring, only chooses the tile shape."""
     dtype = q.dtype
-    _type_code("q", q)
-    _need_dims("q", q, 3)
-    _need_dims("k_cache", k_cache, 4)
-    _need_dims("block_table", block_table, 2)
+    if not (dtype in _TYPES and q.dim() == 3 and k_cache.dim() == 4 and block_table.dim() == 2 and q.stride()[2] == 1
+            and k_cache.dtype is dtype and k_cache.shape[3] == q.shape[2] and k_cache.stride()[3] == 1
+            and v_cache.dtype is dtype and v_cache.shape == k_cache.shape and v_cache.stride()[3] == 1
+            and _is_ints(block_table, block_table.shape) and _is_ints(cu_q, (block_table.shape[0] + 1,))
+            and _is_ints(kv_len, (block_table.shape[0],))
+            and (out is None or (out.dtype is dtype and out.shape == q.shape and out.stride()[2] == 1))
+            and (lse is None or (lse.dtype is torch.float32 and lse.shape == (q.shape[1], q.shape[0]) and lse.is_contiguous()))):
+        _check_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, out, lse)
+    dev = q.get_device()
+    if not (dev >= 0 and k_cache.get_device() == dev and v_cache.get_device() == dev and block_table.get_device() == dev
+            and cu_q.get_device() == dev and kv_len.get_device() == dev and (out is None or out.get_device() == dev)
+            and (lse is None or lse.get_device() == dev) and (workspace is None or workspace.get_device() == dev)):
+        _refuse_devices(q, k_cache, v_cache, block_table, cu_q, kv_len, *(t for t in (out, lse, workspace) if t is not None))
     total_q, hq, d = q.shape
-    pages, hkv, page_size, _ = k_cache.shape
-    num_seqs = block_table.shape[0]
-    if q.stride()[2] != 1 and q.numel() > 0:
-        _refuse("q", q, dtype, q.shape)
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not _is_rows(t, dtype, (pages, hkv, page_size, d)):
-            _refuse(name, t, dtype, (pages, hkv, page_size, d))
-    if not _is_ints(block_table, block_table.shape):
-        _refuse("block_table", block_table, _INT32, block_table.shape)
-    if not _is_ints(cu_q, (num_seqs + 1,)):
-        _refuse("cu_q", cu_q, _INT32, (num_seqs + 1,))
-    if not _is_ints(kv_len, (num_seqs,)):
-        _refuse("kv_len", kv_len, _INT32, (num_seqs,))
-    tensors = [q, k_cache, v_cache, block_table, cu_q, kv_len]
-    if out is not None:
-        if not _is_rows(out, dtype, (total_q, hq, d)):
-            _refuse("out", out, dtype, (total_q, hq, d))
-        tensors.append(out)
-    if lse is not None:
-        if lse.dtype is not torch.float32 or lse.shape != (hq, total_q):
-            _refuse("lse", lse, torch.float32, (hq, total_q))
-        if not lse.is_contiguous():
-            raise ValueError("lse must be contiguous")
-        tensors.append(lse)
-    if workspace is not None:
-        if not workspace.is_contiguous():
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    max_q = _default_max_q(total_q, block_table.shape[0]) if max_q is None else int(max_q)
+    guard = _guard(dev, stream)
+    if guard is not None:
+        guard.__enter__()
+    try:
+        where = q.device
+        if out is None:
+            out = torch.empty((total_q, hq, d), dtype=dtype, device=where)
+        if lse is None:
+            lse = torch.empty((hq, total_q), dtype=torch.float32, device=where)
+        if workspace is None:
+            key = (dev, d, hq, k_cache.shape[1], max_q)
+            nbytes = _workspace_bytes.get(key)
+            if nbytes is None:
+                nbytes = paged_workspace_size(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q=max_q)
+                if nbytes > 0:  # 0: nothing to do, or a call that will be refused
+                    _workspace_bytes[key] = nbytes
+            workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=where)
+        elif workspace.is_contiguous():
+            nbytes = workspace.numel() * workspace.element_size()
+        else:
             raise ValueError("workspace must be contiguous")
-        tensors.append(workspace)
-    return _guarded(_attn_paged, _device(*tensors), stream, q, k_cache, v_cache, block_table, cu_q, kv_len, out, lse,
-                    1.0 / math.sqrt(d) if scale is None else float(scale), causal,
-                    _default_max_q(total_q, num_seqs) if max_q is None else int(max_q), workspace)
+        _launch(lib.attn_paged, dev, _pack_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, out, lse, scale, causal,
+                                                 max_q, workspace.data_ptr(), nbytes))
+    finally:
+        if guard is not None:
+            guard.__exit__(None, None, None)
+    return out, lse
 
 
-def _attn_pages_write(dev, packed):
-    _launch(lib.attn_pages_write, dev, packed)
+def _check_write(k, v, slots, k_cache, v_cache) -> None:
+    _type_code("k", k)
+    _need_dims("k", k, 3)
+    _need_dims("k_cache", k_cache, 4)
+    (rows, heads, d), (pages, _, page_size, _) = k.shape, k_cache.shape
+    for name, t, shape in (("k", k, (rows, heads, d)), ("v", v, (rows, heads, d)),
+                           ("k_cache", k_cache, (pages, heads, page_size, d)),
+                           ("v_cache", v_cache, (pages, heads, page_size, d))):
+        if not _is_rows(t, k.dtype, shape):
+            _refuse(name, t, k.dtype, shape)
+    if not _is_ints(slots, (rows,)):
+        _refuse("slots", slots, _INT32, (rows,))
 
 
 def attn_pages_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
                      v_cache: torch.Tensor, *, stream=None) -> None:
     """Store k, v [rows, Hkv, d] in the caches [pages, Hkv, page_size, d]: row t goes to slot
     slots[t] % page_size of page slots[t] // page_size; rows with a negative slot are skipped."""
-    dtype, code = k.dtype, _type_code("k", k)
-    _need_dims("k", k, 3)
-    _need_dims("k_cache", k_cache, 4)
+    dtype = k.dtype
+    if not (dtype in _TYPES and k.dim() == 3 and k_cache.dim() == 4 and k.stride()[2] == 1
+            and v.dtype is dtype and v.shape == k.shape and v.stride()[2] == 1
+            and k_cache.dtype is dtype and k_cache.shape[1] == k.shape[1] and k_cache.shape[3] == k.shape[2]
+            and k_cache.stride()[3] == 1 and v_cache.dtype is dtype and v_cache.shape == k_cache.shape
+            and v_cache.stride()[3] == 1 and _is_ints(slots, (k.shape[0],))):
+        _check_write(k, v, slots, k_cache, v_cache)
+    dev = k.get_device()
+    if not (dev >= 0 and v.get_device() == dev and slots.get_device() == dev and k_cache.get_device() == dev
+            and v_cache.get_device() == dev):
+        _refuse_devices(k, v, slots, k_cache, v_cache)
     rows, heads, d = k.shape
     pages, _, page_size, _ = k_cache.shape
-    if k.stride()[2] != 1 and k.numel() > 0:
-        _refuse("k", k, dtype, k.shape)
-    if not _is_rows(v, dtype, (rows, heads, d)):
-        _refuse("v", v, dtype, (rows, heads, d))
-    if not _is_ints(slots, (rows,)):
-        _refuse("slots", slots, _INT32, (rows,))
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not _is_rows(t, dtype, (pages, heads, page_size, d)):
-            _refuse(name, t, dtype, (pages, heads, page_size, d))
     kr, kh, _ = k.stride()
     vr, vh, _ = v.stride()
     kp, kch, ks, _ = k_cache.stride()
     vp, vch, vs, _ = v_cache.stride()
-    _guarded(_attn_pages_write, _device(k, v, slots, k_cache, v_cache), stream, _WRITE.pack(
-        rows, heads, d, pages, page_size, code, 0, 0, k.data_ptr(), v.data_ptr(), slots.data_ptr(), k_cache.data_ptr(),
-        v_cache.data_ptr(), kr, kh, vr, vh, kp, kch, ks, vp, vch, vs))
+    packed = _WRITE.pack(rows, heads, d, pages, page_size, _TYPES[dtype], 0, 0, k.data_ptr(), v.data_ptr(), slots.data_ptr(),
+                         k_cache.data_ptr(), v_cache.data_ptr(), kr, kh, vr, vh, kp, kch, ks, vp, vch, vs)
+    guard = _guard(dev, stream)
+    if guard is None:
+        _launch(lib.attn_pages_write, dev, packed)
+    else:
+        with guard:
+            _launch(lib.attn_pages_write, dev, packed)
 
 
-def _check_tables(name: str, first: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor,
-                  free_pages: torch.Tensor, free_count: torch.Tensor) -> int:
-    """The checks that plan and release share; `first` has an entry per sequence. Returns the number of
-    sequences."""
-    _need_dims(name, first, 1)
-    _need_dims("block_table", block_table, 2)
-    n = first.shape[0]
-    if not (_is_ints(first, (n,)) and _is_ints(kv_len, (n,)) and _is_ints(block_table, (n, block_table.shape[1]))
+def _check_tables(name, first, kv_len, block_table, free_pages, free_count) -> int:
+    """The checks that plan and release share; `first` has an entry per sequence. Returns the device."""
+    n, columns = first.numel(), block_table.shape[-1] if block_table.dim() else 0
+    if not (_is_ints(first, (n,)) and _is_ints(kv_len, (n,)) and _is_ints(block_table, (n, columns))
             and _is_ints(free_pages, (free_pages.numel(),)) and _is_ints(free_count, (1,))):
-        for what, t, shape in ((name, first, (n,)), ("kv_len", kv_len, (n,)), ("block_table", block_table, (n, block_table.shape[1])),
+        _need_dims(name, first, 1)
+        _need_dims("block_table", block_table, 2)
+        for what, t, shape in ((name, first, (n,)), ("kv_len", kv_len, (n,)), ("block_table", block_table, (n, columns)),
                                ("free_pages", free_pages, (free_pages.numel(),)), ("free_count", free_count, (1,))):
             if not _is_ints(t, shape):
                 _refuse(what, t, _INT32, shape)
-    return n
+    dev = first.get_device()
+    if not (dev >= 0 and kv_len.get_device() == dev and block_table.get_device() == dev and free_pages.get_device() == dev
+            and free_count.get_device() == dev):
+        _refuse_devices(first, kv_len, block_table, free_pages, free_count)
+    return dev
 
 
-def _attn_pages_plan(dev, q_len, kv_len, block_table, free_pages, free_count, page_size, total_q, outs):
+def _output(name: str, t: Optional[torch.Tensor], n: int, like: torch.Tensor) -> torch.Tensor:
+    """An int32 output of n entries: `t` if it was given."""
+    if t is None:
+        return torch.empty(n, dtype=_INT32, device=like.device)
+    if not _is_ints(t, (n,)):
+        _refuse(name, t, _INT32, (n,))
+    if t.get_device() != like.get_device():
+        _refuse_devices(like, t)
+    return t
+
+
+def _plan_call(dev, q_len, kv_len, block_table, free_pages, free_count, page_size, total_q, cu_q, new_len, slots, positions,
+               free_left):
     n, columns = block_table.shape
-    where = q_len.device
-    outs = cu_q, new_len, slots, positions, free_left = [
-        torch.empty(m, dtype=_INT32, device=where) if t is None else t
-        for t, m in zip(outs, (n + 1, n, total_q, total_q, 1))]
+    cu_q = _output("cu_q", cu_q, n + 1, q_len)
+    new_len = _output("new_len", new_len, n, q_len)
+    slots = _output("slots", slots, total_q, q_len)
+    positions = _output("positions", positions, total_q, q_len)
+    free_left = _output("free_left", free_left, 1, q_len)
     _launch(lib.attn_pages_plan, dev, _PLAN.pack(
-        n, total_q, page_size, columns, free_pages.shape[0], 0, q_len.data_ptr(), kv_len.data_ptr(),
-        block_table.data_ptr(), block_table.stride(0) if n > 1 else columns, free_pages.data_ptr(),
-        free_count.data_ptr(), cu_q.data_ptr(), new_len.data_ptr(), slots.data_ptr(), positions.data_ptr(),
-        free_left.data_ptr()))
-    return tuple(outs)
+        n, total_q, page_size, columns, free_pages.numel(), 0, q_len.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(),
+        block_table.stride()[0] if n > 1 else columns, free_pages.data_ptr(), free_count.data_ptr(), cu_q.data_ptr(),
+        new_len.data_ptr(), slots.data_ptr(), positions.data_ptr(), free_left.data_ptr()))
+    return cu_q, new_len, slots, positions, free_left
 
 
 def attn_pages_plan(q_len: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -331,28 +357,25 @@ def attn_pages_plan(q_len: torch.Tensor, kv_len: torch.Tensor, block_table: torc
     [total_q], positions [total_q], free_left [1]); total_q is the number of query rows, padding
     included, whose slots and positions are -1. All int32 on the GPU. new_len and free_left are the
     next call's kv_len and free_count. free_left < 0: pages were missing."""
-    n = _check_tables("q_len", q_len, kv_len, block_table, free_pages, free_count)
+    dev = _check_tables("q_len", q_len, kv_len, block_table, free_pages, free_count)
     if total_q < 0:
         raise ValueError(f"total_q must not be negative, got {total_q}")
-    outs, given = (cu_q, new_len, slots, positions, free_left), []
-    for name, t, m in zip(("cu_q", "new_len", "slots", "positions", "free_left"), outs, (n + 1, n, total_q, total_q, 1)):
-        if t is not None:
-            if not _is_ints(t, (m,)):
-                _refuse(name, t, _INT32, (m,))
-            given.append(t)
-    return _guarded(_attn_pages_plan, _device(q_len, kv_len, block_table, free_pages, free_count, *given), stream, q_len,
-                    kv_len, block_table, free_pages, free_count, page_size, total_q, outs)
+    args = (dev, q_len, kv_len, block_table, free_pages, free_count, page_size, total_q, cu_q, new_len, slots, positions,
+            free_left)
+    guard = _guard(dev, stream)
+    if guard is None:
+        return _plan_call(*args)
+    with guard:
+        return _plan_call(*args)
 
 
-def _attn_pages_release(dev, done, kv_len, block_table, free_pages, free_count, page_size, new_len, free_left):
+def _release_call(dev, done, kv_len, block_table, free_pages, free_count, page_size, new_len, free_left):
     n, columns = block_table.shape
-    if new_len is None:
-        new_len = torch.empty(n, dtype=_INT32, device=done.device)
-    if free_left is None:
-        free_left = torch.empty(1, dtype=_INT32, device=done.device)
+    new_len = _output("new_len", new_len, n, done)
+    free_left = _output("free_left", free_left, 1, done)
     _launch(lib.attn_pages_release, dev, _RELEASE.pack(
-        n, page_size, columns, free_pages.shape[0], done.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(),
-        block_table.stride(0) if n > 1 else columns, free_pages.data_ptr(), free_count.data_ptr(), new_len.data_ptr(),
+        n, page_size, columns, free_pages.numel(), done.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(),
+        block_table.stride()[0] if n > 1 else columns, free_pages.data_ptr(), free_count.data_ptr(), new_len.data_ptr(),
         free_left.data_ptr()))
     return new_len, free_left
 
@@ -363,12 +386,10 @@ def attn_pages_release(done: torch.Tensor, kv_len: torch.Tensor, block_table: to
     """Push the pages of the sequences with done[b] != 0 onto the stack free_pages, in place from
     free_count[0] on. Returns (new_len [B], free_left [1]): new_len is 0 for those sequences and kv_len
     for the others. All int32 on the GPU."""
-    n = _check_tables("done", done, kv_len, block_table, free_pages, free_count)
-    given = []
-    for name, t, m in (("new_len", new_len, n), ("free_left", free_left, 1)):
-        if t is not None:
-            if not _is_ints(t, (m,)):
-                _refuse(name, t, _INT32, (m,))
-            given.append(t)
-    return _guarded(_attn_pages_release, _device(done, kv_len, block_table, free_pages, free_count, *given), stream, done,
-                    kv_len, block_table, free_pages, free_count, page_size, new_len, free_left)
+    dev = _check_tables("done", done, kv_len, block_table, free_pages, free_count)
+    args = (dev, done, kv_len, block_table, free_pages, free_count, page_size, new_len, free_left)
+    guard = _guard(dev, stream)
+    if guard is None:
+        return _release_call(*args)
+    with guard:
+        return _release_call(*args)
