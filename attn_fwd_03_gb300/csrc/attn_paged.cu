@@ -52,7 +52,7 @@ using namespace ptx;
 constexpr int BM = 128;  // query rows per tile
 constexpr int BN = 128;  // keys per tile
 constexpr float kRescaleThreshold = 8.0f;
-constexpr int kUnitCost = 64;  // what a unit costs beyond its key tiles, in keys
+constexpr int kUnitCost = 384;  // what a unit costs beyond its key tiles, in keys
 constexpr float kPairCost = 1.5f;  // a key tile of a two-tile unit against one of a one-tile unit
 constexpr int kTilesBytes = 224 * 1024;  // shared memory for Q, K and V tiles
 constexpr unsigned kFull = 0xffffffffu;
@@ -125,7 +125,7 @@ struct __align__(16) Shared {
     Place place[12];       // of each warp
     int4 unit[12];         // of each softmax warp, the unit it is in: first row of q, tokens, key/value
                            // head, 1 if it holds the first key tile + 2 if the last
-    long long scan[3][12]; // per warp: sums of either class, running sum
+    long long scan[2][12]; // per warp: its sequences' cost on either line
     int pair;              // whether this CTA works on two-tile units
     int widest[12], sm_warps;  // most rows of a one-tile unit; softmax warps of a tile that hold rows
     uint32_t tmem_base;
@@ -182,83 +182,76 @@ __device__ __forceinline__ void locate(const PagedDev& p, Shared& sh) {
     constexpr int THREADS = Shape<NT>::kThreads, WARPS = THREADS / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     bool bad = false;
-    Seq s{0, 0, 0};
-    long long per_head = 0, sum0 = 0, sum1 = 0;
+    long long done[2] = {0, 0};  // cost of the chunks of sequences before this one, of either line
     int rows = 0;
-    for (int b = tid; b < p.B; b += THREADS) {
-        s = seq_of(p, b, &bad);
-        if (is_pair<NT>(p, s)) {
-            per_head = head_cost(p, s, 2 * p.tok_tile);
-            sum1 += per_head * p.Hkv;
-        } else {
-            per_head = head_cost(p, s, p.tok_tile);
-            sum0 += per_head * p.Hkv;
-            rows = max(rows, min(s.n, p.tok_tile) * p.G);
+    // the last chunk: this thread's sequence, its cost per head, and the lines' ends behind it
+    Seq s{0, 0, 0};
+    long long per_head = 0, end[2] = {0, 0};
+    auto scan = [&](int b0, bool first) {
+        const int b = b0 + tid;
+        s = Seq{0, 0, 0};
+        if (b < p.B) s = seq_of(p, b, first ? &bad : nullptr);
+        const bool two = is_pair<NT>(p, s);
+        per_head = head_cost(p, s, two ? 2 * p.tok_tile : p.tok_tile);
+        if (first && !two) rows = max(rows, min(s.n, p.tok_tile) * p.G);
+#pragma unroll
+        for (int k = 0; k < NT; ++k) {
+            long long x = two == (k == 1) ? per_head * p.Hkv : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(kFull, x, o);
+                if (lane >= o) x += u;
+            }
+            end[k] = done[k] + x;
+            if (lane == 31) sh.scan[k][warp] = x;
         }
+        if (first) {
+            const int widest = __reduce_max_sync(kFull, rows);
+            if (lane == 0) sh.widest[warp] = widest;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < NT; ++k) {
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
+                if (w < warp) end[k] += sh.scan[k][w];
+                done[k] += sh.scan[k][w];
+            }
+        }
+    };
+    if (tid == 0) sh.first.u0 = -1;
+    for (int b0 = 0; b0 < p.B; b0 += THREADS) {
+        if (b0 > 0) __syncthreads();  // the last use of scan
+        scan(b0, true);
     }
     if (bad && blockIdx.x == 0) atomicCAS(p.err, 0, ATTN_ERR_INVALID);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        sum0 += __shfl_xor_sync(kFull, sum0, o);
-        if (NT == 2) sum1 += __shfl_xor_sync(kFull, sum1, o);
-    }
-    rows = __reduce_max_sync(kFull, rows);
-    if (lane == 0) {
-        sh.scan[0][warp] = sum0;
-        sh.scan[1][warp] = sum1;
-        sh.widest[warp] = rows;
-    }
-    if (tid == 0) sh.first.u0 = -1;
-    __syncthreads();
-    long long total0 = 0, total1 = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-        total0 += sh.scan[0][w];
-        if (NT == 2) total1 += sh.scan[1][w];
-        rows = max(rows, sh.widest[w]);
-    }
+    for (int w = 0; w < WARPS; ++w) rows = max(rows, sh.widest[w]);
     int i = blockIdx.x, n = gridDim.x;
     bool pair = false;
     if (NT == 2) {
-        const float c0 = (float)total0, c1 = (float)total1 * kPairCost;
-        int n0 = total0 == 0 ? 0 : max(1, (int)(n * (c0 / (c0 + c1)) + 0.5f));
-        if (total1 > 0) n0 = min(n0, n - 1);
+        const float c0 = (float)done[0], c1 = (float)done[1] * kPairCost;
+        int n0 = done[0] == 0 ? 0 : max(1, (int)(n * (c0 / (c0 + c1)) + 0.5f));
+        if (done[1] > 0) n0 = min(n0, n - 1);
         pair = i >= n0;
         i = pair ? i - n0 : i;
         n = pair ? n - n0 : n0;
     }
-    const long long total = pair ? total1 : total0;
+    const long long total = pair ? done[1] : done[0];
     const long long each = total / max(n, 1), rest = total - each * n;
     const long long x0 = each * i + min((long long)i, rest), x1 = x0 + each + (i < rest ? 1 : 0);
-    long long before = 0;  // cost of the chunks of sequences before this one
+    done[0] = done[1] = 0;
     for (int b0 = 0; b0 < p.B && x0 < x1; b0 += THREADS) {
-        const int b = b0 + tid;
-        if (p.B > THREADS) {
-            s = b < p.B ? seq_of(p, b, nullptr) : Seq{0, 0, 0};
-            per_head = head_cost(p, s, is_pair<NT>(p, s) ? 2 * p.tok_tile : p.tok_tile);
+        if (p.B > THREADS) {  // else the scan above is the one to look at
+            __syncthreads();
+            scan(b0, false);
         }
-        const long long mine = is_pair<NT>(p, s) == pair ? per_head * p.Hkv : 0;
-        long long x = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(kFull, x, o);
-            if (lane >= o) x += u;
-        }
-        if (b0 > 0) __syncthreads();  // the last use of scan
-        if (lane == 31) sh.scan[2][warp] = x;
-        __syncthreads();
-        long long chunk = 0;
-        x += before;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            if (w < warp) x += sh.scan[2][w];
-            chunk += sh.scan[2][w];
-        }
-        if (x - mine <= x0 && x0 < x) {
+        const long long hi_end = pair ? end[1] : end[0];
+        const long long begin = hi_end - (is_pair<NT>(p, s) == pair ? per_head * p.Hkv : 0);
+        if (begin <= x0 && x0 < hi_end) {
             const int step = pair ? 2 * p.tok_tile : p.tok_tile;
-            const long long at = x0 - (x - mine);
-            const int h = (int)(at / per_head);
-            const long long in_head = at - h * per_head;
+            const int h = (int)((x0 - begin) / per_head);
+            const long long in_head = x0 - begin - h * per_head;
             int lo = 0, hi = (s.n + step - 1) / step;  // the last unit that starts at or before in_head
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
@@ -267,10 +260,9 @@ __device__ __forceinline__ void locate(const PagedDev& p, Shared& sh) {
                 else
                     hi = mid;
             }
-            sh.first = Place{x - mine + h * per_head + cost_before(p, s, step, lo), b, h, lo, s};
+            sh.first = Place{begin + h * per_head + cost_before(p, s, step, lo), b0 + tid, h, lo, s};
         }
-        before += chunk;
-        if (before > x0) break;
+        if ((pair ? done[1] : done[0]) > x0) break;
     }
     if (tid == 0) {
         sh.x0 = x0;
@@ -551,7 +543,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                             tc_fence_after();
                             const uint32_t qt = sQ + t * C::kTileBytes, kt = sKV + sK * C::kTileBytes;
                             if (elect_one()) {
-#pragma unroll
+#pragma unroll 2
                                 for (int kk = 0; kk < D / 16; ++kk)
                                     mma_ss(tS, kmajor_desc(qt, kk), kmajor_desc(kt, kk), kIdescS, kk > 0 ? 1u : 0u);
                                 mma_commit(&bar.s_full[t]);
@@ -573,7 +565,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                             tc_fence_after();
                             const uint32_t vt = sKV + sV_prev * C::kTileBytes;
                             if (elect_one()) {
-#pragma unroll
+#pragma unroll 2
                                 for (int kk = 0; kk < BN / 16; ++kk)
                                     mma_ts(tO, tP + kk * 8, vmajor_desc(vt, kk), kIdescO, (j > 1 || kk > 0) ? 1u : 0u);
                                 mma_commit(&bar.pv_done[t]);
@@ -628,7 +620,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                             tc_fence_after();
                             const uint32_t vt = sKV + sV_prev * C::kTileBytes;
                             if (elect_one()) {
-#pragma unroll
+#pragma unroll 2
                                 for (int kk = 0; kk < BN / 16; ++kk)
                                     mma_ts(tO, tS + kk * 8, vmajor_desc(vt, kk), kIdescO, (j > 1 || kk > 0) ? 1u : 0u);
                             }
@@ -637,7 +629,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                         if (j < w.cnt(t)) {
                             const uint32_t qt = sQ + t * C::kTileBytes, kt = sKV + sK * C::kTileBytes;
                             if (elect_one()) {
-#pragma unroll
+#pragma unroll 2
                                 for (int kk = 0; kk < D / 16; ++kk)
                                     mma_ss(tS, kmajor_desc(qt, kk), kmajor_desc(kt, kk), kIdescS, kk > 0 ? 1u : 0u);
                                 mma_commit(&bar.s_full[t]);
@@ -812,7 +804,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                     const float inv = den > 0.f ? 1.f / den : 0.f;
                     const long long row = u.x + my_tok, head = u.z * p.G + my_head;
                     uint16_t* orow = reinterpret_cast<uint16_t*>(p.o) + row * p.o_sr + head * p.o_sh;
-#pragma unroll
+#pragma unroll 1
                     for (int c0 = 0; c0 < D; c0 += 32) {
                         uint32_t ov[32];
                         if (cnt > 0) {
@@ -957,27 +949,38 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Co
     float M = -INFINITY, L = 0.f, Lo = 0.f, out[16];
 #pragma unroll
     for (int c = 0; c < 16; ++c) out[c] = 0.f;
-    // one pass with a running maximum, so that the loads of several parts are in flight at once
-#pragma unroll 3
-    for (int k = 0; k < parts; ++k) {
-        const float4* rec = record(a.part, slots[k], a.tiles, t, a.rows, D) + r;
-        const float4 head = rec[0];
-        float4 o[4];
+    // One pass with a running maximum, four parts' loads in flight at a time. Entries behind the last part
+    // repeat it; their weight is 0.
+    for (int k0 = 0; k0 < parts; k0 += 4) {
+        float4 head[4], o[4][4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) o[c] = rec[(1 + group * 4 + c) * a.rows];
-        const float m = fmaxf(M, head.x);
-        // a part without a key of this row: its o was not written
-        const float was = M == -INFINITY ? 0.f : ex2(M - m), w = head.x == -INFINITY ? 0.f : ex2(head.x - m);
+        for (int q = 0; q < 4; ++q) {
+            const float4* rec = record(a.part, slots[min(k0 + q, parts - 1)], a.tiles, t, a.rows, D) + r;
+            head[q] = rec[0];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[q][c] = rec[(1 + group * 4 + c) * a.rows];
+            if (k0 + q >= parts) head[q].x = -INFINITY;
+        }
+        const float m = fmaxf(fmaxf(M, fmaxf(head[0].x, head[1].x)), fmaxf(head[2].x, head[3].x));
+        const float was = M == -INFINITY ? 0.f : ex2(M - m);
         M = m;
-        L = L * was + w * head.y;
-        Lo = Lo * was + w * head.z;
+        L *= was;
+        Lo *= was;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const float4 v = w > 0.f ? o[c] : make_float4(0.f, 0.f, 0.f, 0.f);
-            out[4 * c] = fmaf(w, v.x, out[4 * c] * was);
-            out[4 * c + 1] = fmaf(w, v.y, out[4 * c + 1] * was);
-            out[4 * c + 2] = fmaf(w, v.z, out[4 * c + 2] * was);
-            out[4 * c + 3] = fmaf(w, v.w, out[4 * c + 3] * was);
+        for (int c = 0; c < 16; ++c) out[c] *= was;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (head[q].x == -INFINITY) continue;  // no key of this row in the part: its o was not written
+            const float w = ex2(head[q].x - m);
+            L = fmaf(w, head[q].y, L);
+            Lo = fmaf(w, head[q].z, Lo);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                out[4 * c] = fmaf(w, o[q][c].x, out[4 * c]);
+                out[4 * c + 1] = fmaf(w, o[q][c].y, out[4 * c + 1]);
+                out[4 * c + 2] = fmaf(w, o[q][c].z, out[4 * c + 2]);
+                out[4 * c + 3] = fmaf(w, o[q][c].w, out[4 * c + 3]);
+            }
         }
     }
     const float inv = Lo > 0.f ? 1.f / Lo : 0.f;
