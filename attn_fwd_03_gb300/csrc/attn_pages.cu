@@ -144,49 +144,72 @@ struct ReleaseArgs {
 };
 
 // Block i handles sequences [i * per_block, (i + 1) * per_block): it adds up the pages that the
-// sequences before them give back, then each warp copies whole sequences' table rows.
+// sequences before them give back, places its own 256 at a time by a prefix sum, and copies their table
+// rows one after another.
 __global__ void __launch_bounds__(kScan) pages_release_kernel(const ReleaseArgs a) {
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const attn_pages_release_params& p = a.p;
-    __shared__ long long s_warp[kScan / 32];
+    __shared__ long long s_warp[kScan / 32], s_base[kScan];  // s_base: where a sequence's first page goes
+    __shared__ int s_pages[kScan];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const long long b0 = (long long)blockIdx.x * a.per_block;
     const int b_end = (int)min((long long)p.num_seqs, b0 + a.per_block);
     bool bad = false;
-    auto pages = [&](int b) -> int {  // pages that sequence b gives back
-        if (p.done[b] == 0) return 0;
-        const int m = pages_of(max(p.kv_len[b], 0), a.shift);
-        return min(m, p.max_pages);
+    auto pages = [&](int gone, int len) -> int {  // pages that a sequence gives back
+        return gone != 0 ? min(pages_of(max(len, 0), a.shift), p.max_pages) : 0;
     };
     long long sum = 0;
-    for (int b = tid; b < b0; b += kScan) sum += pages(b);
+#pragma unroll 4
+    for (int b = tid; b < b0; b += kScan) sum += pages(p.done[b], p.kv_len[b]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
     if (lane == 0) s_warp[warp] = sum;
-    __syncthreads();
     const int count = p.free_count[0];
+    __syncthreads();
     long long base = count;
 #pragma unroll
     for (int w = 0; w < kScan / 32; ++w) base += s_warp[w];
-    for (int b = (int)b0; b < b_end; ++b) {
-        const int m = pages(b);
-        if ((b - (int)b0) % (kScan / 32) == warp) {
-            const int32_t* row = p.block_table + b * p.table_stride;
-            for (int i = lane; i < m; i += 32) {
-                const long long to = base + i;
+    for (int c0 = (int)b0; c0 < b_end; c0 += kScan) {
+        const int b = c0 + tid;
+        int m = 0;
+        if (b < b_end) {
+            const int gone = p.done[b], len = p.kv_len[b];
+            bad |= len < 0 || len > (long long)p.max_pages << a.shift;
+            m = pages(gone, len);
+            p.new_len[b] = gone != 0 ? 0 : len;
+        }
+        long long x = m;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(kFull, x, o);
+            if (lane >= o) x += u;
+        }
+        __syncthreads();  // the last use of the sums and places
+        if (lane == 31) s_warp[warp] = x;
+        __syncthreads();
+        x += base;
+#pragma unroll
+        for (int w = 0; w < kScan / 32; ++w) {
+            if (w < warp) x += s_warp[w];
+            base += s_warp[w];
+        }
+        s_base[tid] = x - m;
+        s_pages[tid] = m;
+        __syncthreads();
+        for (int k = 0; k < min(kScan, b_end - c0); ++k) {
+            const int32_t* row = p.block_table + (c0 + k) * p.table_stride;
+            const long long first = s_base[k];
+            const int n = s_pages[k];
+#pragma unroll 4
+            for (int i = tid; i < n; i += kScan) {
+                const long long to = first + i;
                 if (to >= 0 && to < p.free_capacity)
                     p.free_pages[to] = row[i];
                 else
                     bad = true;
             }
-            if (lane == 0) {
-                const int len = p.kv_len[b];
-                bad |= len < 0 || len > (long long)p.max_pages << a.shift;
-                p.new_len[b] = p.done[b] != 0 ? 0 : len;
-            }
         }
-        base += m;
     }
     if (b_end == p.num_seqs && tid == 0) p.free_left[0] = (int)min(base, (long long)INT32_MAX);
     if (bad) note_bad(a.err);
@@ -242,7 +265,7 @@ cudaError_t launch_pages_plan(const attn_pages_plan_params& p, const LaunchCommo
     PlanArgs a{};
     a.p = p;
     a.shift = log2_of(p.page_size);
-    a.per_block = 4 * kScan;
+    a.per_block = 2 * kScan;  // 5.0 us for 65.6k tokens of 500 sequences, 6.2 with 4 kScan, 5.2 with kScan
     a.err = lc.err;
     const int grid = p.total_q > 0 ? (int)(((long long)p.total_q + a.per_block - 1) / a.per_block) : 1;
     return launch_pdl(pages_plan_kernel, dim3(grid), dim3(kScan), 0, s, a);
@@ -252,11 +275,11 @@ cudaError_t launch_pages_release(const attn_pages_release_params& p, const Launc
     ReleaseArgs a{};
     a.p = p;
     a.shift = log2_of(p.page_size);
-    // one sequence to a warp, more only when that would make more than two blocks an SM (each
+    // one sequence to a block, more only when that would make more than four blocks an SM (each
     // block reads the lengths before its own)
-    const int blocks = 2 * lc.num_sms;
+    const int blocks = 4 * lc.num_sms;
     const int even = (int)(((long long)p.num_seqs + blocks - 1) / blocks);
-    a.per_block = even > kScan / 32 ? even : kScan / 32;
+    a.per_block = even > 1 ? even : 1;
     a.err = lc.err;
     const int grid = p.num_seqs > 0 ? (int)(((long long)p.num_seqs + a.per_block - 1) / a.per_block) : 1;
     return launch_pdl(pages_release_kernel, dim3(grid), dim3(kScan), 0, s, a);
