@@ -173,6 +173,19 @@ def paged_workspace_size(q, k_cache, v_cache, block_table, cu_q, kv_len, *, max_
 
 # (device, d, heads, key/value heads, max_q) -> bytes; all that the size depends on
 _workspace_bytes: Dict[tuple, int] = {}
+# device -> workspace of calls on its default stream, which are in order and cannot be captured. An
+# allocation costs a decode call about a third of its host time. Calls on other streams allocate: a
+# stream's handle may come back for another stream, and a captured graph needs memory of its own.
+_default_workspace: Dict[int, torch.Tensor] = {}
+
+
+def _workspace(dev: int, nbytes: int) -> torch.Tensor:
+    if torch._C._cuda_getCurrentRawStream(dev) != 0:
+        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+    kept = _default_workspace.get(dev)
+    if kept is None or kept.numel() < nbytes:
+        kept = _default_workspace[dev] = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+    return kept
 
 
 def _check_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, out, lse) -> None:
@@ -243,7 +256,7 @@ def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
                 nbytes = paged_workspace_size(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q=max_q)
                 if nbytes > 0:  # 0: nothing to do, or a call that will be refused
                     _workspace_bytes[key] = nbytes
-            workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=where)
+            workspace = _workspace(dev, max(nbytes, 1))
         elif workspace.is_contiguous():
             nbytes = workspace.numel() * workspace.element_size()
         else:

@@ -404,6 +404,15 @@ attn_status_t bwd_check_inputs(const attn_bwd_params* p, bool* empty) {
 attn_status_t launch_setup(LaunchCommon* lc) { return device_setup(lc); }
 
 attn_status_t map_encoder(PFN_cuTensorMapEncodeTiled_v12000* encode) {
+    // A host thread that has made no runtime call yet has no current context, and the encoder (a driver
+    // call) needs one: cudaSetDevice makes the device's primary context current.
+    thread_local int bound = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev != bound) {
+        if ((e = cudaSetDevice(dev)) == cudaSuccess) bound = dev;
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
     const attn_status_t st = get_encoder();
     *encode = g_encode;
     return st;

@@ -40,6 +40,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -1047,8 +1048,13 @@ cudaError_t launch_tc(const CUtensorMap (&maps)[3], const PagedDev& p, int grid,
                       maps[2], p);
 }
 
+// Held from a call's first launch to its last, so that calls of several host threads on one stream may share
+// a workspace: the parts that one call leaves there are merged before the next call's are written.
+std::mutex g_launch_mu;
+
 template <int D, bool F16>
 cudaError_t launch_both(const CUtensorMap (&maps)[3], const PagedDev& p, const Plan& pl, int grid, cudaStream_t s) {
+    std::lock_guard<std::mutex> lock(g_launch_mu);
     const cudaError_t e = pl.tiles == 1 ? launch_tc<D, F16, 1>(maps, p, grid, s) : launch_tc<D, F16, 2>(maps, p, grid, s);
     if (e != cudaSuccess) return e;
     CombineArgs a{};

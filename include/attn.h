@@ -316,7 +316,8 @@ typedef struct attn_paged_params {
     int64_t q_stride[2], o_stride[2];  /* elements, (row, head) */
     int64_t k_stride[3], v_stride[3];  /* elements, (page, head, slot) */
     void *workspace;         /* >= attn_paged_workspace_size(p) bytes, 256-byte aligned; scratch after the
-                                call. Calls that may overlap on the GPU need one each */
+                                call. Calls that may overlap on the GPU need one each; calls on one
+                                stream may share it, from several host threads too */
     size_t workspace_bytes;
 } attn_paged_params;
 

@@ -205,6 +205,30 @@ def test_same_bits_on_every_call_and_stream(A, n, kv):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+def test_threads_on_one_stream(A):
+    # calls of several host threads on the default stream share the binding's workspace there
+    import threading
+    cases = [Case([1] * 3, [900, 1300, 40], 2, 4, 64, 16, torch.bfloat16, 97), Case([90, 2], [900, 700], 2, 2, 64, 16, torch.bfloat16, 98)]
+    args = [c.device() for c in cases]
+    want = [A.attn_paged(*a, causal=True) for a in args]
+    _ok(A)
+    got = [[], []]
+
+    def calls(k):
+        for _ in range(40):
+            got[k].append(A.attn_paged(*args[k], causal=True))
+
+    threads = [threading.Thread(target=calls, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    _ok(A)
+    for c, w, g in zip(cases, want, got):
+        c.check(*w, True)
+        assert len(g) == 40 and all(torch.equal(w[0], o) and torch.equal(w[1], l) for o, l in g)
+
+
 def test_against_attn_fwd_and_decode(A):
     # a whole prompt is the causal forward, its last rows are the causal decode
     B, H, N, d, page = 1, 3, 384, 64, 128
