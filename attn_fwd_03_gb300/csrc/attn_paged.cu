@@ -916,12 +916,12 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Co
     grid_dep_wait();
     const int e = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int4 unit = a.meta[e * 2];
-    if (unit.x != kLast) return;
     // bit c of has[0] / has[1]: CTA c's slot 0 / 1 holds a part (c <= e)
     extern __shared__ unsigned s_mem[];
     const int words = (gridDim.x + 31) / 32;
     unsigned *has0 = s_mem, *has1 = s_mem + words;
     int* slots = reinterpret_cast<int*>(s_mem + 2 * words);  // the unit's, in the order of the keys
+    // read before it is known whether this block has work, so that the reads overlap
     for (int w = warp; w < words; w += kCombineThreads / 32) {
         const int c = w * 32 + lane;
         const unsigned m0 = __ballot_sync(kFull, c <= e && a.meta[min(c, e) * 2].x != kNone);
@@ -931,6 +931,7 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Co
             has1[w] = m1;
         }
     }
+    if (unit.x != kLast) return;
     __syncthreads();
     int first = 0;
     for (int w = 0; w < words; ++w)
