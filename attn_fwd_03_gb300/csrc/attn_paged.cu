@@ -57,6 +57,7 @@ constexpr int kUnitCost = 384;  // what a unit costs beyond its key tiles, in ke
 constexpr float kPairCost = 1.5f;  // a key tile of a two-tile unit against one of a one-tile unit
 constexpr int kTilesBytes = 224 * 1024;  // shared memory for Q, K and V tiles
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kIssueUnroll = 4;  // k-steps of a product in a row: 2 is 1 % slower, 1 11 %, 8 the same
 
 // A CTA that works on units of NT tiles; the warps of its roles begin at FIRST, behind the softmax warps.
 template <int D, int NT, int FIRST>
@@ -68,7 +69,13 @@ struct Cfg {
     static constexpr int kQOff = 0;
     static constexpr int kKVOff = kQOff + NT * kTileBytes;
     static constexpr int kStages = (kTilesBytes - kKVOff) / kTileBytes;  // K and V tiles in flight
-    static constexpr int kProducer = FIRST, kIssuer = FIRST + 1, kTail = FIRST + 2, kIssuer1 = FIRST + 3;  // warps
+    // warps: K (and V) producer, MMA issuer, Q producer and V tail; the fourth is the V producer, except where
+    // it has to issue the second tile's products
+    static constexpr int kProducer = FIRST, kIssuer = FIRST + 1, kTail = FIRST + 2, kFourth = FIRST + 3;
+    static constexpr bool kVProducer = kIssuers == 1;
+    // NT = 2 kernel: registers per thread after the rebalance, 2 x 128 x softmax + 128 x other = 384 x 168
+    static constexpr int kSoftmaxRegs = D == 64 ? 192 : 200, kOtherRegs = D == 64 ? 120 : 104;
+    static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= 384 * 168, "register split");
 };
 
 // The kernel for batches whose sequences all fit one tile (NT = 1), and the one that also takes longer
@@ -76,10 +83,7 @@ struct Cfg {
 template <int NT>
 struct Shape {
     static constexpr int kFirst = 4 * NT;
-    static constexpr int kThreads = NT == 1 ? 224 : 384;
-    // NT = 2: registers per thread after the rebalance, 2 x 128 x softmax + 128 x other = 384 x 168
-    static constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
-    static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= 384 * 168, "register split");
+    static constexpr int kThreads = NT == 1 ? 256 : 384;
 };
 constexpr int kSmemBytes = kTilesBytes + 2048 + 1024;  // barriers and schedule + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory");
@@ -117,7 +121,7 @@ struct Place {
 };
 
 struct __align__(16) Shared {
-    uint64_t q_full, q_empty;
+    uint64_t q_full[4], q_empty[4];  // one tile: of Q slots in turn; two tiles: of either (split P) or of both
     uint64_t kv_full[13], kv_empty[13], v_tail[13];
     uint64_t s_full[2], p_full[2], o_full[2], s_free[2], pv_done[2];
     uint64_t drain[2];
@@ -361,17 +365,47 @@ __device__ __forceinline__ float4* record(float* part, int slot, int tiles, int 
 }
 
 // ---------------------------------------------------------------- helpers of the roles
-__device__ __forceinline__ uint64_t kmajor_desc(uint32_t tile, int kk) {
-    return sdesc_sw128(tile + (kk >> 2) * (BM * 128) + (kk & 3) * 32, 16, 1024);
+__device__ __forceinline__ uint64_t step_desc(uint64_t d, uint32_t by) {
+    return (d & 0xffffffff00000000ull) | ((uint32_t)d + by);
 }
-__device__ __forceinline__ uint64_t vmajor_desc(uint32_t tile, int kk) {
-    return sdesc_sw128(tile + kk * (16 * 128), BN * 128, 1024);
+// Descriptors of a tile's first k-step, and the steps to the others: 16-byte units added to the start
+// address, which sits in the low bits and does not overflow them. `half`: bytes from one 64-column box of a
+// K-major tile to the next.
+__device__ __forceinline__ uint64_t kmajor_desc(uint32_t tile) { return sdesc_sw128(tile, 16, 1024); }
+__device__ __forceinline__ uint64_t kmajor_step(uint64_t d, int kk, uint32_t half) {
+    return step_desc(d, (kk >> 2) * (half >> 4) + (kk & 3) * 2);
 }
+__device__ __forceinline__ uint64_t vmajor_desc(uint32_t tile) { return sdesc_sw128(tile, BN * 128, 1024); }
+__device__ __forceinline__ uint64_t vmajor_step(uint64_t d, int kk) { return step_desc(d, kk * (16 * 128 >> 4)); }
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
     const uint32_t a = smem_u32(bar);
     const uint64_t t0 = globaltimer();
     while (!mbar_try_wait(a, parity))
         if (globaltimer() - t0 > timeout_ns) break;
+}
+
+// Transposes 8 x 8 pieces of 16 bytes among each 8 lanes: lane i's piece j becomes lane j's piece i. The
+// epilogue's threads hold a row each; stored as they are, every store instruction would touch 32 rows, and
+// those requests hold up the copies of the next unit's tiles (2 us of a 14 us unit of a 1024-token prompt).
+__device__ __forceinline__ void transpose8(uint4 (&v)[8], int lane) {
+#pragma unroll
+    for (int s = 1; s < 8; s <<= 1) {
+        const bool up = lane & s;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i & s) continue;
+            const uint4 give = up ? v[i] : v[i | s];
+            uint4 got;
+            got.x = __shfl_xor_sync(kFull, give.x, s);
+            got.y = __shfl_xor_sync(kFull, give.y, s);
+            got.z = __shfl_xor_sync(kFull, give.z, s);
+            got.w = __shfl_xor_sync(kFull, give.w, s);
+            if (up)
+                v[i] = got;
+            else
+                v[i | s] = got;
+        }
+    }
 }
 
 // The page that holds key `key` for this lane: its number, or num_pages (a row of zeros to TMA) for
@@ -394,8 +428,10 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
     const WaitCtl wc{p.err, &bar.abort_flag, p.timeout_ns};
     if (threadIdx.x == 0) {
         const uint32_t rows = 32u * (uint32_t)bar.sm_warps;  // softmax threads of a tile
-        mbar_init(&bar.q_full, 1);
-        mbar_init(&bar.q_empty, C::kIssuers);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&bar.q_full[i], 1);
+            mbar_init(&bar.q_empty[i], 1);
+        }
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&bar.kv_full[s], 1);
             mbar_init(&bar.kv_empty[s], C::kIssuers);
@@ -416,36 +452,33 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
     const uint32_t tmem = bar.tmem_base;
     const uint32_t sQ = smem_u32(smem + C::kQOff);
     const uint32_t sKV = smem_u32(smem + C::kKVOff);
+    // One tile: Q is loaded ahead, into as many slots as the tile's rows leave room for. A product reads 128
+    // rows from a slot's start; what lies behind the tile's own rows only reaches rows that nobody reads.
+    const uint32_t q_half = NT == 1 ? (uint32_t)((p.tok_tile * p.G + 7) / 8 * 1024) : BM * 128;  // bytes of a box
+    const uint32_t q_stride = q_half * C::kBoxes;
+    const uint32_t q_slots = NT == 1 ? min(4u, (uint32_t)C::kTileBytes / q_stride) : 2u;
 
     if (warp >= C::kProducer) {
-        if constexpr (KERNEL == 2) regs_decrease<Shape<2>::kOtherRegs>();
+        if constexpr (KERNEL == 2) regs_decrease<C::kOtherRegs>();
         Walk<NT, KERNEL> walk(p, bar);
         Unit w;
-        if (warp == C::kProducer) {
-            // ------------------------------------------------ Q / K / V producer
+        if (warp == C::kProducer || (C::kVProducer && warp == C::kFourth)) {
+            // ------------------------------------------------ K and V producers
+            // Small pages make many small copies, which one warp issues at about one in 90 cycles: K and V
+            // are issued by a warp each where there is one for V.
+            const bool two = C::kVProducer && p.page_size < 64;
+            const int first = C::kVProducer && warp == C::kFourth ? 1 : 0;  // 0: K, 1: V
+            const int end = two || first == 1 ? first + 1 : 2;
             const int box_rows = min(p.page_size, BN);   // keys a box holds
             const uint32_t box_bytes = (uint32_t)box_rows * 128;
-            const uint32_t q_bytes = (uint32_t)(p.tok_tile * p.G) * 128 * C::kBoxes;
             const int my_key = lane * box_rows;          // of a tile, where this lane has a box
-            uint32_t it = 0, n_units = 0;
+            uint32_t it = 0;                             // ring items: K and V in turn
             bool ok = true, bad = false;
-            while (ok && walk.next(w)) {
+            while (ok && (two || first == 0) && walk.next(w)) {
                 if (w.cnt_max == 0) continue;
                 int page = 0;  // this lane's page of the current tile
                 if (my_key < BN && w.k0 * BN + my_key < w.len) page = page_at(p, w.b, w.k0 * BN + my_key, &bad);
-                ok = mbar_wait_warp(&bar.q_empty, (n_units & 1) ^ 1, wc);
-                if (!ok) break;
-                ++n_units;
-                if (elect_one()) {
-                    const int nt = NT == 2 && w.ntok > p.tok_tile ? 2 : 1;
-                    mbar_arrive_expect_tx(&bar.q_full, nt * q_bytes);
-                    for (int t = 0; t < nt; ++t)
-                        for (int bx = 0; bx < C::kBoxes; ++bx)
-                            tma_load_4d(smem + C::kQOff + t * C::kTileBytes + bx * BM * 128, &tm_q, &bar.q_full, bx * 64,
-                                        0, w.row0 + t * p.tok_tile, w.h);
-                }
-                __syncwarp();
-                for (int j = w.k0; j < w.k0 + w.cnt_max && ok; ++j) {
+                for (int j = w.k0; j < w.k0 + w.cnt_max && ok; ++j, it += 2) {
                     const int key0 = j * BN;
                     const bool active = my_key < BN && key0 + my_key < w.len;
                     const uint32_t boxes = __popc(__ballot_sync(kFull, active));
@@ -455,10 +488,9 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                     if (j + 1 < w.k0 + w.cnt_max && my_key < BN && key0 + BN + my_key < w.len)
                         page = page_at(p, w.b, key0 + BN + my_key, &bad);
                     const bool tail = key0 + BN > w.len;
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv, ++it) {
-                        const uint32_t s = it % C::kStages;
-                        ok = mbar_wait_warp(&bar.kv_empty[s], ((it / C::kStages) & 1) ^ 1, wc);
+                    for (int kv = first; kv < end; ++kv) {
+                        const uint32_t s = (it + kv) % C::kStages;
+                        ok = mbar_wait_warp(&bar.kv_empty[s], (((it + kv) / C::kStages) & 1) ^ 1, wc);
                         if (!ok) break;
                         uint64_t* full = kv == 1 && tail ? &bar.v_tail[s] : &bar.kv_full[s];
                         if (elect_one()) mbar_arrive_expect_tx(full, boxes * box_bytes * C::kBoxes);
@@ -479,11 +511,12 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 const uint32_t last = it < (uint32_t)C::kStages ? it : (uint32_t)C::kStages;
                 for (uint32_t i = it - last; i < it; ++i)
                     drain_wait(&bar.kv_full[i % C::kStages], (i / C::kStages) & 1, p.timeout_ns);
-                if (n_units > 0) drain_wait(&bar.q_full, (n_units - 1) & 1, p.timeout_ns);
             }
         } else if (warp == C::kTail) {
-            // ------------------------------------------------ rows of V beyond the sequence, and the CTA's slots
-            uint32_t it = 0, phases = 0;  // phase of v_tail[s] in bit s
+            // ------------------------------------------------ Q, rows of V beyond the sequence, the CTA's slots
+            const uint32_t q_bytes = (uint32_t)(p.tok_tile * p.G) * 128 * C::kBoxes;
+            uint32_t it = 0, phases = 0;          // ring items; phase of v_tail[s] in bit s
+            uint32_t q_at = 0, q_used = 0;        // slot of the next Q tile; uses of each slot, 8 bits a slot
             int4 slot0 = make_int4(kNone, 0, 0, 0), slot1 = slot0;
             bool ok = true;
             while (walk.next(w)) {
@@ -494,12 +527,32 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                     else
                         slot0 = m;
                 }
+                if (w.cnt_max == 0 || !ok) continue;  // the slots are written whatever happens
+#pragma unroll 1
+                for (int t = 0; t < (C::kSplit ? NT : 1) && ok; ++t) {
+                    if (C::kSplit && w.cnt(t) == 0) continue;
+                    const uint32_t i = NT == 1 ? q_at : (uint32_t)t;
+                    const int nt = !C::kSplit && w.ntok > p.tok_tile ? 2 : 1;  // one issuer: both tiles at once
+                    ok = mbar_wait_warp(&bar.q_empty[i], ((q_used >> (8 * i)) & 1) ^ 1, wc);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&bar.q_full[i], nt * q_bytes);
+                        for (int x = 0; x < nt * C::kBoxes; ++x) {
+                            const int bx = x % C::kBoxes, more = x / C::kBoxes;
+                            tma_load_4d(smem + C::kQOff + (i + more) * q_stride + bx * q_half, &tm_q, &bar.q_full[i], bx * 64, 0,
+                                        w.row0 + (t + more) * p.tok_tile, w.h);
+                        }
+                    }
+                    __syncwarp();
+                    q_used ^= 1u << (8 * i);
+                    q_at = q_at + 1 == q_slots ? 0 : q_at + 1;
+                }
                 it += 2 * w.cnt_max;
                 const int left = w.len - (w.k0 + w.cnt_max - 1) * BN;  // keys in the part's last tile
-                if (w.cnt_max == 0 || left >= BN || !ok) continue;
+                if (left >= BN || !ok) continue;
                 const uint32_t s = (it - 1) % C::kStages;  // the part's last V
                 ok = mbar_wait_warp(&bar.v_tail[s], (phases >> s) & 1, wc);
-                if (!ok) continue;  // the slots are still written
+                if (!ok) continue;
                 phases ^= 1u << s;
                 uint8_t* tile = smem + C::kKVOff + s * C::kTileBytes;
                 for (int bx = 0; bx < C::kBoxes; ++bx)
@@ -511,24 +564,33 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 __syncwarp();
             }
             if (lane < 2) p.meta[blockIdx.x * 2 + lane] = lane == 0 ? slot0 : slot1;
-        } else if (C::kSplit && (warp == C::kIssuer || (NT == 2 && warp == C::kIssuer1))) {
+            // every copy issued must land before the CTA exits: q_used holds the parity of each slot's uses
+            if (lane < 4 && (lane < (int)q_slots)) {
+                const uint32_t parity = (q_used >> (8 * lane)) & 1;
+                drain_wait(&bar.q_full[lane], parity ^ 1, p.timeout_ns);
+            }
+            __syncwarp();
+        } else if (C::kSplit && (warp == C::kIssuer || (!C::kVProducer && warp == C::kFourth))) {
             // ------------------------------------------------ MMA issuers, one per query tile
             // S_t^{j+1} runs as soon as the softmax warps have read S_t^j. Each issuer walks every
             // ring slot and releases it once, used or not.
             const int t = warp == C::kIssuer ? 0 : 1;
             const uint32_t tS = tmem + t * BN, tO = tmem + 256 + t * D, tP = tmem + 384 + t * 64;
-            uint32_t it = 0, n_units = 0, n_s = 0, n_p = 0;
+            uint32_t it = 0, n_s = 0, n_p = 0;
+            uint32_t q_at = NT == 1 ? 0 : t, q_phase = 0;  // Q slot, and the phase of its uses
             bool ok = true;
             while (ok && walk.next(w)) {
                 if (w.cnt_max == 0) continue;
                 const int cnt = w.cnt(t);
-                ok = mbar_wait_warp(&bar.q_full, n_units & 1, wc);
-                if (!ok) break;
-                ++n_units;
-                tc_fence_after();
-                if (cnt == 0) {  // nothing for this tile: release Q at once
-                    if (elect_one()) mbar_arrive(&bar.q_empty);
-                    __syncwarp();
+                const uint32_t q_i = q_at, qt = sQ + q_i * q_stride;
+                if (cnt > 0) {
+                    ok = mbar_wait_warp(&bar.q_full[q_i], q_phase, wc);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (NT == 2 || ++q_at == q_slots) {
+                        if (NT == 1) q_at = 0;
+                        q_phase ^= 1;
+                    }
                 }
                 for (int j = 0; j <= w.cnt_max && ok; ++j) {
                     const uint32_t itK = it;  // ring slot of K_j; V_j follows it
@@ -542,13 +604,15 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                                 if (!ok) break;
                             }
                             tc_fence_after();
-                            const uint32_t qt = sQ + t * C::kTileBytes, kt = sKV + sK * C::kTileBytes;
+                            const uint32_t kt = sKV + sK * C::kTileBytes;
                             if (elect_one()) {
-#pragma unroll 2
+                                const uint64_t qd = kmajor_desc(qt), kd = kmajor_desc(kt);
+#pragma unroll kIssueUnroll
                                 for (int kk = 0; kk < D / 16; ++kk)
-                                    mma_ss(tS, kmajor_desc(qt, kk), kmajor_desc(kt, kk), kIdescS, kk > 0 ? 1u : 0u);
+                                    mma_ss(tS, kmajor_step(qd, kk, q_half), kmajor_step(kd, kk, BN * 128), kIdescS,
+                                           kk > 0 ? 1u : 0u);
                                 mma_commit(&bar.s_full[t]);
-                                if (j == cnt - 1) mma_commit(&bar.q_empty);  // last read of Q_t
+                                if (j == cnt - 1) mma_commit(&bar.q_empty[q_i]);  // last read of Q_t
                             }
                             __syncwarp();
                             ++n_s;
@@ -566,9 +630,10 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                             tc_fence_after();
                             const uint32_t vt = sKV + sV_prev * C::kTileBytes;
                             if (elect_one()) {
-#pragma unroll 2
+                                const uint64_t vd = vmajor_desc(vt);
+#pragma unroll kIssueUnroll
                                 for (int kk = 0; kk < BN / 16; ++kk)
-                                    mma_ts(tO, tP + kk * 8, vmajor_desc(vt, kk), kIdescO, (j > 1 || kk > 0) ? 1u : 0u);
+                                    mma_ts(tO, tP + kk * 8, vmajor_step(vd, kk), kIdescO, (j > 1 || kk > 0) ? 1u : 0u);
                                 mma_commit(&bar.pv_done[t]);
                             }
                             __syncwarp();
@@ -587,13 +652,12 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             __syncwarp();
         } else if (!C::kSplit && warp == C::kIssuer) {
             // ------------------------------------------------ MMA issuer of both tiles
-            uint32_t it = 0, n_units = 0, pcnt0 = 0, pcnt1 = 0;
+            uint32_t it = 0, pcnt0 = 0, pcnt1 = 0, qcnt0 = 0;
             bool ok = true;
             while (ok && walk.next(w)) {
                 if (w.cnt_max == 0) continue;
-                ok = mbar_wait_warp(&bar.q_full, n_units & 1, wc);
+                ok = mbar_wait_warp(&bar.q_full[0], qcnt0++ & 1, wc);
                 if (!ok) break;
-                ++n_units;
                 tc_fence_after();
                 for (int j = 0; j <= w.cnt_max && ok; ++j) {
                     const uint32_t itK = it;  // ring slot of K_j; V_j follows it
@@ -621,18 +685,21 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                             tc_fence_after();
                             const uint32_t vt = sKV + sV_prev * C::kTileBytes;
                             if (elect_one()) {
-#pragma unroll 2
+                                const uint64_t vd = vmajor_desc(vt);
+#pragma unroll kIssueUnroll
                                 for (int kk = 0; kk < BN / 16; ++kk)
-                                    mma_ts(tO, tS + kk * 8, vmajor_desc(vt, kk), kIdescO, (j > 1 || kk > 0) ? 1u : 0u);
+                                    mma_ts(tO, tS + kk * 8, vmajor_step(vd, kk), kIdescO, (j > 1 || kk > 0) ? 1u : 0u);
                             }
                             __syncwarp();
                         }
                         if (j < w.cnt(t)) {
-                            const uint32_t qt = sQ + t * C::kTileBytes, kt = sKV + sK * C::kTileBytes;
+                            const uint32_t qt = sQ + t * q_stride, kt = sKV + sK * C::kTileBytes;
                             if (elect_one()) {
-#pragma unroll 2
+                                const uint64_t qd = kmajor_desc(qt), kd = kmajor_desc(kt);
+#pragma unroll kIssueUnroll
                                 for (int kk = 0; kk < D / 16; ++kk)
-                                    mma_ss(tS, kmajor_desc(qt, kk), kmajor_desc(kt, kk), kIdescS, kk > 0 ? 1u : 0u);
+                                    mma_ss(tS, kmajor_step(qd, kk, q_half), kmajor_step(kd, kk, BN * 128), kIdescS,
+                                           kk > 0 ? 1u : 0u);
                                 mma_commit(&bar.s_full[t]);
                             }
                             __syncwarp();
@@ -643,7 +710,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                     }
                     if (!ok) break;
                     if (elect_one()) {
-                        if (j == w.cnt_max - 1) mma_commit(&bar.q_empty);  // last S of the part issued
+                        if (j == w.cnt_max - 1) mma_commit(&bar.q_empty[0]);
                         if (j < w.cnt_max) mma_commit(&bar.kv_empty[sK]);
                         if (j > 0) mma_commit(&bar.kv_empty[sV_prev]);
                     }
@@ -658,7 +725,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             __syncwarp();
         }
     } else {
-        if constexpr (KERNEL == 2) regs_increase<Shape<2>::kSoftmaxRegs>();
+        if constexpr (KERNEL == 2) regs_increase<C::kSoftmaxRegs>();
         // ------------------------------------------------ softmax (thread = query row)
         const int t = NT == 2 ? warp >> 2 : 0;
         if (warp < 4 * NT && (warp & 3) < bar.sm_warps) {
@@ -672,9 +739,9 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             uint32_t scnt = 0, ocnt = 0;  // ocnt: phases of pv_done (split) or o_full
             bool ok = true;
             Walk<NT, KERNEL> walk(p, bar);
-            while (ok) {
-                Unit w;
-                if (!walk.next(w)) break;
+            Unit w;
+            bool more = walk.next(w);
+            while (ok && more) {
                 if (lane == 0) bar.unit[warp] = make_int4(w.row0, w.ntok, w.h, (w.first ? 1 : 0) + (w.last ? 2 : 0));
                 const int cnt = w.cnt(t), k0 = w.k0;
                 // keys this row sees, and those that the tile's first row sees
@@ -790,6 +857,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                     mbar_arrive(&bar.p_full[t]);
                 }
                 if (!ok) break;
+                more = walk.next(w);  // while the last product runs
                 if (cnt > 0) {
                     ok = mbar_wait(C::kSplit ? &bar.pv_done[t] : &bar.o_full[t], ocnt & 1, wc);
                     ok = __all_sync(kFull, ok);
@@ -804,28 +872,44 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 if (first && last) {
                     const float inv = den > 0.f ? 1.f / den : 0.f;
                     const long long row = u.x + my_tok, head = u.z * p.G + my_head;
-                    uint16_t* orow = reinterpret_cast<uint16_t*>(p.o) + row * p.o_sr + head * p.o_sh;
+                    const long long off = row * p.o_sr + head * p.o_sh;
+                    const unsigned keep = __ballot_sync(kFull, held);
 #pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 32) {
-                        uint32_t ov[32];
-                        if (cnt > 0) {
-                            tmem_ld32(tO + c0, ov);
-                            tmem_wait_ld();
-                        } else {
+                    for (int c0 = 0; c0 < D; c0 += 64) {
+                        uint4 v[8];
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) ov[i] = 0;
-                        }
-                        if (held) {
-                            uint4* dst = reinterpret_cast<uint4*>(orow + c0);
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t ov[32];
+                            if (cnt > 0) {
+                                tmem_ld32(tO + c0 + 32 * h, ov);
+                                tmem_wait_ld();
+                            } else {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                uint4 v;
-                                v.x = pack_h16<F16>(__uint_as_float(ov[8 * q + 0]) * inv, __uint_as_float(ov[8 * q + 1]) * inv);
-                                v.y = pack_h16<F16>(__uint_as_float(ov[8 * q + 2]) * inv, __uint_as_float(ov[8 * q + 3]) * inv);
-                                v.z = pack_h16<F16>(__uint_as_float(ov[8 * q + 4]) * inv, __uint_as_float(ov[8 * q + 5]) * inv);
-                                v.w = pack_h16<F16>(__uint_as_float(ov[8 * q + 6]) * inv, __uint_as_float(ov[8 * q + 7]) * inv);
-                                dst[q] = v;
+                                for (int i = 0; i < 32; ++i) ov[i] = 0;
                             }
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                v[4 * h + q] = make_uint4(
+                                    pack_h16<F16>(__uint_as_float(ov[8 * q + 0]) * inv, __uint_as_float(ov[8 * q + 1]) * inv),
+                                    pack_h16<F16>(__uint_as_float(ov[8 * q + 2]) * inv, __uint_as_float(ov[8 * q + 3]) * inv),
+                                    pack_h16<F16>(__uint_as_float(ov[8 * q + 4]) * inv, __uint_as_float(ov[8 * q + 5]) * inv),
+                                    pack_h16<F16>(__uint_as_float(ov[8 * q + 6]) * inv, __uint_as_float(ov[8 * q + 7]) * inv));
+                        }
+                        if constexpr (NT == 1) {  // mostly a few rows
+                            if (held) {
+                                uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.o) + off + c0);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) dst[e] = v[e];
+                            }
+                            continue;
+                        }
+                        transpose8(v, lane);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int owner = (lane & 24) + e;
+                            const long long at = __shfl_sync(kFull, off, owner);
+                            if (keep >> owner & 1)
+                                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.o) + at + c0 + (lane & 7) * 8) = v[e];
                         }
                     }
                     if (held) p.lse[head * p.T + row] = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
