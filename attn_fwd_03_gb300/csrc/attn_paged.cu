@@ -11,6 +11,14 @@
 // rounded to the 16-bit type, O += P V, with a reference max that moves only when
 // a tile's max exceeds it by more than 8 (log2 units).
 //
+// What bounds it: decode reads every key and value once for a few products each, so
+// HBM (a ragged batch of 64 sequences of 4096-8192 keys, 32 query and 8 key/value
+// heads, d = 128: 240 us, 6.6 TB/s, 99 % of the measured copy rate; 96 % with
+// 16-token pages); long chunks are bound by the tensor pipe and the softmax beside
+// it (4096 rows over 32768 keys: 1.33 ms, 1549 TFLOP/s, 83 % of the measured GEMM
+// rate); small calls by latency (one token over 517 keys: 10.4 us for both
+// launches, of which locating the work takes 1.4, the first copies 2, the merge 4).
+//
 // Work split: lengths are known on the device only, and ragged, so units are not
 // dealt out whole. All units lie one after another on a line, each as long as its
 // visible keys plus a constant for its start and end; CTA i of the grid takes the
@@ -23,21 +31,25 @@
 //
 // A tile's keys are copied page by page with TMA (one box per page and 64
 // columns; the lanes of the producer warp each look one page up). The last tile's
-// rows beyond the sequence's length are not copied: scores there are masked by
+// rows beyond the sequence's length are not used: scores there are masked by
 // selection, and a helper warp zeroes those rows of V in shared memory before the
 // P V product, since 0 * NaN from an unwritten slot would reach O.
 //
-// Warp roles, NT = 2 (12 warps): 0-3 and 4-7 softmax of tile 0 and 1 (one thread
-// per row), 8 producer, 9 MMA issuer (d = 64: of tile 0), 10 V tail, 11 MMA issuer of tile 1
-// (d = 64). NT = 1 (7 warps): 0-3 softmax (only those that hold rows work), 4
-// producer, 5 MMA issuer, 6 V tail.
+// Warp roles: softmax (one thread per row; warps 0-3 of tile 0, 4-7 of tile 1 in the
+// NT = 2 kernel), then K (and V) producer, MMA issuer, Q producer and V tail, and a
+// fourth that produces V or issues the second tile's products. Every role finds
+// the CTA's units for itself.
 // Tensor memory (lane = row): S_t [128 t, +128), O_t [256 + d t, +d), and P_t in
 // columns of its own [384 + 64 t, +64) except for NT = 2 at d = 128, where the
 // columns run out and P_t overwrites S_t ("split P" in attn_fwd_sm103.cu has the
 // reasons for either order of products).
+//
+// Measured and not kept: both softmax warpgroups on one tile's key columns in halves
+// (no faster: one-tile units wait for their copies); loading both Q tiles of a unit
+// under separate barriers (5 % slower: the extra branches lie in the issuer's loop);
+// V by a warp of its own for pages of 64 tokens and more (3 % slower).
 #include <cuda_bf16.h>
 
-#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -53,8 +65,12 @@ using namespace ptx;
 constexpr int BM = 128;  // query rows per tile
 constexpr int BN = 128;  // keys per tile
 constexpr float kRescaleThreshold = 8.0f;
-constexpr int kUnitCost = 384;  // what a unit costs beyond its key tiles, in keys
-constexpr float kPairCost = 1.5f;  // a key tile of a two-tile unit against one of a one-tile unit
+// What a unit costs beyond its key tiles, in keys. From 64 to 384 the verification of 5 drafted tokens of 16
+// sequences went from 20.2 to 19.2 us; 512 is no better.
+constexpr int kUnitCost = 384;
+// A key tile of a two-tile unit against one of a one-tile unit: 1.9 us against 1.3 in a step of 16 decoding
+// sequences and a 512-row chunk (85 us; 1.2 and 2.0 give 89).
+constexpr float kPairCost = 1.5f;
 constexpr int kTilesBytes = 224 * 1024;  // shared memory for Q, K and V tiles
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kIssueUnroll = 4;  // k-steps of a product in a row: 2 is 1 % slower, 1 11 %, 8 the same
@@ -99,8 +115,8 @@ struct PagedDev {
     uint8_t* o;
     float* lse;
     long long o_sr, o_sh;  // elements
-    float* part;      // [grid][2][NT] records of tok_tile * G rows: see Record
-    int4* meta;       // [grid][2]: see Meta
+    float* part;      // [grid][2][NT] records of tok_tile * G rows: see record()
+    int4* meta;       // [grid][2]: see below
     int* err;
     unsigned long long timeout_ns;
 };
@@ -273,7 +289,7 @@ __device__ __forceinline__ void locate(const PagedDev& p, Shared& sh) {
         sh.x0 = x0;
         sh.x1 = x1;
         sh.pair = pair;
-        sh.sm_warps = pair ? (p.tok_tile * p.G + 31) / 32 : (rows + 31) / 32;
+        sh.sm_warps = max(1, ((pair ? p.tok_tile * p.G : rows) + 31) / 32);
     }
 }
 
@@ -386,7 +402,7 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
 
 // Transposes 8 x 8 pieces of 16 bytes among each 8 lanes: lane i's piece j becomes lane j's piece i. The
 // epilogue's threads hold a row each; stored as they are, every store instruction would touch 32 rows, and
-// those requests hold up the copies of the next unit's tiles (2 us of a 14 us unit of a 1024-token prompt).
+// those requests hold up the copies of the next unit's tiles (eight prompts of 1024 tokens: 95 -> 92 us).
 __device__ __forceinline__ void transpose8(uint4 (&v)[8], int lane) {
 #pragma unroll
     for (int s = 1; s < 8; s <<= 1) {
@@ -742,6 +758,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             Unit w;
             bool more = walk.next(w);
             while (ok && more) {
+                __syncwarp();  // the last use of bar.unit
                 if (lane == 0) bar.unit[warp] = make_int4(w.row0, w.ntok, w.h, (w.first ? 1 : 0) + (w.last ? 2 : 0));
                 const int cnt = w.cnt(t), k0 = w.k0;
                 // keys this row sees, and those that the tile's first row sees
@@ -1117,18 +1134,9 @@ CUresult encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, int32_t d
 
 template <int D, bool F16, int NT>
 cudaError_t launch_tc(const CUtensorMap (&maps)[3], const PagedDev& p, int grid, cudaStream_t s) {
-    // The attribute stays with the function on a device: one call instead of one a launch (decode is paced
-    // by the host). Threads that come at the same time both set it, to the same value.
-    static std::atomic<uint64_t> set{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D, F16, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kSmemBytes);
     if (e != cudaSuccess) return e;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (!(set.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(paged_tc_kernel<D, F16, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-        if (e != cudaSuccess) return e;
-        set.fetch_or(bit, std::memory_order_relaxed);
-    }
     return launch_pdl(paged_tc_kernel<D, F16, NT>, dim3(grid), dim3(Shape<NT>::kThreads), kSmemBytes, s, maps[0], maps[1],
                       maps[2], p);
 }

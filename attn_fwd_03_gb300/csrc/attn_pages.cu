@@ -204,8 +204,10 @@ __global__ void __launch_bounds__(kScan) pages_release_kernel(const ReleaseArgs 
 #pragma unroll 4
             for (int i = tid; i < n; i += kScan) {
                 const long long to = first + i;
+                const int page = row[i];
+                bad |= page < 0;  // a sequence that was never given all its pages
                 if (to >= 0 && to < p.free_capacity)
-                    p.free_pages[to] = row[i];
+                    p.free_pages[to] = page;
                 else
                     bad = true;
             }

@@ -362,7 +362,9 @@ ATTN_API attn_status_t attn_pages_write(const attn_pages_write_params *p, void *
  * call again gives the same answer; a step is taken by using new_len and
  * free_left as the next kv_len and free_count.
  * When the stack runs out free_left is negative by the pages that were missing,
- * and the table entries and slots that got none are -1.
+ * and the table entries and slots that got none are -1. Such a step is not taken:
+ * kv_len and free_count stay as they were, and it is planned again once pages
+ * were released (by lengths before the step) or with fewer sequences.
  */
 typedef struct attn_pages_plan_params {
     int32_t num_seqs;
@@ -388,6 +390,7 @@ ATTN_API attn_status_t attn_pages_plan(const attn_pages_plan_params *p, void *st
  * the pages of its kv_len[b] tokens are pushed onto free_pages, the first of them
  * at free_pages[free_count]; new_len[b] becomes 0 (kv_len[b] for the others), and
  * free_left = free_count plus the pages given back. The block table is only read.
+ * Entries below 0 among a sequence's pages are reported (ATTN_ERR_INVALID).
  */
 typedef struct attn_pages_release_params {
     int32_t num_seqs;

@@ -187,6 +187,26 @@ def test_many_sequences(A):
     c.check(o, lse, True)
 
 
+def test_many_sequences_beside_long_chunks(A):
+    # more sequences than the kernel has threads, a few of them in two-tile units
+    rng = np.random.default_rng(4)
+    n, kv = rng.integers(0, 3, 450), rng.integers(0, 40, 450)
+    n[[3, 200, 449]], kv[[3, 200, 449]] = [150, 300, 90], [150, 411, 400]
+    c = Case(n.tolist(), kv.tolist(), 1, 4, 128, 16, torch.bfloat16, 91)
+    o, lse = A.attn_paged(*c.device(), causal=True, max_q=300)
+    _ok(A)
+    c.check(o, lse, True)
+
+
+@pytest.mark.parametrize("max_q", [1, 400])
+def test_no_rows_at_all(A, max_q):
+    c = Case([0, 0], [40, 0], 1, 2, 64, 16, torch.bfloat16, 92, pad=3)
+    out, lse = torch.full(c.q.shape, 5.0, dtype=c.dtype, device="cuda"), torch.full((2, 3), 5.0, device="cuda")
+    A.attn_paged(*c.device(), causal=True, max_q=max_q, out=out, lse=lse)
+    _ok(A)
+    assert torch.all(out == 5.0) and torch.all(lse == 5.0)
+
+
 @pytest.mark.parametrize("n,kv", [([1] * 8, [4000, 10, 900, 1, 128, 2048, 77, 1500]), ([600, 1, 90], [1900, 2500, 90])])
 def test_same_bits_on_every_call_and_stream(A, n, kv):
     c = Case(n, kv, 2, 4, 128, 64, torch.bfloat16, 95)
@@ -430,6 +450,13 @@ def test_release_matches_oracle(A, seqs, page, every):
     new, left = A.attn_pages_release(_i32(done), _i32(lengths), _i32(table), stack, _i32([len(free)]), page)
     _ok(A)
     assert new.tolist() == want[0] and left.tolist() == [want[1]] and stack.tolist() == want[2]
+
+
+def test_release_reports_pages_that_were_never_given(A):
+    stack = _i32([5, 0, 0, 0])
+    A.attn_pages_release(_i32([1]), _i32([40]), _i32([[1, -1, -1]]), stack, _i32([1]), 16)
+    torch.cuda.synchronize()
+    assert A.attn_status() == A.ATTN_ERR_INVALID
 
 
 def test_release_reports_a_stack_that_cannot_hold_the_pages(A):
