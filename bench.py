@@ -564,6 +564,66 @@ def measure_decode(A, dev, hbm_gbs: float, nq: int, B: int = 8, H: int = 32, nk:
             "bytes": nbytes}
 
 
+def measure_paged_step(A, dev, hbm_gbs: float, nq: int, hq: int = 32, hkv: int = 8, d: int = 128, page: int = 64,
+                       steps: int = 20, warmup: int = 3) -> dict:
+    """One step over a paged cache: page tables for nq new tokens a sequence (attn_pages_plan), their keys and
+    values stored (attn_pages_write), attention over everything cached (attn_paged). nq = 1: 64 decoding
+    sequences of 4096 .. 8192 keys, bound by HBM (the algorithmic bytes of the attention are the cached K and V
+    read once plus Q, O and LSE; K and V, 1.6 GB, exceed L2). nq > 1: one sequence that ends at 32768 keys."""
+    import torch
+    g = torch.Generator(device="cpu").manual_seed(740)
+    seqs, keys = (64, 8192) if nq == 1 else (1, 32768)
+    lens = [keys - nq - (b * 379 % 1000) * keys // 2000 for b in range(seqs)]
+    rows = seqs * nq
+    columns = (keys + page - 1) // page
+    need = [(n + page - 1) // page for n in lens]
+    spare = seqs * ((nq + page - 1) // page + 1)
+    order = torch.randperm(sum(need) + spare, generator=g).tolist()
+    table, at = [], 0
+    for m in need:
+        table.append(order[at:at + m] + [-1] * (columns - m))
+        at += m
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
+    table, kv_len, q_len = i32(table), i32(lens), i32([nq] * seqs)
+    free, count = i32(order[at:]), i32([spare])
+    cache = [torch.randn(len(order), page, hkv, d, device=dev).to(torch.bfloat16).transpose(1, 2) for _ in range(2)]
+    q = W.random_tensor((rows, hq, d), 741, torch.bfloat16).to(dev)
+    k, v = (W.random_tensor((rows, hkv, d), 742 + i, torch.bfloat16).to(dev) for i in range(2))
+    o, lse = torch.empty_like(q), torch.empty((hq, rows), dtype=torch.float32, device=dev)
+    cu, new, slots, _, _ = A.attn_pages_plan(q_len, kv_len, table, free, count, page, rows)
+    ws = torch.empty(A.paged_workspace_size(q, *cache, table, cu, new, max_q=nq), dtype=torch.uint8, device=dev)
+
+    def attend():
+        A.attn_paged(q, *cache, table, cu, new, causal=True, max_q=nq, out=o, lse=lse, workspace=ws)
+
+    def step():
+        A.attn_pages_plan(q_len, kv_len, table, free, count, page, rows, cu_q=cu, new_len=new, slots=slots)
+        A.attn_pages_write(k, v, slots, *cache)
+        attend()
+
+    times = {}
+    for name, f in (("attend", attend), ("step", step)):
+        for _ in range(warmup):
+            f()
+        torch.cuda.synchronize()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for _ in range(steps):
+            f()
+        e1.record()
+        torch.cuda.synchronize()
+        times[name] = e0.elapsed_time(e1) / steps
+    if A.attn_status() != A.ATTN_OK:
+        raise RuntimeError(A.last_error())
+    nbytes = 2 * (sum(lens) + rows) * hkv * d * 2 + 2 * rows * hq * d * 2 + rows * hq * 4
+    flops = 4 * d * hq * sum(nq * (n + nq) - nq * (nq - 1) // 2 for n in lens)
+    gbs = nbytes / (times["attend"] * 1e-3) / 1e9
+    return {"shape": {"seqs": seqs, "nq": nq, "max_keys": keys, "q_heads": hq, "kv_heads": hkv, "d": d, "page": page},
+            "dtype": "bf16", "ms": times["attend"], "step_ms": times["step"], "achieved_gbs": gbs,
+            "pct_of_hbm_peak": 100.0 * gbs / hbm_gbs, "tflops": flops / (times["attend"] * 1e-3) / 1e12, "launches": 2,
+            "step_launches": 4, "bytes": nbytes, "flops": flops}
+
+
 def captured_traffic(kernel: str, workload: str):
     """DRAM bytes (read + write) per launch of `kernel` on `workload` from profiles/dram_traffic.json,
     or None when there is no capture or the kernel's sources changed since it was taken."""
@@ -622,6 +682,10 @@ def main():
     ap.add_argument("--decode", type=int, default=None, metavar="NQ",
                     help="time only the split-KV decode entry of the table with NQ query rows "
                          "(B=8 H=32 nk=8192 d=128) and print it as one JSON line")
+    ap.add_argument("--paged", type=int, default=None, metavar="NQ",
+                    help="time one step over a paged cache (32 query and 8 key/value heads, d=128) and print it as one "
+                         "JSON line: NQ = 1, 64 decoding sequences of 4096-8192 keys; NQ > 1, a chunk of NQ tokens of one "
+                         "sequence that ends at 32768 keys")
     ap.add_argument("--table-workload", default=None,
                     help="time only this entry of the per-workload table (a workload name from workloads.py, "
                          "e.g. under a profiler) and print it as one JSON line")
@@ -641,6 +705,14 @@ def main():
         r = measure_decode(A, torch.device("cuda", 0), peaks["hbm_gbs"], args.decode, steps=args.steps,
                            warmup=args.warmup)
         print(json.dumps({"workload": f"decode_b8_h32_nq{args.decode}_nk8192_d128_bf16_causal", **r}), flush=True)
+        return
+    if args.paged is not None:
+        import torch
+        import attn_fwd_03_gb300 as A
+        peaks, _ = load_peaks()
+        r = measure_paged_step(A, torch.device("cuda", 0), peaks["hbm_gbs"], args.paged, steps=args.steps,
+                               warmup=args.warmup)
+        print(json.dumps({"workload": f"paged_nq{args.paged}_h32_kv8_d128_bf16", **r}), flush=True)
         return
     w = W.WORKLOADS[args.workload]
     if args.impl == "reference":
