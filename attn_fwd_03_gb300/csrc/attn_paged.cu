@@ -71,38 +71,50 @@ constexpr int kUnitCost = 384;
 // A key tile of a two-tile unit against one of a one-tile unit: 1.9 us against 1.3 in a step of 16 decoding
 // sequences and a 512-row chunk (85 us; 1.2 and 2.0 give 89).
 constexpr float kPairCost = 1.5f;
-constexpr int kTilesBytes = 224 * 1024;  // shared memory for Q, K and V tiles
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kIssueUnroll = 4;  // k-steps of a product in a row: 2 is 1 % slower, 1 11 %, 8 the same
 
-// A CTA that works on units of NT tiles; the warps of its roles begin at FIRST, behind the softmax warps.
-template <int D, int NT, int FIRST>
+// The kernel for batches whose sequences all fit one tile (NT = 1), and the one that also takes longer
+// chunks (NT = 2): there each CTA works either on the former or on the latter. At d = 64 the copies of a
+// key tile take less time than its softmax, and one CTA with one unit in hand waits for that: two CTAs share
+// an SM then, with half of its shared and tensor memory each.
+template <int D, int NT>
+struct Shape {
+    static constexpr int kPerSm = NT == 1 && D == 64 ? 2 : 1;
+    static constexpr int kFirst = 4 * NT;  // the first warp behind the softmax warps
+    static constexpr int kThreads = NT == 1 ? 256 : 384;
+    static constexpr int kTilesBytes = (kPerSm == 2 ? 96 : 224) * 1024;  // shared memory for Q, K and V tiles
+    static constexpr int kSmemBytes = kTilesBytes + 2048 + 1024;  // barriers and schedule + alignment slack
+    static_assert(kPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory");
+    static constexpr uint32_t kTmemCols = 512 / kPerSm;
+    // registers per thread after the rebalance: the softmax warps hold a row of scores each
+    static constexpr bool kRebalance = NT == 2 || kPerSm == 2;
+    static constexpr int kSoftmaxRegs = NT == 1 ? 184 : D == 64 ? 192 : 200;
+    static constexpr int kOtherRegs = NT == 1 ? 72 : D == 64 ? 120 : 104;
+    static_assert(NT == 1 ? kSoftmaxRegs + kOtherRegs <= 2 * 128 : 2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "register split");
+};
+
+// A CTA of the kernel KERNEL that works on units of NT tiles.
+template <int D, int NT, int KERNEL>
 struct Cfg {
+    using Kernel = Shape<D, KERNEL>;
     static constexpr int kBoxes = D / 64;
     static constexpr int kTileBytes = BM * D * 2;
     static constexpr bool kSplit = D == 64 || NT == 1;  // P in tensor-memory columns of its own
     static constexpr int kIssuers = kSplit ? NT : 1;
     static constexpr int kQOff = 0;
     static constexpr int kKVOff = kQOff + NT * kTileBytes;
-    static constexpr int kStages = (kTilesBytes - kKVOff) / kTileBytes;  // K and V tiles in flight
+    static constexpr int kStages = (Kernel::kTilesBytes - kKVOff) / kTileBytes;  // K and V tiles in flight
+    // tensor-memory columns of tile t; S_t is at BN t
+    static constexpr int o_col(int t) { return NT == 1 && D == 64 ? 192 : 256 + D * t; }
+    static constexpr int p_col(int t) { return !kSplit ? BN * t : NT == 1 && D == 64 ? 128 : 384 + 64 * t; }
+    static_assert(NT == 2 || o_col(0) + D <= (int)Kernel::kTmemCols, "tensor memory");
     // warps: K (and V) producer, MMA issuer, Q producer and V tail; the fourth is the V producer, except where
     // it has to issue the second tile's products
-    static constexpr int kProducer = FIRST, kIssuer = FIRST + 1, kTail = FIRST + 2, kFourth = FIRST + 3;
+    static constexpr int kProducer = Kernel::kFirst, kIssuer = kProducer + 1, kTail = kProducer + 2;
+    static constexpr int kFourth = kProducer + 3;
     static constexpr bool kVProducer = kIssuers == 1;
-    // NT = 2 kernel: registers per thread after the rebalance, 2 x 128 x softmax + 128 x other = 384 x 168
-    static constexpr int kSoftmaxRegs = D == 64 ? 192 : 200, kOtherRegs = D == 64 ? 120 : 104;
-    static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= 384 * 168, "register split");
 };
-
-// The kernel for batches whose sequences all fit one tile (NT = 1), and the one that also takes longer
-// chunks (NT = 2): there each CTA works either on the former or on the latter.
-template <int NT>
-struct Shape {
-    static constexpr int kFirst = 4 * NT;
-    static constexpr int kThreads = NT == 1 ? 256 : 384;
-};
-constexpr int kSmemBytes = kTilesBytes + 2048 + 1024;  // barriers and schedule + alignment slack
-static_assert(kSmemBytes <= 232448, "shared memory");
 
 struct PagedDev {
     int B, G, Hkv, T;
@@ -198,9 +210,9 @@ __device__ __forceinline__ bool is_pair(const PagedDev& p, const Seq& s) {
 // Finds this CTA's piece of the line. All threads take part. In the NT = 2 kernel there are two lines, of
 // one-tile and of two-tile units, and the CTAs are shared out between them by their costs: the former are
 // bound by reading keys and values, the latter by the tensor cores, so they run side by side.
-template <int NT>
+template <int NT, int THREADS>
 __device__ __forceinline__ void locate(const PagedDev& p, Shared& sh) {
-    constexpr int THREADS = Shape<NT>::kThreads, WARPS = THREADS / 32;
+    constexpr int WARPS = THREADS / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     bool bad = false;
     long long done[2] = {0, 0};  // cost of the chunks of sequences before this one, of either line
@@ -437,7 +449,7 @@ __device__ __forceinline__ int page_at(const PagedDev& p, int b, int key, bool* 
 template <int D, bool F16, int NT, int KERNEL>
 __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                      const PagedDev& p, uint8_t* smem, Shared& bar) {
-    using C = Cfg<D, NT, Shape<KERNEL>::kFirst>;
+    using C = Cfg<D, NT, KERNEL>;
     constexpr uint32_t kIdescS = idesc_h16(BM, BN, false, false, F16);
     constexpr uint32_t kIdescO = idesc_h16(BM, D, false, true, F16);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -475,7 +487,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
     const uint32_t q_slots = NT == 1 ? min(4u, (uint32_t)C::kTileBytes / q_stride) : 2u;
 
     if (warp >= C::kProducer) {
-        if constexpr (KERNEL == 2) regs_decrease<C::kOtherRegs>();
+        if constexpr (C::Kernel::kRebalance) regs_decrease<C::Kernel::kOtherRegs>();
         Walk<NT, KERNEL> walk(p, bar);
         Unit w;
         if (warp == C::kProducer || (C::kVProducer && warp == C::kFourth)) {
@@ -591,7 +603,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             // S_t^{j+1} runs as soon as the softmax warps have read S_t^j. Each issuer walks every
             // ring slot and releases it once, used or not.
             const int t = warp == C::kIssuer ? 0 : 1;
-            const uint32_t tS = tmem + t * BN, tO = tmem + 256 + t * D, tP = tmem + 384 + t * 64;
+            const uint32_t tS = tmem + t * BN, tO = tmem + C::o_col(t), tP = tmem + C::p_col(t);
             uint32_t it = 0, n_s = 0, n_p = 0;
             uint32_t q_at = NT == 1 ? 0 : t, q_phase = 0;  // Q slot, and the phase of its uses
             bool ok = true;
@@ -690,7 +702,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         if (!ok || w.cnt(t) == 0 || j > w.cnt(t)) continue;
-                        const uint32_t tS = tmem + t * BN, tO = tmem + 256 + t * D;
+                        const uint32_t tS = tmem + t * BN, tO = tmem + C::o_col(t);
                         if (j > 0) {
                             // O_t += P_t^{j-1} V_{j-1}; the epilogue has read O_t before its threads
                             // arrive on p_full for a new unit
@@ -741,7 +753,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             __syncwarp();
         }
     } else {
-        if constexpr (KERNEL == 2) regs_increase<C::kSoftmaxRegs>();
+        if constexpr (C::Kernel::kRebalance) regs_increase<C::Kernel::kSoftmaxRegs>();
         // ------------------------------------------------ softmax (thread = query row)
         const int t = NT == 2 ? warp >> 2 : 0;
         if (warp < 4 * NT && (warp & 3) < bar.sm_warps) {
@@ -750,8 +762,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             const int my_tok = t * p.tok_tile + r / p.G, my_head = r % p.G;
             const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
             const uint32_t tS = tmem + lane_off + t * BN;
-            const uint32_t tO = tmem + lane_off + 256 + t * D;
-            const uint32_t tP = C::kSplit ? tmem + lane_off + 384 + t * 64 : tS;
+            const uint32_t tO = tmem + lane_off + C::o_col(t), tP = tmem + lane_off + C::p_col(t);
             uint32_t scnt = 0, ocnt = 0;  // ocnt: phases of pv_done (split) or o_full
             bool ok = true;
             Walk<NT, KERNEL> walk(p, bar);
@@ -957,16 +968,16 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
 }
 
 template <int D, bool F16, int NT>
-__global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kPerSm)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const PagedDev p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Shared& bar = *reinterpret_cast<Shared*>(smem + kTilesBytes);
+    Shared& bar = *reinterpret_cast<Shared*>(smem + Shape<D, NT>::kTilesBytes);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) bar.abort_flag = 0;
     if (warp == 0) {
-        tmem_alloc(&bar.tmem_base, 512);
+        tmem_alloc(&bar.tmem_base, Shape<D, NT>::kTmemCols);
         tmem_relinquish();
         if (elect_one()) {
             prefetch_tmap(&tm_q);
@@ -979,7 +990,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     // No global memory is touched above: from here on the previous kernel must be complete.
     grid_dep_launch();
     grid_dep_wait();
-    locate<NT>(p, bar);
+    locate<NT, Shape<D, NT>::kThreads>(p, bar);
     __syncthreads();
     if constexpr (NT == 2) {
         if (bar.pair)
@@ -992,7 +1003,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) tmem_dealloc(bar.tmem_base, 512);
+    if (warp == 0) tmem_dealloc(bar.tmem_base, Shape<D, NT>::kTmemCols);
 }
 
 // ---------------------------------------------------------------- merging parts
@@ -1105,7 +1116,7 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Co
 // The tile shape of a call. One tile per unit while the rows that a sequence is expected to bring fit
 // it, so that decode does not carry an empty second tile; two beyond.
 struct Plan {
-    int tiles, tok_tile, rows;
+    int tiles, tok_tile, rows, ctas;
     size_t meta_bytes, bytes;
 };
 
@@ -1116,12 +1127,17 @@ Plan plan_of(const attn_paged_params& p, int num_sms) {
     pl.tok_tile = BM / G;
     if (pl.tiles == 1 && p.max_q < pl.tok_tile) pl.tok_tile = p.max_q;
     pl.rows = pl.tok_tile * G;
-    pl.meta_bytes = ((size_t)num_sms * 2 * sizeof(int4) + 255) / 256 * 256;
-    pl.bytes = pl.meta_bytes + (size_t)num_sms * 2 * pl.tiles * pl.rows * (p.d + 4) * sizeof(float);
+    pl.ctas = num_sms * (pl.tiles == 2 ? 1 : p.d == 64 ? Shape<64, 1>::kPerSm : Shape<128, 1>::kPerSm);
+    pl.meta_bytes = ((size_t)pl.ctas * 2 * sizeof(int4) + 255) / 256 * 256;
+    pl.bytes = pl.meta_bytes + (size_t)pl.ctas * 2 * pl.tiles * pl.rows * (p.d + 4) * sizeof(float);
     return pl;
 }
 
 // 4-D map of 16-bit elements over the given extents, dimension 0 contiguous, 64-column boxes.
+// Rows of 64 columns that do not follow one another (pages that hold [slot, head, d]) are fetched in
+// 128-byte pieces, or half of every fetch would be another head's row: 64 sequences of 4096 keys at d = 64 took
+// 113 us with 256-byte promotion and take 86 (79 % of the measured HBM). At d = 128, 256 bytes are a row, and
+// 128-byte promotion is 6 % slower with 16-token pages.
 CUresult encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, int32_t dtype, const void* base,
                 const cuuint64_t (&dims)[4], const int64_t (&st)[3], cuuint32_t box1, cuuint32_t box2) {
     cuuint64_t strides[3];
@@ -1129,15 +1145,16 @@ CUresult encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, int32_t d
     const cuuint32_t box[4] = {64, box1, box2, 1}, es[4] = {1, 1, 1, 1};
     return enc(m, dtype == ATTN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+               dims[0] == 64 && st[0] != 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 template <int D, bool F16, int NT>
 cudaError_t launch_tc(const CUtensorMap (&maps)[3], const PagedDev& p, int grid, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D, F16, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kSmemBytes);
+                                               Shape<D, NT>::kSmemBytes);
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_tc_kernel<D, F16, NT>, dim3(grid), dim3(Shape<NT>::kThreads), kSmemBytes, s, maps[0], maps[1],
+    return launch_pdl(paged_tc_kernel<D, F16, NT>, dim3(grid), dim3(Shape<D, NT>::kThreads), Shape<D, NT>::kSmemBytes, s, maps[0], maps[1],
                       maps[2], p);
 }
 
@@ -1213,9 +1230,9 @@ attn_status_t launch_paged(const attn_paged_params& p, const LaunchCommon& lc, c
     a.timeout_ns = lc.timeout_ns;
     const bool f16 = p.dtype == ATTN_F16;
     const cudaError_t e =
-        p.d == 64 ? (f16 ? launch_both<64, true>(maps, a, pl, lc.num_sms, s) : launch_both<64, false>(maps, a, pl, lc.num_sms, s))
-                  : (f16 ? launch_both<128, true>(maps, a, pl, lc.num_sms, s)
-                         : launch_both<128, false>(maps, a, pl, lc.num_sms, s));
+        p.d == 64 ? (f16 ? launch_both<64, true>(maps, a, pl, pl.ctas, s) : launch_both<64, false>(maps, a, pl, pl.ctas, s))
+                  : (f16 ? launch_both<128, true>(maps, a, pl, pl.ctas, s)
+                         : launch_both<128, false>(maps, a, pl, pl.ctas, s));
     return e == cudaSuccess ? ATTN_OK : report_error(ATTN_ERR_CUDA, "attn_paged launch: %s", cudaGetErrorString(e));
 }
 
