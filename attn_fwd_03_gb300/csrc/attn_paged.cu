@@ -74,24 +74,33 @@ constexpr float kPairCost = 1.5f;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kIssueUnroll = 4;  // k-steps of a product in a row: 2 is 1 % slower, 1 11 %, 8 the same
 
-// The kernel for batches whose sequences all fit one tile (NT = 1), and the one that also takes longer
-// chunks (NT = 2): there each CTA works either on the former or on the latter. At d = 64 the copies of a
-// key tile take less time than its softmax, and one CTA with one unit in hand waits for that: two CTAs share
-// an SM then, with half of its shared and tensor memory each.
-template <int D, int NT>
+// The kernels: kFew and kOne for batches whose sequences all fit one tile, kMixed for those with longer
+// chunks (there each CTA works either on one-tile or on two-tile units). With one unit in hand a CTA waits
+// between its steps: for the softmax where d = 64, and from one unit to the next where keys are few. So two
+// CTAs share an SM, with half of its shared and tensor memory each, where that is enough: at d = 64, and at
+// d = 128 for up to kFewRows rows if the block table has room for up to kFewKeys keys (kFew: 512 sequences of
+// 128 keys take 60 us, 97 with kOne, 2000 of 300 keys 115 and 127, 256 of 512 keys 87 and 86; longer ones
+// stream better with all of the SM's memory, 64 sequences of 8192 keys 245 us against 251).
+enum : int { kFew = 0, kOne = 1, kMixed = 2 };
+constexpr int kFewRows = 32, kFewKeys = 384;
+
+template <int D, int KERNEL>
 struct Shape {
-    static constexpr int kPerSm = NT == 1 && D == 64 ? 2 : 1;
-    static constexpr int kFirst = 4 * NT;  // the first warp behind the softmax warps
-    static constexpr int kThreads = NT == 1 ? 256 : 384;
-    static constexpr int kTilesBytes = (kPerSm == 2 ? 96 : 224) * 1024;  // shared memory for Q, K and V tiles
+    static constexpr int kTiles = KERNEL == kMixed ? 2 : 1;  // of a unit, at most
+    static constexpr int kPerSm = KERNEL == kFew || (KERNEL == kOne && D == 64) ? 2 : 1;
+    static constexpr int kFirst = 4 * kTiles;  // the first warp behind the softmax warps
+    static constexpr int kThreads = KERNEL == kMixed ? 384 : 256;
+    // shared memory for Q, K and V tiles
+    static constexpr int kTilesBytes = (KERNEL == kFew ? 104 : kPerSm == 2 ? 96 : 224) * 1024;
     static constexpr int kSmemBytes = kTilesBytes + 2048 + 1024;  // barriers and schedule + alignment slack
     static_assert(kPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory");
     static constexpr uint32_t kTmemCols = 512 / kPerSm;
     // registers per thread after the rebalance: the softmax warps hold a row of scores each
-    static constexpr bool kRebalance = NT == 2 || kPerSm == 2;
-    static constexpr int kSoftmaxRegs = NT == 1 ? 184 : D == 64 ? 192 : 200;
-    static constexpr int kOtherRegs = NT == 1 ? 72 : D == 64 ? 120 : 104;
-    static_assert(NT == 1 ? kSoftmaxRegs + kOtherRegs <= 2 * 128 : 2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "register split");
+    static constexpr bool kRebalance = KERNEL == kMixed || kPerSm == 2;
+    static constexpr int kSoftmaxRegs = KERNEL != kMixed ? 184 : D == 64 ? 192 : 200;
+    static constexpr int kOtherRegs = KERNEL != kMixed ? 72 : D == 64 ? 120 : 104;
+    static_assert(KERNEL != kMixed ? kSoftmaxRegs + kOtherRegs <= 2 * 128 : 2 * kSoftmaxRegs + kOtherRegs <= 3 * 168,
+                  "register split");
 };
 
 // A CTA of the kernel KERNEL that works on units of NT tiles.
@@ -100,13 +109,15 @@ struct Cfg {
     using Kernel = Shape<D, KERNEL>;
     static constexpr int kBoxes = D / 64;
     static constexpr int kTileBytes = BM * D * 2;
-    static constexpr bool kSplit = D == 64 || NT == 1;  // P in tensor-memory columns of its own
+    // P in tensor-memory columns of its own, where there are enough
+    static constexpr bool kSplit = D == 64 || (NT == 1 && KERNEL != kFew);
     static constexpr int kIssuers = kSplit ? NT : 1;
     static constexpr int kQOff = 0;
-    static constexpr int kKVOff = kQOff + NT * kTileBytes;
+    static constexpr int kQBytes = KERNEL == kFew ? kFewRows * D * 2 : NT * kTileBytes;
+    static constexpr int kKVOff = kQOff + kQBytes;
     static constexpr int kStages = (Kernel::kTilesBytes - kKVOff) / kTileBytes;  // K and V tiles in flight
     // tensor-memory columns of tile t; S_t is at BN t
-    static constexpr int o_col(int t) { return NT == 1 && D == 64 ? 192 : 256 + D * t; }
+    static constexpr int o_col(int t) { return KERNEL == kFew ? 128 : NT == 1 && D == 64 ? 192 : 256 + D * t; }
     static constexpr int p_col(int t) { return !kSplit ? BN * t : NT == 1 && D == 64 ? 128 : 384 + 64 * t; }
     static_assert(NT == 2 || o_col(0) + D <= (int)Kernel::kTmemCols, "tensor memory");
     // warps: K (and V) producer, MMA issuer, Q producer and V tail; the fourth is the V producer, except where
@@ -317,7 +328,7 @@ struct Unit {
 
 // Walks this CTA's units of NT tiles in order. Every warp role walks for itself and finds the same units;
 // its place is kept in shared memory, since the softmax warps need their registers for a row of scores.
-// KERNEL is the NT of the kernel: where it is 2, sequences of the other kind are passed over.
+// In the mixed kernel sequences of the other kind are passed over.
 template <int NT, int KERNEL>
 struct Walk {
     const PagedDev& p;
@@ -376,7 +387,7 @@ struct Walk {
                             break;
                         }
                         at.seq = seq_of(p, at.b, nullptr);
-                    } while (at.seq.n == 0 || (KERNEL == 2 && is_pair<2>(p, at.seq) != (NT == 2)));
+                    } while (at.seq.n == 0 || (KERNEL == kMixed && is_pair<2>(p, at.seq) != (NT == 2)));
                 }
             }
         }
@@ -484,7 +495,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
     // rows from a slot's start; what lies behind the tile's own rows only reaches rows that nobody reads.
     const uint32_t q_half = NT == 1 ? (uint32_t)((p.tok_tile * p.G + 7) / 8 * 1024) : BM * 128;  // bytes of a box
     const uint32_t q_stride = q_half * C::kBoxes;
-    const uint32_t q_slots = NT == 1 ? min(4u, (uint32_t)C::kTileBytes / q_stride) : 2u;
+    const uint32_t q_slots = NT == 1 ? min(4u, (uint32_t)C::kQBytes / q_stride) : 2u;
 
     if (warp >= C::kProducer) {
         if constexpr (C::Kernel::kRebalance) regs_decrease<C::Kernel::kOtherRegs>();
@@ -679,14 +690,20 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             }
             __syncwarp();
         } else if (!C::kSplit && warp == C::kIssuer) {
-            // ------------------------------------------------ MMA issuer of both tiles
-            uint32_t it = 0, pcnt0 = 0, pcnt1 = 0, qcnt0 = 0;
+            // ------------------------------------------------ the one MMA issuer of P over S
+            uint32_t it = 0, pcnt0 = 0, pcnt1 = 0;
+            uint32_t q_at = 0, q_phase = 0;  // Q slot (one tile), and the phase of its uses
             bool ok = true;
             while (ok && walk.next(w)) {
                 if (w.cnt_max == 0) continue;
-                ok = mbar_wait_warp(&bar.q_full[0], qcnt0++ & 1, wc);
+                const uint32_t q_i = q_at, q_tile = sQ + q_i * q_stride;
+                ok = mbar_wait_warp(&bar.q_full[q_i], q_phase, wc);
                 if (!ok) break;
                 tc_fence_after();
+                if (NT == 2 || ++q_at == q_slots) {
+                    q_at = 0;
+                    q_phase ^= 1;
+                }
                 for (int j = 0; j <= w.cnt_max && ok; ++j) {
                     const uint32_t itK = it;  // ring slot of K_j; V_j follows it
                     const uint32_t sK = itK % C::kStages, sV_prev = (itK + C::kStages - 1) % C::kStages;
@@ -721,7 +738,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                             __syncwarp();
                         }
                         if (j < w.cnt(t)) {
-                            const uint32_t qt = sQ + t * q_stride, kt = sKV + sK * C::kTileBytes;
+                            const uint32_t qt = q_tile + t * q_stride, kt = sKV + sK * C::kTileBytes;
                             if (elect_one()) {
                                 const uint64_t qd = kmajor_desc(qt), kd = kmajor_desc(kt);
 #pragma unroll kIssueUnroll
@@ -738,9 +755,11 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                     }
                     if (!ok) break;
                     if (elect_one()) {
-                        if (j == w.cnt_max - 1) mma_commit(&bar.q_empty[0]);
-                        if (j < w.cnt_max) mma_commit(&bar.kv_empty[sK]);
+                        if (j == w.cnt_max - 1) mma_commit(&bar.q_empty[q_i]);
+                        // V before K: with an odd number of stages either producer waits on slots that the other
+                        // used last, and may only see K_j's release when V_{j-1}'s is out
                         if (j > 0) mma_commit(&bar.kv_empty[sV_prev]);
+                        if (j < w.cnt_max) mma_commit(&bar.kv_empty[sK]);
                     }
                     __syncwarp();
                     if (j < w.cnt_max) it += 2;
@@ -943,7 +962,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                     if (held) p.lse[head * p.T + row] = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
                 } else {
                     // the part's state of this row; a row without keys in it is m = -inf, and its o is not read
-                    float4* rec = record(p.part, blockIdx.x * 2 + (first ? 1 : 0), KERNEL, t, rows, D);
+                    float4* rec = record(p.part, blockIdx.x * 2 + (first ? 1 : 0), C::Kernel::kTiles, t, rows, D);
                     if (held) rec[r] = make_float4(l > 0.f ? m_ref : -INFINITY, l, den, 0.f);
                     if (cnt > 0) {
 #pragma unroll 1
@@ -967,17 +986,18 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
     }
 }
 
-template <int D, bool F16, int NT>
-__global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kPerSm)
+template <int D, bool F16, int KERNEL>
+__global__ void __launch_bounds__(Shape<D, KERNEL>::kThreads, Shape<D, KERNEL>::kPerSm)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const PagedDev p) {
+    using Kernel = Shape<D, KERNEL>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Shared& bar = *reinterpret_cast<Shared*>(smem + Shape<D, NT>::kTilesBytes);
+    Shared& bar = *reinterpret_cast<Shared*>(smem + Kernel::kTilesBytes);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) bar.abort_flag = 0;
     if (warp == 0) {
-        tmem_alloc(&bar.tmem_base, Shape<D, NT>::kTmemCols);
+        tmem_alloc(&bar.tmem_base, Kernel::kTmemCols);
         tmem_relinquish();
         if (elect_one()) {
             prefetch_tmap(&tm_q);
@@ -990,20 +1010,20 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kPerSm)
     // No global memory is touched above: from here on the previous kernel must be complete.
     grid_dep_launch();
     grid_dep_wait();
-    locate<NT, Shape<D, NT>::kThreads>(p, bar);
+    locate<Kernel::kTiles, Kernel::kThreads>(p, bar);
     __syncthreads();
-    if constexpr (NT == 2) {
+    if constexpr (KERNEL == kMixed) {
         if (bar.pair)
-            work<D, F16, 2, 2>(tm_q, tm_k, tm_v, p, smem, bar);
+            work<D, F16, 2, KERNEL>(tm_q, tm_k, tm_v, p, smem, bar);
         else
-            work<D, F16, 1, 2>(tm_q, tm_k, tm_v, p, smem, bar);
+            work<D, F16, 1, KERNEL>(tm_q, tm_k, tm_v, p, smem, bar);
     } else {
-        work<D, F16, 1, 1>(tm_q, tm_k, tm_v, p, smem, bar);
+        work<D, F16, 1, KERNEL>(tm_q, tm_k, tm_v, p, smem, bar);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) tmem_dealloc(bar.tmem_base, Shape<D, NT>::kTmemCols);
+    if (warp == 0) tmem_dealloc(bar.tmem_base, Kernel::kTmemCols);
 }
 
 // ---------------------------------------------------------------- merging parts
@@ -1116,7 +1136,7 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Co
 // The tile shape of a call. One tile per unit while the rows that a sequence is expected to bring fit
 // it, so that decode does not carry an empty second tile; two beyond.
 struct Plan {
-    int tiles, tok_tile, rows, ctas;
+    int kernel, tiles, tok_tile, rows, ctas;
     size_t meta_bytes, bytes;
 };
 
@@ -1127,9 +1147,13 @@ Plan plan_of(const attn_paged_params& p, int num_sms) {
     pl.tok_tile = BM / G;
     if (pl.tiles == 1 && p.max_q < pl.tok_tile) pl.tok_tile = p.max_q;
     pl.rows = pl.tok_tile * G;
-    pl.ctas = num_sms * (pl.tiles == 2 ? 1 : p.d == 64 ? Shape<64, 1>::kPerSm : Shape<128, 1>::kPerSm);
-    pl.meta_bytes = ((size_t)pl.ctas * 2 * sizeof(int4) + 255) / 256 * 256;
-    pl.bytes = pl.meta_bytes + (size_t)pl.ctas * 2 * pl.tiles * pl.rows * (p.d + 4) * sizeof(float);
+    const bool few = p.d == 128 && pl.rows <= kFewRows && (long long)p.max_pages * p.page_size <= kFewKeys;
+    pl.kernel = pl.tiles == 2 ? kMixed : few ? kFew : kOne;
+    pl.ctas = num_sms * (pl.kernel == kFew || (pl.kernel == kOne && p.d == 64) ? 2 : 1);  // Shape::kPerSm
+    // the workspace has room for either one-tile kernel, so that its size does not go by the table's
+    const int room = num_sms * (pl.tiles == 1 && (p.d == 64 || pl.rows <= kFewRows) ? 2 : 1);
+    pl.meta_bytes = ((size_t)room * 2 * sizeof(int4) + 255) / 256 * 256;
+    pl.bytes = pl.meta_bytes + (size_t)room * 2 * pl.tiles * pl.rows * (p.d + 4) * sizeof(float);
     return pl;
 }
 
@@ -1149,13 +1173,14 @@ CUresult encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, int32_t d
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-template <int D, bool F16, int NT>
+template <int D, bool F16, int KERNEL>
 cudaError_t launch_tc(const CUtensorMap (&maps)[3], const PagedDev& p, int grid, cudaStream_t s) {
-    const cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D, F16, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               Shape<D, NT>::kSmemBytes);
+    using Kernel = Shape<D, KERNEL>;
+    const cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D, F16, KERNEL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Kernel::kSmemBytes);
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_tc_kernel<D, F16, NT>, dim3(grid), dim3(Shape<D, NT>::kThreads), Shape<D, NT>::kSmemBytes, s, maps[0], maps[1],
-                      maps[2], p);
+    return launch_pdl(paged_tc_kernel<D, F16, KERNEL>, dim3(grid), dim3(Kernel::kThreads), Kernel::kSmemBytes, s, maps[0],
+                      maps[1], maps[2], p);
 }
 
 // Held from a call's first launch to its last, so that calls of several host threads on one stream may share
@@ -1165,7 +1190,14 @@ std::mutex g_launch_mu;
 template <int D, bool F16>
 cudaError_t launch_both(const CUtensorMap (&maps)[3], const PagedDev& p, const Plan& pl, int grid, cudaStream_t s) {
     std::lock_guard<std::mutex> lock(g_launch_mu);
-    const cudaError_t e = pl.tiles == 1 ? launch_tc<D, F16, 1>(maps, p, grid, s) : launch_tc<D, F16, 2>(maps, p, grid, s);
+    cudaError_t e;
+    if (pl.kernel == kMixed) {
+        e = launch_tc<D, F16, kMixed>(maps, p, grid, s);
+    } else if (D == 128 && pl.kernel == kFew) {
+        e = launch_tc<128, F16, kFew>(maps, p, grid, s);
+    } else {
+        e = launch_tc<D, F16, kOne>(maps, p, grid, s);
+    }
     if (e != cudaSuccess) return e;
     CombineArgs a{};
     a.part = p.part;

@@ -198,6 +198,20 @@ def test_many_sequences_beside_long_chunks(A):
     c.check(o, lse, True)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("page", [16, 64, 128])
+@pytest.mark.parametrize("n", [1, 3, 8])
+def test_short_tables(A, n, page, dtype):
+    # tables of up to 384 keys at d = 128: 4 to 32 rows, two CTAs to an SM, one to four query tiles ahead
+    rng = np.random.default_rng(n + page)
+    kv = rng.integers(0, 385, 37)
+    kv[:4] = [384, 0, 128, 1]
+    c = Case([n] * 36 + [0], kv.tolist(), 3, 4, 128, page, dtype, 93)
+    o, lse = A.attn_paged(*c.device(), causal=True, max_q=n)
+    _ok(A)
+    c.check(o, lse, True)
+
+
 @pytest.mark.parametrize("max_q", [1, 400])
 def test_no_rows_at_all(A, max_q):
     c = Case([0, 0], [40, 0], 1, 2, 64, 16, torch.bfloat16, 92, pad=3)
