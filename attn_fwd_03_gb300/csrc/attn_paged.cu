@@ -113,7 +113,10 @@ struct Cfg {
     static constexpr bool kSplit = D == 64 || (NT == 1 && KERNEL != kFew);
     static constexpr int kIssuers = kSplit ? NT : 1;
     static constexpr int kQOff = 0;
-    static constexpr int kQBytes = KERNEL == kFew ? kFewRows * D * 2 : NT * kTileBytes;
+    // Q tiles are loaded ahead of their unit: with one tile into as many slots as its rows leave room for, with
+    // two into two more slots at d = 64 (at d = 128 a third Q tile is no faster than a fifth K or V tile)
+    static constexpr int kQTiles = NT == 1 ? 1 : D == 128 ? 2 : 4;
+    static constexpr int kQBytes = KERNEL == kFew ? kFewRows * D * 2 : kQTiles * kTileBytes;
     static constexpr int kKVOff = kQOff + kQBytes;
     static constexpr int kStages = (Kernel::kTilesBytes - kKVOff) / kTileBytes;  // K and V tiles in flight
     // tensor-memory columns of tile t; S_t is at BN t
@@ -160,7 +163,7 @@ struct Place {
 };
 
 struct __align__(16) Shared {
-    uint64_t q_full[4], q_empty[4];  // one tile: of Q slots in turn; two tiles: of either (split P) or of both
+    uint64_t q_full[4], q_empty[4];  // of the Q slots, which are used in turn
     uint64_t kv_full[13], kv_empty[13], v_tail[13];
     uint64_t s_full[2], p_full[2], o_full[2], s_free[2], pv_done[2];
     uint64_t drain[2];
@@ -423,30 +426,6 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
         if (globaltimer() - t0 > timeout_ns) break;
 }
 
-// Transposes 8 x 8 pieces of 16 bytes among each 8 lanes: lane i's piece j becomes lane j's piece i. The
-// epilogue's threads hold a row each; stored as they are, every store instruction would touch 32 rows, and
-// those requests hold up the copies of the next unit's tiles (eight prompts of 1024 tokens: 95 -> 92 us).
-__device__ __forceinline__ void transpose8(uint4 (&v)[8], int lane) {
-#pragma unroll
-    for (int s = 1; s < 8; s <<= 1) {
-        const bool up = lane & s;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (i & s) continue;
-            const uint4 give = up ? v[i] : v[i | s];
-            uint4 got;
-            got.x = __shfl_xor_sync(kFull, give.x, s);
-            got.y = __shfl_xor_sync(kFull, give.y, s);
-            got.z = __shfl_xor_sync(kFull, give.z, s);
-            got.w = __shfl_xor_sync(kFull, give.w, s);
-            if (up)
-                v[i] = got;
-            else
-                v[i | s] = got;
-        }
-    }
-}
-
 // The page that holds key `key` for this lane: its number, or num_pages (a row of zeros to TMA) for
 // one that the cache does not have.
 __device__ __forceinline__ int page_at(const PagedDev& p, int b, int key, bool* bad) {
@@ -455,6 +434,18 @@ __device__ __forceinline__ int page_at(const PagedDev& p, int b, int key, bool* 
     *bad = true;
     return p.num_pages;
 }
+
+// The Q slot to come, and the phase of its uses.
+struct QRing {
+    uint32_t slots, at = 0, phase = 0;
+    __device__ __forceinline__ explicit QRing(uint32_t n) : slots(n) {}
+    __device__ __forceinline__ void next() {
+        if (++at == slots) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
+};
 
 // The work of a CTA on units of NT tiles, from the located piece of the line to its end.
 template <int D, bool F16, int NT, int KERNEL>
@@ -491,11 +482,11 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
     const uint32_t tmem = bar.tmem_base;
     const uint32_t sQ = smem_u32(smem + C::kQOff);
     const uint32_t sKV = smem_u32(smem + C::kKVOff);
-    // One tile: Q is loaded ahead, into as many slots as the tile's rows leave room for. A product reads 128
-    // rows from a slot's start; what lies behind the tile's own rows only reaches rows that nobody reads.
+    // One tile: a product reads 128 rows from a slot's start; what lies behind the tile's own rows only reaches
+    // rows that nobody reads.
     const uint32_t q_half = NT == 1 ? (uint32_t)((p.tok_tile * p.G + 7) / 8 * 1024) : BM * 128;  // bytes of a box
     const uint32_t q_stride = q_half * C::kBoxes;
-    const uint32_t q_slots = NT == 1 ? min(4u, (uint32_t)C::kQBytes / q_stride) : 2u;
+    const uint32_t q_slots = NT == 1 ? min(4u, (uint32_t)C::kQBytes / q_stride) : C::kQTiles;
 
     if (warp >= C::kProducer) {
         if constexpr (C::Kernel::kRebalance) regs_decrease<C::Kernel::kOtherRegs>();
@@ -568,19 +559,16 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 }
                 if (w.cnt_max == 0 || !ok) continue;  // the slots are written whatever happens
 #pragma unroll 1
-                for (int t = 0; t < (C::kSplit ? NT : 1) && ok; ++t) {
-                    if (C::kSplit && w.cnt(t) == 0) continue;
-                    const uint32_t i = NT == 1 ? q_at : (uint32_t)t;
-                    const int nt = !C::kSplit && w.ntok > p.tok_tile ? 2 : 1;  // one issuer: both tiles at once
+                for (int t = 0; t < NT && ok; ++t) {
+                    if (w.cnt(t) == 0) continue;
+                    const uint32_t i = q_at;
                     ok = mbar_wait_warp(&bar.q_empty[i], ((q_used >> (8 * i)) & 1) ^ 1, wc);
                     if (!ok) break;
                     if (elect_one()) {
-                        mbar_arrive_expect_tx(&bar.q_full[i], nt * q_bytes);
-                        for (int x = 0; x < nt * C::kBoxes; ++x) {
-                            const int bx = x % C::kBoxes, more = x / C::kBoxes;
-                            tma_load_4d(smem + C::kQOff + (i + more) * q_stride + bx * q_half, &tm_q, &bar.q_full[i], bx * 64, 0,
-                                        w.row0 + (t + more) * p.tok_tile, w.h);
-                        }
+                        mbar_arrive_expect_tx(&bar.q_full[i], q_bytes);
+                        for (int bx = 0; bx < C::kBoxes; ++bx)
+                            tma_load_4d(smem + C::kQOff + i * q_stride + bx * q_half, &tm_q, &bar.q_full[i], bx * 64, 0,
+                                        w.row0 + t * p.tok_tile, w.h);
                     }
                     __syncwarp();
                     q_used ^= 1u << (8 * i);
@@ -616,21 +604,20 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             const int t = warp == C::kIssuer ? 0 : 1;
             const uint32_t tS = tmem + t * BN, tO = tmem + C::o_col(t), tP = tmem + C::p_col(t);
             uint32_t it = 0, n_s = 0, n_p = 0;
-            uint32_t q_at = NT == 1 ? 0 : t, q_phase = 0;  // Q slot, and the phase of its uses
+            QRing ring(q_slots);
             bool ok = true;
             while (ok && walk.next(w)) {
                 if (w.cnt_max == 0) continue;
                 const int cnt = w.cnt(t);
-                const uint32_t q_i = q_at, qt = sQ + q_i * q_stride;
+                if (NT == 2 && t == 1 && w.cnt0 > 0) ring.next();  // tile 0's
+                const uint32_t q_i = ring.at, qt = sQ + q_i * q_stride;
                 if (cnt > 0) {
-                    ok = mbar_wait_warp(&bar.q_full[q_i], q_phase, wc);
+                    ok = mbar_wait_warp(&bar.q_full[q_i], ring.phase, wc);
                     if (!ok) break;
+                    ring.next();
                     tc_fence_after();
-                    if (NT == 2 || ++q_at == q_slots) {
-                        if (NT == 1) q_at = 0;
-                        q_phase ^= 1;
-                    }
                 }
+                if (NT == 2 && t == 0 && w.cnt1 > 0) ring.next();  // tile 1's
                 for (int j = 0; j <= w.cnt_max && ok; ++j) {
                     const uint32_t itK = it;  // ring slot of K_j; V_j follows it
                     const uint32_t sK = itK % C::kStages, sV_prev = (itK + C::kStages - 1) % C::kStages;
@@ -691,79 +678,81 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             __syncwarp();
         } else if (!C::kSplit && warp == C::kIssuer) {
             // ------------------------------------------------ the one MMA issuer of P over S
+            // S_t^0 of every tile, then per key tile O_t += P_t^{j-1} V_{j-1} and S_t^j in turn. The epilogue has
+            // read O_t before its threads arrive on p_full for a new unit.
             uint32_t it = 0, pcnt0 = 0, pcnt1 = 0;
-            uint32_t q_at = 0, q_phase = 0;  // Q slot (one tile), and the phase of its uses
+            QRing ring(q_slots);
             bool ok = true;
+            auto issue_s = [&](int t, uint32_t q_i, uint32_t sK) {
+                if (elect_one()) {
+                    const uint64_t qd = kmajor_desc(sQ + q_i * q_stride), kd = kmajor_desc(sKV + sK * C::kTileBytes);
+#pragma unroll kIssueUnroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        mma_ss(tmem + t * BN, kmajor_step(qd, kk, q_half), kmajor_step(kd, kk, BN * 128), kIdescS,
+                               kk > 0 ? 1u : 0u);
+                    mma_commit(&bar.s_full[t]);
+                }
+                __syncwarp();
+            };
             while (ok && walk.next(w)) {
                 if (w.cnt_max == 0) continue;
-                const uint32_t q_i = q_at, q_tile = sQ + q_i * q_stride;
-                ok = mbar_wait_warp(&bar.q_full[q_i], q_phase, wc);
-                if (!ok) break;
-                tc_fence_after();
-                if (NT == 2 || ++q_at == q_slots) {
-                    q_at = 0;
-                    q_phase ^= 1;
+                uint32_t sK = it % C::kStages, q_of[2];
+                ok = mbar_wait_warp(&bar.kv_full[sK], (it / C::kStages) & 1, wc);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    q_of[t] = ring.at;
+                    if (!ok || w.cnt(t) == 0) continue;
+                    ok = mbar_wait_warp(&bar.q_full[ring.at], ring.phase, wc);
+                    ring.next();
+                    tc_fence_after();
+                    if (ok) issue_s(t, q_of[t], sK);
                 }
-                for (int j = 0; j <= w.cnt_max && ok; ++j) {
-                    const uint32_t itK = it;  // ring slot of K_j; V_j follows it
-                    const uint32_t sK = itK % C::kStages, sV_prev = (itK + C::kStages - 1) % C::kStages;
+                if (!ok) break;
+                for (int j = 1; j <= w.cnt_max && ok; ++j) {
+                    const uint32_t itV = it + 1, sV = itV % C::kStages;  // V_{j-1}
+                    if (elect_one()) {
+                        // V before K: with an odd number of stages either producer waits on slots that the other
+                        // used last, and may only see K_j's release when V_{j-1}'s is out
+                        if (j > 1) mma_commit(&bar.kv_empty[(it + C::kStages - 1) % C::kStages]);
+                        mma_commit(&bar.kv_empty[sK]);
+                        if (j == w.cnt_max) {  // every S of the part is issued
+                            if (w.cnt0 > 0) mma_commit(&bar.q_empty[q_of[0]]);
+                            if (NT == 2 && w.cnt1 > 0) mma_commit(&bar.q_empty[q_of[NT - 1]]);
+                        }
+                    }
+                    __syncwarp();
+                    it += 2;
+                    sK = it % C::kStages;
                     if (j < w.cnt_max) {
-                        ok = mbar_wait_warp(&bar.kv_full[sK], (itK / C::kStages) & 1, wc);
+                        ok = mbar_wait_warp(&bar.kv_full[sK], (it / C::kStages) & 1, wc);
                         if (!ok) break;
                     }
-                    if (j > 0) {  // V_{j-1} lives in the slot before K_j
-                        ok = mbar_wait_warp(&bar.kv_full[sV_prev], ((itK - 1) / C::kStages) & 1, wc);
-                        if (!ok) break;
-                    }
+                    ok = mbar_wait_warp(&bar.kv_full[sV], (itV / C::kStages) & 1, wc);
+                    if (!ok) break;
                     tc_fence_after();
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        if (!ok || w.cnt(t) == 0 || j > w.cnt(t)) continue;
-                        const uint32_t tS = tmem + t * BN, tO = tmem + C::o_col(t);
-                        if (j > 0) {
-                            // O_t += P_t^{j-1} V_{j-1}; the epilogue has read O_t before its threads
-                            // arrive on p_full for a new unit
-                            uint32_t& pcnt = t == 0 ? pcnt0 : pcnt1;
-                            ok = mbar_wait_warp(&bar.p_full[t], pcnt & 1, wc);
-                            if (!ok) continue;
-                            ++pcnt;
-                            tc_fence_after();
-                            const uint32_t vt = sKV + sV_prev * C::kTileBytes;
-                            if (elect_one()) {
-                                const uint64_t vd = vmajor_desc(vt);
+                        if (!ok || j > w.cnt(t)) continue;
+                        uint32_t& pcnt = t == 0 ? pcnt0 : pcnt1;
+                        ok = mbar_wait_warp(&bar.p_full[t], pcnt & 1, wc);
+                        if (!ok) continue;
+                        ++pcnt;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t vd = vmajor_desc(sKV + sV * C::kTileBytes);
 #pragma unroll kIssueUnroll
-                                for (int kk = 0; kk < BN / 16; ++kk)
-                                    mma_ts(tO, tS + kk * 8, vmajor_step(vd, kk), kIdescO, (j > 1 || kk > 0) ? 1u : 0u);
-                            }
-                            __syncwarp();
+                            for (int kk = 0; kk < BN / 16; ++kk)
+                                mma_ts(tmem + C::o_col(t), tmem + t * BN + kk * 8, vmajor_step(vd, kk), kIdescO,
+                                       (j > 1 || kk > 0) ? 1u : 0u);
+                            if (j == w.cnt(t)) mma_commit(&bar.o_full[t]);  // last product of this tile
                         }
-                        if (j < w.cnt(t)) {
-                            const uint32_t qt = q_tile + t * q_stride, kt = sKV + sK * C::kTileBytes;
-                            if (elect_one()) {
-                                const uint64_t qd = kmajor_desc(qt), kd = kmajor_desc(kt);
-#pragma unroll kIssueUnroll
-                                for (int kk = 0; kk < D / 16; ++kk)
-                                    mma_ss(tS, kmajor_step(qd, kk, q_half), kmajor_step(kd, kk, BN * 128), kIdescS,
-                                           kk > 0 ? 1u : 0u);
-                                mma_commit(&bar.s_full[t]);
-                            }
-                            __syncwarp();
-                        } else {
-                            if (elect_one()) mma_commit(&bar.o_full[t]);  // last product of this tile issued
-                            __syncwarp();
-                        }
+                        __syncwarp();
+                        if (j < w.cnt(t)) issue_s(t, q_of[t], sK);
                     }
-                    if (!ok) break;
-                    if (elect_one()) {
-                        if (j == w.cnt_max - 1) mma_commit(&bar.q_empty[q_i]);
-                        // V before K: with an odd number of stages either producer waits on slots that the other
-                        // used last, and may only see K_j's release when V_{j-1}'s is out
-                        if (j > 0) mma_commit(&bar.kv_empty[sV_prev]);
-                        if (j < w.cnt_max) mma_commit(&bar.kv_empty[sK]);
-                    }
-                    __syncwarp();
-                    if (j < w.cnt_max) it += 2;
                 }
+                if (!ok) break;
+                if (elect_one()) mma_commit(&bar.kv_empty[(it + C::kStages - 1) % C::kStages]);  // the last V
+                __syncwarp();
             }
             if (elect_one()) {
                 mma_commit(&bar.drain[0]);
@@ -919,44 +908,29 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 if (first && last) {
                     const float inv = den > 0.f ? 1.f / den : 0.f;
                     const long long row = u.x + my_tok, head = u.z * p.G + my_head;
-                    const long long off = row * p.o_sr + head * p.o_sh;
-                    const unsigned keep = __ballot_sync(kFull, held);
+                    uint16_t* orow = reinterpret_cast<uint16_t*>(p.o) + row * p.o_sr + head * p.o_sh;
 #pragma unroll 1
                     for (int c0 = 0; c0 < D; c0 += 64) {
-                        uint4 v[8];
+                        uint32_t ov[64];
+                        if (cnt > 0) {
+                            tmem_ld32_at<0>(tO + c0, ov);
+                            tmem_ld32_at<32>(tO + c0 + 32, ov);
+                            tmem_wait_ld();
+                        } else {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t ov[32];
-                            if (cnt > 0) {
-                                tmem_ld32(tO + c0 + 32 * h, ov);
-                                tmem_wait_ld();
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) ov[i] = 0;
-                            }
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                v[4 * h + q] = make_uint4(
-                                    pack_h16<F16>(__uint_as_float(ov[8 * q + 0]) * inv, __uint_as_float(ov[8 * q + 1]) * inv),
-                                    pack_h16<F16>(__uint_as_float(ov[8 * q + 2]) * inv, __uint_as_float(ov[8 * q + 3]) * inv),
-                                    pack_h16<F16>(__uint_as_float(ov[8 * q + 4]) * inv, __uint_as_float(ov[8 * q + 5]) * inv),
-                                    pack_h16<F16>(__uint_as_float(ov[8 * q + 6]) * inv, __uint_as_float(ov[8 * q + 7]) * inv));
+                            for (int i = 0; i < 64; ++i) ov[i] = 0;
                         }
-                        if constexpr (NT == 1) {  // mostly a few rows
-                            if (held) {
-                                uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.o) + off + c0);
+                        if (held) {
+                            uint4* dst = reinterpret_cast<uint4*>(orow + c0);
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) dst[e] = v[e];
+                            for (int q = 0; q < 8; ++q) {
+                                uint4 v;
+                                v.x = pack_h16<F16>(__uint_as_float(ov[8 * q + 0]) * inv, __uint_as_float(ov[8 * q + 1]) * inv);
+                                v.y = pack_h16<F16>(__uint_as_float(ov[8 * q + 2]) * inv, __uint_as_float(ov[8 * q + 3]) * inv);
+                                v.z = pack_h16<F16>(__uint_as_float(ov[8 * q + 4]) * inv, __uint_as_float(ov[8 * q + 5]) * inv);
+                                v.w = pack_h16<F16>(__uint_as_float(ov[8 * q + 6]) * inv, __uint_as_float(ov[8 * q + 7]) * inv);
+                                dst[q] = v;
                             }
-                            continue;
-                        }
-                        transpose8(v, lane);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int owner = (lane & 24) + e;
-                            const long long at = __shfl_sync(kFull, off, owner);
-                            if (keep >> owner & 1)
-                                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.o) + at + c0 + (lane & 7) * 8) = v[e];
                         }
                     }
                     if (held) p.lse[head * p.T + row] = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
