@@ -45,9 +45,12 @@
 // reasons for either order of products).
 //
 // Measured and not kept: both softmax warpgroups on one tile's key columns in halves
-// (no faster: one-tile units wait for their copies); loading both Q tiles of a unit
-// under separate barriers (5 % slower: the extra branches lie in the issuer's loop);
-// V by a warp of its own for pages of 64 tokens and more (3 % slower).
+// (no faster: one-tile units wait for their copies); separate barriers for the two Q
+// tiles of a unit inside the issuer's loop (5 % slower), or a third Q tile loaded
+// ahead in place of a fifth K or V tile (no faster); V by a warp of its own for pages of 64
+// tokens and more (3 % slower); O transposed between lanes into whole 128-byte
+// lines (as slow as the 32 rows a store touches without; 32-byte stores gain 5 % on
+// eight prompts of 1024 tokens).
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -141,6 +144,7 @@ struct PagedDev {
     uint8_t* o;
     float* lse;
     long long o_sr, o_sh;  // elements
+    int o_wide;       // rows of o are 32-byte aligned
     float* part;      // [grid][2][NT] records of tok_tile * G rows: see record()
     int4* meta;       // [grid][2]: see below
     int* err;
@@ -424,6 +428,14 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
     const uint64_t t0 = globaltimer();
     while (!mbar_try_wait(a, parity))
         if (globaltimer() - t0 > timeout_ns) break;
+}
+
+// One store of 32 bytes (sm_100 on): the epilogue's threads hold a row each, and every store instruction
+// touches 32 rows whatever its width.
+__device__ __forceinline__ void store32(void* dst, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 
 // The page that holds key `key` for this lane: its number, or num_pages (a row of zeros to TMA) for
@@ -920,16 +932,18 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
 #pragma unroll
                             for (int i = 0; i < 64; ++i) ov[i] = 0;
                         }
-                        if (held) {
-                            uint4* dst = reinterpret_cast<uint4*>(orow + c0);
 #pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                uint4 v;
-                                v.x = pack_h16<F16>(__uint_as_float(ov[8 * q + 0]) * inv, __uint_as_float(ov[8 * q + 1]) * inv);
-                                v.y = pack_h16<F16>(__uint_as_float(ov[8 * q + 2]) * inv, __uint_as_float(ov[8 * q + 3]) * inv);
-                                v.z = pack_h16<F16>(__uint_as_float(ov[8 * q + 4]) * inv, __uint_as_float(ov[8 * q + 5]) * inv);
-                                v.w = pack_h16<F16>(__uint_as_float(ov[8 * q + 6]) * inv, __uint_as_float(ov[8 * q + 7]) * inv);
-                                dst[q] = v;
+                        for (int i = 0; i < 32; ++i)
+                            ov[i] = pack_h16<F16>(__uint_as_float(ov[2 * i]) * inv, __uint_as_float(ov[2 * i + 1]) * inv);
+                        if (held) {
+                            if (p.o_wide) {
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) store32(orow + c0 + 16 * q, &ov[8 * q]);
+                            } else {
+#pragma unroll
+                                for (int q = 0; q < 8; ++q)
+                                    *reinterpret_cast<uint4*>(orow + c0 + 8 * q) =
+                                        make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
                             }
                         }
                     }
@@ -1230,6 +1244,8 @@ attn_status_t launch_paged(const attn_paged_params& p, const LaunchCommon& lc, c
     a.lse = p.lse;
     a.o_sr = p.o_stride[0];
     a.o_sh = p.o_stride[1];
+    a.o_wide = ((reinterpret_cast<uintptr_t>(p.o) | (uintptr_t)(p.total_q > 1 ? p.o_stride[0] * 2 : 0) |
+                 (uintptr_t)(p.num_q_heads > 1 ? p.o_stride[1] * 2 : 0)) & 31) == 0;
     a.meta = static_cast<int4*>(p.workspace);
     a.part = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + pl.meta_bytes);
     a.err = lc.err;

@@ -130,6 +130,19 @@ def test_heads_first_pages_and_strided_rows(A, n):
     assert torch.all(out[:, :2] == 0) and torch.all(out[:, 10:] == 0)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 100])
+def test_output_rows_aligned_to_16_bytes_only(A, n, d):
+    c = Case([n, 2], [n + 200, 70], 1, 4, d, 32, torch.bfloat16, 62)
+    flat = torch.zeros(c.q.numel() + 8, dtype=c.dtype, device="cuda")
+    out = flat[8:].view(c.q.shape)
+    assert out.data_ptr() % 32 == 16
+    o, lse = A.attn_paged(*c.device(), causal=True, out=out, max_q=n)
+    _ok(A)
+    c.check(o, lse, True)
+    assert torch.all(flat[:8] == 0)
+
+
 def test_keys_and_values_interleaved_in_one_tensor(A):
     c = Case([1, 2], [70, 100], 3, 2, 128, 16, torch.float16, 65)
     q, k, v, table, cu, kv = c.device()
