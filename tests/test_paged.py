@@ -143,6 +143,34 @@ def test_output_rows_aligned_to_16_bytes_only(A, n, d):
     assert torch.all(flat[:8] == 0)
 
 
+def test_keys_and_values_in_different_page_orders(A):
+    c = Case([2, 1], [90, 40], 2, 3, 64, 16, torch.bfloat16, 63)
+    q, k, v, table, cu, kv = c.device()
+    o, lse = A.attn_paged(q, k.contiguous(), v, table, cu, kv, causal=True)
+    _ok(A)
+    assert k.stride() != k.contiguous().stride()
+    c.check(o, lse, True)
+
+
+def test_workspace_of_the_callers(A):
+    c = Case([1, 3], [400, 70], 2, 4, 128, 16, torch.float16, 64)
+    args = c.device()
+    need = A.paged_workspace_size(*args, max_q=3)
+    assert need > 0
+    with pytest.raises(A.AttnError) as e:
+        A.attn_paged(*args, causal=True, max_q=3, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == A.ATTN_ERR_WORKSPACE
+    with pytest.raises(A.AttnError) as e:
+        A.attn_paged(*args, causal=True, max_q=3, workspace=torch.empty(need + 8, dtype=torch.uint8, device="cuda")[8:])
+    assert e.value.status == A.ATTN_ERR_ALIGN
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")  # NaN everywhere: nothing of it is read before it is written
+    o, lse = A.attn_paged(*args, causal=True, max_q=3, workspace=ws)
+    _ok(A)
+    c.check(o, lse, True)
+    with pytest.raises(ValueError):
+        A.attn_paged(*args, causal=True, workspace=torch.empty(need, dtype=torch.uint8))
+
+
 def test_keys_and_values_interleaved_in_one_tensor(A):
     c = Case([1, 2], [70, 100], 3, 2, 128, 16, torch.float16, 65)
     q, k, v, table, cu, kv = c.device()
@@ -462,6 +490,20 @@ def test_plan_reports_lengths_out_of_range(A):
         A.attn_pages_plan(_i32([14]), _i32([old]), _i32(t), free, _i32([count]), 16, 14)
         torch.cuda.synchronize()
         assert A.attn_status() == A.ATTN_ERR_INVALID
+
+
+def test_tables_into_given_tensors_on_another_stream(A):
+    side = torch.cuda.Stream()
+    lens, table, free, count = _i32([5, 16]), _i32([[3, -1], [2, -1]]), _i32([0, 1, 4, 0]), _i32([3])
+    outs = {n: _i32([9] * m) for n, m in (("cu_q", 3), ("new_len", 2), ("slots", 5), ("positions", 5), ("free_left", 1))}
+    side.wait_stream(torch.cuda.current_stream())
+    got = A.attn_pages_plan(_i32([2, 1]), lens, table, free, count, 16, 5, stream=side, **outs)
+    new, left = A.attn_pages_release(_i32([0, 1]), got[1], table, free, got[4], 16, new_len=_i32([8, 8]), stream=side)
+    _ok(A)
+    assert all(g is outs[n] for g, n in zip(got, outs))
+    assert [outs[n].tolist() for n in outs] == [[0, 2, 3], [7, 17], [53, 54, 64, -1, -1], [5, 6, 16, -1, -1], [2]]
+    assert table.tolist() == [[3, -1], [2, 4]] and new.tolist() == [7, 0] and left.tolist() == [4]
+    assert free.tolist() == [0, 1, 2, 4]
 
 
 @pytest.mark.parametrize("seqs,page,every", [(1, 16, 1), (9, 32, 2), (777, 16, 3), (5000, 16, 7), (40, 256, 1), (6, 16, 99)])
