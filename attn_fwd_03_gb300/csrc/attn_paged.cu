@@ -13,11 +13,11 @@
 //
 // What bounds it: decode reads every key and value once for a few products each, so
 // HBM (a ragged batch of 64 sequences of 4096-8192 keys, 32 query and 8 key/value
-// heads, d = 128: 240 us, 6.6 TB/s, 99 % of the measured copy rate; 96 % with
+// heads, d = 128: 245 us, 6.6 TB/s, 98 % of the measured copy rate; 96 % with
 // 16-token pages); long chunks are bound by the tensor pipe and the softmax beside
-// it (4096 rows over 32768 keys: 1.33 ms, 1549 TFLOP/s, 83 % of the measured GEMM
+// it (4096 rows over 32768 keys: 1.30 ms, 1585 TFLOP/s, 85 % of the measured GEMM
 // rate); small calls by latency (one token over 517 keys: 10.4 us for both
-// launches, of which locating the work takes 1.4, the first copies 2, the merge 4).
+// launches, of which locating the work takes 1.4, the first copies 2, the merge 3).
 //
 // Work split: lengths are known on the device only, and ragged, so units are not
 // dealt out whole. All units lie one after another on a line, each as long as its
@@ -49,8 +49,9 @@
 // tiles of a unit inside the issuer's loop (5 % slower), or a third Q tile loaded
 // ahead in place of a fifth K or V tile (no faster); V by a warp of its own for pages of 64
 // tokens and more (3 % slower); O transposed between lanes into whole 128-byte
-// lines (as slow as the 32 rows a store touches without; 32-byte stores gain 5 % on
-// eight prompts of 1024 tokens).
+// lines (as slow as the 32 rows a store touches without); the P V product begun on the
+// first half of P (3 % slower: the issuer waits for one tile's second half while the
+// other tile could go on).
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -68,22 +69,23 @@ using namespace ptx;
 constexpr int BM = 128;  // query rows per tile
 constexpr int BN = 128;  // keys per tile
 constexpr float kRescaleThreshold = 8.0f;
-// What a unit costs beyond its key tiles, in keys. From 64 to 384 the verification of 5 drafted tokens of 16
-// sequences went from 20.2 to 19.2 us; 512 is no better.
+// What a unit costs beyond its key tiles, in keys: with 64 a prompt of 8192 tokens takes 410 us, with 384 it
+// takes 382, and the verification of 5 drafted tokens of 16 sequences 19.7 and 18.6.
 constexpr int kUnitCost = 384;
 // A key tile of a two-tile unit against one of a one-tile unit: 1.9 us against 1.3 in a step of 16 decoding
-// sequences and a 512-row chunk (85 us; 1.2 and 2.0 give 89).
+// sequences and a 512-row chunk (70 us; 1.2 gives 74, 2.0 73).
 constexpr float kPairCost = 1.5f;
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kIssueUnroll = 4;  // k-steps of a product in a row: 2 is 1 % slower, 1 11 %, 8 the same
+constexpr int kIssueUnroll = 4;  // k-steps of a product in a row: 2 and 8 are within 1 %, 1 is 11 % slower
 
 // The kernels: kFew and kOne for batches whose sequences all fit one tile, kMixed for those with longer
 // chunks (there each CTA works either on one-tile or on two-tile units). With one unit in hand a CTA waits
 // between its steps: for the softmax where d = 64, and from one unit to the next where keys are few. So two
-// CTAs share an SM, with half of its shared and tensor memory each, where that is enough: at d = 64, and at
-// d = 128 for up to kFewRows rows if the block table has room for up to kFewKeys keys (kFew: 512 sequences of
-// 128 keys take 60 us, 97 with kOne, 2000 of 300 keys 115 and 127, 256 of 512 keys 87 and 86; longer ones
-// stream better with all of the SM's memory, 64 sequences of 8192 keys 245 us against 251).
+// CTAs share an SM, with half of its shared and tensor memory each, where that is enough: at d = 64 (128
+// sequences of 1000 keys 50 us, 59 with one CTA; 64 of 4096 keys 86 and 90), and at d = 128 for up to
+// kFewRows rows if the block table has room for up to kFewKeys keys (kFew: 512 sequences of 128 keys take
+// 63 us, 100 with kOne, 2000 of 300 keys 119 and 126, 256 of 512 keys 87 and 86; longer ones stream better
+// with all of the SM's memory, 64 sequences of 8192 keys 245 us against 250).
 enum : int { kFew = 0, kOne = 1, kMixed = 2 };
 constexpr int kFewRows = 32, kFewKeys = 384;
 
@@ -431,7 +433,7 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
 }
 
 // One store of 32 bytes (sm_100 on): the epilogue's threads hold a row each, and every store instruction
-// touches 32 rows whatever its width.
+// touches 32 rows whatever its width (eight prompts of 1024 tokens 86 us, 90 with 16-byte stores).
 __device__ __forceinline__ void store32(void* dst, const uint32_t* v) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
                  "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
@@ -506,8 +508,9 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
         Unit w;
         if (warp == C::kProducer || (C::kVProducer && warp == C::kFourth)) {
             // ------------------------------------------------ K and V producers
-            // Small pages make many small copies, which one warp issues at about one in 90 cycles: K and V
-            // are issued by a warp each where there is one for V.
+            // Small pages make many small copies, which one warp issues at about one in 90 cycles: K and V are
+            // issued by a warp each where there is one for V (64 sequences of 8192 keys in 16-token pages 282 us,
+            // 329 by one warp; in 64-token pages 252 by two, 245 by one).
             const bool two = C::kVProducer && p.page_size < 64;
             const int first = C::kVProducer && warp == C::kFourth ? 1 : 0;  // 0: K, 1: V
             const int end = two || first == 1 ? first + 1 : 2;
@@ -1148,7 +1151,7 @@ Plan plan_of(const attn_paged_params& p, int num_sms) {
 // 4-D map of 16-bit elements over the given extents, dimension 0 contiguous, 64-column boxes.
 // Rows of 64 columns that do not follow one another (pages that hold [slot, head, d]) are fetched in
 // 128-byte pieces, or half of every fetch would be another head's row: 64 sequences of 4096 keys at d = 64 took
-// 113 us with 256-byte promotion and take 86 (79 % of the measured HBM). At d = 128, 256 bytes are a row, and
+// 112 us with 256-byte promotion and take 86 (80 % of the measured HBM). At d = 128, 256 bytes are a row, and
 // 128-byte promotion is 6 % slower with 16-token pages.
 CUresult encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, int32_t dtype, const void* base,
                 const cuuint64_t (&dims)[4], const int64_t (&st)[3], cuuint32_t box1, cuuint32_t box2) {
