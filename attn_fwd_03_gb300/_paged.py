@@ -85,6 +85,7 @@ lib.attn_paged_workspace_size.argtypes = [ctypes.c_void_p]
 lib.attn_paged_workspace_size.restype = ctypes.c_size_t
 
 _INT32 = torch.int32
+_INT32_MAX = 2 ** 31 - 1
 _TYPES = {torch.bfloat16: _dtype_code(torch.bfloat16), torch.float16: _dtype_code(torch.float16)}
 
 
@@ -164,8 +165,7 @@ def _pack_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, out, lse, scale,
 
 def paged_workspace_size(q, k_cache, v_cache, block_table, cu_q, kv_len, *, max_q: Optional[int] = None) -> int:
     """Bytes of workspace attn_paged needs for these shapes."""
-    if max_q is None:
-        max_q = _default_max_q(q.shape[0], block_table.shape[0])
+    max_q = _default_max_q(q.shape[0], block_table.shape[0]) if max_q is None else min(int(max_q), _INT32_MAX)
     # out and lse are not read: q stands in for both
     return int(lib.attn_paged_workspace_size(
         _pack_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, q, q, 1.0, False, max_q, 0, 0)))
@@ -239,7 +239,7 @@ def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
     total_q, hq, d = q.shape
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    max_q = _default_max_q(total_q, block_table.shape[0]) if max_q is None else int(max_q)
+    max_q = _default_max_q(total_q, block_table.shape[0]) if max_q is None else min(int(max_q), _INT32_MAX)
     guard = _guard(dev, stream)
     if guard is not None:
         guard.__enter__()
@@ -332,6 +332,13 @@ def _check_tables(name, first, kv_len, block_table, free_pages, free_count) -> i
     return dev
 
 
+def _page_size(page_size) -> int:
+    """As the C ABI's int32; the library checks the rest."""
+    if not 0 < page_size <= _INT32_MAX:
+        raise ValueError(f"page_size must be a positive 32-bit integer, got {page_size}")
+    return int(page_size)
+
+
 def _output(name: str, t: Optional[torch.Tensor], n: int, like: torch.Tensor) -> torch.Tensor:
     """An int32 output of n entries: `t` if it was given."""
     if t is None:
@@ -371,9 +378,9 @@ def attn_pages_plan(q_len: torch.Tensor, kv_len: torch.Tensor, block_table: torc
     included, whose slots and positions are -1. All int32 on the GPU. new_len and free_left are the
     next call's kv_len and free_count. free_left < 0: pages were missing."""
     dev = _check_tables("q_len", q_len, kv_len, block_table, free_pages, free_count)
-    if total_q < 0:
-        raise ValueError(f"total_q must not be negative, got {total_q}")
-    args = (dev, q_len, kv_len, block_table, free_pages, free_count, page_size, total_q, cu_q, new_len, slots, positions,
+    if not 0 <= total_q <= _INT32_MAX:
+        raise ValueError(f"total_q must be a 32-bit integer that is not negative, got {total_q}")
+    args = (dev, q_len, kv_len, block_table, free_pages, free_count, _page_size(page_size), total_q, cu_q, new_len, slots, positions,
             free_left)
     guard = _guard(dev, stream)
     if guard is None:
@@ -400,7 +407,7 @@ def attn_pages_release(done: torch.Tensor, kv_len: torch.Tensor, block_table: to
     free_count[0] on. Returns (new_len [B], free_left [1]): new_len is 0 for those sequences and kv_len
     for the others. All int32 on the GPU."""
     dev = _check_tables("done", done, kv_len, block_table, free_pages, free_count)
-    args = (dev, done, kv_len, block_table, free_pages, free_count, page_size, new_len, free_left)
+    args = (dev, done, kv_len, block_table, free_pages, free_count, _page_size(page_size), new_len, free_left)
     guard = _guard(dev, stream)
     if guard is None:
         return _release_call(*args)

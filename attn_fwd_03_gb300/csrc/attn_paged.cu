@@ -998,8 +998,10 @@ __global__ void __launch_bounds__(Shape<D, KERNEL>::kThreads, Shape<D, KERNEL>::
         __syncwarp();
     }
     tc_fence_before();
-    // No global memory is touched above: from here on the previous kernel must be complete.
+    // The next kernel may come once every CTA has its tensor memory, or it could take it and wait for this one.
+    __syncthreads();
     grid_dep_launch();
+    // No global memory is touched above: from here on the previous kernel must be complete.
     grid_dep_wait();
     locate<Kernel::kTiles, Kernel::kThreads>(p, bar);
     __syncthreads();
