@@ -165,6 +165,7 @@ def _pack_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, out, lse, scale,
 
 def paged_workspace_size(q, k_cache, v_cache, block_table, cu_q, kv_len, *, max_q: Optional[int] = None) -> int:
     """Bytes of workspace attn_paged needs for these shapes."""
+    _check_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, None, None)
     max_q = _default_max_q(q.shape[0], block_table.shape[0]) if max_q is None else min(int(max_q), _INT32_MAX)
     # out and lse are not read: q stands in for both
     return int(lib.attn_paged_workspace_size(
