@@ -227,8 +227,9 @@ def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
     if not (dtype in _TYPES and q.dim() == 3 and k_cache.dim() == 4 and block_table.dim() == 2 and q.stride()[2] == 1
             and k_cache.dtype is dtype and k_cache.shape[3] == q.shape[2] and k_cache.stride()[3] == 1
             and v_cache.dtype is dtype and v_cache.shape == k_cache.shape and v_cache.stride()[3] == 1
-            and _is_ints(block_table, block_table.shape) and _is_ints(cu_q, (block_table.shape[0] + 1,))
-            and _is_ints(kv_len, (block_table.shape[0],))
+            and block_table.dtype is _INT32 and block_table.is_contiguous()
+            and cu_q.dtype is _INT32 and cu_q.shape == (block_table.shape[0] + 1,) and cu_q.is_contiguous()
+            and kv_len.dtype is _INT32 and kv_len.shape == (block_table.shape[0],) and kv_len.is_contiguous()
             and (out is None or (out.dtype is dtype and out.shape == q.shape and out.stride()[2] == 1))
             and (lse is None or (lse.dtype is torch.float32 and lse.shape == (q.shape[1], q.shape[0]) and lse.is_contiguous()))):
         _check_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, out, lse)
@@ -293,7 +294,8 @@ def attn_pages_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_ca
             and v.dtype is dtype and v.shape == k.shape and v.stride()[2] == 1
             and k_cache.dtype is dtype and k_cache.shape[1] == k.shape[1] and k_cache.shape[3] == k.shape[2]
             and k_cache.stride()[3] == 1 and v_cache.dtype is dtype and v_cache.shape == k_cache.shape
-            and v_cache.stride()[3] == 1 and _is_ints(slots, (k.shape[0],))):
+            and v_cache.stride()[3] == 1
+            and slots.dtype is _INT32 and slots.shape == (k.shape[0],) and slots.is_contiguous()):
         _check_write(k, v, slots, k_cache, v_cache)
     dev = k.get_device()
     if not (dev >= 0 and v.get_device() == dev and slots.get_device() == dev and k_cache.get_device() == dev
@@ -317,19 +319,23 @@ def attn_pages_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_ca
 
 def _check_tables(name, first, kv_len, block_table, free_pages, free_count) -> int:
     """The checks that plan and release share; `first` has an entry per sequence. Returns the device."""
-    n, columns = first.numel(), block_table.shape[-1] if block_table.dim() else 0
-    if not (_is_ints(first, (n,)) and _is_ints(kv_len, (n,)) and _is_ints(block_table, (n, columns))
-            and _is_ints(free_pages, (free_pages.numel(),)) and _is_ints(free_count, (1,))):
+    shape, dev = first.shape, first.get_device()
+    if not (first.dtype is _INT32 and first.dim() == 1 and first.is_contiguous()
+            and kv_len.dtype is _INT32 and kv_len.shape == shape and kv_len.is_contiguous()
+            and block_table.dtype is _INT32 and block_table.dim() == 2 and block_table.shape[0] == shape[0]
+            and block_table.is_contiguous() and free_pages.dtype is _INT32 and free_pages.dim() == 1
+            and free_pages.is_contiguous() and free_count.dtype is _INT32 and free_count.shape == (1,)
+            and dev >= 0 and kv_len.get_device() == dev and block_table.get_device() == dev
+            and free_pages.get_device() == dev and free_count.get_device() == dev):
         _need_dims(name, first, 1)
         _need_dims("block_table", block_table, 2)
-        for what, t, shape in ((name, first, (n,)), ("kv_len", kv_len, (n,)), ("block_table", block_table, (n, columns)),
-                               ("free_pages", free_pages, (free_pages.numel(),)), ("free_count", free_count, (1,))):
-            if not _is_ints(t, shape):
-                _refuse(what, t, _INT32, shape)
-    dev = first.get_device()
-    if not (dev >= 0 and kv_len.get_device() == dev and block_table.get_device() == dev and free_pages.get_device() == dev
-            and free_count.get_device() == dev):
-        _refuse_devices(first, kv_len, block_table, free_pages, free_count)
+        n = shape[0]
+        for what, t, want in ((name, first, (n,)), ("kv_len", kv_len, (n,)), ("block_table", block_table, (n, block_table.shape[1])),
+                              ("free_pages", free_pages, (free_pages.numel(),)), ("free_count", free_count, (1,))):
+            if not _is_ints(t, want):
+                _refuse(what, t, _INT32, want)
+        if dev < 0 or any(t.get_device() != dev for t in (kv_len, block_table, free_pages, free_count)):
+            _refuse_devices(first, kv_len, block_table, free_pages, free_count)
     return dev
 
 
@@ -340,10 +346,8 @@ def _page_size(page_size) -> int:
     return int(page_size)
 
 
-def _output(name: str, t: Optional[torch.Tensor], n: int, like: torch.Tensor) -> torch.Tensor:
-    """An int32 output of n entries: `t` if it was given."""
-    if t is None:
-        return torch.empty(n, dtype=_INT32, device=like.device)
+def _given(name: str, t: torch.Tensor, n: int, like: torch.Tensor) -> torch.Tensor:
+    """Checks an output of n entries that the caller brought."""
     if not _is_ints(t, (n,)):
         _refuse(name, t, _INT32, (n,))
     if t.get_device() != like.get_device():
@@ -354,11 +358,13 @@ def _output(name: str, t: Optional[torch.Tensor], n: int, like: torch.Tensor) ->
 def _plan_call(dev, q_len, kv_len, block_table, free_pages, free_count, page_size, total_q, cu_q, new_len, slots, positions,
                free_left):
     n, columns = block_table.shape
-    cu_q = _output("cu_q", cu_q, n + 1, q_len)
-    new_len = _output("new_len", new_len, n, q_len)
-    slots = _output("slots", slots, total_q, q_len)
-    positions = _output("positions", positions, total_q, q_len)
-    free_left = _output("free_left", free_left, 1, q_len)
+    empty, where = torch.empty, q_len.device
+    cu_q = empty(n + 1, dtype=_INT32, device=where) if cu_q is None else _given("cu_q", cu_q, n + 1, q_len)
+    new_len = empty(n, dtype=_INT32, device=where) if new_len is None else _given("new_len", new_len, n, q_len)
+    slots = empty(total_q, dtype=_INT32, device=where) if slots is None else _given("slots", slots, total_q, q_len)
+    positions = (empty(total_q, dtype=_INT32, device=where) if positions is None
+                 else _given("positions", positions, total_q, q_len))
+    free_left = empty(1, dtype=_INT32, device=where) if free_left is None else _given("free_left", free_left, 1, q_len)
     _launch(lib.attn_pages_plan, dev, _PLAN.pack(
         n, total_q, page_size, columns, free_pages.numel(), 0, q_len.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(),
         block_table.stride()[0] if n > 1 else columns, free_pages.data_ptr(), free_count.data_ptr(), cu_q.data_ptr(),
@@ -381,19 +387,22 @@ def attn_pages_plan(q_len: torch.Tensor, kv_len: torch.Tensor, block_table: torc
     dev = _check_tables("q_len", q_len, kv_len, block_table, free_pages, free_count)
     if not 0 <= total_q <= _INT32_MAX:
         raise ValueError(f"total_q must be a 32-bit integer that is not negative, got {total_q}")
-    args = (dev, q_len, kv_len, block_table, free_pages, free_count, _page_size(page_size), total_q, cu_q, new_len, slots, positions,
-            free_left)
+    page_size = _page_size(page_size)
     guard = _guard(dev, stream)
     if guard is None:
-        return _plan_call(*args)
+        return _plan_call(dev, q_len, kv_len, block_table, free_pages, free_count, page_size, total_q, cu_q, new_len, slots,
+                          positions, free_left)
     with guard:
-        return _plan_call(*args)
+        return _plan_call(dev, q_len, kv_len, block_table, free_pages, free_count, page_size, total_q, cu_q, new_len, slots,
+                          positions, free_left)
 
 
 def _release_call(dev, done, kv_len, block_table, free_pages, free_count, page_size, new_len, free_left):
     n, columns = block_table.shape
-    new_len = _output("new_len", new_len, n, done)
-    free_left = _output("free_left", free_left, 1, done)
+    new_len = (torch.empty(n, dtype=_INT32, device=done.device) if new_len is None
+               else _given("new_len", new_len, n, done))
+    free_left = (torch.empty(1, dtype=_INT32, device=done.device) if free_left is None
+                 else _given("free_left", free_left, 1, done))
     _launch(lib.attn_pages_release, dev, _RELEASE.pack(
         n, page_size, columns, free_pages.numel(), done.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(),
         block_table.stride()[0] if n > 1 else columns, free_pages.data_ptr(), free_count.data_ptr(), new_len.data_ptr(),
@@ -408,9 +417,9 @@ def attn_pages_release(done: torch.Tensor, kv_len: torch.Tensor, block_table: to
     free_count[0] on. Returns (new_len [B], free_left [1]): new_len is 0 for those sequences and kv_len
     for the others. All int32 on the GPU."""
     dev = _check_tables("done", done, kv_len, block_table, free_pages, free_count)
-    args = (dev, done, kv_len, block_table, free_pages, free_count, _page_size(page_size), new_len, free_left)
+    page_size = _page_size(page_size)
     guard = _guard(dev, stream)
     if guard is None:
-        return _release_call(*args)
+        return _release_call(dev, done, kv_len, block_table, free_pages, free_count, page_size, new_len, free_left)
     with guard:
-        return _release_call(*args)
+        return _release_call(dev, done, kv_len, block_table, free_pages, free_count, page_size, new_len, free_left)
