@@ -51,10 +51,13 @@ attn_status_t check_16bit(int32_t dtype, int32_t d) {
     return ATTN_OK;
 }
 
+// Keys of a sequence: the kernels add up to a few tiles to such a number in 32 bits.
+constexpr int64_t kMaxLength = (int64_t)INT32_MAX - 1023;
+
 attn_status_t check_table(int32_t max_pages, int32_t page_size) {
     if (max_pages < 1) return report_error(ATTN_ERR_INVALID, "max_pages must be at least 1, got %d", max_pages);
-    if ((int64_t)max_pages * page_size > INT32_MAX)
-        return report_error(ATTN_ERR_UNSUPPORTED, "max_pages * page_size must stay below 2^31");
+    if ((int64_t)max_pages * page_size > kMaxLength)
+        return report_error(ATTN_ERR_UNSUPPORTED, "max_pages * page_size must not exceed 2^31 - 1024");
     return ATTN_OK;
 }
 

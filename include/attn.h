@@ -300,7 +300,7 @@ typedef struct attn_paged_params {
     int32_t max_q;           /* the most query rows a sequence is expected to bring, >= 1: chooses
                                 the tile shape. More rows than this are still right, only slower */
     int32_t num_pages, page_size;
-    int32_t max_pages;       /* columns of the block table, >= 1; max_pages * page_size < 2^31 */
+    int32_t max_pages;       /* columns of the block table, >= 1; max_pages * page_size <= 2^31 - 1024 */
     int32_t dtype;           /* ATTN_BF16 or ATTN_F16 (q, caches and o alike) */
     int32_t causal;          /* 0 or 1 */
     float scale;             /* > 0 */
@@ -370,7 +370,7 @@ typedef struct attn_pages_plan_params {
     int32_t num_seqs;
     int32_t total_q;         /* entries of slots and positions, >= the sum of q_len */
     int32_t page_size;
-    int32_t max_pages;       /* columns of the block table, >= 1; max_pages * page_size < 2^31 */
+    int32_t max_pages;       /* columns of the block table, >= 1; max_pages * page_size <= 2^31 - 1024 */
     int32_t free_capacity;   /* entries of free_pages */
     int32_t reserved0;       /* must be 0 */
     const int32_t *q_len, *kv_len;   /* [num_seqs] */
@@ -395,7 +395,7 @@ ATTN_API attn_status_t attn_pages_plan(const attn_pages_plan_params *p, void *st
 typedef struct attn_pages_release_params {
     int32_t num_seqs;
     int32_t page_size;
-    int32_t max_pages;       /* columns of the block table, >= 1; max_pages * page_size < 2^31 */
+    int32_t max_pages;       /* columns of the block table, >= 1; max_pages * page_size <= 2^31 - 1024 */
     int32_t free_capacity;   /* entries of free_pages */
     const int32_t *done, *kv_len;    /* [num_seqs] */
     const int32_t *block_table;      /* [num_seqs, max_pages] */

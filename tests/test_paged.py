@@ -366,6 +366,26 @@ def test_captured_call_follows_the_lengths(A):
         c.check(out, lse, True)
 
 
+def test_longest_table(A):
+    # as many keys as a table may have: four pages named over and over. Softmax weights are the pages'
+    # multiplicities times exp(s). O's accumulator takes 8 products of 16 keys a tile, each rounded or
+    # cut to 2^-23 of it (v > 0, so it only grows), l two additions of 2^-24; P and O round to bf16.
+    page, cols, d = 1024, 2 ** 21 - 1, 64
+    g = torch.Generator().manual_seed(150)
+    k, q = (torch.randn(shape, generator=g).bfloat16() for shape in ((4, 1, page, d), (1, 1, d)))
+    v = (1 + torch.rand((4, 1, page, d), generator=g)).bfloat16()
+    table = torch.arange(cols, dtype=torch.int32, device="cuda").view(1, -1) % 4
+    o, lse = A.attn_paged(q.cuda(), k.cuda(), v.cuda(), table, *(torch.tensor(x, dtype=torch.int32, device="cuda")
+                                                                 for x in ([0, 1], [cols * page])), causal=True, max_q=1)
+    _ok(A)
+    w = np.exp(to64(k)[:, 0] @ to64(q)[0, 0] / math.sqrt(d)) * np.bincount(np.arange(cols) % 4)[:, None]
+    want = np.einsum("ps,psd->d", w, to64(v)[:, 0]) / w.sum()
+    tiles = cols * page / 128 / torch.cuda.get_device_properties(0).multi_processor_count + 1  # of a CTA, at most
+    of_l = tiles * 2 * 2.0 ** -24 + 2.0 ** -20  # and the merge
+    assert np.abs(to64(o)[0, 0] / want - 1).max() <= tiles * 8 * 2.0 ** -23 + of_l + 2 * 2.0 ** -8
+    assert abs(float(lse[0, 0]) - math.log(w.sum())) <= of_l + 32 * 2.0 ** -24
+
+
 @pytest.mark.parametrize("n", [1, 200])
 def test_bad_lengths_and_pages_are_reported(A, n):
     # a page out of range, a length that the table cannot hold: no access follows them, attn_status

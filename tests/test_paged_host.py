@@ -141,6 +141,8 @@ def _paged(A, **kw):
     (dict(page_size=48), "ATTN_ERR_UNSUPPORTED"),
     (dict(max_pages=0), "ATTN_ERR_INVALID"),
     (dict(max_pages=1 << 27), "ATTN_ERR_UNSUPPORTED"),
+    (dict(max_pages=(1 << 27) - 1), "ATTN_ERR_UNSUPPORTED"),
+    (dict(page_size=512, max_pages=(1 << 22) - 1), "ATTN_ERR_UNSUPPORTED"),
     (dict(num_pages=0), "ATTN_ERR_INVALID"),
     (dict(num_pages=1 << 27), "ATTN_ERR_UNSUPPORTED"),
     (dict(table_stride=-1), "ATTN_ERR_INVALID"),
