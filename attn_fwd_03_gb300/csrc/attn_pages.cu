@@ -111,10 +111,8 @@ __global__ void __launch_bounds__(kScan) pages_plan_kernel(const PlanArgs a) {
                 } else {
                     const long long k = count - 1 - (s_page[i] + col - had);
                     if (k >= 0) {
-                        if (k < p.free_capacity)
-                            page = p.free_pages[k];
-                        else
-                            bad = true;
+                        if (k < p.free_capacity) page = max(p.free_pages[k], -1);
+                        bad |= page < 0;
                     }
                     if ((pos & mask) == 0) *entry = page;  // the token that opens the page
                 }

@@ -362,7 +362,8 @@ ATTN_API attn_status_t attn_pages_write(const attn_pages_write_params *p, void *
  * call again gives the same answer; a step is taken by using new_len and
  * free_left as the next kv_len and free_count.
  * When the stack runs out free_left is negative by the pages that were missing,
- * and the table entries and slots that got none are -1. Such a step is not taken:
+ * and the table entries and slots that got none are -1 (a page below 0 on the stack
+ * gives -1 too, and is reported). Such a step is not taken:
  * kv_len and free_count stay as they were, and it is planned again once pages
  * were released (by lengths before the step) or with fewer sequences.
  */

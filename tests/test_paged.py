@@ -512,6 +512,16 @@ def test_plan_reports_lengths_out_of_range(A):
         assert A.attn_status() == A.ATTN_ERR_INVALID
 
 
+def test_plan_reports_pages_below_zero_on_the_stack(A):
+    # as a release of a sequence that was never given all its pages leaves them
+    table = _i32([[-1, -1], [-1, -1]])
+    cu, new, slots, pos, left = A.attn_pages_plan(_i32([17, 2]), _i32([0, 0]), table, _i32([5, -1, 7]), _i32([3]), 16, 19)
+    torch.cuda.synchronize()
+    assert A.attn_status() == A.ATTN_ERR_INVALID and A.attn_status() == A.ATTN_OK
+    assert slots.tolist() == list(range(7 * 16, 8 * 16)) + [-1] + [80, 81] and left.tolist() == [0]
+    assert table.tolist() == [[7, -1], [5, -1]]
+
+
 def test_tables_into_given_tensors_on_another_stream(A):
     side = torch.cuda.Stream()
     lens, table, free, count = _i32([5, 16]), _i32([[3, -1], [2, -1]]), _i32([0, 1, 4, 0]), _i32([3])
