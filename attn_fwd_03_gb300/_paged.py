@@ -149,6 +149,10 @@ def _default_max_q(total_q: int, num_seqs: int) -> int:
     return max(1, total_q - num_seqs + 1)
 
 
+def _as_int32(x) -> int:
+    return min(max(int(x), -_INT32_MAX), _INT32_MAX)
+
+
 def _pack_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, out, lse, scale, causal, max_q, workspace, nbytes) -> bytes:
     total_q, hq, d = q.shape
     num_seqs, columns = block_table.shape
@@ -166,7 +170,7 @@ def _pack_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, out, lse, scale,
 def paged_workspace_size(q, k_cache, v_cache, block_table, cu_q, kv_len, *, max_q: Optional[int] = None) -> int:
     """Bytes of workspace attn_paged needs for these shapes."""
     _check_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, None, None)
-    max_q = _default_max_q(q.shape[0], block_table.shape[0]) if max_q is None else min(int(max_q), _INT32_MAX)
+    max_q = _default_max_q(q.shape[0], block_table.shape[0]) if max_q is None else _as_int32(max_q)
     # out and lse are not read: q stands in for both
     return int(lib.attn_paged_workspace_size(
         _pack_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, q, q, 1.0, False, max_q, 0, 0)))
@@ -241,7 +245,7 @@ def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
     total_q, hq, d = q.shape
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    max_q = _default_max_q(total_q, block_table.shape[0]) if max_q is None else min(int(max_q), _INT32_MAX)
+    max_q = _default_max_q(total_q, block_table.shape[0]) if max_q is None else _as_int32(max_q)
     guard = _guard(dev, stream)
     if guard is not None:
         guard.__enter__()

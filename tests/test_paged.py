@@ -116,6 +116,14 @@ def test_max_q_is_only_a_hint(A, max_q, d):
     c.check(o, lse, True)
 
 
+@pytest.mark.parametrize("max_q", [0, -1, -2 ** 40])
+def test_max_q_below_one_is_refused(A, max_q):
+    args = Case([1], [5], 1, 1, 64, 16, torch.bfloat16, 51).device()
+    with pytest.raises(A.AttnError, match="max_q must be at least 1"):
+        A.attn_paged(*args, max_q=max_q)
+    assert A.paged_workspace_size(*args, max_q=max_q) == 0
+
+
 @pytest.mark.parametrize("n", [1, 60])
 def test_heads_first_pages_and_strided_rows(A, n):
     # pages hold [heads, slots, d]; q is part of a wider row, O is written into one
