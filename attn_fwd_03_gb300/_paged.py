@@ -176,7 +176,8 @@ def paged_workspace_size(q, k_cache, v_cache, block_table, cu_q, kv_len, *, max_
         _pack_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, q, q, 1.0, False, max_q, 0, 0)))
 
 
-# (device, d, heads, key/value heads, max_q) -> bytes; all that the size depends on
+# (device, d, heads, key/value heads, max_q) -> bytes; all that the size depends on. No head group fits more
+# than 128 rows in one tile, so it is the same for every max_q beyond, and the table stays small.
 _workspace_bytes: Dict[tuple, int] = {}
 # device -> workspace of calls on its default stream, which are in order and cannot be captured. An
 # allocation costs a decode call about a third of its host time. Calls on other streams allocate: a
@@ -256,7 +257,7 @@ def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
         if lse is None:
             lse = torch.empty((hq, total_q), dtype=torch.float32, device=where)
         if workspace is None:
-            key = (dev, d, hq, k_cache.shape[1], max_q)
+            key = (dev, d, hq, k_cache.shape[1], max_q if max_q < 129 else 129)
             nbytes = _workspace_bytes.get(key)
             if nbytes is None:
                 nbytes = paged_workspace_size(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q=max_q)

@@ -179,6 +179,13 @@ def test_workspace_of_the_callers(A):
         A.attn_paged(*args, causal=True, workspace=torch.empty(need, dtype=torch.uint8))
 
 
+def test_workspace_size_goes_by_max_q_up_to_a_tile(A):
+    for group, d in ((1, 64), (3, 128), (128, 64)):
+        args = Case([1], [5], 2, group, d, 16, torch.bfloat16, 52).device()
+        sizes = [A.paged_workspace_size(*args, max_q=m) for m in (129, 130, 5000, 2 ** 31 - 1)]
+        assert sizes[0] > 0 and len(set(sizes)) == 1
+
+
 def test_keys_and_values_interleaved_in_one_tensor(A):
     c = Case([1, 2], [70, 100], 3, 2, 128, 16, torch.float16, 65)
     q, k, v, table, cu, kv = c.device()
