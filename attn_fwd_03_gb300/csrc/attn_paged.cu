@@ -51,7 +51,12 @@
 // tokens and more (3 % slower); O transposed between lanes into whole 128-byte
 // lines (as slow as the 32 rows a store touches without); the P V product begun on the
 // first half of P (3 % slower: the issuer waits for one tile's second half while the
-// other tile could go on).
+// other tile could go on); the part of a unit that an earlier CTA starts taken last, so
+// that the CTAs sweep the keys in step (a 4096-row chunk over 32768 keys 1.26 ms, 1.30
+// without, but its longer walk costs short units up to 12 %: 512 sequences of 128 keys
+// 69 us, 62 without; limited to two-tile units 1.29 ms, a mixed step 72 us, 70 without);
+// the next part's first page looked up before a part's last copies (no faster, 512
+// sequences of 128 keys 65 us).
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -1023,6 +1028,7 @@ __global__ void __launch_bounds__(Shape<D, KERNEL>::kThreads, Shape<D, KERNEL>::
 struct CombineArgs {
     float* part;
     const int4* meta;
+    int ctas;
     int tiles, rows;     // tiles of a slot, rows of a tile
     int tok_tile, G, T;
     uint8_t* o;
@@ -1032,104 +1038,157 @@ struct CombineArgs {
 
 constexpr int kCombineThreads = 256;
 
-// Blocks (e, y) merge the unit whose last part CTA e wrote, if there is one: its first part is in slot 1
-// of the nearest CTA before e that has one, the parts between in the slots 0. A thread takes 16 columns of
-// a row, threads side by side the rows; the parts are merged as tiles are, in the order of the keys.
-template <int D, bool F16>
+// Merges the units that were cut. The CTA that wrote a unit's last part names the unit: its first part is in
+// slot 1 of the nearest CTA before that one that has one, the parts between in the slots 0. A thread takes 16
+// columns of a row, threads side by side the rows; the parts are merged as tiles are, in the order of the
+// keys.
+// How many units there are and how large is known here only. With SHARE every block counts the work (in
+// blocks' worth of threads, by the units in order) and takes its shares of it; without, block (e, y) takes the
+// y-th share of the unit that CTA e ended, if there is one. SHARE is for units that may have more than 4
+// shares (two tiles at d = 128 have 8), where most blocks would find nothing to do: a step of 16 decoding
+// sequences and a 512-row chunk takes 70.1 us without SHARE and 67.8 with it, 16 chunks of 40 rows 44.2 and
+// 41.4. With up to 4, blocks that know their unit start sooner: one token takes 10.5 us and 11.3 with SHARE,
+// at d = 64 16 chunks of 40 rows 28.6 and 30.2, 8 chunks of 448 rows 39.6 and 40.0.
+template <int D, bool F16, bool SHARE>
 __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const CombineArgs a) {
+    constexpr int kGroups = D / 16, kWarps = kCombineThreads / 32;
     grid_dep_launch();
     grid_dep_wait();
-    const int e = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int4 unit = a.meta[e * 2];
-    // bit c of has[0] / has[1]: CTA c's slot 0 / 1 holds a part (c <= e)
-    extern __shared__ unsigned s_mem[];
-    const int words = (gridDim.x + 31) / 32;
-    unsigned *has0 = s_mem, *has1 = s_mem + words;
-    int* slots = reinterpret_cast<int*>(s_mem + 2 * words);  // the unit's, in the order of the keys
-    // read before it is known whether this block has work, so that the reads overlap
-    for (int w = warp; w < words; w += kCombineThreads / 32) {
-        const int c = w * 32 + lane;
-        const unsigned m0 = __ballot_sync(kFull, c <= e && a.meta[min(c, e) * 2].x != kNone);
-        const unsigned m1 = __ballot_sync(kFull, c < e && a.meta[min(c, e) * 2 + 1].x != kNone);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int ctas = SHARE ? a.ctas : blockIdx.x + 1;  // that the block looks at
+    const int words = (ctas + 31) / 32;
+    extern __shared__ int4 s_units[];  // slot 0 of every CTA
+    // bit c of has0 / has1: CTA c's slot 0 / 1 holds a part
+    unsigned* has0 = reinterpret_cast<unsigned*>(s_units + 32 * words);
+    unsigned* has1 = has0 + words;
+    int* sums = reinterpret_cast<int*>(has1 + words);  // shares of 32 CTAs' units
+    int* ends = sums + words;                          // of the CTAs of a word up to this one
+    int4 own = make_int4(kNone, 0, 0, 0);
+    if (!SHARE) own = a.meta[(ctas - 1) * 2];  // read along with the others
+    for (int w = warp; w < words; w += kWarps) {
+        const int c = w * 32 + lane, at = min(c, ctas - 1) * 2;
+        const int4 m = a.meta[at];
+        const int other = a.meta[at + 1].x;
+        const unsigned b0 = __ballot_sync(kFull, c < ctas && m.x != kNone);
+        const unsigned b1 = __ballot_sync(kFull, c < ctas && other != kNone);
         if (lane == 0) {
-            has0[w] = m0;
-            has1[w] = m1;
+            has0[w] = b0;
+            has1[w] = b1;
+        }
+        if (SHARE) {
+            int x = c < ctas && m.x == kLast ? (m.z * a.G * kGroups + kCombineThreads - 1) / kCombineThreads : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(kFull, x, o);
+                if (lane >= o) x += u;
+            }
+            s_units[c] = m;
+            ends[c] = x;
+            if (lane == 31) sums[w] = x;
         }
     }
-    if (unit.x != kLast) return;
+    if (!SHARE && own.x != kLast) return;
     __syncthreads();
-    int first = 0;
-    for (int w = 0; w < words; ++w)
-        if (has1[w]) first = w * 32 + 31 - __clz(has1[w]);
-    int parts = 1;  // the first, then every slot 0 behind it
-    for (int w = first / 32; w < words; ++w) {
-        const unsigned m = w == first / 32 ? has0[w] & ~(0xffffffffu >> (31 - (first & 31))) : has0[w];
-        if (w % (kCombineThreads / 32) == warp && (m >> lane & 1)) slots[parts + __popc(m & ((1u << lane) - 1))] = (w * 32 + lane) * 2;
-        parts += __popc(m);
-    }
-    if (tid == 0) slots[0] = first * 2 + 1;
-    __syncthreads();
-    const int i = blockIdx.y * kCombineThreads + tid;
-    const int r = i % a.rows, group = i / a.rows % (D / 16), t = i / a.rows / (D / 16);
-    const int tok = t * a.tok_tile + r / a.G;
-    if (t >= a.tiles || tok >= unit.z) return;
-    float M = -INFINITY, L = 0.f, Lo = 0.f, out[16];
-#pragma unroll
-    for (int c = 0; c < 16; ++c) out[c] = 0.f;
-    // One pass with a running maximum, four parts' loads in flight at a time. Entries behind the last part
-    // repeat it; their weight is 0.
-    for (int k0 = 0; k0 < parts; k0 += 4) {
-        float4 head[4], o[4][4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float4* rec = record(a.part, slots[min(k0 + q, parts - 1)], a.tiles, t, a.rows, D) + r;
-            head[q] = rec[0];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) o[q][c] = rec[(1 + group * 4 + c) * a.rows];
-            if (k0 + q >= parts) head[q].x = -INFINITY;
+    int total = SHARE ? 0 : 1;
+    if (SHARE)
+        for (int w = 0; w < words; ++w) total += sums[w];
+    for (int share = SHARE ? blockIdx.x : 0; share < total; share += gridDim.x) {
+        int e = ctas - 1, left = blockIdx.y;  // the unit that CTA e ended, which of its shares
+        int4 unit = own;
+        if (SHARE) {
+            int w = 0;
+            left = share;
+            while (left >= sums[w]) left -= sums[w++];
+            const int c = __ffs(__ballot_sync(kFull, ends[w * 32 + lane] > left)) - 1;
+            e = w * 32 + c;
+            if (c > 0) left -= ends[e - 1];
+            unit = s_units[e];
         }
-        const float m = fmaxf(fmaxf(M, fmaxf(head[0].x, head[1].x)), fmaxf(head[2].x, head[3].x));
-        const float was = M == -INFINITY ? 0.f : ex2(M - m);
-        M = m;
-        L *= was;
-        Lo *= was;
+        int word = e / 32;
+        unsigned before = has1[word] & ((1u << (e & 31)) - 1);
+        while (before == 0 && word > 0) before = has1[--word];
+        if (before == 0) continue;
+        const int bit = 31 - __clz(before);
+        int slot = (word * 32 + bit) * 2 + 1;  // of the part to come
+        unsigned behind = has0[word] & ~(0xffffffffu >> (31 - bit));  // the word's slots 0 after it
+        const int rows = unit.z * a.G, i = left * kCombineThreads + tid;
+        if (i >= rows * kGroups) continue;
+        const int group = i / rows, row_of = i % rows;
+        const int t = row_of / a.rows, r = row_of % a.rows;
+        const int tok = t * a.tok_tile + r / a.G;
+        float M = -INFINITY, L = 0.f, Lo = 0.f, out[16];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) out[c] *= was;
+        for (int c = 0; c < 16; ++c) out[c] = 0.f;
+        // One pass with a running maximum, four parts' loads in flight at a time. Entries behind the last part
+        // repeat it; their weight is 0.
+        bool more = true;
+        while (more) {
+            float4 head[4], o[4][4];
+            int from[4], parts = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if (head[q].x == -INFINITY) continue;  // no key of this row in the part: its o was not written
-            const float w = ex2(head[q].x - m);
-            L = fmaf(w, head[q].y, L);
-            Lo = fmaf(w, head[q].z, Lo);
+            for (int q = 0; q < 4; ++q) {
+                from[q] = slot;
+                if (!more) continue;
+                parts = q + 1;
+                more = slot != e * 2;
+                if (!more) continue;
+                while (behind == 0) behind = has0[++word];
+                slot = (word * 32 + __ffs(behind) - 1) * 2;
+                behind &= behind - 1;
+            }
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                out[4 * c] = fmaf(w, o[q][c].x, out[4 * c]);
-                out[4 * c + 1] = fmaf(w, o[q][c].y, out[4 * c + 1]);
-                out[4 * c + 2] = fmaf(w, o[q][c].z, out[4 * c + 2]);
-                out[4 * c + 3] = fmaf(w, o[q][c].w, out[4 * c + 3]);
+            for (int q = 0; q < 4; ++q) {
+                const float4* rec = record(a.part, from[q], a.tiles, t, a.rows, D) + r;
+                head[q] = rec[0];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[q][c] = rec[(1 + group * 4 + c) * a.rows];
+            }
+#pragma unroll
+            for (int q = 1; q < 4; ++q)
+                if (q >= parts) head[q].x = -INFINITY;
+            const float m = fmaxf(fmaxf(M, fmaxf(head[0].x, head[1].x)), fmaxf(head[2].x, head[3].x));
+            const float was = M == -INFINITY ? 0.f : ex2(M - m);
+            M = m;
+            L *= was;
+            Lo *= was;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) out[c] *= was;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (head[q].x == -INFINITY) continue;  // no key of this row in the part: its o was not written
+                const float f = ex2(head[q].x - m);
+                L = fmaf(f, head[q].y, L);
+                Lo = fmaf(f, head[q].z, Lo);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    out[4 * c] = fmaf(f, o[q][c].x, out[4 * c]);
+                    out[4 * c + 1] = fmaf(f, o[q][c].y, out[4 * c + 1]);
+                    out[4 * c + 2] = fmaf(f, o[q][c].z, out[4 * c + 2]);
+                    out[4 * c + 3] = fmaf(f, o[q][c].w, out[4 * c + 3]);
+                }
             }
         }
-    }
-    const float inv = Lo > 0.f ? 1.f / Lo : 0.f;
-    const long long row = unit.y + tok, head = unit.w * a.G + r % a.G;
-    uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.o) + row * a.o_sr + head * a.o_sh + group * 16);
+        const float inv = Lo > 0.f ? 1.f / Lo : 0.f;
+        const long long row = unit.y + tok, head = unit.w * a.G + r % a.G;
+        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.o) + row * a.o_sr + head * a.o_sh + group * 16);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        uint4 v;
-        v.x = pack_h16<F16>(out[8 * q + 0] * inv, out[8 * q + 1] * inv);
-        v.y = pack_h16<F16>(out[8 * q + 2] * inv, out[8 * q + 3] * inv);
-        v.z = pack_h16<F16>(out[8 * q + 4] * inv, out[8 * q + 5] * inv);
-        v.w = pack_h16<F16>(out[8 * q + 6] * inv, out[8 * q + 7] * inv);
-        dst[q] = v;
+        for (int q = 0; q < 2; ++q) {
+            uint4 v;
+            v.x = pack_h16<F16>(out[8 * q + 0] * inv, out[8 * q + 1] * inv);
+            v.y = pack_h16<F16>(out[8 * q + 2] * inv, out[8 * q + 3] * inv);
+            v.z = pack_h16<F16>(out[8 * q + 4] * inv, out[8 * q + 5] * inv);
+            v.w = pack_h16<F16>(out[8 * q + 6] * inv, out[8 * q + 7] * inv);
+            dst[q] = v;
+        }
+        if (group == 0) a.lse[head * a.T + row] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
     }
-    if (group == 0) a.lse[head * a.T + row] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
 }
 
 // ---------------------------------------------------------------- host side
 // The tile shape of a call. One tile per unit while the rows that a sequence is expected to bring fit
 // it, so that decode does not carry an empty second tile; two beyond.
 struct Plan {
-    int kernel, tiles, tok_tile, rows, ctas;
+    int kernel, tiles, tok_tile, rows, ctas, num_sms;
     size_t meta_bytes, bytes;
 };
 
@@ -1137,6 +1196,7 @@ Plan plan_of(const attn_paged_params& p, int num_sms) {
     const int G = p.num_q_heads / p.num_kv_heads;
     Plan pl;
     pl.tiles = (long long)p.max_q * G > BM ? 2 : 1;
+    pl.num_sms = num_sms;
     pl.tok_tile = BM / G;
     if (pl.tiles == 1 && p.max_q < pl.tok_tile) pl.tok_tile = p.max_q;
     pl.rows = pl.tok_tile * G;
@@ -1195,6 +1255,7 @@ cudaError_t launch_both(const CUtensorMap (&maps)[3], const PagedDev& p, const P
     CombineArgs a{};
     a.part = p.part;
     a.meta = p.meta;
+    a.ctas = grid;
     a.tiles = pl.tiles;
     a.rows = pl.rows;
     a.tok_tile = p.tok_tile;
@@ -1204,8 +1265,13 @@ cudaError_t launch_both(const CUtensorMap (&maps)[3], const PagedDev& p, const P
     a.lse = p.lse;
     a.o_sr = p.o_sr;
     a.o_sh = p.o_sh;
-    const int chunks = (pl.tiles * pl.rows * (D / 16) + kCombineThreads - 1) / kCombineThreads;
-    return launch_pdl(paged_combine_kernel<D, F16>, dim3(grid, chunks), dim3(kCombineThreads), (2 * ((grid + 31) / 32) + grid) * sizeof(int), s, a);
+    const int words = (grid + 31) / 32, most = (pl.tiles * pl.rows * (D / 16) + kCombineThreads - 1) / kCombineThreads;
+    const size_t smem = 32 * words * sizeof(int4) + 35 * words * sizeof(int);
+    if constexpr (D == 128)
+        if (most > 4)
+            return launch_pdl(paged_combine_kernel<D, F16, true>, dim3(min(grid * most, 2 * pl.num_sms)), dim3(kCombineThreads),
+                              smem, s, a);
+    return launch_pdl(paged_combine_kernel<D, F16, false>, dim3(grid, most), dim3(kCombineThreads), smem, s, a);
 }
 
 }  // namespace
