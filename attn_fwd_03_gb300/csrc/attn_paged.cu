@@ -437,6 +437,15 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
         if (globaltimer() - t0 > timeout_ns) break;
 }
 
+// Which of four barriers have completed the given phases, for a whole converged warp. Looking at a barrier
+// takes some 130 cycles; one after another, ready or not, the issuers' waits made up half of a key tile's time
+// at d = 64 and in one-tile units.
+__device__ __forceinline__ unsigned look(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c, uint32_t pc,
+                                         uint64_t* d, uint32_t pd) {
+    const unsigned ra = mbar_test(a, pa), rb = mbar_test(b, pb), rc = mbar_test(c, pc), rd = mbar_test(d, pd);
+    return __reduce_and_sync(kFull, ra | rb << 1 | rc << 2 | rd << 3);
+}
+
 // One store of 32 bytes (sm_100 on): the epilogue's threads hold a row each, and every store instruction
 // touches 32 rows whatever its width (eight prompts of 1024 tokens 86 us, 90 with 16-byte stores).
 __device__ __forceinline__ void store32(void* dst, const uint32_t* v) {
@@ -641,12 +650,15 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 for (int j = 0; j <= w.cnt_max && ok; ++j) {
                     const uint32_t itK = it;  // ring slot of K_j; V_j follows it
                     const uint32_t sK = itK % C::kStages, sV_prev = (itK + C::kStages - 1) % C::kStages;
+                    const uint32_t k_phase = (itK / C::kStages) & 1, v_phase = ((itK - 1) / C::kStages) & 1;
+                    const unsigned ready = look(&bar.kv_full[sK], k_phase, &bar.s_free[t], (n_s - 1) & 1, &bar.kv_full[sV_prev],
+                                                v_phase, &bar.p_full[t], n_p & 1);
                     if (j < w.cnt_max) {
-                        ok = mbar_wait_warp(&bar.kv_full[sK], (itK / C::kStages) & 1, wc);
+                        ok = (ready & 1) || mbar_wait_warp(&bar.kv_full[sK], k_phase, wc);
                         if (!ok) break;
                         if (j < cnt) {
                             if (n_s > 0) {
-                                ok = mbar_wait_warp(&bar.s_free[t], (n_s - 1) & 1, wc);
+                                ok = (ready & 2) || mbar_wait_warp(&bar.s_free[t], (n_s - 1) & 1, wc);
                                 if (!ok) break;
                             }
                             tc_fence_after();
@@ -667,10 +679,10 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                         __syncwarp();
                     }
                     if (j > 0) {  // V_{j-1} lives in the slot before K_j
-                        ok = mbar_wait_warp(&bar.kv_full[sV_prev], ((itK - 1) / C::kStages) & 1, wc);
+                        ok = (ready & 4) || mbar_wait_warp(&bar.kv_full[sV_prev], v_phase, wc);
                         if (!ok) break;
                         if (j <= cnt) {
-                            ok = mbar_wait_warp(&bar.p_full[t], n_p & 1, wc);
+                            ok = (ready & 8) || mbar_wait_warp(&bar.p_full[t], n_p & 1, wc);
                             if (!ok) break;
                             ++n_p;
                             tc_fence_after();
@@ -743,18 +755,21 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                     __syncwarp();
                     it += 2;
                     sK = it % C::kStages;
+                    const uint32_t k_phase = (it / C::kStages) & 1, v_phase = (itV / C::kStages) & 1;
+                    const unsigned ready = look(&bar.kv_full[sK], k_phase, &bar.kv_full[sV], v_phase, &bar.p_full[0], pcnt0 & 1,
+                                                &bar.p_full[NT - 1], pcnt1 & 1);
                     if (j < w.cnt_max) {
-                        ok = mbar_wait_warp(&bar.kv_full[sK], (it / C::kStages) & 1, wc);
+                        ok = (ready & 1) || mbar_wait_warp(&bar.kv_full[sK], k_phase, wc);
                         if (!ok) break;
                     }
-                    ok = mbar_wait_warp(&bar.kv_full[sV], (itV / C::kStages) & 1, wc);
+                    ok = (ready & 2) || mbar_wait_warp(&bar.kv_full[sV], v_phase, wc);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         if (!ok || j > w.cnt(t)) continue;
                         uint32_t& pcnt = t == 0 ? pcnt0 : pcnt1;
-                        ok = mbar_wait_warp(&bar.p_full[t], pcnt & 1, wc);
+                        ok = (ready & (t == 0 ? 4 : 8)) || mbar_wait_warp(&bar.p_full[t], pcnt & 1, wc);
                         if (!ok) continue;
                         ++pcnt;
                         tc_fence_after();
@@ -804,8 +819,9 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 const int lim = p.causal ? min(w.len, w.base + my_tok + 1) : w.len;
                 const int lim_first = p.causal ? min(w.len, w.base + t * p.tok_tile + 1) : w.len;
                 float m_ref = -INFINITY, m_row = -INFINITY, l = 0.f;
+                bool s_ready = false;
                 for (int j = 0; j < cnt; ++j) {
-                    ok = mbar_wait(&bar.s_full[t], scnt & 1, wc);
+                    ok = s_ready || mbar_wait(&bar.s_full[t], scnt & 1, wc);
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
                     ++scnt;
@@ -867,8 +883,12 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                     const float2 cc2 = make_float2(p.c, p.c), nm2 = make_float2(neg_m, neg_m);
                     float2 suma = make_float2(0.f, 0.f), sumb = make_float2(0.f, 0.f);
                     if (C::kSplit) {
+                        // Looking at a barrier takes some 130 cycles. The product of tile j-1 has mostly ended by
+                        // now, and S_{j+1} before this tile does: both are looked at early, beside other work.
+                        bool o_ready = false;
 #pragma unroll
                         for (int i = 0; i < BN / 2; ++i) {
+                            if (i == BN / 2 - 16 && j > 0) o_ready = mbar_test(&bar.pv_done[t], ocnt & 1);
                             const float2 x = ffma2(make_float2(__uint_as_float(su[2 * i]), __uint_as_float(su[2 * i + 1])),
                                                    cc2, nm2);
                             const float2 pp = make_float2(ex2(x.x), ex2(x.y));
@@ -879,7 +899,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                             su[i] = pack_h16<F16>(pp.x, pp.y);
                         }
                         if (j > 0) {  // the product of tile j-1 has read P_t and written O_t
-                            ok = mbar_wait(&bar.pv_done[t], ocnt & 1, wc);
+                            ok = o_ready || mbar_wait(&bar.pv_done[t], ocnt & 1, wc);
                             ok = __all_sync(kFull, ok);
                             if (!ok) break;
                             ++ocnt;
@@ -888,6 +908,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                         }
                         tmem_st32_at<0>(tP + 0, su);
                         tmem_st32_at<32>(tP + 32, su);
+                        s_ready = j + 1 < cnt && mbar_test(&bar.s_full[t], scnt & 1);
                     } else {
 #pragma unroll
                         for (int c0 = 0; c0 < BN; c0 += 32) {
