@@ -670,12 +670,13 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                                     mma_ss(tS, kmajor_step(qd, kk, q_half), kmajor_step(kd, kk, BN * 128), kIdescS,
                                            kk > 0 ? 1u : 0u);
                                 mma_commit(&bar.s_full[t]);
+                                mma_commit(&bar.kv_empty[sK]);
                                 if (j == cnt - 1) mma_commit(&bar.q_empty[q_i]);  // last read of Q_t
                             }
-                            __syncwarp();
                             ++n_s;
+                        } else if (elect_one()) {
+                            mma_commit(&bar.kv_empty[sK]);
                         }
-                        if (elect_one()) mma_commit(&bar.kv_empty[sK]);
                         __syncwarp();
                     }
                     if (j > 0) {  // V_{j-1} lives in the slot before K_j
@@ -693,10 +694,11 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                                 for (int kk = 0; kk < BN / 16; ++kk)
                                     mma_ts(tO, tP + kk * 8, vmajor_step(vd, kk), kIdescO, (j > 1 || kk > 0) ? 1u : 0u);
                                 mma_commit(&bar.pv_done[t]);
+                                mma_commit(&bar.kv_empty[sV_prev]);
                             }
-                            __syncwarp();
+                        } else if (elect_one()) {
+                            mma_commit(&bar.kv_empty[sV_prev]);
                         }
-                        if (elect_one()) mma_commit(&bar.kv_empty[sV_prev]);
                         __syncwarp();
                     }
                     if (j < w.cnt_max) it += 2;
@@ -756,8 +758,9 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                     it += 2;
                     sK = it % C::kStages;
                     const uint32_t k_phase = (it / C::kStages) & 1, v_phase = (itV / C::kStages) & 1;
-                    const unsigned ready = look(&bar.kv_full[sK], k_phase, &bar.kv_full[sV], v_phase, &bar.p_full[0], pcnt0 & 1,
-                                                &bar.p_full[NT - 1], pcnt1 & 1);
+                    const unsigned ready = NT == 1 ? 0  // one tile waits for P in any case
+                                                   : look(&bar.kv_full[sK], k_phase, &bar.kv_full[sV], v_phase,
+                                                          &bar.p_full[0], pcnt0 & 1, &bar.p_full[NT - 1], pcnt1 & 1);
                     if (j < w.cnt_max) {
                         ok = (ready & 1) || mbar_wait_warp(&bar.kv_full[sK], k_phase, wc);
                         if (!ok) break;
