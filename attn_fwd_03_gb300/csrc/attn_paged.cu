@@ -15,8 +15,8 @@
 // HBM (a ragged batch of 64 sequences of 4096-8192 keys, 32 query and 8 key/value
 // heads, d = 128: 245 us, 6.6 TB/s, 98 % of the measured copy rate; 96 % with
 // 16-token pages); long chunks are bound by the tensor pipe and the softmax beside
-// it (4096 rows over 32768 keys: 1.30 ms, 1585 TFLOP/s, 85 % of the measured GEMM
-// rate); small calls by latency (one token over 517 keys: 10.4 us for both
+// it (4096 rows over 32768 keys: 1.27 ms, 1620 TFLOP/s, 87 % of the measured GEMM
+// rate); small calls by latency (one token over 517 keys: 10.3 us for both
 // launches, of which locating the work takes 1.4, the first copies 2, the merge 3).
 //
 // Work split: lengths are known on the device only, and ragged, so units are not
@@ -52,11 +52,11 @@
 // lines (as slow as the 32 rows a store touches without); the P V product begun on the
 // first half of P (3 % slower: the issuer waits for one tile's second half while the
 // other tile could go on); the part of a unit that an earlier CTA starts taken last, so
-// that the CTAs sweep the keys in step (a 4096-row chunk over 32768 keys 1.26 ms, 1.30
-// without, but its longer walk costs short units up to 12 %: 512 sequences of 128 keys
-// 69 us, 62 without; limited to two-tile units 1.29 ms, a mixed step 72 us, 70 without);
-// the next part's first page looked up before a part's last copies (no faster, 512
-// sequences of 128 keys 65 us).
+// that the CTAs sweep the keys in step (3 % on a 4096-row chunk over 32768 keys, but its
+// longer walk costs short units up to 12 %: 512 sequences of 128 keys 69 us, 62 without;
+// limited to two-tile units 2 %, and 3 % lost on a mixed step); the next part's first page
+// looked up before a part's last copies (512 sequences of 128 keys 65 us, 62 without).
+// Exponentials are not a bound: with 7 in 8 of them left out everything takes 92-101 %.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -74,14 +74,14 @@ using namespace ptx;
 constexpr int BM = 128;  // query rows per tile
 constexpr int BN = 128;  // keys per tile
 constexpr float kRescaleThreshold = 8.0f;
-// What a unit costs beyond its key tiles, in keys: with 64 a prompt of 8192 tokens takes 410 us, with 384 it
-// takes 382, and the verification of 5 drafted tokens of 16 sequences 19.7 and 18.6.
+// What a unit costs beyond its key tiles, in keys: with 64 a prompt of 8192 tokens takes 400 us, with 384 it
+// takes 369, and the verification of 5 drafted tokens of 16 sequences 19.3 and 18.0.
 constexpr int kUnitCost = 384;
-// A key tile of a two-tile unit against one of a one-tile unit: 1.9 us against 1.3 in a step of 16 decoding
-// sequences and a 512-row chunk (70 us; 1.2 gives 74, 2.0 73).
+// A key tile of a two-tile unit against one of a one-tile unit: a step of 16 decoding sequences and a
+// 512-row chunk takes 68 us; 1.2 gives 72, 2.0 70.
 constexpr float kPairCost = 1.5f;
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kIssueUnroll = 4;  // k-steps of a product in a row: 2 and 8 are within 1 %, 1 is 11 % slower
+constexpr int kIssueUnroll = 4;  // k-steps of a product in a row: 2 and 8 are within 2 %, 1 is 13 % slower
 
 // The kernels: kFew and kOne for batches whose sequences all fit one tile, kMixed for those with longer
 // chunks (there each CTA works either on one-tile or on two-tile units). With one unit in hand a CTA waits
@@ -89,8 +89,8 @@ constexpr int kIssueUnroll = 4;  // k-steps of a product in a row: 2 and 8 are w
 // CTAs share an SM, with half of its shared and tensor memory each, where that is enough: at d = 64 (128
 // sequences of 1000 keys 50 us, 59 with one CTA; 64 of 4096 keys 86 and 90), and at d = 128 for up to
 // kFewRows rows if the block table has room for up to kFewKeys keys (kFew: 512 sequences of 128 keys take
-// 63 us, 100 with kOne, 2000 of 300 keys 119 and 126, 256 of 512 keys 87 and 86; longer ones stream better
-// with all of the SM's memory, 64 sequences of 8192 keys 245 us against 250).
+// 60 us, 100 with kOne, 2000 of 300 keys 117 and 129, 256 of 512 keys 85 and 85; longer ones stream better
+// with all of the SM's memory, 64 sequences of 8192 keys 239 us against 243).
 enum : int { kFew = 0, kOne = 1, kMixed = 2 };
 constexpr int kFewRows = 32, kFewKeys = 384;
 
@@ -447,7 +447,7 @@ __device__ __forceinline__ unsigned look(uint64_t* a, uint32_t pa, uint64_t* b, 
 }
 
 // One store of 32 bytes (sm_100 on): the epilogue's threads hold a row each, and every store instruction
-// touches 32 rows whatever its width (eight prompts of 1024 tokens 86 us, 90 with 16-byte stores).
+// touches 32 rows whatever its width (eight prompts of 1024 tokens 85 us, 89 with 16-byte stores).
 __device__ __forceinline__ void store32(void* dst, const uint32_t* v) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
                  "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
@@ -523,8 +523,8 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
         if (warp == C::kProducer || (C::kVProducer && warp == C::kFourth)) {
             // ------------------------------------------------ K and V producers
             // Small pages make many small copies, which one warp issues at about one in 90 cycles: K and V are
-            // issued by a warp each where there is one for V (64 sequences of 8192 keys in 16-token pages 282 us,
-            // 329 by one warp; in 64-token pages 252 by two, 245 by one).
+            // issued by a warp each where there is one for V (64 sequences of 8192 keys in 16-token pages 275 us,
+            // 335 by one warp; in 64-token pages 244 by two, 239 by one).
             const bool two = C::kVProducer && p.page_size < 64;
             const int first = C::kVProducer && warp == C::kFourth ? 1 : 0;  // 0: K, 1: V
             const int end = two || first == 1 ? first + 1 : 2;
