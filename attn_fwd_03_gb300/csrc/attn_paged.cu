@@ -121,7 +121,10 @@ struct Cfg {
     static constexpr int kTileBytes = BM * D * 2;
     // P in tensor-memory columns of its own, where there are enough
     static constexpr bool kSplit = D == 64 || (NT == 1 && KERNEL != kFew);
-    static constexpr int kIssuers = kSplit ? NT : 1;
+    // One issuer for both tiles where P lies over S: the tiles' products must not mix, or their softmaxes run at
+    // the same time and the tensor pipe waits for both (two issuers 20 % slower, two that take turns 2 %).
+    static constexpr bool kOneIssuer = !kSplit && NT == 2;
+    static constexpr int kIssuers = kOneIssuer ? 1 : NT;
     static constexpr int kQOff = 0;
     // Q tiles are loaded ahead of their unit: with one tile into as many slots as its rows leave room for, with
     // two into two more slots at d = 64 (at d = 128 a third Q tile is no faster than a fifth K or V tile)
@@ -626,10 +629,11 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 drain_wait(&bar.q_full[lane], parity ^ 1, p.timeout_ns);
             }
             __syncwarp();
-        } else if (C::kSplit && (warp == C::kIssuer || (!C::kVProducer && warp == C::kFourth))) {
+        } else if (!C::kOneIssuer && (warp == C::kIssuer || (NT == 2 && warp == C::kFourth))) {
             // ------------------------------------------------ MMA issuers, one per query tile
-            // S_t^{j+1} runs as soon as the softmax warps have read S_t^j. Each issuer walks every
-            // ring slot and releases it once, used or not.
+            // Each issuer walks every ring slot and releases it once, used or not. With P in columns of its own
+            // S_t^{j+1} runs as soon as the softmax warps have read S_t^j, before P_t^j V; with P over S behind
+            // it. (In that case the epilogue has read O_t before its threads arrive on p_full for a new unit.)
             const int t = warp == C::kIssuer ? 0 : 1;
             const uint32_t tS = tmem + t * BN, tO = tmem + C::o_col(t), tP = tmem + C::p_col(t);
             uint32_t it = 0, n_s = 0, n_p = 0;
@@ -649,22 +653,31 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 if (NT == 2 && t == 0 && w.cnt1 > 0) ring.next();  // tile 1's
                 for (int j = 0; j <= w.cnt_max && ok; ++j) {
                     const uint32_t itK = it;  // ring slot of K_j; V_j follows it
-                    const uint32_t sK = itK % C::kStages, sV_prev = (itK + C::kStages - 1) % C::kStages;
+                    const uint32_t sK = itK % C::kStages, sV = (itK + C::kStages - 1) % C::kStages;
                     const uint32_t k_phase = (itK / C::kStages) & 1, v_phase = ((itK - 1) / C::kStages) & 1;
-                    const unsigned ready = look(&bar.kv_full[sK], k_phase, &bar.s_free[t], (n_s - 1) & 1, &bar.kv_full[sV_prev],
-                                                v_phase, &bar.p_full[t], n_p & 1);
-                    if (j < w.cnt_max) {
+                    // with P over S the wait for P is the long one
+                    const unsigned ready = !C::kSplit
+                                               ? 0
+                                               : look(&bar.kv_full[sK], k_phase, &bar.s_free[t], (n_s - 1) & 1, &bar.kv_full[sV],
+                                                      v_phase, &bar.p_full[t], n_p & 1);
+                    auto wait_s = [&]() {
                         ok = (ready & 1) || mbar_wait_warp(&bar.kv_full[sK], k_phase, wc);
-                        if (!ok) break;
-                        if (j < cnt) {
-                            if (n_s > 0) {
-                                ok = (ready & 2) || mbar_wait_warp(&bar.s_free[t], (n_s - 1) & 1, wc);
-                                if (!ok) break;
-                            }
+                        if (C::kSplit && ok && j < cnt && n_s > 0)
+                            ok = (ready & 2) || mbar_wait_warp(&bar.s_free[t], (n_s - 1) & 1, wc);
+                        if (j < cnt) tc_fence_after();
+                    };
+                    auto wait_pv = [&]() {
+                        ok = (ready & 4) || mbar_wait_warp(&bar.kv_full[sV], v_phase, wc);
+                        if (ok && j <= cnt) {
+                            ok = (ready & 8) || mbar_wait_warp(&bar.p_full[t], n_p & 1, wc);
+                            ++n_p;
                             tc_fence_after();
-                            const uint32_t kt = sKV + sK * C::kTileBytes;
+                        }
+                    };
+                    auto issue_s = [&]() {  // S_t^j
+                        if (j < cnt) {
                             if (elect_one()) {
-                                const uint64_t qd = kmajor_desc(qt), kd = kmajor_desc(kt);
+                                const uint64_t qd = kmajor_desc(qt), kd = kmajor_desc(sKV + sK * C::kTileBytes);
 #pragma unroll kIssueUnroll
                                 for (int kk = 0; kk < D / 16; ++kk)
                                     mma_ss(tS, kmajor_step(qd, kk, q_half), kmajor_step(kd, kk, BN * 128), kIdescS,
@@ -678,28 +691,36 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                             mma_commit(&bar.kv_empty[sK]);
                         }
                         __syncwarp();
-                    }
-                    if (j > 0) {  // V_{j-1} lives in the slot before K_j
-                        ok = (ready & 4) || mbar_wait_warp(&bar.kv_full[sV_prev], v_phase, wc);
-                        if (!ok) break;
+                    };
+                    auto issue_pv = [&]() {  // O_t += P_t^{j-1} V_{j-1}
                         if (j <= cnt) {
-                            ok = (ready & 8) || mbar_wait_warp(&bar.p_full[t], n_p & 1, wc);
-                            if (!ok) break;
-                            ++n_p;
-                            tc_fence_after();
-                            const uint32_t vt = sKV + sV_prev * C::kTileBytes;
                             if (elect_one()) {
-                                const uint64_t vd = vmajor_desc(vt);
+                                const uint64_t vd = vmajor_desc(sKV + sV * C::kTileBytes);
 #pragma unroll kIssueUnroll
                                 for (int kk = 0; kk < BN / 16; ++kk)
                                     mma_ts(tO, tP + kk * 8, vmajor_step(vd, kk), kIdescO, (j > 1 || kk > 0) ? 1u : 0u);
-                                mma_commit(&bar.pv_done[t]);
-                                mma_commit(&bar.kv_empty[sV_prev]);
+                                if (C::kSplit)
+                                    mma_commit(&bar.pv_done[t]);
+                                else if (j == cnt)
+                                    mma_commit(&bar.o_full[t]);  // last product of this tile
+                                mma_commit(&bar.kv_empty[sV]);
                             }
                         } else if (elect_one()) {
-                            mma_commit(&bar.kv_empty[sV_prev]);
+                            mma_commit(&bar.kv_empty[sV]);
                         }
                         __syncwarp();
+                    };
+                    const bool has_s = j < w.cnt_max, has_pv = j > 0;
+                    if (C::kSplit) {
+                        if (has_s) wait_s();
+                        if (ok && has_s) issue_s();
+                        if (ok && has_pv) wait_pv();
+                        if (ok && has_pv) issue_pv();
+                    } else {
+                        if (has_pv) wait_pv();
+                        if (ok && has_pv) issue_pv();
+                        if (ok && has_s) wait_s();
+                        if (ok && has_s) issue_s();
                     }
                     if (j < w.cnt_max) it += 2;
                 }
@@ -710,8 +731,8 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 drain_wait(&bar.drain[t], 0, p.timeout_ns);
             }
             __syncwarp();
-        } else if (!C::kSplit && warp == C::kIssuer) {
-            // ------------------------------------------------ the one MMA issuer of P over S
+        } else if (C::kOneIssuer && warp == C::kIssuer) {
+            // ------------------------------------------------ the one MMA issuer of two tiles with P over S
             // S_t^0 of every tile, then per key tile O_t += P_t^{j-1} V_{j-1} and S_t^j in turn. The epilogue has
             // read O_t before its threads arrive on p_full for a new unit.
             uint32_t it = 0, pcnt0 = 0, pcnt1 = 0;
@@ -758,9 +779,8 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                     it += 2;
                     sK = it % C::kStages;
                     const uint32_t k_phase = (it / C::kStages) & 1, v_phase = (itV / C::kStages) & 1;
-                    const unsigned ready = NT == 1 ? 0  // one tile waits for P in any case
-                                                   : look(&bar.kv_full[sK], k_phase, &bar.kv_full[sV], v_phase,
-                                                          &bar.p_full[0], pcnt0 & 1, &bar.p_full[NT - 1], pcnt1 & 1);
+                    const unsigned ready = look(&bar.kv_full[sK], k_phase, &bar.kv_full[sV], v_phase, &bar.p_full[0],
+                                                pcnt0 & 1, &bar.p_full[1], pcnt1 & 1);
                     if (j < w.cnt_max) {
                         ok = (ready & 1) || mbar_wait_warp(&bar.kv_full[sK], k_phase, wc);
                         if (!ok) break;
