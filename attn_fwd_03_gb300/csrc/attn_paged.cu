@@ -14,10 +14,13 @@
 // What bounds it: decode reads every key and value once for a few products each, so
 // HBM (a ragged batch of 64 sequences of 4096-8192 keys, 32 query and 8 key/value
 // heads, d = 128: 245 us, 6.6 TB/s, 98 % of the measured copy rate; 96 % with
-// 16-token pages); long chunks are bound by the tensor pipe and the softmax beside
-// it (4096 rows over 32768 keys: 1.27 ms, 1620 TFLOP/s, 87 % of the measured GEMM
-// rate); small calls by latency (one token over 517 keys: 10.3 us for both
-// launches, of which locating the work takes 1.4, the first copies 2, the merge 3).
+// 16-token pages); long chunks by the products and their issue (4096 rows over 32768
+// keys: 1.26 ms, 1635 TFLOP/s, 88 % of the measured GEMM rate: of about 3000 cycles a
+// key tile the products take 2050 at their nominal rate, an S product rather 72-87
+// cycles than 64 since it reads 8 KB of shared memory, and the issuer's turns between
+// the two tiles the rest; the softmax of a tile takes 1140 and waits); small calls by
+// latency (one token over 517 keys: 10.3 us for both launches, of which locating the
+// work takes 1.4, the first copies 2, the merge 3).
 //
 // Work split: lengths are known on the device only, and ragged, so units are not
 // dealt out whole. All units lie one after another on a line, each as long as its
@@ -441,8 +444,8 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
 }
 
 // Which of four barriers have completed the given phases, for a whole converged warp. Looking at a barrier
-// takes some 130 cycles; one after another, ready or not, the issuers' waits made up half of a key tile's time
-// at d = 64 and in one-tile units.
+// takes some 130 cycles, ready or not, and an issuer looks at four a key tile (4096 rows over 32768 keys 1305 us
+// one after another, 1268 with this).
 __device__ __forceinline__ unsigned look(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c, uint32_t pc,
                                          uint64_t* d, uint32_t pd) {
     const unsigned ra = mbar_test(a, pa), rb = mbar_test(b, pb), rc = mbar_test(c, pc), rd = mbar_test(d, pd);
