@@ -720,6 +720,8 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                         if (ok && has_pv) wait_pv();
                         if (ok && has_pv) issue_pv();
                     } else {
+                        // V_{j-1} is released before K_j: with an odd number of stages either producer waits on slots
+                        // that the other used last, and may only see K_j's release when V_{j-1}'s is out
                         if (has_pv) wait_pv();
                         if (ok && has_pv) issue_pv();
                         if (ok && has_s) wait_s();
@@ -769,8 +771,8 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 for (int j = 1; j <= w.cnt_max && ok; ++j) {
                     const uint32_t itV = it + 1, sV = itV % C::kStages;  // V_{j-1}
                     if (elect_one()) {
-                        // V before K: with an odd number of stages either producer waits on slots that the other
-                        // used last, and may only see K_j's release when V_{j-1}'s is out
+                        // V before K here too; later in the key tile (behind the look at the barriers, or tile 0's
+                        // products) these cost 3 %
                         if (j > 1) mma_commit(&bar.kv_empty[(it + C::kStages - 1) % C::kStages]);
                         mma_commit(&bar.kv_empty[sK]);
                         if (j == w.cnt_max) {  // every S of the part is issued
