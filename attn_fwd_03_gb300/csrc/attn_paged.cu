@@ -62,6 +62,7 @@
 // Exponentials are not a bound: with 7 in 8 of them left out everything takes 92-101 %.
 #include <cuda_bf16.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -422,6 +423,9 @@ struct Walk {
 __device__ __forceinline__ float4* record(float* part, int slot, int tiles, int t, int rows, int d) {
     return reinterpret_cast<float4*>(part) + ((long long)slot * tiles + t) * rows * (1 + d / 4);
 }
+
+// LSE of a row from its reference maximum and sum: -inf where it has no key (sum 0), NaN where the sum is.
+__device__ __forceinline__ float row_lse(float m, float l) { return l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2; }
 
 // ---------------------------------------------------------------- helpers of the roles
 __device__ __forceinline__ uint64_t step_desc(uint64_t d, uint32_t by) {
@@ -1004,11 +1008,12 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                             }
                         }
                     }
-                    if (held) p.lse[head * p.T + row] = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
+                    if (held) p.lse[head * p.T + row] = row_lse(m_ref, l);
                 } else {
-                    // the part's state of this row; a row without keys in it is m = -inf, and its o is not read
+                    // the part's state of this row; a row without keys in it is m = -inf, and its o is not read. NaN
+                    // scores leave m_ref at -inf and l NaN: such a row has keys, and its m is any other number.
                     float4* rec = record(p.part, blockIdx.x * 2 + (first ? 1 : 0), C::Kernel::kTiles, t, rows, D);
-                    if (held) rec[r] = make_float4(l > 0.f ? m_ref : -INFINITY, l, den, 0.f);
+                    if (held) rec[r] = make_float4(l == 0.f ? -INFINITY : fmaxf(m_ref, -FLT_MAX), l, den, 0.f);
                     if (cnt > 0) {
 #pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -1229,7 +1234,7 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Co
             v.w = pack_h16<F16>(out[8 * q + 6] * inv, out[8 * q + 7] * inv);
             dst[q] = v;
         }
-        if (group == 0) a.lse[head * a.T + row] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+        if (group == 0) a.lse[head * a.T + row] = row_lse(M, L);
     }
 }
 

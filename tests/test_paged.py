@@ -227,6 +227,30 @@ def test_large_scores(A, n):
     c.check(o, lse, True)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 150])
+@pytest.mark.parametrize("where", ["q", "k"])
+def test_nan_scores_stay_nan(A, where, n, d):
+    # a row with NaN among its scores is NaN in O and LSE, whether its keys are split over CTAs (3000 keys)
+    # or not (90); every other row is as it would be without
+    c = Case([n, 1], [3000, 90], 2, 2, d, 32, torch.bfloat16, 82)
+    O, L = c.oracle(True)
+    spoilt = np.zeros((n + 1, 4), dtype=bool)
+    if where == "q":
+        spoilt[0, 1] = spoilt[n, 2] = True
+        c.q[torch.from_numpy(spoilt)] = float("nan")
+    else:  # the last key but one of head 0: its sequence's last two rows see it
+        for b, kv in enumerate(c.kv):
+            c.k[int(c.table[b, (kv - 2) // 32]), 0, (kv - 2) % 32] = float("nan")
+        spoilt[max(n - 2, 0):, :2] = True
+    o, lse = A.attn_paged(*c.device(), causal=True, max_q=n)
+    _ok(A)
+    got, got_lse = to64(o), to64(lse).T
+    assert np.all(np.isnan(got[spoilt])) and np.all(np.isnan(got_lse[spoilt]))
+    assert_close_bf16("O", got[~spoilt], O[~spoilt])
+    assert_lse(got_lse[~spoilt], L.T[~spoilt])
+
+
 def test_explicit_scale(A):
     c = Case([2], [50], 1, 2, 64, 16, torch.float16, 85)
     o, lse = A.attn_paged(*c.device(), causal=True, scale=0.31)
