@@ -994,8 +994,9 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                             for (int i = 0; i < 64; ++i) ov[i] = 0;
                         }
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            ov[i] = pack_h16<F16>(__uint_as_float(ov[2 * i]) * inv, __uint_as_float(ov[2 * i + 1]) * inv);
+                        for (int i = 0; i < 32; ++i)  // a row without keys is 0, though 0 * NaN of a value may be in its O
+                            ov[i] = l == 0.f ? 0u : pack_h16<F16>(__uint_as_float(ov[2 * i]) * inv,
+                                                                  __uint_as_float(ov[2 * i + 1]) * inv);
                         if (held) {
                             if (p.o_wide) {
 #pragma unroll

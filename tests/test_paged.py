@@ -258,6 +258,22 @@ def test_explicit_scale(A):
     c.check(o, lse, True, 0.31)
 
 
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [3, 40, 200])
+def test_rows_without_keys_are_zero_whatever_the_values(A, n, d, value):
+    # more rows than keys: the rows before the first key's are 0 though the tile's other rows meet values
+    # that are not finite
+    c = Case([n, 2], [n // 2, 1], 2, 2, d, 16, torch.float16, 86)
+    for b in range(2):
+        c.v[int(c.table[b, 0]), :, 0] = value
+    o, lse = A.attn_paged(*c.device(), causal=True, max_q=n)
+    _ok(A)
+    empty = np.array([i < n - n // 2 for i in range(n)] + [True, False])
+    assert np.all(to64(o)[empty] == 0) and np.all(np.isneginf(to64(lse)[:, empty]))
+    assert not np.isfinite(to64(o)[~empty]).any() and np.isfinite(to64(lse)[:, ~empty]).all()
+
+
 def test_many_sequences(A):
     rng = np.random.default_rng(3)
     n, kv = rng.integers(0, 3, 700), rng.integers(0, 70, 700)
