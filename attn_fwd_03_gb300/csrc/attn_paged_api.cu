@@ -108,6 +108,35 @@ attn_status_t check_paged(const attn_paged_params* p, bool* empty) {
     return check_ints("block_table", p->block_table);
 }
 
+// 32-bit integers that a table call reads or writes: `rows` of `n` side by side, `stride` apart.
+struct Ints {
+    const char* name;
+    const void* p;
+    int64_t n, rows = 1, stride = 0;
+};
+
+// Whether a row of `a` and the array `b` share an element.
+bool overlap(const Ints& a, const Ints& b) {
+    if (a.n <= 0 || a.rows <= 0 || b.n <= 0) return false;
+    // b in elements from a's first; row r of a is [r * stride, r * stride + n)
+    const int64_t lo = ((int64_t)reinterpret_cast<uintptr_t>(b.p) - (int64_t)reinterpret_cast<uintptr_t>(a.p)) / 4, hi = lo + b.n;
+    if (hi <= 0) return false;
+    if (a.rows == 1) return lo < a.n;
+    const int64_t first = lo < a.n ? 0 : (lo - a.n) / a.stride + 1;  // the first row that ends behind lo
+    return first < a.rows && first * a.stride < hi;
+}
+
+// The blocks of the table kernels read and write in no order: an array that is written (the first
+// `written` of them) shares no element with any other. Only one of them may have several rows.
+template <int N>
+attn_status_t check_apart(const Ints (&a)[N], int written) {
+    for (int i = 0; i < written; ++i)
+        for (int j = i + 1; j < N; ++j)
+            if (a[j].rows > 1 ? overlap(a[j], a[i]) : overlap(a[i], a[j]))
+                return report_error(ATTN_ERR_INVALID, "%s and %s overlap", a[i].name, a[j].name);
+    return ATTN_OK;
+}
+
 attn_status_t launched(cudaError_t e, const char* what) {
     return e == cudaSuccess ? ATTN_OK : report_error(ATTN_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
 }
@@ -173,20 +202,23 @@ attn_status_t attn_pages_plan(const attn_pages_plan_params* p, void* stream) {
     if ((st = check_ints("free_count", p->free_count)) != ATTN_OK) return st;
     if ((st = check_ints("free_left", p->free_left)) != ATTN_OK) return st;
     if ((st = check_ints("cu_q", p->cu_q)) != ATTN_OK) return st;
-    if (p->free_left == p->free_count) return report_error(ATTN_ERR_INVALID, "free_left must not be free_count itself");
     if (p->num_seqs > 0) {
         if ((st = check_ints("q_len", p->q_len)) != ATTN_OK) return st;
         if ((st = check_ints("kv_len", p->kv_len)) != ATTN_OK) return st;
         if ((st = check_ints("new_len", p->new_len)) != ATTN_OK) return st;
         if ((st = check_ints("block_table", p->block_table)) != ATTN_OK) return st;
-        if (p->new_len == p->kv_len || p->new_len == p->q_len)
-            return report_error(ATTN_ERR_INVALID, "new_len must not be kv_len or q_len itself");
     }
     if (p->total_q > 0) {
         if ((st = check_ints("slots", p->slots)) != ATTN_OK) return st;
         if ((st = check_ints("positions", p->positions)) != ATTN_OK) return st;
     }
     if (p->free_capacity > 0 && (st = check_ints("free_pages", p->free_pages)) != ATTN_OK) return st;
+    const int64_t seqs = p->num_seqs;
+    const Ints arrays[] = {{"block_table", p->block_table, p->max_pages, seqs, p->table_stride}, {"cu_q", p->cu_q, seqs + 1},
+                           {"new_len", p->new_len, seqs}, {"slots", p->slots, p->total_q}, {"positions", p->positions, p->total_q},
+                           {"free_left", p->free_left, 1}, {"q_len", p->q_len, seqs}, {"kv_len", p->kv_len, seqs},
+                           {"free_pages", p->free_pages, p->free_capacity}, {"free_count", p->free_count, 1}};
+    if ((st = check_apart(arrays, 6)) != ATTN_OK) return st;
     LaunchCommon lc;
     if ((st = launch_setup(&lc)) != ATTN_OK) return st;
     return launched(launch_pages_plan(*p, lc, static_cast<cudaStream_t>(stream)), "attn_pages_plan");
@@ -204,16 +236,19 @@ attn_status_t attn_pages_release(const attn_pages_release_params* p, void* strea
         return report_error(ATTN_ERR_INVALID, "table_stride must be at least max_pages");
     if ((st = check_ints("free_count", p->free_count)) != ATTN_OK) return st;
     if ((st = check_ints("free_left", p->free_left)) != ATTN_OK) return st;
-    if (p->free_left == p->free_count) return report_error(ATTN_ERR_INVALID, "free_left must not be free_count itself");
     if (p->num_seqs > 0) {
         if ((st = check_ints("done", p->done)) != ATTN_OK) return st;
         if ((st = check_ints("kv_len", p->kv_len)) != ATTN_OK) return st;
         if ((st = check_ints("new_len", p->new_len)) != ATTN_OK) return st;
         if ((st = check_ints("block_table", p->block_table)) != ATTN_OK) return st;
-        if (p->new_len == p->kv_len || p->new_len == p->done)
-            return report_error(ATTN_ERR_INVALID, "new_len must not be kv_len or done itself");
     }
     if (p->free_capacity > 0 && (st = check_ints("free_pages", p->free_pages)) != ATTN_OK) return st;
+    const int64_t seqs = p->num_seqs;
+    const Ints arrays[] = {{"free_pages", p->free_pages, p->free_capacity}, {"new_len", p->new_len, seqs},
+                           {"free_left", p->free_left, 1}, {"done", p->done, seqs}, {"kv_len", p->kv_len, seqs},
+                           {"block_table", p->block_table, p->max_pages, seqs, p->table_stride},
+                           {"free_count", p->free_count, 1}};
+    if ((st = check_apart(arrays, 3)) != ATTN_OK) return st;
     LaunchCommon lc;
     if ((st = launch_setup(&lc)) != ATTN_OK) return st;
     return launched(launch_pages_release(*p, lc, static_cast<cudaStream_t>(stream)), "attn_pages_release");

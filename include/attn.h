@@ -366,6 +366,9 @@ ATTN_API attn_status_t attn_pages_write(const attn_pages_write_params *p, void *
  * gives -1 too, and is reported). Such a step is not taken:
  * kv_len and free_count stay as they were, and it is planned again once pages
  * were released (by lengths before the step) or with fewer sequences.
+ * The arrays that are written (block_table, cu_q, new_len, slots, positions,
+ * free_left) share no element with one another or with the others
+ * (ATTN_ERR_INVALID): kv_len cannot be updated in place.
  */
 typedef struct attn_pages_plan_params {
     int32_t num_seqs;
@@ -379,9 +382,9 @@ typedef struct attn_pages_plan_params {
     int64_t table_stride;    /* elements, >= max_pages */
     const int32_t *free_pages, *free_count;  /* [free_capacity], [1] */
     int32_t *cu_q;           /* [num_seqs + 1] */
-    int32_t *new_len;        /* [num_seqs]; not kv_len itself */
+    int32_t *new_len;        /* [num_seqs] */
     int32_t *slots, *positions;  /* [total_q] */
-    int32_t *free_left;      /* [1]; not free_count itself */
+    int32_t *free_left;      /* [1] */
 } attn_pages_plan_params;
 
 ATTN_API attn_status_t attn_pages_plan(const attn_pages_plan_params *p, void *stream);
@@ -391,7 +394,10 @@ ATTN_API attn_status_t attn_pages_plan(const attn_pages_plan_params *p, void *st
  * the pages of its kv_len[b] tokens are pushed onto free_pages, the first of them
  * at free_pages[free_count]; new_len[b] becomes 0 (kv_len[b] for the others), and
  * free_left = free_count plus the pages given back. The block table is only read.
- * Entries below 0 among a sequence's pages are reported (ATTN_ERR_INVALID).
+ * Entries below 0 among a sequence's pages are reported (ATTN_ERR_INVALID). A
+ * page that several sequences name is pushed once for each of them that ended.
+ * The arrays that are written (free_pages, new_len, free_left) share no element
+ * with one another or with the others (ATTN_ERR_INVALID).
  */
 typedef struct attn_pages_release_params {
     int32_t num_seqs;
@@ -403,8 +409,8 @@ typedef struct attn_pages_release_params {
     int64_t table_stride;    /* elements, >= max_pages */
     int32_t *free_pages;     /* [free_capacity], updated from free_count on */
     const int32_t *free_count;       /* [1] */
-    int32_t *new_len;        /* [num_seqs]; not kv_len itself */
-    int32_t *free_left;      /* [1]; not free_count itself */
+    int32_t *new_len;        /* [num_seqs] */
+    int32_t *free_left;      /* [1] */
 } attn_pages_release_params;
 
 ATTN_API attn_status_t attn_pages_release(const attn_pages_release_params *p, void *stream);

@@ -591,6 +591,20 @@ def test_tables_into_given_tensors_on_another_stream(A):
     assert free.tolist() == [0, 1, 2, 4]
 
 
+def test_arrays_between_the_rows_of_a_wider_table(A):
+    # the counts lie in the columns that the table leaves over: no overlap
+    wide = _i32([[3, -1, 3, 9], [2, -1, 9, 9], [0, -1, 9, 9]])
+    table, count, left = wide[:, :2], wide[0, 2:3], wide[1, 3:4]
+    cu, new, slots, _, got = A.attn_pages_plan(_i32([2, 1, 1]), _i32([15, 16, 3]), table, _i32([4, 5, 6]), count, 16, 4, free_left=left)
+    _ok(A)
+    assert got is left and wide.tolist() == [[3, 6, 3, 9], [2, 5, 9, 1], [0, -1, 9, 9]]
+    assert slots.tolist() == [63, 96, 80, 3]
+    stack = _i32([4, 0, 0, 0])
+    A.attn_pages_release(_i32([0, 1, 1]), new, table, stack, left, 16, new_len=new.clone(), free_left=wide[0, 3:4])
+    _ok(A)
+    assert stack.tolist() == [4, 2, 5, 0] and wide[0].tolist() == [3, 6, 3, 4]
+
+
 @pytest.mark.parametrize("seqs,page,every", [(1, 16, 1), (9, 32, 2), (777, 16, 3), (5000, 16, 7), (40, 256, 1), (6, 16, 99)])
 def test_release_matches_oracle(A, seqs, page, every):
     rng = np.random.default_rng(seqs + 1)

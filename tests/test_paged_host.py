@@ -243,6 +243,42 @@ def test_release_refusals(A, kw, status):
     assert A.last_error() != ""
 
 
+# a plan's or release's arrays: entries, and whether the call writes them (2 sequences of 4 table columns, 5 rows)
+ARRAYS = {
+    "plan": dict(q_len=(2, False), kv_len=(2, False), block_table=(8, True), free_pages=(8, False), free_count=(1, False),
+                 cu_q=(3, True), new_len=(2, True), slots=(5, True), positions=(5, True), free_left=(1, True)),
+    "release": dict(done=(2, False), kv_len=(2, False), block_table=(8, False), free_pages=(8, True), free_count=(1, False),
+                    new_len=(2, True), free_left=(1, True)),
+}
+
+
+@pytest.mark.parametrize("call,first,second", [(call, a, b) for call, arrays in ARRAYS.items() for a in arrays for b in arrays
+                                               if a != b and arrays[a][1]])
+def test_overlapping_table_arrays_are_refused(A, call, first, second):
+    # the second array starts at the first one's last entry, or ends in its first one
+    arrays = ARRAYS[call]
+    for ends in (False, True):
+        at = {name: FAKE + 64 * i for i, name in enumerate(arrays)}
+        at[second] = at[first] - 4 * (arrays[second][0] - 1) if ends else at[first] + 4 * (arrays[first][0] - 1)
+        sizes = dict(num_seqs=2, page_size=16, max_pages=4, free_capacity=8, table_stride=4)
+        if call == "plan":
+            p = _filled(A.PagesPlanParams, total_q=5, **sizes, **at)
+        else:
+            p = _filled(A.PagesReleaseParams, **sizes, **at)
+        assert getattr(A.lib, f"attn_pages_{call}")(ctypes.byref(p), None) == A.ATTN_ERR_INVALID
+        assert "overlap" in A.last_error() and first in A.last_error() and second in A.last_error()
+
+
+@pytest.mark.parametrize("name,entries", [("free_left", [0, 3, 7, 10, 14, 17]), ("cu_q", [-3, 0, 4, 10, 11, 17])])
+def test_overlap_with_a_row_of_a_wider_table_is_refused(A, name, entries):
+    # 3 rows of 4 columns, 7 entries apart; free_left has 1 entry, cu_q 4
+    for entry in entries:
+        table = FAKE + 4096
+        p = _plan(A, num_seqs=3, table_stride=7, block_table=table, **{name: table + 4 * entry})
+        assert A.lib.attn_pages_plan(ctypes.byref(p), None) == A.ATTN_ERR_INVALID
+        assert f"block_table and {name} overlap" in A.last_error()
+
+
 def test_null_params(A):
     for name in ("attn_paged", "attn_pages_write", "attn_pages_plan", "attn_pages_release"):
         assert getattr(A.lib, name)(None, None) == A.ATTN_ERR_INVALID
