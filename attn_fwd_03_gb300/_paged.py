@@ -168,12 +168,17 @@ def _pack_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, out, lse, scale,
 
 
 def paged_workspace_size(q, k_cache, v_cache, block_table, cu_q, kv_len, *, max_q: Optional[int] = None) -> int:
-    """Bytes of workspace attn_paged needs for these shapes."""
+    """Bytes of workspace attn_paged needs for these shapes on q's device."""
     _check_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, None, None)
     max_q = _default_max_q(q.shape[0], block_table.shape[0]) if max_q is None else _as_int32(max_q)
     # out and lse are not read: q stands in for both
-    return int(lib.attn_paged_workspace_size(
-        _pack_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, q, q, 1.0, False, max_q, 0, 0)))
+    packed = _pack_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, q, q, 1.0, False, max_q, 0, 0)
+    dev = q.get_device()
+    guard = _guard(dev, None) if dev >= 0 else None  # the size goes by the current device's number of SMs
+    if guard is None:
+        return int(lib.attn_paged_workspace_size(packed))
+    with guard:
+        return int(lib.attn_paged_workspace_size(packed))
 
 
 # (device, d, heads, key/value heads, max_q) -> bytes; all that the size depends on. No head group fits more

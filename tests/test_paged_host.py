@@ -315,6 +315,35 @@ def test_binding_attend_refusals(A, kw, error):
         A.attn_paged(*args, **opts)
 
 
+class _OnDevice(torch.Tensor):
+    """A CPU tensor that says it is on cuda:1."""
+
+    def get_device(self):
+        return 1
+
+
+def test_workspace_size_is_asked_on_the_tensors_device(A, monkeypatch):
+    import contextlib
+    import types
+
+    from attn_fwd_03_gb300 import _paged
+    current, asked = [0], []
+
+    @contextlib.contextmanager
+    def device(dev):
+        before, current[0] = current[0], dev
+        yield
+        current[0] = before
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(_paged, "lib", types.SimpleNamespace(attn_paged_workspace_size=lambda p: asked.append(current[0]) or 4096))
+    args, _ = _attend_args()
+    assert A.paged_workspace_size(*args) == 4096
+    assert A.paged_workspace_size(args[0].as_subclass(_OnDevice), *args[1:]) == 4096
+    assert asked == [0, 1] and current == [0]
+
+
 def test_binding_write_refusals(A):
     k = torch.zeros(3, 2, 64, dtype=torch.float16)
     cache = torch.zeros(4, 2, 16, 64, dtype=torch.float16)
