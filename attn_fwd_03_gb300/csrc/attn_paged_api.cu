@@ -54,6 +54,12 @@ attn_status_t check_16bit(int32_t dtype, int32_t d) {
 // Keys of a sequence: the kernels add up to a few tiles to such a number in 32 bits.
 constexpr int64_t kMaxLength = (int64_t)INT32_MAX - 1023;
 
+// The kernels step through the sequences, and through a sequence's rows, in 32 bits, some hundred at a time.
+attn_status_t check_count(const char* name, int32_t n) {
+    if (n > INT32_MAX - 1023) return report_error(ATTN_ERR_UNSUPPORTED, "%s must not exceed 2^31 - 1024, got %d", name, n);
+    return ATTN_OK;
+}
+
 attn_status_t check_table(int32_t max_pages, int32_t page_size) {
     if (max_pages < 1) return report_error(ATTN_ERR_INVALID, "max_pages must be at least 1, got %d", max_pages);
     if ((int64_t)max_pages * page_size > kMaxLength)
@@ -84,6 +90,8 @@ attn_status_t check_paged(const attn_paged_params* p, bool* empty) {
         return report_error(ATTN_ERR_INVALID, "scale must be positive and finite");
     if (p->max_q < 1) return report_error(ATTN_ERR_INVALID, "max_q must be at least 1, got %d", p->max_q);
     attn_status_t st;
+    if ((st = check_count("num_seqs", p->num_seqs)) != ATTN_OK) return st;
+    if ((st = check_count("total_q", p->total_q)) != ATTN_OK) return st;
     if ((st = check_16bit(p->dtype, p->d)) != ATTN_OK) return st;
     if ((st = check_page_size(p->page_size)) != ATTN_OK) return st;
     if (p->num_q_heads % p->num_kv_heads != 0)
@@ -195,6 +203,7 @@ attn_status_t attn_pages_plan(const attn_pages_plan_params* p, void* stream) {
                             p->total_q, p->free_capacity);
     if (p->reserved0 != 0) return report_error(ATTN_ERR_INVALID, "reserved0 must be 0");
     attn_status_t st;
+    if ((st = check_count("num_seqs", p->num_seqs)) != ATTN_OK) return st;
     if ((st = check_page_size(p->page_size)) != ATTN_OK) return st;
     if ((st = check_table(p->max_pages, p->page_size)) != ATTN_OK) return st;
     if (p->table_stride < p->max_pages)
@@ -230,6 +239,7 @@ attn_status_t attn_pages_release(const attn_pages_release_params* p, void* strea
         return report_error(ATTN_ERR_INVALID, "negative size num_seqs=%d free_capacity=%d", p->num_seqs,
                             p->free_capacity);
     attn_status_t st;
+    if ((st = check_count("num_seqs", p->num_seqs)) != ATTN_OK) return st;
     if ((st = check_page_size(p->page_size)) != ATTN_OK) return st;
     if ((st = check_table(p->max_pages, p->page_size)) != ATTN_OK) return st;
     if (p->table_stride < p->max_pages)

@@ -292,11 +292,11 @@ ATTN_API attn_status_t attn_decode(const attn_decode_params *p, void *stream);
  * are the same bits for the same inputs on a given GPU model.
  */
 typedef struct attn_paged_params {
-    int32_t num_seqs;
+    int32_t num_seqs;        /* at most 2^31 - 1024 */
     int32_t num_q_heads;     /* a multiple of num_kv_heads, at most 128 times as many */
     int32_t num_kv_heads;
     int32_t d;               /* 64 or 128 */
-    int32_t total_q;         /* rows of q and o, columns of lse */
+    int32_t total_q;         /* rows of q and o, columns of lse; at most 2^31 - 1024 */
     int32_t max_q;           /* the most query rows a sequence is expected to bring, >= 1: chooses
                                 the tile shape. More rows than this are still right, only slower */
     int32_t num_pages, page_size;
@@ -371,7 +371,7 @@ ATTN_API attn_status_t attn_pages_write(const attn_pages_write_params *p, void *
  * (ATTN_ERR_INVALID): kv_len cannot be updated in place.
  */
 typedef struct attn_pages_plan_params {
-    int32_t num_seqs;
+    int32_t num_seqs;        /* at most 2^31 - 1024 */
     int32_t total_q;         /* entries of slots and positions, >= the sum of q_len */
     int32_t page_size;
     int32_t max_pages;       /* columns of the block table, >= 1; max_pages * page_size <= 2^31 - 1024 */
@@ -400,7 +400,7 @@ ATTN_API attn_status_t attn_pages_plan(const attn_pages_plan_params *p, void *st
  * with one another or with the others (ATTN_ERR_INVALID).
  */
 typedef struct attn_pages_release_params {
-    int32_t num_seqs;
+    int32_t num_seqs;        /* at most 2^31 - 1024 */
     int32_t page_size;
     int32_t max_pages;       /* columns of the block table, >= 1; max_pages * page_size <= 2^31 - 1024 */
     int32_t free_capacity;   /* entries of free_pages */

@@ -279,6 +279,18 @@ def test_overlap_with_a_row_of_a_wider_table_is_refused(A, name, entries):
         assert f"block_table and {name} overlap" in A.last_error()
 
 
+@pytest.mark.parametrize("num_seqs", [2 ** 31 - 1023, 2 ** 31 - 1])
+def test_too_many_sequences_or_rows_are_refused(A, num_seqs):
+    # the kernels' 32-bit loops over the sequences and over a sequence's rows would wrap and not end
+    assert A.lib.attn_paged(ctypes.byref(_paged(A, total_q=num_seqs)), None) == A.ATTN_ERR_UNSUPPORTED
+    assert "total_q" in A.last_error()
+    release = _filled(A.PagesReleaseParams, num_seqs=num_seqs, page_size=16, max_pages=4, free_capacity=8, table_stride=4)
+    for name, p in (("attn_paged", _paged(A, num_seqs=num_seqs)), ("attn_pages_plan", _plan(A, num_seqs=num_seqs)),
+                    ("attn_pages_release", release)):
+        assert getattr(A.lib, name)(ctypes.byref(p), None) == A.ATTN_ERR_UNSUPPORTED
+        assert "num_seqs" in A.last_error()
+
+
 def test_null_params(A):
     for name in ("attn_paged", "attn_pages_write", "attn_pages_plan", "attn_pages_release"):
         assert getattr(A.lib, name)(None, None) == A.ATTN_ERR_INVALID
