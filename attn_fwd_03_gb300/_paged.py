@@ -351,7 +351,7 @@ def _check_tables(name, first, kv_len, block_table, free_pages, free_count) -> i
 
 def _page_size(page_size) -> int:
     """As the C ABI's int32; the library checks the rest."""
-    if not 0 < page_size <= _INT32_MAX:
+    if not 0 < page_size <= _INT32_MAX or int(page_size) != page_size:
         raise ValueError(f"page_size must be a positive 32-bit integer, got {page_size}")
     return int(page_size)
 

@@ -370,6 +370,14 @@ def test_binding_write_refusals(A):
             A.attn_pages_write(*args)
 
 
+@pytest.mark.parametrize("page_size", [16.5, 0.5, 0, -16, 2 ** 31, float("nan")])
+def test_binding_page_size_refusals(A, page_size):
+    from attn_fwd_03_gb300 import _paged
+    with pytest.raises(ValueError, match="page_size"):
+        _paged._page_size(page_size)
+    assert _paged._page_size(16) == 16
+
+
 def test_binding_tables_refusals(A):
     i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
     for args, kw, error in [((i(2), i(2), i(2, 3), i(9), i(1), 16, 4), {}, ValueError),  # on the CPU
