@@ -163,6 +163,7 @@ struct PagedDev {
     int4* meta;       // [grid][2]: see below
     int* err;
     unsigned long long timeout_ns;
+    int stall_after;  // test hook: the K and V producers stop after this many key tiles (0 = off)
 };
 
 // What the combine kernel reads about a CTA's slot: x = 0 nothing, 1 a part, 2 the unit's last part;
@@ -193,6 +194,7 @@ struct __align__(16) Shared {
     long long scan[2][12]; // per warp: its sequences' cost on either line
     int pair;              // whether this CTA works on two-tile units
     int widest[12], sm_warps;  // most rows of a one-tile unit; softmax warps of a tile that hold rows
+    uint32_t issued[2];    // ring items issued: of K (even numbers) all below the first, of V all below the second
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -542,12 +544,18 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             const uint32_t box_bytes = (uint32_t)box_rows * 128;
             const int my_key = lane * box_rows;          // of a tile, where this lane has a box
             uint32_t it = 0;                             // ring items: K and V in turn
+            uint32_t stop = 0;                           // where a wait ran out: the first item not issued here
             bool ok = true, bad = false;
             while (ok && (two || first == 0) && walk.next(w)) {
                 if (w.cnt_max == 0) continue;
                 int page = 0;  // this lane's page of the current tile
                 if (my_key < BN && w.k0 * BN + my_key < w.len) page = page_at(p, w.b, w.k0 * BN + my_key, &bad);
                 for (int j = w.k0; j < w.k0 + w.cnt_max && ok; ++j, it += 2) {
+                    if (p.stall_after > 0 && it >= 2u * (uint32_t)p.stall_after) {
+                        ok = false;
+                        stop = it + first;
+                        break;
+                    }
                     const int key0 = j * BN;
                     const bool active = my_key < BN && key0 + my_key < w.len;
                     const uint32_t boxes = __popc(__ballot_sync(kFull, active));
@@ -560,7 +568,10 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                     for (int kv = first; kv < end; ++kv) {
                         const uint32_t s = (it + kv) % C::kStages;
                         ok = mbar_wait_warp(&bar.kv_empty[s], (((it + kv) / C::kStages) & 1) ^ 1, wc);
-                        if (!ok) break;
+                        if (!ok) {
+                            stop = it + kv;
+                            break;
+                        }
                         uint64_t* full = kv == 1 && tail ? &bar.v_tail[s] : &bar.kv_full[s];
                         if (elect_one()) mbar_arrive_expect_tx(full, boxes * box_bytes * C::kBoxes);
                         __syncwarp();
@@ -575,11 +586,10 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 }
             }
             if (bad) atomicCAS(p.err, 0, ATTN_ERR_INVALID);
-            // every copy issued must land before the CTA exits
-            if (lane == 0) {
-                const uint32_t last = it < (uint32_t)C::kStages ? it : (uint32_t)C::kStages;
-                for (uint32_t i = it - last; i < it; ++i)
-                    drain_wait(&bar.kv_full[i % C::kStages], (i / C::kStages) & 1, p.timeout_ns);
+            if (lane == 0 && (two || first == 0)) {
+                if (ok) stop = it;
+                bar.issued[first] = stop;
+                if (!two) bar.issued[1] = stop;
             }
         } else if (warp == C::kTail) {
             // ------------------------------------------------ Q, rows of V beyond the sequence, the CTA's slots
@@ -1035,6 +1045,19 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             }
         }
     }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // Every copy issued must land before the CTA exits. The issuers have waited for each, unless a wait ran out:
+    // then the last one issued into each slot is waited for (none was issued over one that had not landed).
+    if (threadIdx.x == 0 && bar.abort_flag != 0) {
+        const uint32_t end = max(bar.issued[0], bar.issued[1]);
+        for (uint32_t s = 0; s < (uint32_t)C::kStages && s < end; ++s) {
+            uint32_t i = s + (end - 1 - s) / C::kStages * C::kStages;
+            while (i >= bar.issued[i & 1] && i >= (uint32_t)C::kStages) i -= C::kStages;
+            if (i < bar.issued[i & 1]) drain_wait(&bar.kv_full[s], (i / C::kStages) & 1, p.timeout_ns);
+        }
+    }
 }
 
 template <int D, bool F16, int KERNEL>
@@ -1073,9 +1096,6 @@ __global__ void __launch_bounds__(Shape<D, KERNEL>::kThreads, Shape<D, KERNEL>::
     } else {
         work<D, F16, 1, KERNEL>(tm_q, tm_k, tm_v, p, smem, bar);
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     if (warp == 0) tmem_dealloc(bar.tmem_base, Kernel::kTmemCols);
 }
 
@@ -1376,6 +1396,7 @@ attn_status_t launch_paged(const attn_paged_params& p, const LaunchCommon& lc, c
     a.part = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + pl.meta_bytes);
     a.err = lc.err;
     a.timeout_ns = lc.timeout_ns;
+    a.stall_after = lc.stall_after;
     const bool f16 = p.dtype == ATTN_F16;
     const cudaError_t e =
         p.d == 64 ? (f16 ? launch_both<64, true>(maps, a, pl, pl.ctas, s) : launch_both<64, false>(maps, a, pl, pl.ctas, s))

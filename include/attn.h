@@ -417,8 +417,10 @@ ATTN_API attn_status_t attn_pages_release(const attn_pages_release_params *p, vo
 
 /* Synchronizes `stream`, then reports (and clears) the current device's
  * error word: ATTN_ERR_TIMEOUT if a kernel gave up on a bounded wait since
- * the last call, ATTN_ERR_INVALID if a paged-cache kernel met a length, page or
- * slot out of range, ATTN_ERR_CUDA for an asynchronous CUDA error, else ATTN_OK. */
+ * the last call (outputs of calls since then are unspecified; their inputs and
+ * workspaces can be used again), ATTN_ERR_INVALID if a paged-cache kernel met a
+ * length, page or slot out of range, ATTN_ERR_CUDA for an asynchronous CUDA
+ * error, else ATTN_OK. */
 ATTN_API attn_status_t attn_status(void *stream);
 
 /* Message for the last non-OK status returned on this host thread ("" if none). */
@@ -429,9 +431,9 @@ ATTN_API const char *attn_last_error(void);
  * Default 2e9 (2 s); values below 1e6 are raised to 1e6. Process-wide. */
 ATTN_API void attn_set_wait_timeout_ns(uint64_t ns);
 
-/* Test hook for failure detection: when > 0, the next forward launches on
- * this host thread have their load warp stop after this many key/value
- * tiles, so the consumers' bounded waits run out and report
+/* Test hook for failure detection: when > 0, the next forward and paged
+ * attention launches on this host thread have their load warps stop after this
+ * many key/value tiles (of a CTA), so the consumers' bounded waits run out and report
  * ATTN_ERR_TIMEOUT. 0 (the default) disables it. */
 ATTN_API void attn_debug_set_producer_stall(int32_t kv_tiles);
 
