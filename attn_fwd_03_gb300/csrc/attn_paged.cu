@@ -487,6 +487,17 @@ struct QRing {
     }
 };
 
+// Waits for the last item issued into each slot (none was issued over one that had not landed). Out of line: short
+// units run the kernel's code cold, and what they never use costs them its place (512 sequences of 128 keys 61 us).
+__device__ __noinline__ void drain_ring(Shared& bar, uint32_t stages, uint64_t timeout_ns) {
+    const uint32_t end = max(bar.issued[0], bar.issued[1]);
+    for (uint32_t s = 0; s < stages && s < end; ++s) {
+        uint32_t i = s + (end - 1 - s) / stages * stages;
+        while (i >= bar.issued[i & 1] && i >= stages) i -= stages;
+        if (i < bar.issued[i & 1]) drain_wait(&bar.kv_full[s], (i / stages) & 1, timeout_ns);
+    }
+}
+
 // The work of a CTA on units of NT tiles, from the located piece of the line to its end.
 template <int D, bool F16, int NT, int KERNEL>
 __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
@@ -544,18 +555,14 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             const uint32_t box_bytes = (uint32_t)box_rows * 128;
             const int my_key = lane * box_rows;          // of a tile, where this lane has a box
             uint32_t it = 0;                             // ring items: K and V in turn
-            uint32_t stop = 0;                           // where a wait ran out: the first item not issued here
+            const uint32_t limit = p.stall_after > 0 ? 2u * (uint32_t)p.stall_after : UINT32_MAX;
             bool ok = true, bad = false;
-            while (ok && (two || first == 0) && walk.next(w)) {
+            while (ok && (two || first == 0) && it < limit && walk.next(w)) {
                 if (w.cnt_max == 0) continue;
                 int page = 0;  // this lane's page of the current tile
                 if (my_key < BN && w.k0 * BN + my_key < w.len) page = page_at(p, w.b, w.k0 * BN + my_key, &bad);
+                w.cnt_max = min(w.cnt_max, (int)((limit - it) / 2));
                 for (int j = w.k0; j < w.k0 + w.cnt_max && ok; ++j, it += 2) {
-                    if (p.stall_after > 0 && it >= 2u * (uint32_t)p.stall_after) {
-                        ok = false;
-                        stop = it + first;
-                        break;
-                    }
                     const int key0 = j * BN;
                     const bool active = my_key < BN && key0 + my_key < w.len;
                     const uint32_t boxes = __popc(__ballot_sync(kFull, active));
@@ -569,7 +576,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                         const uint32_t s = (it + kv) % C::kStages;
                         ok = mbar_wait_warp(&bar.kv_empty[s], (((it + kv) / C::kStages) & 1) ^ 1, wc);
                         if (!ok) {
-                            stop = it + kv;
+                            it += kv - 2;  // ends as the first item not issued here
                             break;
                         }
                         uint64_t* full = kv == 1 && tail ? &bar.v_tail[s] : &bar.kv_full[s];
@@ -587,9 +594,8 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             }
             if (bad) atomicCAS(p.err, 0, ATTN_ERR_INVALID);
             if (lane == 0 && (two || first == 0)) {
-                if (ok) stop = it;
-                bar.issued[first] = stop;
-                if (!two) bar.issued[1] = stop;
+                bar.issued[first] = it;
+                if (!two) bar.issued[1] = it;
             }
         } else if (warp == C::kTail) {
             // ------------------------------------------------ Q, rows of V beyond the sequence, the CTA's slots
@@ -990,6 +996,8 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 const float den = o_divisor<F16>(l, m_row, m_ref);
                 if (first && last) {
                     const float inv = den > 0.f ? 1.f / den : 0.f;
+                    // a row without keys is 0, though its products of 0 and a value may be NaN
+                    const uint32_t keep = l == 0.f ? 0u : ~0u;
                     const long long row = u.x + my_tok, head = u.z * p.G + my_head;
                     uint16_t* orow = reinterpret_cast<uint16_t*>(p.o) + row * p.o_sr + head * p.o_sh;
 #pragma unroll 1
@@ -1004,9 +1012,11 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                             for (int i = 0; i < 64; ++i) ov[i] = 0;
                         }
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)  // a row without keys is 0, though 0 * NaN of a value may be in its O
-                            ov[i] = l == 0.f ? 0u : pack_h16<F16>(__uint_as_float(ov[2 * i]) * inv,
-                                                                  __uint_as_float(ov[2 * i + 1]) * inv);
+                        for (int i = 0; i < 32; ++i) {
+                            const float2 x = fmul2(make_float2(__uint_as_float(ov[2 * i]), __uint_as_float(ov[2 * i + 1])),
+                                                   make_float2(inv, inv));
+                            ov[i] = pack_h16<F16>(x.x, x.y) & keep;
+                        }
                         if (held) {
                             if (p.o_wide) {
 #pragma unroll
@@ -1048,16 +1058,8 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // Every copy issued must land before the CTA exits. The issuers have waited for each, unless a wait ran out:
-    // then the last one issued into each slot is waited for (none was issued over one that had not landed).
-    if (threadIdx.x == 0 && bar.abort_flag != 0) {
-        const uint32_t end = max(bar.issued[0], bar.issued[1]);
-        for (uint32_t s = 0; s < (uint32_t)C::kStages && s < end; ++s) {
-            uint32_t i = s + (end - 1 - s) / C::kStages * C::kStages;
-            while (i >= bar.issued[i & 1] && i >= (uint32_t)C::kStages) i -= C::kStages;
-            if (i < bar.issued[i & 1]) drain_wait(&bar.kv_full[s], (i / C::kStages) & 1, p.timeout_ns);
-        }
-    }
+    // Every copy issued must land before the CTA exits. The issuers have waited for each, unless a wait ran out.
+    if (threadIdx.x == 0 && bar.abort_flag != 0) drain_ring(bar, C::kStages, p.timeout_ns);
 }
 
 template <int D, bool F16, int KERNEL>
