@@ -441,6 +441,28 @@ def test_longest_table(A):
     assert abs(float(lse[0, 0]) - math.log(w.sum())) <= of_l + 32 * 2.0 ** -24
 
 
+def test_longest_table_every_page_counts(A):
+    # 64 pages that differ in V alone, page p 1 in column p and 0 elsewhere, each named for a 64th of the table in
+    # turn: column p of O is that page's share. The keys are the same on every page, so that a CTA's sums grow
+    # evenly and the n roundings of a running sum (2^-24 each; 8 of 2^-23 a tile in the accumulator) weigh half of
+    # what they do at its end. Keys of one CTA that were left out would take 10 % or more from some column.
+    page, cols, d = 1024, 2 ** 21 - 1, 64
+    g = torch.Generator().manual_seed(151)
+    k1, q = (torch.randn(shape, generator=g).bfloat16() for shape in ((1, 1, page, d), (1, 1, d)))
+    k = k1.expand(64, -1, -1, -1).contiguous()
+    v = torch.eye(64)[:, None, None, :].expand(-1, 1, page, -1).bfloat16().contiguous()
+    table = torch.arange(cols, dtype=torch.int64) * 64 // cols
+    o, lse = A.attn_paged(q.cuda(), k.cuda(), v.cuda(), table.int().view(1, -1).cuda(), _i32([0, 1]), _i32([cols * page]),
+                          causal=True, max_q=1)
+    _ok(A)
+    share = np.bincount(table.numpy()) / cols
+    tiles = cols * page / 128 / torch.cuda.get_device_properties(0).multi_processor_count + 9  # of a CTA, at most
+    of_l = (tiles / 2 + 48) * 2.0 ** -24  # and 35 additions inside a tile, 10 in the merge
+    assert np.abs(to64(o)[0, 0] / share - 1).max() <= tiles / 2 * 8 * 2.0 ** -23 + of_l + 2 * 2.0 ** -8
+    want = math.log(np.exp(to64(k1)[0, 0] @ to64(q)[0, 0] / math.sqrt(d)).sum() * cols)
+    assert abs(float(lse[0, 0]) - want) <= of_l + 2.0 ** -18
+
+
 @pytest.mark.parametrize("n", [1, 200])
 def test_bad_lengths_and_pages_are_reported(A, n):
     # a page out of range, a length that the table cannot hold: no access follows them, attn_status
@@ -461,6 +483,29 @@ def test_bad_lengths_and_pages_are_reported(A, n):
         rest = slice(int(c.cu[1]), int(c.cu[3]))
         assert_close_bf16("O", o[rest], O[rest])
         assert_lse(lse[:, rest], L[:, rest])
+
+
+@pytest.mark.parametrize("n", [1, 200])
+@pytest.mark.parametrize("entry,value,right", [(0, 1, [1, 2]), (0, -1, [0, 1, 2]), (1, -4, [2]), (1, 2 ** 31 - 1, []), (2, 0, []),
+                                               (3, 10 ** 6, [0, 1, 2]), (3, -2 ** 31, [0, 1])])
+def test_bad_row_offsets_are_reported(A, n, entry, value, right):
+    # cu_q that does not begin at 0, decreases or passes the rows of q: nothing outside out and lse is written,
+    # attn_status tells, and the sequences whose rows no other one claims are right
+    c = Case([n, 1, n], [300, 90, 210], 2, 2, 64, 32, torch.bfloat16, 131)
+    q, k, v, table, cu, kv = c.device()
+    cu[entry] = value
+    room = torch.full((len(q) + 2, 4, 64), 7.0, dtype=c.dtype, device="cuda")
+    flat = torch.full((4 * len(q) + 128,), 7.0, device="cuda")
+    out, lse = room[1:-1], flat[64:-64].view(4, len(q))
+    A.attn_paged(q, k, v, table, cu, kv, max_q=n, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert A.attn_status() == A.ATTN_ERR_INVALID and A.attn_status() == A.ATTN_OK
+    assert torch.all(room[[0, -1]] == 7.0) and torch.all(flat[:64] == 7.0) and torch.all(flat[-64:] == 7.0)
+    O, L = c.oracle(False)
+    for b in right:
+        rows = slice(int(c.cu[b]), int(c.cu[b + 1]))
+        assert_close_bf16("O", out[rows], O[rows])
+        assert_lse(lse[:, rows], L[:, rows])
 
 
 # ---------------------------------------------------------------- writes
