@@ -232,7 +232,9 @@ def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
     d], LSE fp32 [Hq, rows]. With causal each sequence's rows are its last positions. Rows behind the
     last sequence are left as they are in out and lse (unset in tensors allocated here).
 
-    max_q, the most rows that a sequence is expected to bring, only chooses the tile shape."""
+    max_q, the most rows that a sequence is expected to bring, only chooses the tile shape. out may be q
+    itself. Without a workspace, calls on the device's default stream keep one for good (the largest
+    that was needed, tens of MB), and others allocate one."""
     dtype = q.dtype
     if not (dtype in _TYPES and q.dim() == 3 and k_cache.dim() == 4 and block_table.dim() == 2 and q.stride()[2] == 1
             and k_cache.dtype is dtype and k_cache.shape[3] == q.shape[2] and k_cache.stride()[3] == 1

@@ -12,15 +12,28 @@
 // a tile's max exceeds it by more than 8 (log2 units).
 //
 // What bounds it: decode reads every key and value once for a few products each, so
-// HBM (a ragged batch of 64 sequences of 4096-8192 keys, 32 query and 8 key/value
-// heads, d = 128: 245 us, 6.6 TB/s, 98 % of the measured copy rate; 96 % with
-// 16-token pages); long chunks by the products and their issue (4096 rows over 32768
-// keys: 1.26 ms, 1635 TFLOP/s, 88 % of the measured GEMM rate: of about 3000 cycles a
-// key tile the products take 2050 at their nominal rate, an S product rather 72-87
-// cycles than 64 since it reads 8 KB of shared memory, and the issuer's turns between
-// the two tiles the rest; the softmax of a tile takes 1140 and waits); small calls by
-// latency (one token over 517 keys: 10.3 us for both launches, of which locating the
-// work takes 1.4, the first copies 2, the merge 3).
+// HBM (a ragged batch of 64 sequences of 4096-8192 keys: 238-245 us from one GPU to
+// another, 6.6-6.8 TB/s, 98-101 % of the measured copy rate; 96-99 % with 16-token
+// pages); long chunks by the products and their issue (4096 rows over 32768 keys: 1.26
+// ms, 1635 TFLOP/s, 88 % of the GEMM rate measured in bursts, where single calls are
+// timed; call after call the power cap lowers the clock, 1.41-1.46 ms, 83-86 % of the
+// sustained GEMM rate. Of about 3000 cycles a key tile the products take 2050 at their
+// nominal rate, an S product rather 72-87 cycles than 64 since it reads 8 KB of shared
+// memory, and the issuer's turns between the two tiles the rest; the softmax of a tile
+// takes 1140 and waits); small calls by latency (one token over 517 keys: 10.3 us for
+// both launches, of which locating the work takes 1.4, the first copies 2, the merge 3).
+//
+// The calls that figures here and below name have 32 query and 8 key/value heads,
+// d = 128, bf16, pages of 64 tokens, one new token a sequence and causal rows, unless
+// they say otherwise. "N sequences of K keys" are ragged: lengths from 70 % of K to K
+// (64 sequences of 8192 keys: from 50 %). 512 sequences of 128 and 256 of 512 keys have
+// 16-token pages; 2000 of 300 keys 16 query and 2 key/value heads and 16-token pages;
+// at d = 64, 64 sequences of 4096 keys have 64 query heads, 128 of 1000 keys 32-token
+// pages. Chunks of 40 rows are over 1434-2048 keys; 8 chunks of 448 rows are not causal,
+// over 1050-1500 states with 16 query and key/value heads and 128-token pages; 5 drafted
+// tokens of 16 sequences have 28 query and 4 key/value heads, d = 64, fp16, 32-token
+// pages and up to 4001 keys; the mixed step is 16 decoding sequences and a 512-row chunk
+// of up to 4096 keys each; the chunk of 4096 rows has 128-token pages.
 //
 // Work split: lengths are known on the device only, and ragged, so units are not
 // dealt out whole. All units lie one after another on a line, each as long as its
@@ -81,8 +94,8 @@ constexpr float kRescaleThreshold = 8.0f;
 // What a unit costs beyond its key tiles, in keys: with 64 a prompt of 8192 tokens takes 400 us, with 384 it
 // takes 369, and the verification of 5 drafted tokens of 16 sequences 19.3 and 18.0.
 constexpr int kUnitCost = 384;
-// A key tile of a two-tile unit against one of a one-tile unit: a step of 16 decoding sequences and a
-// 512-row chunk takes 68 us; 1.2 gives 72, 2.0 70.
+// A key tile of a two-tile unit against one of a one-tile unit: the mixed step takes 68.5 us (1.2: 72.3, 2.0:
+// 70.0), at d = 64 51.7 us (54.6, 57.0).
 constexpr float kPairCost = 1.5f;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kIssueUnroll = 4;  // k-steps of a product in a row: 2 and 8 are within 2 %, 1 is 13 % slower

@@ -283,13 +283,18 @@ ATTN_API attn_status_t attn_decode(const attn_decode_params *p, void *stream);
  * j <= L - n + i. causal = 0: every row sees all L keys (a decoder's rows
  * against an encoder's states of another length, kept in the same pages).
  * A row that sees no key (L = 0, or i < n - L) gets O = 0 and LSE = -inf.
- * n = 0 is allowed. Rows of q from cu_q[num_seqs] to total_q (padding) are not
- * read, and their O and LSE are left as they were. cu_q[0] must be 0 and cu_q
- * must not decrease. Slots of the last page beyond L are not used: they may
- * hold anything, NaN too.
+ * n = 0 is allowed. Rows of q from cu_q[num_seqs] to total_q (padding) may be
+ * read but reach no result (they may hold anything, NaN too), and their O and LSE
+ * are left as they were. cu_q[0] must be 0 and cu_q must not decrease. Slots of
+ * the last page beyond L are not used: they may hold anything, NaN too. o may be
+ * q itself, with the same strides.
+ * A row with a NaN among the scores it sees gets NaN in O and LSE. A V row that
+ * is not finite may reach O of every row of its sequence, those too that causal
+ * keeps from seeing it (a probability of 0 times it); LSE does not depend on V.
  *
- * Results depend on a call's lengths only through the order of fp32 sums, and
- * are the same bits for the same inputs on a given GPU model.
+ * The same call gives the same bits on a given GPU model. Lengths, max_q and the
+ * table's width (one tile shape is for tables of up to 384 keys) choose the order
+ * of the fp32 sums, and so may change the last bits.
  */
 typedef struct attn_paged_params {
     int32_t num_seqs;        /* at most 2^31 - 1024 */
@@ -331,7 +336,8 @@ ATTN_API attn_status_t attn_paged(const attn_paged_params *p, void *stream);
  * Stores keys and values of new tokens: row t of k and v goes to slot
  * slots[t] % page_size of page slots[t] / page_size, for every head. Rows whose
  * slot is negative are skipped. Slots named twice in one call end up holding
- * either row's values, piece by piece: name each once.
+ * either row's values, piece by piece: name each once. k and v may lie in the
+ * caches, but not in a slot that the call writes.
  */
 typedef struct attn_pages_write_params {
     int32_t rows;            /* rows of k and v */

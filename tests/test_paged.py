@@ -151,6 +151,30 @@ def test_output_rows_aligned_to_16_bytes_only(A, n, d):
     assert torch.all(flat[:8] == 0)
 
 
+@pytest.mark.parametrize("n,max_q", [(1, 1), (3, 3), (3, 2), (200, 200)])
+def test_output_over_q(A, n, max_q):
+    # the tiles of neighbouring sequences overlap in the rows that they load, not in those that they write
+    c = Case([n] * 5, [n + 200, n, 3000, n + 1, n + 130], 2, 3, 128, 16, torch.bfloat16, 66, pad=2)
+    args = c.device()
+    want, want_lse = A.attn_paged(*args, causal=True, max_q=max_q)
+    o, lse = A.attn_paged(*args, causal=True, max_q=max_q, out=args[0])
+    _ok(A)
+    rows = 5 * n
+    assert o is args[0] and torch.equal(o[:rows], want[:rows]) and torch.equal(lse[:, :rows], want_lse[:, :rows])
+    assert torch.equal(o[rows:].cpu(), c.q[rows:])
+    c.check(o, lse, True)
+
+
+def test_write_from_other_slots_of_the_cache(A):
+    # a page moved within the caches: its rows are k and v, the slots another page's
+    kc, vc = (W.random_tensor((4, 16, 3, 64), 67 + i, torch.float16).cuda() for i in range(2))
+    before = [t.clone() for t in (kc, vc)]
+    A.attn_pages_write(kc[2], vc[2], torch.arange(16, 32, dtype=torch.int32, device="cuda"), kc.transpose(1, 2), vc.transpose(1, 2))
+    _ok(A)
+    for t, was in zip((kc, vc), before):
+        assert torch.equal(t[1], was[2]) and torch.equal(t[[0, 2, 3]], was[[0, 2, 3]])
+
+
 def test_keys_and_values_in_different_page_orders(A):
     c = Case([2, 1], [90, 40], 2, 3, 64, 16, torch.bfloat16, 63)
     q, k, v, table, cu, kv = c.device()
