@@ -445,6 +445,36 @@ def test_captured_call_follows_the_lengths(A):
         c.check(out, lse, True)
 
 
+def test_two_captured_calls_and_an_eager_one_at_once(A):
+    # each capture allocates a workspace of its own, and the default stream's is neither
+    cases = [Case([1] * 6, [3000, 10, 900, 1, 128, 2048], 2, 4, 64, 32, torch.bfloat16, 121),
+             Case([200, 1], [900, 1500], 2, 4, 64, 32, torch.bfloat16, 122)]
+    args = [c.device() for c in cases]
+    want = [A.attn_paged(*a, causal=True, max_q=max(c.n)) for a, c in zip(args, cases)]
+    _ok(A)
+    graphs, got, side = [], [], [torch.cuda.Stream() for _ in cases]
+    for a, c in zip(args, cases):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(A.attn_paged(*a, causal=True, max_q=max(c.n)))
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for o, lse in got:
+            o.fill_(9.0)
+            lse.fill_(9.0)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, side):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = A.attn_paged(*args[1], causal=True, max_q=200)
+        _ok(A)
+        for (o, lse), (w, wl) in zip(got + [eager], want + [want[1]]):
+            assert torch.equal(o, w) and torch.equal(lse, wl)
+    for c, (o, lse) in zip(cases, got):
+        c.check(o, lse, True)
+
+
 def test_longest_table(A):
     # as many keys as a table may have: four pages named over and over. Softmax weights are the pages'
     # multiplicities times exp(s). O's accumulator takes 8 products of 16 keys a tile, each rounded or
