@@ -434,7 +434,9 @@ ATTN_API const char *attn_last_error(void);
 
 /* Upper bound, in nanoseconds, on any single in-kernel wait (mbarrier or
  * pipeline slot) before the kernel records ATTN_ERR_TIMEOUT and returns.
- * Default 2e9 (2 s); values below 1e6 are raised to 1e6. Process-wide. */
+ * Default 2e9 (2 s); values below 1e6 are raised to 1e6. Process-wide. A wait may
+ * last while one CTA walks a sequence's keys, 1 to 1.6 us per 128 of them in
+ * attn_paged: beyond 100 million keys a sequence, raise it. */
 ATTN_API void attn_set_wait_timeout_ns(uint64_t ns);
 
 /* Test hook for failure detection: when > 0, the next forward and paged
