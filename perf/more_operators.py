@@ -18,7 +18,7 @@ import torch
 own = False
 
 _TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
-_LEAST, _MOST = -119, 120  # exponents of the scales
+_LEAST, _MOST = -119, 119  # exponents of the scales
 
 
 # ---------------------------------------------------------------- the cases
