@@ -8,6 +8,11 @@ thin Python binding.
     cu_q, kv_len, slots, pos, left = attn_pages_plan(q_len, cached, table, free, count, 64, rows)  # paged cache
     attn_pages_write(k, v, slots, k_cache, v_cache)
     o2, lse2 = attn_paged(q2, k_cache, v_cache, table, cu_q, kv_len, causal=True)  # q2: [rows, Hq, d]
+    qr, kr = attn_rotary(q2, k, pos, rotary_frequencies(128))        # rotary positions; attn_rotary_bwd: their gradients
+    attn_pages_write_fp8(kr, v, slots, k8_cache, v8_cache, k_scale, v_scale)  # the same cache in 8 bits
+    o3, lse3 = attn_paged_fp8(qr, k8_cache, v8_cache, k_scale, v_scale, table, cu_q, kv_len, causal=True)
+    tree, pos = attn_tree_plan(parents, cu_q, kv_len, 64)            # trees of drafted tokens
+    o4, lse4 = attn_paged_tree(q2, k_cache, v_cache, table, cu_q, kv_len, tree)
     o8, lse8 = attn_fwd_fp8(q8, k8, v8, q_descale, k_descale, v_descale)  # E4M3 inputs, d = 128
 
 The kernels live in csrc/ (built in-tree by build.py); the public C header is
@@ -24,3 +29,8 @@ from ._paged import (  # noqa: F401
     PagedParams, PagesPlanParams, PagesReleaseParams, PagesWriteParams, attn_paged, attn_pages_plan,
     attn_pages_release, attn_pages_write, paged_workspace_size,
 )
+from ._paged8 import (  # noqa: F401
+    PagedFp8Params, PagedTreeParams, PagesFp8Params, TreePlanParams, attn_paged_fp8, attn_paged_tree, attn_pages_read_fp8,
+    attn_pages_write_fp8, attn_tree_plan, paged_fp8_workspace_size,
+)
+from ._rotary import RotaryParams, attn_rotary, attn_rotary_bwd, rotary_frequencies  # noqa: F401

@@ -39,7 +39,9 @@ STATUS_NAMES = {
 EXPORTED = ("attn_fwd", "attn_fwd_fp8", "attn_bwd", "attn_bwd_noalloc", "attn_bwd_deterministic", "attn_bwd_workspace_size",
             "attn_decode",
             "attn_decode_workspace_size", "attn_paged", "attn_paged_workspace_size", "attn_pages_write",
-            "attn_pages_plan", "attn_pages_release", "attn_status", "attn_last_error",
+            "attn_pages_plan", "attn_pages_release", "attn_pages_write_fp8", "attn_pages_read_fp8", "attn_tree_plan",
+            "attn_paged_tree", "attn_paged_fp8", "attn_paged_fp8_workspace_size", "attn_rotary", "attn_rotary_bwd",
+            "attn_status", "attn_last_error",
             "attn_set_wait_timeout_ns", "attn_debug_set_producer_stall", "attn_debug_set_bwd_events",
             "attn_debug_launch_count", "attn_debug_launch_name", "attn_version")
 

@@ -20,15 +20,15 @@ attn_status_t check_ints(const char* name, const void* p) {
     return ATTN_OK;
 }
 
-// 16-bit tensor with `n` strides over the extents `dims`; the last dimension is contiguous.
-attn_status_t check_strided(const char* name, const void* p, const int64_t* st, const int64_t* dims, int n) {
+// Tensor of `es`-byte elements with `n` strides over the extents `dims`; the last dimension is contiguous.
+attn_status_t check_strided(const char* name, const void* p, const int64_t* st, const int64_t* dims, int n, int es = 2) {
     if (!p) return report_error(ATTN_ERR_INVALID, "%s is NULL", name);
     if (misaligned(p, 16)) return report_error(ATTN_ERR_ALIGN, "%s is not 16-byte aligned", name);
     for (int i = 0; i < n; ++i) {
         if (dims[i] <= 1) continue;
         if (st[i] <= 0)
             return report_error(ATTN_ERR_INVALID, "%s stride[%d] = %lld is not positive", name, i, (long long)st[i]);
-        if (st[i] % 8 != 0)
+        if (st[i] % (16 / es) != 0)
             return report_error(ATTN_ERR_ALIGN, "%s stride[%d] = %lld elements is not a multiple of 16 bytes", name, i,
                                 (long long)st[i]);
         if (st[i] >= (1ll << 38)) return report_error(ATTN_ERR_UNSUPPORTED, "%s stride[%d] too large", name, i);
@@ -68,17 +68,32 @@ attn_status_t check_table(int32_t max_pages, int32_t page_size) {
 }
 
 attn_status_t check_cache(int32_t num_pages, int32_t page_size, int32_t heads, const void* k, const void* v,
-                          const int64_t* ks, const int64_t* vs) {
+                          const int64_t* ks, const int64_t* vs, int es = 2) {
     if (num_pages < 1) return report_error(ATTN_ERR_INVALID, "num_pages must be at least 1, got %d", num_pages);
     if ((int64_t)num_pages * page_size > INT32_MAX)
         return report_error(ATTN_ERR_UNSUPPORTED, "num_pages * page_size must stay below 2^31");
     const int64_t dims[3] = {num_pages, heads, page_size};
-    const attn_status_t st = check_strided("k_cache", k, ks, dims, 3);
-    return st != ATTN_OK ? st : check_strided("v_cache", v, vs, dims, 3);
+    const attn_status_t st = check_strided("k_cache", k, ks, dims, 3, es);
+    return st != ATTN_OK ? st : check_strided("v_cache", v, vs, dims, 3, es);
+}
+
+// Scales of an 8-bit cache: [pages, heads, page_size] bytes, the slots contiguous.
+attn_status_t check_scales(int32_t num_pages, int32_t heads, const void* k, const void* v, const int64_t* ks, const int64_t* vs) {
+    const int64_t dims[2] = {num_pages, heads};
+    const attn_status_t st = check_strided("k_scale", k, ks, dims, 2, 1);
+    return st != ATTN_OK ? st : check_strided("v_scale", v, vs, dims, 2, 1);
+}
+
+// Bits of trees, a row of `words` for each of the call's rows.
+attn_status_t check_mask(const int32_t* mask, int64_t stride, int32_t words) {
+    if (words < 1 || words > 32) return report_error(ATTN_ERR_INVALID, "words must be 1 to 32, got %d", words);
+    if (stride < 0) return report_error(ATTN_ERR_INVALID, "mask_stride must not be negative");
+    if (stride >= (1ll << 38)) return report_error(ATTN_ERR_UNSUPPORTED, "mask_stride too large");
+    return check_ints("mask", mask);
 }
 
 // All of a paged attention call but the workspace. *empty = nothing to compute.
-attn_status_t check_paged(const attn_paged_params* p, bool* empty) {
+attn_status_t check_paged(const attn_paged_params* p, bool* empty, int es = 2) {
     if (!p) return report_error(ATTN_ERR_INVALID, "params is NULL");
     if (p->num_seqs < 0 || p->total_q < 0 || p->num_q_heads < 1 || p->num_kv_heads < 1)
         return report_error(ATTN_ERR_INVALID, "bad size num_seqs=%d total_q=%d num_q_heads=%d num_kv_heads=%d", p->num_seqs,
@@ -107,13 +122,45 @@ attn_status_t check_paged(const attn_paged_params* p, bool* empty) {
     const int64_t rows[2] = {p->total_q, p->num_q_heads};
     if ((st = check_strided("q", p->q, p->q_stride, rows, 2)) != ATTN_OK) return st;
     if ((st = check_strided("o", p->o, p->o_stride, rows, 2)) != ATTN_OK) return st;
-    if ((st = check_cache(p->num_pages, p->page_size, p->num_kv_heads, p->k_cache, p->v_cache, p->k_stride,
-                          p->v_stride)) != ATTN_OK)
+    if ((st = check_cache(p->num_pages, p->page_size, p->num_kv_heads, p->k_cache, p->v_cache, p->k_stride, p->v_stride,
+                          es)) != ATTN_OK)
         return st;
     if ((st = check_ints("lse", p->lse)) != ATTN_OK) return st;
     if ((st = check_ints("cu_q", p->cu_q)) != ATTN_OK) return st;
     if ((st = check_ints("kv_len", p->kv_len)) != ATTN_OK) return st;
     return check_ints("block_table", p->block_table);
+}
+
+// A tree call's, on top.
+attn_status_t check_tree(const attn_paged_tree_params* p, bool* empty, int es = 2) {
+    if (!p) return report_error(ATTN_ERR_INVALID, "params is NULL");
+    if (p->reserved1 != 0) return report_error(ATTN_ERR_INVALID, "reserved1 must be 0");
+    attn_status_t st = check_paged(&p->f, empty, es);
+    if (st != ATTN_OK) return st;
+    if (p->f.causal != 0) return report_error(ATTN_ERR_INVALID, "causal must be 0 in a call of trees");
+    return *empty ? ATTN_OK : check_mask(p->mask, p->mask_stride, p->words);
+}
+
+attn_status_t check_fp8(const attn_paged_fp8_params* p, bool* empty) {
+    if (!p) return report_error(ATTN_ERR_INVALID, "params is NULL");
+    attn_status_t st;
+    if (p->t.mask) {
+        if ((st = check_tree(&p->t, empty, 1)) != ATTN_OK) return st;
+    } else {
+        if (p->t.words != 0 || p->t.mask_stride != 0 || p->t.reserved1 != 0)
+            return report_error(ATTN_ERR_INVALID, "words, mask_stride and reserved1 must be 0 without a mask");
+        if ((st = check_paged(&p->t.f, empty, 1)) != ATTN_OK) return st;
+    }
+    if (*empty) return ATTN_OK;
+    return check_scales(p->t.f.num_pages, p->t.f.num_kv_heads, p->k_scale, p->v_scale, p->k_scale_stride, p->v_scale_stride);
+}
+
+// The workspace of a paged attention call.
+attn_status_t check_workspace(const attn_paged_params& p, size_t need) {
+    if (!p.workspace || p.workspace_bytes < need)
+        return report_error(ATTN_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", p.workspace_bytes, need);
+    if (misaligned(p.workspace, 256)) return report_error(ATTN_ERR_ALIGN, "workspace is not 256-byte aligned");
+    return ATTN_OK;
 }
 
 // 32-bit integers that a table call reads or writes: `rows` of `n` side by side, `stride` apart.
@@ -167,11 +214,93 @@ attn_status_t attn_paged(const attn_paged_params* p, void* stream) {
     if (st != ATTN_OK || empty) return st;
     LaunchCommon lc;
     if ((st = launch_setup(&lc)) != ATTN_OK) return st;
-    const size_t need = paged_workspace_bytes(*p, lc.num_sms);
-    if (!p->workspace || p->workspace_bytes < need)
-        return report_error(ATTN_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", p->workspace_bytes, need);
-    if (misaligned(p->workspace, 256)) return report_error(ATTN_ERR_ALIGN, "workspace is not 256-byte aligned");
+    if ((st = check_workspace(*p, paged_workspace_bytes(*p, lc.num_sms))) != ATTN_OK) return st;
     return launch_paged(*p, lc, static_cast<cudaStream_t>(stream));
+}
+
+attn_status_t attn_paged_tree(const attn_paged_tree_params* p, void* stream) {
+    bool empty = false;
+    attn_status_t st = check_tree(p, &empty);
+    if (st != ATTN_OK || empty) return st;
+    LaunchCommon lc;
+    if ((st = launch_setup(&lc)) != ATTN_OK) return st;
+    if ((st = check_workspace(p->f, paged_workspace_bytes(p->f, lc.num_sms))) != ATTN_OK) return st;
+    return launch_paged_tree(*p, lc, static_cast<cudaStream_t>(stream));
+}
+
+size_t attn_paged_fp8_workspace_size(const attn_paged_fp8_params* p) {
+    bool empty = false;
+    if (check_fp8(p, &empty) != ATTN_OK || empty) return 0;
+    LaunchCommon lc;
+    if (launch_setup(&lc) != ATTN_OK) return 0;
+    return paged_workspace_bytes(p->t.f, lc.num_sms);
+}
+
+attn_status_t attn_paged_fp8(const attn_paged_fp8_params* p, void* stream) {
+    bool empty = false;
+    attn_status_t st = check_fp8(p, &empty);
+    if (st != ATTN_OK || empty) return st;
+    LaunchCommon lc;
+    if ((st = launch_setup(&lc)) != ATTN_OK) return st;
+    if ((st = check_workspace(p->t.f, paged_workspace_bytes(p->t.f, lc.num_sms))) != ATTN_OK) return st;
+    return launch_paged_fp8(*p, lc, static_cast<cudaStream_t>(stream));
+}
+
+static attn_status_t pages_fp8(const attn_pages_write_fp8_params* p, bool read, void* stream) {
+    if (!p) return report_error(ATTN_ERR_INVALID, "params is NULL");
+    if (p->rows < 0 || p->num_kv_heads < 1)
+        return report_error(ATTN_ERR_INVALID, "bad size rows=%d num_kv_heads=%d", p->rows, p->num_kv_heads);
+    if (p->reserved0[0] != 0 || p->reserved0[1] != 0) return report_error(ATTN_ERR_INVALID, "reserved0 must be 0");
+    attn_status_t st;
+    if ((st = check_16bit(p->dtype, p->d)) != ATTN_OK) return st;
+    if ((st = check_page_size(p->page_size)) != ATTN_OK) return st;
+    if (p->num_kv_heads > 65535) return report_error(ATTN_ERR_UNSUPPORTED, "num_kv_heads is limited to 65535");
+    if (p->rows == 0) return ATTN_OK;
+    const int64_t dims[2] = {p->rows, p->num_kv_heads};
+    if ((st = check_strided("k", p->k, p->k_row_stride, dims, 2)) != ATTN_OK) return st;
+    if ((st = check_strided("v", p->v, p->v_row_stride, dims, 2)) != ATTN_OK) return st;
+    if ((st = check_ints("slots", p->slots)) != ATTN_OK) return st;
+    if ((st = check_cache(p->num_pages, p->page_size, p->num_kv_heads, p->k_cache, p->v_cache, p->k_stride, p->v_stride, 1)) !=
+        ATTN_OK)
+        return st;
+    if ((st = check_scales(p->num_pages, p->num_kv_heads, p->k_scale, p->v_scale, p->k_scale_stride, p->v_scale_stride)) != ATTN_OK)
+        return st;
+    if ((int64_t)p->rows * p->num_kv_heads > (int64_t)INT32_MAX * 32)  // blocks of 32 (row, head)s
+        return report_error(ATTN_ERR_UNSUPPORTED, "rows * num_kv_heads must stay below 2^36");
+    LaunchCommon lc;
+    if ((st = launch_setup(&lc)) != ATTN_OK) return st;
+    return launched(launch_pages_fp8(*p, read, lc, static_cast<cudaStream_t>(stream)),
+                    read ? "attn_pages_read_fp8" : "attn_pages_write_fp8");
+}
+
+attn_status_t attn_pages_write_fp8(const attn_pages_write_fp8_params* p, void* stream) { return pages_fp8(p, false, stream); }
+
+attn_status_t attn_pages_read_fp8(const attn_pages_write_fp8_params* p, void* stream) { return pages_fp8(p, true, stream); }
+
+attn_status_t attn_tree_plan(const attn_tree_plan_params* p, void* stream) {
+    if (!p) return report_error(ATTN_ERR_INVALID, "params is NULL");
+    if (p->num_seqs < 0 || p->total_q < 0)
+        return report_error(ATTN_ERR_INVALID, "negative size num_seqs=%d total_q=%d", p->num_seqs, p->total_q);
+    if (p->reserved0 != 0) return report_error(ATTN_ERR_INVALID, "reserved0 must be 0");
+    attn_status_t st;
+    if ((st = check_count("num_seqs", p->num_seqs)) != ATTN_OK) return st;
+    if ((st = check_count("total_q", p->total_q)) != ATTN_OK) return st;
+    if (p->words < 1 || p->words > 32) return report_error(ATTN_ERR_INVALID, "words must be 1 to 32, got %d", p->words);
+    if (p->total_q == 0) return ATTN_OK;
+    if (p->mask_stride < p->words) return report_error(ATTN_ERR_INVALID, "mask_stride must be at least words");
+    if (p->mask_stride >= (1ll << 38)) return report_error(ATTN_ERR_UNSUPPORTED, "mask_stride too large");
+    if ((st = check_ints("parents", p->parents)) != ATTN_OK) return st;
+    if ((st = check_ints("cu_q", p->cu_q)) != ATTN_OK) return st;
+    if (p->num_seqs > 0 && (st = check_ints("kv_len", p->kv_len)) != ATTN_OK) return st;
+    if ((st = check_ints("mask", p->mask)) != ATTN_OK) return st;
+    if ((st = check_ints("positions", p->positions)) != ATTN_OK) return st;
+    const int64_t seqs = p->num_seqs, rows = p->total_q;
+    const Ints arrays[] = {{"mask", p->mask, p->words, rows, p->mask_stride}, {"positions", p->positions, rows},
+                           {"parents", p->parents, rows}, {"cu_q", p->cu_q, seqs + 1}, {"kv_len", p->kv_len, seqs}};
+    if ((st = check_apart(arrays, 2)) != ATTN_OK) return st;
+    LaunchCommon lc;
+    if ((st = launch_setup(&lc)) != ATTN_OK) return st;
+    return launched(launch_tree_plan(*p, lc, static_cast<cudaStream_t>(stream)), "attn_tree_plan");
 }
 
 attn_status_t attn_pages_write(const attn_pages_write_params* p, void* stream) {

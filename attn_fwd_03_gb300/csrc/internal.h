@@ -6,6 +6,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
 
 #include "../../include/attn.h"
 
@@ -142,6 +143,16 @@ cudaError_t launch_bwd_dq(const attn_bwd_params& p, const BwdMaps& maps, const B
 // attn_paged.cu — attention over a paged cache.
 size_t paged_workspace_bytes(const attn_paged_params& p, int num_sms);
 attn_status_t launch_paged(const attn_paged_params& p, const LaunchCommon& lc, cudaStream_t s);
+std::mutex& paged_launch_mutex();  // of all variants: their calls may share a workspace
+// attn_paged_tree.cu, attn_paged_fp8.cu — its variants; their workspace is attn_paged's.
+attn_status_t launch_paged_tree(const attn_paged_tree_params& p, const LaunchCommon& lc, cudaStream_t s);
+attn_status_t launch_paged_fp8(const attn_paged_fp8_params& p, const LaunchCommon& lc, cudaStream_t s);
+
+// attn_pages_fp8.cu — writes to an 8-bit cache, and rows read back from one.
+cudaError_t launch_pages_fp8(const attn_pages_write_fp8_params& p, bool read, const LaunchCommon& lc, cudaStream_t s);
+
+// attn_tree.cu — masks and positions of trees of drafted tokens.
+cudaError_t launch_tree_plan(const attn_tree_plan_params& p, const LaunchCommon& lc, cudaStream_t s);
 
 // attn_pages.cu — the paged cache's tables and writes.
 cudaError_t launch_pages_write(const attn_pages_write_params& p, const LaunchCommon& lc, cudaStream_t s);

@@ -421,6 +421,152 @@ typedef struct attn_pages_release_params {
 
 ATTN_API attn_status_t attn_pages_release(const attn_pages_release_params *p, void *stream);
 
+/*
+ * The paged cache in 8 bits. A row of d values (one token and head, keys and values
+ * apart) is held as E4M3 codes and one power of two, its scale: the smallest
+ * 2^e, e in [-119, 119], with max|x| <= 448 * 2^e; code = x / 2^e rounded to nearest
+ * even. A power of two keeps the quotient exact (the only rounding is the code's, at most
+ * 2^-4 of the value, or 2^-10 * 2^e below 2^-6 * 2^e), and code * 2^e is a bf16 number, so
+ * attention works on exactly the values that the cache stands for. The codes' caches are
+ * laid out as those of 16 bits, one byte per element; scales are one byte each, e + 127 (the
+ * E8M0 format), in [num_pages, num_kv_heads, page_size] with the slots contiguous. bf16
+ * and fp16 rows, head dims 64 and 128.
+ * A NaN is held as NaN, and does not count for the scale; values beyond 448 * 2^119,
+ * infinities among them, are held as that.
+ */
+
+/*
+ * Stores keys and values of new tokens in 8 bits, as attn_pages_write stores them in 16.
+ * Rows whose slot is negative are skipped; slots named twice in one call end up
+ * holding either row, piece by piece.
+ */
+typedef struct attn_pages_write_fp8_params {
+    int32_t rows, num_kv_heads;
+    int32_t d;               /* 64 or 128 */
+    int32_t num_pages, page_size;  /* num_pages * page_size < 2^31 */
+    int32_t dtype;           /* ATTN_BF16 or ATTN_F16: type of k and v */
+    int32_t reserved0[2];    /* must be 0 */
+    const void *k, *v;       /* [rows, num_kv_heads, d] */
+    const int32_t *slots;    /* [rows] */
+    void *k_cache, *v_cache; /* E4M3 codes, [num_pages, num_kv_heads, page_size, d] */
+    void *k_scale, *v_scale; /* E8M0 bytes, [num_pages, num_kv_heads, page_size] */
+    int64_t k_row_stride[2], v_row_stride[2];  /* elements, (row, head) */
+    int64_t k_stride[3], v_stride[3];          /* bytes, (page, head, slot): multiples of 16 */
+    int64_t k_scale_stride[2], v_scale_stride[2];  /* bytes, (page, head): multiples of 16 */
+} attn_pages_write_fp8_params;
+
+ATTN_API attn_status_t attn_pages_write_fp8(const attn_pages_write_fp8_params *p, void *stream);
+
+/*
+ * Reads keys and values of an 8-bit cache back into 16-bit rows, by the same struct: row t of
+ * k and v (written here) becomes code * scale of slot slots[t], rounded to the rows' type
+ * (exact in bf16; values beyond fp16's range become infinities). Rows whose slot is
+ * negative are left as they were. The same slot may be named any number of times.
+ */
+ATTN_API attn_status_t attn_pages_read_fp8(const attn_pages_write_fp8_params *p, void *stream);
+
+/*
+ * Trees of drafted tokens. A sequence may bring the nodes of a tree in place of a run
+ * of tokens: node i (its i-th new row) follows node parents[i] < i, or the context where
+ * that is -1. Its keys are the context, its ancestors and itself. attn_tree_plan turns the
+ * parents into what attention and rotary positions need: for each row its visible nodes
+ * as bits (bit c % 32 of word c / 32: node c) and its position, the context's length plus
+ * its depth.
+ * A sequence of more than 32 * words rows is a chunk of a prompt that shares the
+ * step: its parents are not read, its words are 0 and its positions consecutive; the
+ * attention calls treat it as causal.
+ * Rows from cu_q[num_seqs] to total_q get words 0 and position -1. Parents that are
+ * not below their node or below -1 are taken as -1 and reported (ATTN_ERR_INVALID), and so
+ * are fewer keys than rows.
+ */
+typedef struct attn_tree_plan_params {
+    int32_t num_seqs;        /* at most 2^31 - 1024 */
+    int32_t total_q;         /* at most 2^31 - 1024 */
+    int32_t words;           /* of a row, 1 to 32 */
+    int32_t reserved0;       /* must be 0 */
+    const int32_t *parents;  /* [total_q] */
+    const int32_t *cu_q;     /* [num_seqs + 1] */
+    const int32_t *kv_len;   /* [num_seqs]: keys with the new rows' own */
+    int32_t *mask;           /* [total_q, words] */
+    int64_t mask_stride;     /* elements from one row to the next, >= words */
+    int32_t *positions;      /* [total_q] */
+} attn_tree_plan_params;
+
+ATTN_API attn_status_t attn_tree_plan(const attn_tree_plan_params *p, void *stream);
+
+/*
+ * attn_paged for trees: row i of a sequence of up to 32 * words rows sees its context (keys
+ * j < L - n) and, of its new rows' keys, L - n + c for every c < n whose bit is set in
+ * the row's words. Any bits are allowed, below or above the row's own; a row that
+ * sees no key gets O = 0 and LSE = -inf. Sequences with more rows than the mask has bits are
+ * causal, as attn_paged has it. `f.causal` must be 0. Workspace and everything else as
+ * attn_paged (attn_paged_workspace_size(&f)).
+ */
+typedef struct attn_paged_tree_params {
+    attn_paged_params f;
+    const int32_t *mask;     /* [total_q, words] */
+    int64_t mask_stride;     /* elements from one row to the next; 0 = one row for all */
+    int32_t words;           /* 1 to 32 */
+    int32_t reserved1;       /* must be 0 */
+} attn_paged_tree_params;
+
+ATTN_API attn_status_t attn_paged_tree(const attn_paged_tree_params *p, void *stream);
+
+/*
+ * Attention over a paged cache in 8 bits, of a run of tokens (t.mask NULL; t.words, t.mask_stride
+ * 0) or of trees (t.mask given). t.f as for attn_paged, with f.dtype the type of q and o, the
+ * caches E4M3 codes and k_stride, v_stride in bytes. Keys and values are code * scale, made in
+ * f.dtype on chip: exact in bf16; in fp16 they have to be within its range, and are rounded below
+ * 2^-14. The products, the softmax and their accuracy are attn_paged's. Slots beyond a
+ * sequence's length may hold any codes and scales.
+ */
+typedef struct attn_paged_fp8_params {
+    attn_paged_tree_params t;
+    const void *k_scale, *v_scale;  /* E8M0 bytes, [num_pages, num_kv_heads, page_size], 16-byte aligned */
+    int64_t k_scale_stride[2], v_scale_stride[2];  /* bytes, (page, head): multiples of 16 */
+} attn_paged_fp8_params;
+
+/* Bytes of workspace attn_paged_fp8 needs: a bound of the same kind as attn_paged's. */
+ATTN_API size_t attn_paged_fp8_workspace_size(const attn_paged_fp8_params *p);
+
+ATTN_API attn_status_t attn_paged_fp8(const attn_paged_fp8_params *p, void *stream);
+
+/*
+ * Rotary positions of queries and keys, in one launch. Pair i < rotary_dim / 2 of a row at
+ * position x is turned by the angle t = x * inv_freq[i]:
+ *   y0 = magnitude * (x0 cos t - x1 sin t),  y1 = magnitude * (x1 cos t + x0 sin t),
+ * where the pair is columns (i, i + rotary_dim / 2) or, interleaved, (2 i, 2 i + 1). Columns from
+ * rotary_dim on are copied. Angles are taken modulo a turn in 64-bit integers, to 2^-32 of a
+ * turn for any 32-bit position and |inv_freq| < 2^32, and sums in fp32, rounded once.
+ * Tensors are [B, H, N, d] as for attn_fwd (a ragged batch of rows [N, H, d] is B = 1); bf16, fp16
+ * and fp32. Rows whose position is negative (the padding of attn_pages_plan and
+ * attn_tree_plan) are left as they were in the outputs. An output may be its input, with the
+ * same strides; otherwise the two share no memory.
+ */
+typedef struct attn_rotary_params {
+    int32_t B, N;
+    int32_t Hq, Hk;          /* heads of q and of k; either may be 0, and its pointers are not read then */
+    int32_t d;               /* a multiple of 16, up to 256 */
+    int32_t rotary_dim;      /* a multiple of 16, up to d */
+    int32_t dtype;           /* ATTN_BF16, ATTN_F16 or ATTN_F32 */
+    int32_t interleaved;     /* 0 or 1 */
+    float magnitude;         /* > 0 */
+    int32_t reserved0;       /* must be 0 */
+    const int32_t *positions;
+    int64_t position_stride[2];  /* elements, (b, n); 0 broadcasts */
+    const float *inv_freq;   /* [rotary_dim / 2] */
+    const void *q, *k;
+    void *q_out, *k_out;
+    int64_t q_stride[3], k_stride[3], q_out_stride[3], k_out_stride[3];  /* elements, (b, h, n) */
+} attn_rotary_params;
+
+ATTN_API attn_status_t attn_rotary(const attn_rotary_params *p, void *stream);
+
+/* The backward pass of attn_rotary: q and k hold the gradients of its outputs, q_out and k_out
+ * receive those of its inputs (the transpose: the same turn, backwards; columns from rotary_dim on
+ * are copied). Rows whose position is negative are left as they were. */
+ATTN_API attn_status_t attn_rotary_bwd(const attn_rotary_params *p, void *stream);
+
 /* Synchronizes `stream`, then reports (and clears) the current device's
  * error word: ATTN_ERR_TIMEOUT if a kernel gave up on a bounded wait since
  * the last call (outputs of calls since then are unspecified; their inputs and
