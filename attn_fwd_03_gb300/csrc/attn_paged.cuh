@@ -85,6 +85,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "ptx_f8.cuh"
 
 namespace attn {
 namespace {
@@ -117,8 +118,7 @@ constexpr int kFewRows = 32, kFewKeys = 384;
 // Variants of each: kRun attends to runs of tokens over a 16-bit cache, kTree to trees (each row has bits
 // that say which of the sequence's new rows it sees), kBytes to either over a cache of E4M3 codes.
 //
-// kBytes: the producers fetch codes and scales into a ring of their own, and a warpgroup of converters makes
-// 16-bit tiles of them, in the layout that TMA would have given them, in the ring that the issuers read.
+// The roles of kBytes and what they do are further down, with its Cfg8.
 enum : int { kRun = 0, kTree = 1, kBytes = 2 };
 
 template <int D, int KERNEL, int VAR>
@@ -127,7 +127,8 @@ struct Shape {
     static constexpr int kTiles = KERNEL == kMixed ? 2 : 1;  // of a unit, at most
     static constexpr int kPerSm = !kF8 && (KERNEL == kFew || (KERNEL == kOne && D == 64)) ? 2 : 1;
     static constexpr int kFirst = 4 * kTiles;  // the first warp behind the softmax warps
-    static constexpr int kThreads = (KERNEL == kMixed ? 384 : 256) + (kF8 ? 128 : 0);
+    static constexpr int kConverters = !kF8 ? 0 : KERNEL == kMixed ? 4 : 8;  // warps
+    static constexpr int kThreads = (KERNEL == kMixed ? 384 : 256) + 32 * kConverters;
     // shared memory for Q, K and V tiles
     static constexpr int kTilesBytes = (KERNEL == kFew ? 104 : kPerSm == 2 ? 96 : 224) * 1024;
     static constexpr int kSmemBytes = kTilesBytes + 2048 + 1024;  // barriers and schedule + alignment slack
@@ -136,8 +137,8 @@ struct Shape {
     // registers per thread after the rebalance: the softmax warps hold a row of scores each
     static constexpr bool kRebalance = KERNEL == kMixed || kPerSm == 2 || kF8;
     static constexpr int kLaunchRegs = kThreads * kPerSm == 384 ? 168 : 128;
-    static constexpr int kSoftmaxRegs = KERNEL != kMixed ? (kF8 ? 216 : 184) : D == 64 || kF8 ? 192 : 200;
-    static constexpr int kOtherRegs = KERNEL != kMixed ? (kF8 ? 144 : 72) : kF8 ? 64 : D == 64 ? 120 : 104;
+    static constexpr int kSoftmaxRegs = KERNEL != kMixed ? (kF8 ? 240 : 184) : D == 64 || kF8 ? 192 : 200;
+    static constexpr int kOtherRegs = KERNEL != kMixed ? (kF8 ? 88 : 72) : kF8 ? 64 : D == 64 ? 120 : 104;
     static_assert(!kRebalance || 4 * kTiles * kSoftmaxRegs + (kThreads / 32 - 4 * kTiles) * kOtherRegs <= kThreads / 32 * kLaunchRegs,
                   "register split");
 };
@@ -161,14 +162,7 @@ struct Cfg {
     static constexpr int kQTiles = NT == 1 ? 1 : D == 128 ? 2 : 4;
     static constexpr int kQBytes = KERNEL == kFew ? kFewRows * D * 2 : kQTiles * kTileBytes;
     static constexpr int kKVOff = kQOff + kQBytes;
-    // K and V tiles in flight; of 8-bit caches 16-bit tiles, and then tiles of codes with a byte of scale a row
-    static constexpr int kStages = kF8 ? (D == 64 ? 4 : 3) : (Kernel::kTilesBytes - kKVOff) / kTileBytes;
-    static constexpr int kRawOff = kKVOff + kStages * kTileBytes;
-    static constexpr int kRawBytes = BN * D + BN;
-    static constexpr int kRawRoom = (Kernel::kTilesBytes - kRawOff) / kRawBytes;
-    static constexpr int kRawStages = !kF8 ? 0 : kRawRoom < 13 ? kRawRoom : 13;
-    static constexpr int kFetched = kF8 ? kRawStages : kStages;  // of the ring that the producers fill
-    static_assert(!kF8 || kRawStages >= 3, "shared memory");
+    static constexpr int kStages = (Kernel::kTilesBytes - kKVOff) / kTileBytes;  // K and V tiles in flight
     // tensor-memory columns of tile t; S_t is at BN t
     static constexpr int o_col(int t) { return KERNEL == kFew ? 128 : NT == 1 && D == 64 ? 192 : 256 + D * t; }
     static constexpr int p_col(int t) { return !kSplit ? BN * t : NT == 1 && D == 64 ? 128 : 384 + 64 * t; }
@@ -176,8 +170,47 @@ struct Cfg {
     // warps: K (and V) producer, MMA issuer, Q producer and V tail; the fourth is the V producer, except where
     // it has to issue the second tile's products
     static constexpr int kProducer = Kernel::kFirst, kIssuer = kProducer + 1, kTail = kProducer + 2;
-    static constexpr int kFourth = kProducer + 3, kConvert = kProducer + 4;
+    static constexpr int kFourth = kProducer + 3;
     static constexpr bool kVProducer = kIssuers == 1;
+};
+
+// A CTA of the kBytes variant that works on units of NT tiles.
+//
+// Keys go to the tensor cores as the codes they are, since a product of E4M3 codes is exact in fp32: Q is split
+// into kPieces 8-bit numbers whose sum it is (split_pair), and S is the sum of their products with the codes,
+// times the key's scale and the row's. Values are widened to 16 bits by a group of converter warps, scales
+// included: P in 8 bits would not do, since pieces of it would lose the many small probabilities of a long row.
+//
+// Widening the keys too, with Q as it is, takes 335 us for 64 sequences of 8192 keys: the converters' integer
+// instructions issue at 64 lanes a cycle.
+template <int D, bool F16, int NT, int KERNEL>
+struct Cfg8 {
+    using Kernel = Shape<D, KERNEL, kBytes>;
+    static constexpr int kTileBytes = BN * D;      // of codes
+    static constexpr int kPieces = F16 ? 3 : 2;    // of 4, 4 and 3 bits of Q's 11 or 8
+    // Q's pieces in tensor memory where there are columns left: a product then reads keys alone from shared memory
+    static constexpr bool kQTmem = NT == 1;
+    static constexpr int kQCol = D == 128 ? 128 : 256;
+    static constexpr int kQBytes = kQTmem ? 0 : NT * kPieces * kTileBytes;
+    // widened values, then rings of codes and of their scales, and the keys' scales as floats
+    static constexpr int kWide = D == 128 ? 2 : 3;
+    static constexpr int kWideOff = kQBytes, kKeyOff = kWideOff + kWide * 2 * kTileBytes;
+    // for units of one tile: where copies of rows are merged (softmax_copies)
+    static constexpr int kStateBytes = NT == 1 ? 4 * 32 * 16 : 0, kMergeBytes = NT == 1 ? 4 * 32 * 36 * 4 : 0;
+    static constexpr int kRoom = Kernel::kTilesBytes - kKeyOff - kStateBytes - kMergeBytes;
+    static constexpr int kFit = (kRoom - 3 * BN * 4) / (kTileBytes + BN + BN * 2);
+    static constexpr int kBoth = kFit < 16 ? kFit : 16;
+    static constexpr int kKeys = (kBoth + 1) / 2, kValues = kBoth / 2;  // stages
+    static constexpr int kValueOff = kKeyOff + kKeys * kTileBytes;
+    static constexpr int kKeyScaleOff = kValueOff + kValues * kTileBytes, kValueScaleOff = kKeyScaleOff + kKeys * BN;
+    // Two stages more than keys have: a tile of keys arrives when the products with the one kKeys before it are done,
+    // and by then the softmax has read what came two before that (an issuer releases a tile of keys at most one
+    // tile ahead of the softmax's last read).
+    static constexpr int kFactors = kKeys + 2;
+    static constexpr int kFactorOff = kValueScaleOff + kValues * BN;
+    static constexpr int kStateOff = kFactorOff + kFactors * BN * 4, kMergeOff = kStateOff + kStateBytes;
+    static_assert(kValues >= 1 && kMergeOff + kMergeBytes <= Kernel::kTilesBytes, "shared memory");
+    static_assert(!kQTmem || kQCol + kPieces * D / 4 <= (D == 128 ? 256 : 512), "tensor memory");
 };
 
 struct PagedDev {
@@ -205,6 +238,8 @@ struct PagedDev {
     // kBytes: scales of keys and values, and their strides over (page, head)
     const uint8_t *k_scale, *v_scale;
     long long ks_page, ks_head, vs_page, vs_head;
+    const uint16_t* q;
+    long long q_sr, q_sh;  // elements
 };
 
 // What the combine kernel reads about a CTA's slot: x = 0 nothing, 1 a part, 2 the unit's last part;
@@ -225,9 +260,10 @@ struct Place {
 struct __align__(16) Shared {
     uint64_t q_full[4], q_empty[4];  // of the Q slots, which are used in turn
     uint64_t kv_full[13], kv_empty[13], v_tail[13];
-    uint64_t raw_full[13], raw_empty[13];  // of the tiles of codes
+    // kBytes: codes fetched, of keys their factors made, released; kv_full and kv_empty are the widened values'
+    uint64_t k_full[8], k_ready[8], k_empty[8], v_full[8], v_empty[8];
     uint64_t s_full[2], p_full[2], o_full[2], s_free[2], pv_done[2];
-    uint64_t drain[2];
+    uint64_t drain[2], merged;
     long long x0, x1;      // this CTA's piece of the line
     Place first;           // the unit that holds x0; u0 = -1 if there is none
     Place place[16];       // of each warp
@@ -235,7 +271,7 @@ struct __align__(16) Shared {
                            // head, 1 if it holds the first key tile + 2 if the last
     long long scan[2][16]; // per warp: its sequences' cost on either line
     int pair;              // whether this CTA works on two-tile units
-    int widest[16], sm_warps;  // most rows of a one-tile unit; softmax warps of a tile that hold rows
+    int widest[16], most_rows, sm_warps;  // most rows of a one-tile unit; softmax warps of a tile that hold rows
     uint32_t issued[2];    // ring items issued: of K (even numbers) all below the first, of V all below the second
     uint32_t tmem_base;
     int abort_flag;
@@ -385,6 +421,7 @@ __device__ __forceinline__ void locate(const PagedDev& p, Shared& sh) {
         sh.x0 = x0;
         sh.x1 = x1;
         sh.pair = pair;
+        sh.most_rows = rows;
         sh.sm_warps = max(1, ((pair ? p.tok_tile * p.G : rows) + 31) / 32);
     }
 }
@@ -544,24 +581,33 @@ struct QRing {
 // Waits for the last item issued into each slot (none was issued over one that had not landed). Out of line: short
 // units run the kernel's code cold, and what they never use costs them its place (512 sequences of 128 keys 59 us, 61
 // with it inline).
-__device__ __noinline__ void drain_ring(Shared& bar, uint64_t* full, uint32_t stages, uint64_t timeout_ns) {
+__device__ __noinline__ void drain_ring(Shared& bar, uint32_t stages, uint64_t timeout_ns) {
     const uint32_t end = max(bar.issued[0], bar.issued[1]);
     for (uint32_t s = 0; s < stages && s < end; ++s) {
         uint32_t i = s + (end - 1 - s) / stages * stages;
         while (i >= bar.issued[i & 1] && i >= stages) i -= stages;
-        if (i < bar.issued[i & 1]) drain_wait(&full[s], (i / stages) & 1, timeout_ns);
+        if (i < bar.issued[i & 1]) drain_wait(&bar.kv_full[s], (i / stages) & 1, timeout_ns);
+    }
+}
+
+// ---------------------------------------------------------------- trees
+// Bits of the 32 N keys from key0 on that a row sees, whose words are at `row` (NULL: none of the new rows).
+template <int N>
+__device__ __forceinline__ void tree_bits(const PagedDev& p, const uint32_t* row, int key0, int ctx, int len, uint32_t (&bits)[N]) {
+    const int rel = key0 - ctx;  // of the first key among the new rows'
+    const int at = rel >> 5;
+    uint32_t w[N + 1];
+#pragma unroll
+    for (int k = 0; k <= N; ++k) w[k] = at + k < 0 ? ~0u : at + k < p.tree_words && row ? row[at + k] : 0u;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        bits[k] = __funnelshift_r(w[k], w[k + 1], rel & 31);
+        const int held = len - key0 - 32 * k;
+        if (held < 32) bits[k] &= held <= 0 ? 0u : (1u << held) - 1;
     }
 }
 
 // ---------------------------------------------------------------- 8-bit caches
-// Two E4M3 codes, in the upper bytes of either half of x, as 16-bit values times a power of two: the sign and
-// the seven bits below it are the value's in either 16-bit type, 2^8 too small in fp16 and 2^120 too small in
-// bf16 (subnormal codes become subnormal values, to the same factor).
-template <bool F16>
-__device__ __forceinline__ uint32_t widen(uint32_t x) {
-    const uint32_t mag = x & 0x7f007f00u, sign = x & 0x80008000u;
-    return (F16 ? mag >> 1 : mag >> 4) | sign;
-}
 template <bool F16>
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -571,72 +617,686 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
         asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-// 2^x in both halves, x as the type has it.
-template <bool F16>
-__device__ __forceinline__ uint32_t power2(int x) {
-    uint32_t h;
-    if constexpr (F16)
-        h = x >= -14 ? (uint32_t)(min(x, 15) + 15) << 10 : x >= -24 ? 1u << (x + 24) : 0u;
-    else
-        h = (uint32_t)(x + 127) << 7;
-    return h * 0x10001u;
+__device__ __forceinline__ uint32_t mad(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
 }
 
-// Makes a quarter (of warp c) of a 16-bit tile from a tile of codes: rows of 128 bytes per 64 columns, 16-byte
-// chunks swizzled by the row as TMA does. Rows from `left` on become 0. A code times its scale is exact in
-// bf16; the factor that widen() leaves goes into the same multiplication, for scales up to 2^7 (others take a
-// second one).
-template <int D, bool F16>
-__device__ __forceinline__ void convert_tile(const uint8_t* raw, uint8_t* tile, int left, int c, int lane) {
-    constexpr int kLanes = D / 16, kAtOnce = 32 / kLanes;  // lanes of a row, rows of a warp's pass
-    constexpr int kOff = F16 ? 8 : 120;
-    const int ch = lane % kLanes;
-    const uint8_t* scales = raw + BN * D;
-#pragma unroll 4
-    for (int i = 0; i < BN / kAtOnce / 4; ++i) {
-        const int row = (i * 4 + c) * kAtOnce + lane / kLanes;
-        const uint4 v = *reinterpret_cast<const uint4*>(raw + row * D + ch * 16);
-        const int e = (int)scales[row] - 127;
-        const uint32_t f = power2<F16>(kOff + min(e, 7));
-        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-        uint32_t out[8];
+// 16 codes times the scale 2^(s - 127). fp16 has an instruction that widens codes. For bf16, the seven bits below
+// a code's sign are moved to where bf16 has exponent and fraction, which makes a number 2^120 too small
+// (subnormal codes become subnormal numbers, to the same factor), and the factor goes into the multiplication
+// by the scale; byte * 16 + sign * 240 moves the sign, too. Multiply-adds issue at 128 lanes a cycle, shifts and
+// logic at 64. Scales beyond 2^7 (not FAST) take a second multiplication.
+template <bool F16, bool FAST>
+__device__ __forceinline__ void widen16(uint4 v, int s, uint32_t (&out)[8]) {
+    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (F16) {
+        const float scale = __uint_as_float((uint32_t)s << 23);
+        const uint32_t f = pack_f16(scale, scale);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            out[2 * k] = mul2<F16>(widen<F16>(__byte_perm(in[k], 0, 0x1404)), f);
-            out[2 * k + 1] = mul2<F16>(widen<F16>(__byte_perm(in[k], 0, 0x3424)), f);
+        for (int k = 0; k < 8; ++k) {
+            uint32_t h;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(in[k / 2] >> (16 * (k & 1)))));
+            out[k] = mul2<true>(h, f);
         }
-        if (__any_sync(kFull, e > 7)) {
-            const uint32_t more = power2<F16>(max(e - 7, 0));
+    } else {
+        const uint32_t f = (uint32_t)((FAST ? s : min(s, 134)) + 120) * 0x800080u;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) out[k] = mul2<F16>(out[k], more);
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t b = __byte_perm(in[k / 2], 0, k & 1 ? 0x4342 : 0x4140);
+            out[k] = mul2<false>(mad(b & 0x00800080u, 240, mad(b, 16, 0)), f);
         }
-        if (row >= left) {
+        if constexpr (!FAST) {
+            const uint32_t more = (uint32_t)(max(s - 134, 0) + 127) * 0x800080u;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) out[k] = 0;
+            for (int k = 0; k < 8; ++k) out[k] = mul2<false>(out[k], more);
         }
-        uint8_t* dst = tile + (ch >> 2) * BN * 128 + row * 128;
-        const int k0 = (ch & 3) * 2, sw = row & 7;
-        // at d = 128 the lanes of a row's second box begin with the odd chunk: eight lanes then write to all banks
-        const bool odd = D == 128 && ch >= 4;
-        const uint4 lo = make_uint4(out[0], out[1], out[2], out[3]), hi = make_uint4(out[4], out[5], out[6], out[7]);
-        *reinterpret_cast<uint4*>(dst + ((k0 + (odd ? 1 : 0)) ^ sw) * 16) = odd ? hi : lo;
-        *reinterpret_cast<uint4*>(dst + ((k0 + (odd ? 0 : 1)) ^ sw) * 16) = odd ? lo : hi;
     }
 }
 
-// ---------------------------------------------------------------- trees
-// Bits of the 128 keys from key0 on that a row sees, whose words are at `row` (NULL: none of the new rows).
-__device__ __forceinline__ void tree_bits(const PagedDev& p, const uint32_t* row, int key0, int ctx, int len, uint32_t (&bits)[4]) {
-    const int rel = key0 - ctx;  // of the first key among the new rows'
-    const int at = rel >> 5;
-    uint32_t w[5];
+// Makes the share of warp c of W of a 16-bit tile from a tile of codes: rows of 128 bytes per 64 columns, 16-byte
+// chunks swizzled by the row as TMA does. Rows from `left` on become 0.
+// A lane has 16 codes of a row at a time, and the same row of every 8 and the same columns in all of its turns,
+// so that its addresses differ by constants. Eight lanes that access memory together read and write all
+// banks: at d = 128 (codes swizzled like the tile) four lanes on the first columns of a row and four on those of
+// the row that differs in bits 0 and 2, at d = 64 four on each of two rows.
+template <int D, bool F16, int W>
+__device__ __forceinline__ void widen_tile(const uint8_t* raw, const uint8_t* scale, uint8_t* tile, int left, int c, int lane) {
+    constexpr int kTurns = D == 128 ? 2 : 1;  // for 8 rows
+    constexpr int kRows = BN / W, kEach = kRows / 8;
+    const int ch = D == 128 ? (lane & 3) | (lane & 8) >> 1 : lane & 3;
+    const int r0 = D == 128 ? (lane >> 4) ^ (lane & 4 ? 5 : 0) : lane >> 2;
+    // scales that take a second multiplication are looked for once a tile
+    const uint32_t s4 = *reinterpret_cast<const uint32_t*>(scale + lane * 4);
+    const bool plain = (F16 || !__any_sync(kFull, __vcmpgtu4(s4, 0x86868686u) != 0)) && left >= BN;
 #pragma unroll
-    for (int k = 0; k < 5; ++k) w[k] = at + k < 0 ? ~0u : at + k < p.tree_words && row ? row[at + k] : 0u;
+    for (int turn = 0; turn < kTurns; ++turn) {
+        const int row7 = r0 ^ (turn * 2), row = c * kRows + row7;  // and every 8th row behind it
+        const uint8_t* from = raw + row * D + (D == 128 ? (ch ^ row7) * 16 : ch * 16);
+        uint8_t* to = tile + (ch >> 2) * BN * 128 + row * 128;
+        const int a0 = (((ch & 3) * 2) ^ row7) * 16, a1 = (((ch & 3) * 2 + 1) ^ row7) * 16;
+        if (plain) {
+            uint4 v[kEach];
+            int s[kEach];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        bits[k] = __funnelshift_r(w[k], w[k + 1], rel & 31);
-        const int held = len - key0 - 32 * k;
-        if (held < 32) bits[k] &= held <= 0 ? 0u : (1u << held) - 1;
+            for (int i = 0; i < kEach; ++i) {
+                v[i] = *reinterpret_cast<const uint4*>(from + i * 8 * D);
+                s[i] = scale[row + i * 8];
+            }
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                uint32_t out[8];
+                widen16<F16, true>(v[i], s[i], out);
+                *reinterpret_cast<uint4*>(to + i * 1024 + a0) = make_uint4(out[0], out[1], out[2], out[3]);
+                *reinterpret_cast<uint4*>(to + i * 1024 + a1) = make_uint4(out[4], out[5], out[6], out[7]);
+            }
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < kEach; ++i) {
+                uint32_t out[8];
+                widen16<F16, false>(*reinterpret_cast<const uint4*>(from + i * 8 * D), scale[row + i * 8], out);
+                if (row + i * 8 >= left) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) out[k] = 0;
+                }
+                *reinterpret_cast<uint4*>(to + i * 1024 + a0) = make_uint4(out[0], out[1], out[2], out[3]);
+                *reinterpret_cast<uint4*>(to + i * 1024 + a1) = make_uint4(out[4], out[5], out[6], out[7]);
+            }
+        }
+    }
+}
+
+// Two values of Q over the row's factor (at most 448) as sums of 8-bit numbers. The nearest E4M3 number leaves a
+// remainder of 4 bits less, whose nearest E4M3 number leaves nothing of a bf16 value; of an fp16 value it leaves
+// 3 bits, which E5M2 holds. All exact while the value is above 2^-2 (2^-6 in fp16), else to 2^-10 (2^-17): of a row's
+// largest value 2^-18 or less, where the row's fp32 sums end at 2^-24 of their largest term.
+template <bool F16>
+__device__ __forceinline__ void split_pair(uint32_t x, float f, uint16_t& a, uint16_t& b, uint16_t& c) {
+    const float2 y2 = fmul2(unpack_h16<F16>(x), make_float2(f, f));
+    uint32_t y = pack_f16(y2.x, y2.y), back;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(a) : "r"(y));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(a));
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(y) : "r"(back));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b) : "r"(y));
+    if constexpr (F16) {
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(b));
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(y) : "r"(back));
+        asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(c) : "r"(y));
+    }
+}
+
+// Splits a thread's row of Q (NULL: a row that nobody reads) into the pieces of its tile, in tensor memory at `tmem` or
+// in shared memory at `tile` as row r of K-major tiles, and returns the row's factor 2^e.
+template <int D, bool F16, bool TMEM>
+__device__ __forceinline__ float split_row(const uint16_t* src, uint32_t tmem, uint8_t* tile, int r) {
+    constexpr int kPieces = F16 ? 3 : 2;
+    uint32_t x[D / 2];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+        const uint4 v = src ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
+        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < D / 2; ++i) {
+        const uint32_t mag = x[i] & 0x7fff7fffu;
+        if constexpr (F16)
+            asm("max.f16x2 %0, %0, %1;" : "+r"(top) : "r"(mag));  // a NaN does not count
+        else
+            asm("max.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(mag));
+    }
+    const float2 t2 = unpack_h16<F16>(top);
+    // the smallest e with max <= 448 * 2^e, 448 = 1.75 * 2^8
+    const uint32_t bits = __float_as_uint(fmaxf(t2.x, t2.y));
+    const int e = min(max((int)(bits >> 23) - 135 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0), -119), 119);
+    const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int c0 = 0; c0 < D / 4; c0 += 16) {  // 64 columns at a time
+        uint32_t out[kPieces][16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            uint16_t a[2], b[2], c[2] = {0, 0};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) split_pair<F16>(x[2 * (c0 + i) + k], f, a[k], b[k], c[k]);
+            out[0][i] = a[0] | (uint32_t)a[1] << 16;
+            out[1][i] = b[0] | (uint32_t)b[1] << 16;
+            if constexpr (F16) out[kPieces - 1][i] = c[0] | (uint32_t)c[1] << 16;
+        }
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            if constexpr (TMEM) {
+                tmem_st16(tmem + k * (D / 4) + c0, out[k]);
+            } else {
+                uint8_t* dst = tile + k * BM * D + r * D;
+                const int sw = D == 128 ? r & 7 : (r >> 1) & 3;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4*>(dst + (((c0 / 4 + i) ^ sw) << 4)) =
+                        make_uint4(out[k][4 * i], out[k][4 * i + 1], out[k][4 * i + 2], out[k][4 * i + 3]);
+            }
+        }
+    }
+    if constexpr (TMEM) {
+        tmem_wait_st();
+        tc_fence_before();
+    } else {
+        fence_proxy_async_smem();
+    }
+    return __uint_as_float((uint32_t)(127 + e) << 23);
+}
+
+// Descriptor of a K-major tile of codes: rows of 128 bytes with the 128-byte swizzle, or of 64 with the 64-byte one
+// (layout 4). A product's k-step is 32 codes.
+template <int D>
+__device__ __forceinline__ uint64_t codes_desc(uint32_t tile) {
+    if constexpr (D == 128) return sdesc_sw128(tile, 16, 1024);
+    return (sdesc_sw128(tile, 16, 512) & ~((uint64_t)7 << 61)) | ((uint64_t)4 << 61);
+}
+
+// drain_ring for the rings of codes.
+__device__ __noinline__ void drain_codes(Shared& bar, uint32_t keys, uint32_t values, uint64_t timeout_ns) {
+    for (uint32_t s = 0; s < keys && s < bar.issued[0]; ++s)
+        drain_wait(&bar.k_full[s], ((bar.issued[0] - 1 - s) / keys) & 1, timeout_ns);
+    for (uint32_t s = 0; s < values && s < bar.issued[1]; ++s)
+        drain_wait(&bar.v_full[s], ((bar.issued[1] - 1 - s) / values) & 1, timeout_ns);
+}
+
+// The roles of kBytes but the softmax's.
+template <int D, bool F16, int NT, int KERNEL>
+__device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedDev& p, uint8_t* smem,
+                                       Shared& bar) {
+    using C = Cfg<D, NT, KERNEL, kBytes>;
+    using E = Cfg8<D, F16, NT, KERNEL>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const WaitCtl wc{p.err, &bar.abort_flag, p.timeout_ns};
+    const uint32_t tmem = bar.tmem_base;
+    Walk<NT, KERNEL, kBytes> walk(p, bar);
+    Unit w;
+    constexpr int kConvert = C::kProducer + 4;
+    // Scores of tile t with the keys of stage s: the sum over Q's pieces.
+    auto issue_s = [&](int t, uint32_t s) {
+        constexpr uint32_t kIdesc = ptx_f8::idesc_e4m3(BM, BN, false, false);
+        const uint64_t kd = codes_desc<D>(smem_u32(smem + E::kKeyOff + s * E::kTileBytes));
+#pragma unroll
+        for (int piece = 0; piece < E::kPieces; ++piece) {
+            const uint32_t idesc = piece == 2 ? kIdesc | 1u << 7 : kIdesc;  // A in E5M2
+            const uint64_t qd = codes_desc<D>(smem_u32(smem + (t * E::kPieces + piece) * E::kTileBytes));
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk) {
+                const uint32_t more = piece > 0 || kk > 0 ? 1u : 0u;
+                if constexpr (E::kQTmem)
+                    ptx_f8::mma_f8_ts(tmem + t * BN, tmem + E::kQCol + piece * (D / 4) + kk * 8, step_desc(kd, kk * 2), idesc, more);
+                else
+                    ptx_f8::mma_f8_ss(tmem + t * BN, step_desc(qd, kk * 2), step_desc(kd, kk * 2), idesc, more);
+            }
+        }
+    };
+    constexpr uint32_t kIdescO = idesc_h16(BM, D, false, true, F16);
+    auto issue_pv = [&](int t, uint32_t s, bool first) {
+        const uint64_t vd = vmajor_desc(smem_u32(smem + E::kWideOff + s * 2 * E::kTileBytes));
+#pragma unroll kIssueUnroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ts(tmem + C::o_col(t), tmem + C::p_col(t) + kk * 8, vmajor_step(vd, kk), kIdescO, !first || kk > 0 ? 1u : 0u);
+    };
+    if (warp == C::kProducer || (C::kVProducer && warp == C::kFourth)) {
+        // ------------------------------------------------ producers: as those of 16 bits, with a copy of scales a page
+        const bool two = C::kVProducer && p.page_size < 64;
+        const int first = C::kVProducer && warp == C::kFourth ? 1 : 0;  // 0: K, 1: V
+        const int end = two || first == 1 ? first + 1 : 2;
+        const int box_rows = min(p.page_size, BN);
+        const int my_key = lane * box_rows;
+        uint32_t issued[2] = {0, 0};
+        const uint32_t limit = p.stall_after > 0 ? (uint32_t)p.stall_after : UINT32_MAX;
+        bool ok = true, bad = false;
+        uint32_t n = 0;  // key tiles
+        while (ok && (two || first == 0) && n < limit && walk.next(w)) {
+            if (w.cnt_max == 0) continue;
+            int page = 0;
+            if (my_key < BN && w.k0 * BN + my_key < w.len) page = page_at(p, w.b, w.k0 * BN + my_key, &bad);
+            w.cnt_max = min(w.cnt_max, (int)min(limit - n, (uint32_t)INT_MAX));
+            for (int j = w.k0; j < w.k0 + w.cnt_max && ok; ++j, ++n) {
+                const int key0 = j * BN;
+                const bool active = my_key < BN && key0 + my_key < w.len;
+                const uint32_t boxes = __popc(__ballot_sync(kFull, active));
+                const int slot_row = (key0 + my_key) & (p.page_size - 1);
+                const int my_page = page;
+                if (j + 1 < w.k0 + w.cnt_max && my_key < BN && key0 + BN + my_key < w.len)
+                    page = page_at(p, w.b, key0 + BN + my_key, &bad);
+                // a page that the cache does not have reads as zeros, whatever the scales
+                const long long at_page = my_page < p.num_pages ? my_page : 0;
+                for (int kv = first; kv < end; ++kv) {
+                    const uint32_t s = n % (kv == 0 ? E::kKeys : E::kValues), use = n / (kv == 0 ? E::kKeys : E::kValues);
+                    uint64_t* full = kv == 0 ? &bar.k_full[s] : &bar.v_full[s];
+                    ok = mbar_wait_warp(kv == 0 ? &bar.k_empty[s] : &bar.v_empty[s], (use & 1) ^ 1, wc);
+                    if (!ok) break;
+                    if (elect_one()) mbar_arrive_expect_tx(full, boxes * (uint32_t)(box_rows * (D + 1)));
+                    __syncwarp();
+                    if (active) {
+                        uint8_t* dst = smem + (kv == 0 ? E::kKeyOff : E::kValueOff) + s * E::kTileBytes + my_key * D;
+                        uint8_t* scales = smem + (kv == 0 ? E::kKeyScaleOff : E::kValueScaleOff) + s * BN + my_key;
+                        const uint8_t* src = kv == 0 ? p.k_scale + at_page * p.ks_page + w.h * p.ks_head
+                                                     : p.v_scale + at_page * p.vs_page + w.h * p.vs_head;
+                        tma_load_4d(dst, kv == 0 ? &tm_k : &tm_v, full, 0, slot_row, w.h, my_page);
+                        bulk_load(scales, src + slot_row, (uint32_t)box_rows, full);
+                    }
+                    __syncwarp();
+                    issued[kv] = n + 1;
+                }
+            }
+        }
+        if (bad) atomicCAS(p.err, 0, ATTN_ERR_INVALID);
+        if (lane == 0) {
+            if (first == 0) bar.issued[0] = issued[0];
+            if (end == 2 && (two || first == 0)) bar.issued[1] = issued[1];
+        }
+    } else if (warp == C::kTail) {
+        // ------------------------------------------------ the CTA's slots
+        int4 slot0 = make_int4(kNone, 0, 0, 0), slot1 = slot0;
+        while (walk.next(w)) {
+            if (w.first && w.last) continue;
+            const int4 m = make_int4(w.last ? kLast : kPart, w.row0, w.ntok, w.h);
+            if (w.first)
+                slot1 = m;
+            else
+                slot0 = m;
+        }
+        if (lane < 2) p.meta[blockIdx.x * 2 + lane] = lane == 0 ? slot0 : slot1;
+    } else if (warp >= kConvert) {
+        // ------------------------------------------------ converters: the keys' factors, the values in 16 bits
+        // All on every tile, in order: a wait tells the phases of a stage apart only while no use of it is passed
+        // over, and none can pass while the wait stands.
+        constexpr int W = E::Kernel::kConverters;
+        const int c = warp - kConvert;
+        uint32_t n = 0;
+        bool ok = true;
+        while (ok && walk.next(w)) {
+            for (int j = 0; j < w.cnt_max && ok; ++j, ++n) {
+                const uint32_t sk = n % E::kKeys, sv = n % E::kValues, so = n % E::kWide;
+                const uint32_t pk = (n / E::kKeys) & 1, pv = (n / E::kValues) & 1, po = ((n / E::kWide) & 1) ^ 1;
+                const unsigned ready = look(&bar.k_full[sk], pk, &bar.v_full[sv], pv, &bar.kv_empty[so], po, &bar.k_full[sk], pk);
+                ok = (ready & 1) || mbar_wait_warp(&bar.k_full[sk], pk, wc);
+                if (!ok) break;
+                if (c < BN / 32) {
+                    const int at = c * 32 + lane;
+                    reinterpret_cast<uint32_t*>(smem + E::kFactorOff)[n % E::kFactors * BN + at] =
+                        (uint32_t)smem[E::kKeyScaleOff + sk * BN + at] << 23;
+                    __syncwarp();
+                    if (elect_one()) mbar_arrive(&bar.k_ready[sk]);
+                }
+                ok = ((ready & 2) || mbar_wait_warp(&bar.v_full[sv], pv, wc)) &&
+                     ((ready & 4) || mbar_wait_warp(&bar.kv_empty[so], po, wc));
+                if (!ok) break;
+                widen_tile<D, F16, W>(smem + E::kValueOff + sv * E::kTileBytes, smem + E::kValueScaleOff + sv * BN,
+                                      smem + E::kWideOff + so * 2 * E::kTileBytes, w.len - (w.k0 + j) * BN, c, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (elect_one()) {
+                    mbar_arrive(&bar.kv_full[so]);
+                    mbar_arrive(&bar.v_empty[sv]);
+                }
+                __syncwarp();
+            }
+        }
+    } else if (!C::kOneIssuer && (warp == C::kIssuer || (NT == 2 && warp == C::kFourth))) {
+        // ------------------------------------------------ issuers, one per query tile: as those of 16 bits with P in
+        // columns of its own
+        const int t = warp == C::kIssuer ? 0 : 1;
+        uint32_t n = 0, n_s = 0, n_p = 0, units = 0;
+        bool ok = true;
+        while (ok && walk.next(w)) {
+            if (w.cnt_max == 0) continue;
+            const int cnt = w.cnt(t);
+            if (cnt > 0) {
+                ok = mbar_wait_warp(&bar.q_full[t], units++ & 1, wc);
+                if (!ok) break;
+                tc_fence_after();
+            }
+            for (int j = 0; j <= w.cnt_max && ok; ++j) {
+                const uint32_t sK = n % E::kKeys, sV = (n + E::kWide - 1) % E::kWide;  // V of the tile before
+                const uint32_t k_phase = (n / E::kKeys) & 1, v_phase = ((n - 1) / E::kWide) & 1;
+                const unsigned ready = look(&bar.k_ready[sK], k_phase, &bar.s_free[t], (n_s - 1) & 1, &bar.kv_full[sV], v_phase,
+                                            &bar.p_full[t], n_p & 1);
+                if (j < w.cnt_max) {
+                    ok = (ready & 1) || mbar_wait_warp(&bar.k_ready[sK], k_phase, wc);
+                    if (ok && j < cnt && n_s > 0) ok = (ready & 2) || mbar_wait_warp(&bar.s_free[t], (n_s - 1) & 1, wc);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (j < cnt) {
+                            issue_s(t, sK);
+                            mma_commit(&bar.s_full[t]);
+                        }
+                        mma_commit(&bar.k_empty[sK]);
+                    }
+                    __syncwarp();
+                    if (j < cnt) ++n_s;
+                }
+                if (j > 0) {
+                    ok = (ready & 4) || mbar_wait_warp(&bar.kv_full[sV], v_phase, wc);
+                    if (ok && j <= cnt) {
+                        ok = (ready & 8) || mbar_wait_warp(&bar.p_full[t], n_p & 1, wc);
+                        ++n_p;
+                    }
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (j <= cnt) {
+                            issue_pv(t, sV, j == 1);
+                            mma_commit(&bar.pv_done[t]);
+                        }
+                        mma_commit(&bar.kv_empty[sV]);
+                    }
+                    __syncwarp();
+                }
+                if (j < w.cnt_max) ++n;
+            }
+        }
+        if (elect_one()) {
+            mma_commit(&bar.drain[t]);
+            drain_wait(&bar.drain[t], 0, p.timeout_ns);
+        }
+        __syncwarp();
+    } else if (C::kOneIssuer && warp == C::kIssuer) {
+        // ------------------------------------------------ the one issuer of two tiles with P over S: as that of 16 bits
+        uint32_t n = 0, pcnt0 = 0, pcnt1 = 0, units0 = 0, units1 = 0;
+        bool ok = true;
+        while (ok && walk.next(w)) {
+            if (w.cnt_max == 0) continue;
+            uint32_t sK = n % E::kKeys;
+            ok = mbar_wait_warp(&bar.k_ready[sK], (n / E::kKeys) & 1, wc);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (!ok || w.cnt(t) == 0) continue;
+                uint32_t& units = t == 0 ? units0 : units1;
+                ok = mbar_wait_warp(&bar.q_full[t], units++ & 1, wc);
+                tc_fence_after();
+                if (ok && elect_one()) {
+                    issue_s(t, sK);
+                    mma_commit(&bar.s_full[t]);
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            for (int j = 1; j <= w.cnt_max && ok; ++j) {
+                const uint32_t sV = n % E::kWide, v_phase = (n / E::kWide) & 1;  // V of tile j - 1
+                if (elect_one()) {
+                    if (j > 1) mma_commit(&bar.kv_empty[(n + E::kWide - 1) % E::kWide]);
+                    mma_commit(&bar.k_empty[sK]);
+                }
+                __syncwarp();
+                ++n;
+                sK = n % E::kKeys;
+                const uint32_t k_phase = (n / E::kKeys) & 1;
+                const unsigned ready = look(&bar.k_ready[sK], k_phase, &bar.kv_full[sV], v_phase, &bar.p_full[0], pcnt0 & 1,
+                                            &bar.p_full[1], pcnt1 & 1);
+                if (j < w.cnt_max) {
+                    ok = (ready & 1) || mbar_wait_warp(&bar.k_ready[sK], k_phase, wc);
+                    if (!ok) break;
+                }
+                ok = (ready & 2) || mbar_wait_warp(&bar.kv_full[sV], v_phase, wc);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if (!ok || j > w.cnt(t)) continue;
+                    uint32_t& pcnt = t == 0 ? pcnt0 : pcnt1;
+                    ok = (ready & (t == 0 ? 4 : 8)) || mbar_wait_warp(&bar.p_full[t], pcnt & 1, wc);
+                    if (!ok) continue;
+                    ++pcnt;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        issue_pv(t, sV, j == 1);
+                        if (j == w.cnt(t)) mma_commit(&bar.o_full[t]);  // last product of this tile
+                        if (j < w.cnt(t)) {
+                            issue_s(t, sK);
+                            mma_commit(&bar.s_full[t]);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok) break;
+            if (elect_one()) mma_commit(&bar.kv_empty[(n + E::kWide - 1) % E::kWide]);  // the last V
+            __syncwarp();
+        }
+        if (elect_one()) {
+            mma_commit(&bar.drain[0]);
+            drain_wait(&bar.drain[0], 0, p.timeout_ns);
+        }
+        __syncwarp();
+    }
+}
+
+// The softmax of one-tile units of up to 32 rows. A row has a lane of tensor memory in each of the four warps: every
+// warp has a copy of Q's rows, so S too, and takes 32 of a tile's 128 keys. The copies' P are 0 at the other keys, so
+// that their O add up to the row's, each with a running maximum of its own; they are merged at the unit's end like the
+// parts of a unit that was cut. With all keys of a row in one thread a tile takes some 2000 cycles beside the
+// converters (64 sequences of 8192 keys 240 us), and its keys arrive every 1400.
+template <int D, bool F16, int KERNEL>
+__device__ __forceinline__ void softmax_copies(const PagedDev& p, uint8_t* smem, Shared& bar) {
+    using C = Cfg<D, 1, KERNEL, kBytes>;
+    using E = Cfg8<D, F16, 1, KERNEL>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const WaitCtl wc{p.err, &bar.abort_flag, p.timeout_ns};
+    const int rows = p.tok_tile * p.G;
+    const int my_tok = lane / p.G, my_head = lane % p.G;
+    const uint32_t lane_off = bar.tmem_base + ((uint32_t)(warp * 32) << 16);
+    const uint32_t tS = lane_off + warp * 32, tO = lane_off + C::o_col(0), tP = lane_off + C::p_col(0);
+    // merging: rows of a round, and as many columns as the area holds of them
+    const int span = bar.most_rows <= 8 ? 8 : bar.most_rows <= 16 ? 16 : 32;
+    const int most = 32 * 32 / span, cols = min(D, most), pitch = most + 4;
+    float4* states = reinterpret_cast<float4*>(smem + E::kStateOff);
+    float* area = reinterpret_cast<float*>(smem + E::kMergeOff);
+    uint32_t scnt = 0, ocnt = 0, mcnt = 0;
+    bool ok = true;
+    {
+        uint32_t zero[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) zero[i] = 0;
+        tmem_st32(tP, zero);
+        tmem_st32(tP + 32, zero);
+        tmem_wait_st();
+    }
+    Walk<1, KERNEL, kBytes> walk(p, bar);
+    Unit w;
+    bool more = walk.next(w);
+    float row_c = p.c;
+    int factors = 0;
+    auto take_q = [&]() {
+        const uint16_t* src = nullptr;
+        if (lane < rows && my_tok < w.ntok) src = p.q + (w.row0 + my_tok) * p.q_sr + (w.h * p.G + my_head) * p.q_sh;
+        __syncwarp();
+        row_c = p.c * split_row<D, F16, true>(src, lane_off + E::kQCol, nullptr, lane);
+        mbar_arrive(&bar.q_full[0]);
+    };
+    auto meet = [&]() {
+        mbar_arrive(&bar.merged);
+        ok = __all_sync(kFull, mbar_wait(&bar.merged, mcnt & 1, wc));
+        ++mcnt;
+    };
+    if (more && w.cnt0 > 0) take_q();
+    while (ok && more) {
+        const int4 u = make_int4(w.row0, w.ntok, w.h, (w.first ? 1 : 0) + (w.last ? 2 : 0));
+        const int cnt = w.cnt0, k0 = w.k0;
+        const int lim = w.causal ? min(w.len, w.base + my_tok + 1) : w.len;
+        const int lim_first = w.causal ? min(w.len, w.base + 1) : w.len;
+        const int ctx = !w.causal && p.tree != nullptr ? w.ctx : INT_MAX;
+        float m_ref = -INFINITY, m_row = -INFINITY, l = 0.f;
+        bool s_ready = false;
+        for (int j = 0; j < cnt; ++j) {
+            ok = s_ready || mbar_wait(&bar.s_full[0], scnt & 1, wc);
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            ++scnt;
+            tc_fence_after();
+            uint32_t su[32];
+            tmem_ld32(tS, su);
+            const float4* f = reinterpret_cast<const float4*>(smem + E::kFactorOff) + factors * (BN / 4) + warp * 8;
+            float4 f4[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f4[i] = f[i];
+            factors = factors + 1 == E::kFactors ? 0 : factors + 1;
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 a = fmul2(make_float2(__uint_as_float(su[4 * i]), __uint_as_float(su[4 * i + 1])),
+                                       make_float2(f4[i].x, f4[i].y));
+                const float2 b = fmul2(make_float2(__uint_as_float(su[4 * i + 2]), __uint_as_float(su[4 * i + 3])),
+                                       make_float2(f4[i].z, f4[i].w));
+                su[4 * i] = __float_as_uint(a.x), su[4 * i + 1] = __float_as_uint(a.y);
+                su[4 * i + 2] = __float_as_uint(b.x), su[4 * i + 3] = __float_as_uint(b.y);
+            }
+            tc_fence_before();
+            mbar_arrive(&bar.s_free[0]);
+            const int key0 = (k0 + j) * BN + warp * 32;
+            if (key0 > ctx - 32) {
+                uint32_t bits[1];
+                tree_bits(p, lane < rows && my_tok < w.ntok ? p.tree + (w.row0 + my_tok) * p.tree_stride : nullptr, key0, ctx,
+                          w.len, bits);
+#pragma unroll
+                for (int col = 0; col < 32; ++col)
+                    if (!(bits[0] >> col & 1)) su[col] = __float_as_uint(-INFINITY);
+            } else if (key0 + 32 > lim_first) {
+                const int out = lim - key0;
+#pragma unroll
+                for (int col = 0; col < 32; ++col)
+                    if (col >= out) su[col] = __float_as_uint(-INFINITY);
+            }
+            float mx[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                mx[c] = fmaxf(__uint_as_float(su[16 * c]), __uint_as_float(su[16 * c + 1]));
+#pragma unroll
+                for (int e = 2; e < 16; e += 2)
+                    mx[c] = fmax3(mx[c], __uint_as_float(su[16 * c + e]), __uint_as_float(su[16 * c + e + 1]));
+            }
+            const float m_tile = fmaxf(mx[0], mx[1]) * row_c;
+            m_row = fmaxf(m_row, m_tile);
+            float m_new = m_ref;
+            if (m_tile > m_ref + kRescaleThreshold) m_new = m_tile;
+            const bool moved = m_new != m_ref;
+            const float alpha = moved ? ex2(m_ref - m_new) : 1.f;  // 0 when m_ref = -inf
+            const bool rescale = j > 0 && __any_sync(kFull, moved && m_ref != -INFINITY);
+            m_ref = m_new;
+            const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
+            const float2 cc2 = make_float2(row_c, row_c), nm2 = make_float2(neg_m, neg_m);
+            float2 suma = make_float2(0.f, 0.f), sumb = make_float2(0.f, 0.f);
+            const bool o_ready = j > 0 && mbar_test(&bar.pv_done[0], ocnt & 1);
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float2 x = ffma2(make_float2(__uint_as_float(su[2 * i]), __uint_as_float(su[2 * i + 1])), cc2, nm2);
+                const float2 pp = make_float2(ex2(x.x), ex2(x.y));
+                if (i & 1)
+                    sumb = fadd2(sumb, pp);
+                else
+                    suma = fadd2(suma, pp);
+                pk[i] = pack_h16<F16>(pp.x, pp.y);
+            }
+            if (j > 0) {  // the product of tile j-1 has read P and written O
+                ok = o_ready || mbar_wait(&bar.pv_done[0], ocnt & 1, wc);
+                ok = __all_sync(kFull, ok);
+                if (!ok) break;
+                ++ocnt;
+                tc_fence_after();
+                if (rescale) {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t ov[32];
+                        tmem_ld32(tO + c0, ov);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                        tmem_st32(tO + c0, ov);
+                    }
+                }
+            }
+            tmem_st16(tP + warp * 16, pk);
+            s_ready = j + 1 < cnt && mbar_test(&bar.s_full[0], scnt & 1);
+            l = l * alpha + ((suma.x + suma.y) + (sumb.x + sumb.y));
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bar.p_full[0]);
+        }
+        if (!ok) break;
+        more = walk.next(w);  // while the last product runs
+        if (more && w.cnt0 > 0) take_q();  // every product with this unit's has been waited for
+        const bool first = u.w & 1, last = u.w & 2;
+        if (cnt > 0) {
+            ok = mbar_wait(&bar.pv_done[0], ocnt & 1, wc);
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            ++ocnt;
+            tc_fence_after();
+            // The copy's state, as that of a part of a unit. Every warp is done with the unit before, or there would be
+            // no P for the product above.
+            if (lane < span)
+                states[warp * span + lane] =
+                    make_float4(l == 0.f ? -INFINITY : fmaxf(m_ref, -FLT_MAX), l, o_divisor<F16>(l, m_row, m_ref), 0.f);
+        }
+        const int r = threadIdx.x % span, group = threadIdx.x / span;  // merges 8 columns of row r
+        const int tok = r / p.G;
+        const bool held = r < rows && tok < u.y && group * 8 < cols;
+        const long long row = u.x + tok, head = u.z * p.G + r % p.G;
+        uint16_t* orow = reinterpret_cast<uint16_t*>(p.o) + row * p.o_sr + head * p.o_sh;
+        float4* rec = record(p.part, blockIdx.x * 2 + (first ? 1 : 0), C::Kernel::kTiles, 0, rows, D) + r;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D && ok; c0 += cols) {
+            if (cnt > 0) {
+                if (c0 > 0) meet();  // the area has been read
+#pragma unroll 1
+                for (int c1 = 0; c1 < cols && ok; c1 += 32) {
+                    uint32_t ov[32];
+                    tmem_ld32(tO + c0 + c1, ov);
+                    tmem_wait_ld();
+                    if (lane < span) {
+                        float4* dst = reinterpret_cast<float4*>(area + (warp * span + lane) * pitch + c1);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            dst[q] = make_float4(__uint_as_float(ov[4 * q]), __uint_as_float(ov[4 * q + 1]),
+                                                 __uint_as_float(ov[4 * q + 2]), __uint_as_float(ov[4 * q + 3]));
+                    }
+                }
+                tc_fence_before();
+                meet();
+                if (!ok) break;
+            }
+            float m = -INFINITY, sum = 0.f, den = 0.f, out[8];
+            float4 st[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                st[k] = cnt > 0 ? states[k * span + r] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+                m = fmaxf(m, st[k].x);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) out[i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (st[k].x == -INFINITY) continue;  // no key of this row in the copy
+                const float f = ex2(st[k].x - m);
+                sum = fmaf(f, st[k].y, sum);
+                den = fmaf(f, st[k].z, den);
+                const float4* src = reinterpret_cast<const float4*>(area + (k * span + r) * pitch + group * 8);
+                const float4 a = src[0], b = src[1];
+                out[0] = fmaf(f, a.x, out[0]), out[1] = fmaf(f, a.y, out[1]), out[2] = fmaf(f, a.z, out[2]);
+                out[3] = fmaf(f, a.w, out[3]), out[4] = fmaf(f, b.x, out[4]), out[5] = fmaf(f, b.y, out[5]);
+                out[6] = fmaf(f, b.z, out[6]), out[7] = fmaf(f, b.w, out[7]);
+            }
+            if (!held) continue;
+            if (first && last) {
+                const float inv = den > 0.f ? 1.f / den : 0.f;
+                *reinterpret_cast<uint4*>(orow + c0 + group * 8) =
+                    make_uint4(pack_h16<F16>(out[0] * inv, out[1] * inv), pack_h16<F16>(out[2] * inv, out[3] * inv),
+                               pack_h16<F16>(out[4] * inv, out[5] * inv), pack_h16<F16>(out[6] * inv, out[7] * inv));
+                if (c0 == 0 && group == 0) p.lse[head * p.T + row] = row_lse(m, sum);
+            } else {
+                if (c0 == 0 && group == 0) rec[0] = make_float4(m, sum, den, 0.f);
+                const int g4 = (c0 + group * 8) / 4;
+                rec[(1 + g4) * rows] = make_float4(out[0], out[1], out[2], out[3]);
+                rec[(2 + g4) * rows] = make_float4(out[4], out[5], out[6], out[7]);
+            }
+        }
     }
 }
 
@@ -649,20 +1309,35 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
     constexpr uint32_t kIdescO = idesc_h16(BM, D, false, true, F16);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const WaitCtl wc{p.err, &bar.abort_flag, p.timeout_ns};
+    const bool copies = VAR == kBytes && NT == 1 && bar.sm_warps == 1;
     if (threadIdx.x == 0) {
-        const uint32_t rows = 32u * (uint32_t)bar.sm_warps;  // softmax threads of a tile
+        const uint32_t rows = copies ? 128u : 32u * (uint32_t)bar.sm_warps;  // softmax threads of a tile
         for (int i = 0; i < 4; ++i) {
-            mbar_init(&bar.q_full[i], 1);
+            mbar_init(&bar.q_full[i], VAR == kBytes ? rows : 1);
             mbar_init(&bar.q_empty[i], 1);
         }
-        for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(&bar.kv_full[s], C::kF8 ? 4 : 1);
-            mbar_init(&bar.kv_empty[s], C::kIssuers);
-            mbar_init(&bar.v_tail[s], 1);
-        }
-        for (int s = 0; s < C::kRawStages; ++s) {
-            mbar_init(&bar.raw_full[s], 1);
-            mbar_init(&bar.raw_empty[s], 4);
+        if constexpr (VAR == kBytes) {
+            using E = Cfg8<D, F16, NT, KERNEL>;
+            constexpr uint32_t kConverters = E::Kernel::kConverters;
+            for (int s = 0; s < E::kKeys; ++s) {
+                mbar_init(&bar.k_full[s], 1);
+                mbar_init(&bar.k_ready[s], BN / 32);
+                mbar_init(&bar.k_empty[s], C::kIssuers);
+            }
+            for (int s = 0; s < E::kValues; ++s) {
+                mbar_init(&bar.v_full[s], 1);
+                mbar_init(&bar.v_empty[s], kConverters);
+            }
+            for (int s = 0; s < E::kWide; ++s) {
+                mbar_init(&bar.kv_full[s], kConverters);
+                mbar_init(&bar.kv_empty[s], C::kIssuers);
+            }
+        } else {
+            for (int s = 0; s < C::kStages; ++s) {
+                mbar_init(&bar.kv_full[s], 1);
+                mbar_init(&bar.kv_empty[s], C::kIssuers);
+                mbar_init(&bar.v_tail[s], 1);
+            }
         }
         for (int t = 0; t < NT; ++t) {
             mbar_init(&bar.s_full[t], 1);
@@ -671,6 +1346,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             mbar_init(&bar.s_free[t], rows);
             mbar_init(&bar.pv_done[t], 1);
             mbar_init(&bar.drain[t], 1);
+            if (VAR == kBytes && NT == 1) mbar_init(&bar.merged, 128);
         }
         fence_mbar_init();
     }
@@ -687,6 +1363,9 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
 
     if (warp >= C::kProducer) {
         if constexpr (C::Kernel::kRebalance) regs_decrease<C::Kernel::kOtherRegs>();
+        if constexpr (VAR == kBytes) {
+            roles8<D, F16, NT, KERNEL>(tm_k, tm_v, p, smem, bar);
+        } else {
         Walk<NT, KERNEL, VAR> walk(p, bar);
         Unit w;
         if (warp == C::kProducer || (C::kVProducer && warp == C::kFourth)) {
@@ -698,7 +1377,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             const int first = C::kVProducer && warp == C::kFourth ? 1 : 0;  // 0: K, 1: V
             const int end = two || first == 1 ? first + 1 : 2;
             const int box_rows = min(p.page_size, BN);   // keys a box holds
-            const uint32_t box_bytes = (uint32_t)box_rows * (C::kF8 ? D + 1 : 128 * C::kBoxes);
+            const uint32_t box_bytes = (uint32_t)box_rows * 128;
             const int my_key = lane * box_rows;          // of a tile, where this lane has a box
             uint32_t it = 0;                             // ring items: K and V in turn
             const uint32_t limit = p.stall_after > 0 ? 2u * (uint32_t)p.stall_after : UINT32_MAX;
@@ -719,25 +1398,16 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                         page = page_at(p, w.b, key0 + BN + my_key, &bad);
                     const bool tail = key0 + BN > w.len;
                     for (int kv = first; kv < end; ++kv) {
-                        const uint32_t s = (it + kv) % C::kFetched;
-                        ok = mbar_wait_warp(C::kF8 ? &bar.raw_empty[s] : &bar.kv_empty[s], (((it + kv) / C::kFetched) & 1) ^ 1,
-                                            wc);
+                        const uint32_t s = (it + kv) % C::kStages;
+                        ok = mbar_wait_warp(&bar.kv_empty[s], (((it + kv) / C::kStages) & 1) ^ 1, wc);
                         if (!ok) {
                             it += kv - 2;  // ends as the first item not issued here
                             break;
                         }
-                        uint64_t* full = C::kF8 ? &bar.raw_full[s] : kv == 1 && tail ? &bar.v_tail[s] : &bar.kv_full[s];
-                        if (elect_one()) mbar_arrive_expect_tx(full, boxes * box_bytes);
+                        uint64_t* full = kv == 1 && tail ? &bar.v_tail[s] : &bar.kv_full[s];
+                        if (elect_one()) mbar_arrive_expect_tx(full, boxes * box_bytes * C::kBoxes);
                         __syncwarp();
-                        if (active && C::kF8) {
-                            uint8_t* dst = smem + C::kRawOff + s * C::kRawBytes;
-                            tma_load_4d(dst + my_key * D, kv == 0 ? &tm_k : &tm_v, full, 0, slot_row, w.h, my_page);
-                            // a page that the cache does not have reads as zeros, whatever the scales
-                            const long long at_page = my_page < p.num_pages ? my_page : 0;
-                            const uint8_t* src = kv == 0 ? p.k_scale + at_page * p.ks_page + w.h * p.ks_head
-                                                         : p.v_scale + at_page * p.vs_page + w.h * p.vs_head;
-                            bulk_load(dst + BN * D + my_key, src + slot_row, (uint32_t)box_rows, full);
-                        } else if (active) {
+                        if (active) {
                             uint8_t* dst = smem + C::kKVOff + s * C::kTileBytes + my_key * 128;
                             for (int bx = 0; bx < C::kBoxes; ++bx)
                                 tma_load_4d(dst + bx * BN * 128, kv == 0 ? &tm_k : &tm_v, full, bx * 64, slot_row, w.h,
@@ -786,7 +1456,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 }
                 it += 2 * w.cnt_max;
                 const int left = w.len - (w.k0 + w.cnt_max - 1) * BN;  // keys in the part's last tile
-                if (C::kF8 || left >= BN || !ok) continue;  // the converters write the zeros
+                if (left >= BN || !ok) continue;
                 const uint32_t s = (it - 1) % C::kStages;  // the part's last V
                 ok = mbar_wait_warp(&bar.v_tail[s], (phases >> s) & 1, wc);
                 if (!ok) continue;
@@ -807,28 +1477,6 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 drain_wait(&bar.q_full[lane], parity ^ 1, p.timeout_ns);
             }
             __syncwarp();
-        } else if (C::kF8 && warp >= C::kConvert) {
-            // ------------------------------------------------ converters of 8-bit tiles
-            uint32_t it = 0;
-            bool ok = true;
-            while (ok && walk.next(w)) {
-                for (int i = 0; i < 2 * w.cnt_max && ok; ++i, ++it) {
-                    constexpr uint32_t kRaw = C::kF8 ? C::kRawStages : 1;
-                    const uint32_t r = it % kRaw, s = it % C::kStages;
-                    ok = mbar_wait_warp(&bar.raw_full[r], (it / kRaw) & 1, wc) &&
-                         mbar_wait_warp(&bar.kv_empty[s], ((it / C::kStages) & 1) ^ 1, wc);
-                    if (!ok) break;
-                    convert_tile<D, F16>(smem + C::kRawOff + r * C::kRawBytes, smem + C::kKVOff + s * C::kTileBytes,
-                                         w.len - (w.k0 + i / 2) * BN, warp - C::kConvert, lane);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (elect_one()) {
-                        mbar_arrive(&bar.kv_full[s]);
-                        mbar_arrive(&bar.raw_empty[r]);
-                    }
-                    __syncwarp();
-                }
-            }
         } else if (!C::kOneIssuer && (warp == C::kIssuer || (NT == 2 && warp == C::kFourth))) {
             // ------------------------------------------------ MMA issuers, one per query tile
             // Each issuer walks every ring slot and releases it once, used or not. With P in columns of its own
@@ -1020,11 +1668,17 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             }
             __syncwarp();
         }
+        }
     } else {
         if constexpr (C::Kernel::kRebalance) regs_increase<C::Kernel::kSoftmaxRegs>();
         // ------------------------------------------------ softmax (thread = query row)
         const int t = NT == 2 ? warp >> 2 : 0;
-        if (warp < 4 * NT && (warp & 3) < bar.sm_warps) {
+        bool whole_rows = true;
+        if constexpr (VAR == kBytes && NT == 1) {
+            whole_rows = !copies;
+            if (copies && warp < 4) softmax_copies<D, F16, KERNEL>(p, smem, bar);
+        }
+        if (whole_rows && warp < 4 * NT && (warp & 3) < bar.sm_warps) {
             const int r = (warp & 3) * 32 + lane;
             const int rows = p.tok_tile * p.G;
             const int my_tok = t * p.tok_tile + r / p.G, my_head = r % p.G;
@@ -1036,6 +1690,21 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             Walk<NT, KERNEL, VAR> walk(p, bar);
             Unit w;
             bool more = walk.next(w);
+            // kBytes: the factor of this thread's row, and the stage of the keys' factors
+            float row_c = p.c;
+            int factors = 0;
+            auto take_q = [&]() {
+                if constexpr (VAR == kBytes) {
+                    using E = Cfg8<D, F16, NT, KERNEL>;
+                    const uint16_t* src = nullptr;
+                    if (r < rows && my_tok < w.ntok) src = p.q + (w.row0 + my_tok) * p.q_sr + (w.h * p.G + my_head) * p.q_sh;
+                    __syncwarp();
+                    row_c = p.c * split_row<D, F16, E::kQTmem>(src, tmem + lane_off + E::kQCol,
+                                                           smem + t * E::kPieces * E::kTileBytes, r);
+                    mbar_arrive(&bar.q_full[t]);
+                }
+            };
+            if (more && w.cnt(t) > 0) take_q();
             while (ok && more) {
                 __syncwarp();  // the last use of bar.unit
                 if (lane == 0) bar.unit[warp] = make_int4(w.row0, w.ntok, w.h, (w.first ? 1 : 0) + (w.last ? 2 : 0));
@@ -1043,18 +1712,12 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 // keys this row sees, and those that the tile's first row sees
                 const int lim = w.causal ? min(w.len, w.base + my_tok + 1) : w.len;
                 const int lim_first = w.causal ? min(w.len, w.base + t * p.tok_tile + 1) : w.len;
-                // a tree's rows: where its keys begin, and the row's words
-                const bool treed = VAR != kRun && !w.causal && p.tree != nullptr;
-                const int ctx = treed ? w.ctx : INT_MAX;
-                const uint32_t* tree_row = nullptr;
-                if (treed && r < rows && my_tok < w.ntok) tree_row = p.tree + (w.row0 + my_tok) * p.tree_stride;
+                // where a tree's keys begin
+                const int ctx = VAR != kRun && !w.causal && p.tree != nullptr ? w.ctx : INT_MAX;
                 float m_ref = -INFINITY, m_row = -INFINITY, l = 0.f;
                 bool s_ready = false;
                 for (int j = 0; j < cnt; ++j) {
                     const int key0 = (k0 + j) * BN;
-                    uint32_t bits[4];
-                    const bool at_tree = VAR != kRun && treed && key0 + BN > ctx;
-                    if (at_tree) tree_bits(p, tree_row, key0, ctx, w.len, bits);  // loaded during the wait
                     ok = s_ready || mbar_wait(&bar.s_full[t], scnt & 1, wc);
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
@@ -1066,11 +1729,29 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                     tmem_ld32_at<64>(tS + 64, su);
                     tmem_ld32_at<96>(tS + 96, su);
                     tmem_wait_ld();
+                    if constexpr (VAR == kBytes) {
+                        using E = Cfg8<D, F16, NT, KERNEL>;
+                        const float4* f = reinterpret_cast<const float4*>(smem + E::kFactorOff) + factors * (BN / 4);
+#pragma unroll
+                        for (int i = 0; i < BN / 4; ++i) {
+                            const float4 f4 = f[i];
+                            const float2 a = fmul2(make_float2(__uint_as_float(su[4 * i]), __uint_as_float(su[4 * i + 1])),
+                                                   make_float2(f4.x, f4.y));
+                            const float2 b = fmul2(make_float2(__uint_as_float(su[4 * i + 2]), __uint_as_float(su[4 * i + 3])),
+                                                   make_float2(f4.z, f4.w));
+                            su[4 * i] = __float_as_uint(a.x), su[4 * i + 1] = __float_as_uint(a.y);
+                            su[4 * i + 2] = __float_as_uint(b.x), su[4 * i + 3] = __float_as_uint(b.y);
+                        }
+                        factors = factors + 1 == E::kFactors ? 0 : factors + 1;
+                    }
                     if (C::kSplit) {  // S_t is in registers: the next S_t may overwrite it
                         tc_fence_before();
                         mbar_arrive(&bar.s_free[t]);
                     }
-                    if (at_tree) {
+                    if (VAR != kRun && key0 > ctx - BN) {
+                        uint32_t bits[4];
+                        tree_bits(p, r < rows && my_tok < w.ntok ? p.tree + (w.row0 + my_tok) * p.tree_stride : nullptr, key0, ctx,
+                                  w.len, bits);
 #pragma unroll
                         for (int col = 0; col < BN; ++col)
                             if (!(bits[col / 32] >> (col & 31) & 1)) su[col] = __float_as_uint(-INFINITY);
@@ -1090,7 +1771,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                         mx[c] = m;
                     }
                     const float m_tile =
-                        fmaxf(fmax3(fmax3(mx[0], mx[1], mx[2]), mx[3], mx[4]), fmax3(mx[5], mx[6], mx[7])) * p.c;
+                        fmaxf(fmax3(fmax3(mx[0], mx[1], mx[2]), mx[3], mx[4]), fmax3(mx[5], mx[6], mx[7])) * row_c;
                     m_row = fmaxf(m_row, m_tile);
                     float m_new = m_ref;
                     if (m_tile > m_ref + kRescaleThreshold) m_new = m_tile;
@@ -1117,7 +1798,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                     if (!C::kSplit && rescale) rescale_o();
                     m_ref = m_new;
                     const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
-                    const float2 cc2 = make_float2(p.c, p.c), nm2 = make_float2(neg_m, neg_m);
+                    const float2 cc2 = make_float2(row_c, row_c), nm2 = make_float2(neg_m, neg_m);
                     float2 suma = make_float2(0.f, 0.f), sumb = make_float2(0.f, 0.f);
                     if (C::kSplit) {
                         // Looking at a barrier takes some 130 cycles. The product of tile j-1 has mostly ended by
@@ -1171,7 +1852,10 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                     mbar_arrive(&bar.p_full[t]);
                 }
                 if (!ok) break;
+                if constexpr (VAR == kBytes)
+                    factors = (factors + w.cnt_max - cnt) % Cfg8<D, F16, NT, KERNEL>::kFactors;  // of tiles that only the other saw
                 more = walk.next(w);  // while the last product runs
+                if (more && w.cnt(t) > 0) take_q();  // every product with this unit's has been waited for
                 if (cnt > 0) {
                     ok = mbar_wait(C::kSplit ? &bar.pv_done[t] : &bar.o_full[t], ocnt & 1, wc);
                     ok = __all_sync(kFull, ok);
@@ -1248,7 +1932,14 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
     __syncthreads();
     tc_fence_after();
     // Every copy issued must land before the CTA exits. The issuers have waited for each, unless a wait ran out.
-    if (threadIdx.x == 0 && bar.abort_flag != 0) drain_ring(bar, C::kF8 ? bar.raw_full : bar.kv_full, C::kFetched, p.timeout_ns);
+    if (threadIdx.x == 0 && bar.abort_flag != 0) {
+        if constexpr (VAR == kBytes) {
+            using E = Cfg8<D, F16, NT, KERNEL>;
+            drain_codes(bar, E::kKeys, E::kValues, p.timeout_ns);
+        } else {
+            drain_ring(bar, C::kStages, p.timeout_ns);
+        }
+    }
 }
 
 template <int D, bool F16, int KERNEL, int VAR>
@@ -1493,14 +2184,18 @@ CUresult encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, int32_t d
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-// The same for caches of codes: whole rows of bytes, not swizzled, strides in bytes.
+// The same for caches of codes: whole rows of bytes, swizzled as the products (keys) or the converters read them, strides
+// in bytes.
 CUresult encode_codes(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, const void* base, const cuuint64_t (&dims)[4],
-                      const int64_t (&st)[3], cuuint32_t box_rows) {
+                      const int64_t (&st)[3], cuuint32_t box_rows, bool keys) {
     cuuint64_t strides[3];
     for (int i = 0; i < 3; ++i) strides[i] = dims[i + 1] > 1 ? (cuuint64_t)st[i] : 16;
     const cuuint32_t box[4] = {(cuuint32_t)dims[0], box_rows, 1, 1}, es[4] = {1, 1, 1, 1};
+    const CUtensorMapSwizzle swizzle = dims[0] == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                       : keys         ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                      : CU_TENSOR_MAP_SWIZZLE_NONE;
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+               swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 template <int D, bool F16, int KERNEL, int VAR>
@@ -1577,8 +2272,8 @@ attn_status_t launch_variant(const attn_paged_params& p, const Extra& x, const L
     const cuuint32_t box_rows = (cuuint32_t)(p.page_size < BN ? p.page_size : BN);
     CUresult r = encode(enc, &maps[0], p.dtype, p.q, qd, qs, (cuuint32_t)G, (cuuint32_t)pl.tok_tile);
     if (VAR == kBytes) {
-        if (r == CUDA_SUCCESS) r = encode_codes(enc, &maps[1], p.k_cache, cd, ks, box_rows);
-        if (r == CUDA_SUCCESS) r = encode_codes(enc, &maps[2], p.v_cache, cd, vs, box_rows);
+        if (r == CUDA_SUCCESS) r = encode_codes(enc, &maps[1], p.k_cache, cd, ks, box_rows, true);
+        if (r == CUDA_SUCCESS) r = encode_codes(enc, &maps[2], p.v_cache, cd, vs, box_rows, false);
     } else {
         if (r == CUDA_SUCCESS) r = encode(enc, &maps[1], p.dtype, p.k_cache, cd, ks, box_rows, 1);
         if (r == CUDA_SUCCESS) r = encode(enc, &maps[2], p.dtype, p.v_cache, cd, vs, box_rows, 1);
@@ -1617,6 +2312,9 @@ attn_status_t launch_variant(const attn_paged_params& p, const Extra& x, const L
     a.tree_nodes = x.mask ? 32 * x.words : p.causal ? 0 : INT_MAX;
     a.k_scale = static_cast<const uint8_t*>(x.k_scale);
     a.v_scale = static_cast<const uint8_t*>(x.v_scale);
+    a.q = static_cast<const uint16_t*>(p.q);
+    a.q_sr = p.q_stride[0];
+    a.q_sh = p.q_stride[1];
     a.ks_page = x.k_scale_stride[0];
     a.ks_head = x.k_scale_stride[1];
     a.vs_page = x.v_scale_stride[0];
