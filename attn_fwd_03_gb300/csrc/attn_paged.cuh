@@ -188,16 +188,20 @@ struct Cfg8 {
     using Kernel = Shape<D, KERNEL, kBytes>;
     static constexpr int kTileBytes = BN * D;      // of codes
     static constexpr int kPieces = F16 ? 3 : 2;    // of 4, 4 and 3 bits of Q's 11 or 8
-    // Q's pieces in tensor memory where there are columns left: a product then reads keys alone from shared memory
+    // Tensor memory of units of one tile: two tiles of scores, P over the scores it is made of, O, and Q's pieces (a
+    // product then reads keys alone from shared memory). Two tiles leave no room for Q there.
     static constexpr bool kQTmem = NT == 1;
-    static constexpr int kQCol = D == 128 ? 128 : 256;
+    static constexpr int kOCol = 256, kQCol = 384;
     static constexpr int kQBytes = kQTmem ? 0 : NT * kPieces * kTileBytes;
     // widened values, then rings of codes and of their scales, and the keys' scales as floats
     static constexpr int kWide = D == 128 ? 2 : 3;
     static constexpr int kWideOff = kQBytes, kKeyOff = kWideOff + kWide * 2 * kTileBytes;
-    // for units of one tile: where copies of rows are merged (softmax_copies)
-    static constexpr int kStateBytes = NT == 1 ? 4 * 32 * 16 : 0, kMergeBytes = NT == 1 ? 4 * 32 * 36 * 4 : 0;
-    static constexpr int kRoom = Kernel::kTilesBytes - kKeyOff - kStateBytes - kMergeBytes;
+    // For units of up to 32 rows: pieces of Q and factors of its rows for two units, and where copies of rows are
+    // merged (softmax_one).
+    static constexpr int kQSlots = 2, kQPitch = D + 16, kQSlot = 32 * kPieces * kQPitch + 32 * 4;
+    static constexpr int kStateBytes = 4 * 32 * 16, kMergeBytes = 4 * 32 * 36 * 4;
+    static constexpr int kExtraBytes = NT == 1 ? kQSlots * kQSlot + kStateBytes + kMergeBytes : 0;
+    static constexpr int kRoom = Kernel::kTilesBytes - kKeyOff - kExtraBytes;
     static constexpr int kFit = (kRoom - 3 * BN * 4) / (kTileBytes + BN + BN * 2);
     static constexpr int kBoth = kFit < 16 ? kFit : 16;
     static constexpr int kKeys = (kBoth + 1) / 2, kValues = kBoth / 2;  // stages
@@ -208,9 +212,10 @@ struct Cfg8 {
     // tile ahead of the softmax's last read).
     static constexpr int kFactors = kKeys + 2;
     static constexpr int kFactorOff = kValueScaleOff + kValues * BN;
-    static constexpr int kStateOff = kFactorOff + kFactors * BN * 4, kMergeOff = kStateOff + kStateBytes;
-    static_assert(kValues >= 1 && kMergeOff + kMergeBytes <= Kernel::kTilesBytes, "shared memory");
-    static_assert(!kQTmem || kQCol + kPieces * D / 4 <= (D == 128 ? 256 : 512), "tensor memory");
+    static constexpr int kQSlotOff = kFactorOff + kFactors * BN * 4;
+    static constexpr int kStateOff = kQSlotOff + kQSlots * kQSlot, kMergeOff = kStateOff + kStateBytes;
+    static_assert(kValues >= 1 && kQSlotOff + kExtraBytes <= Kernel::kTilesBytes, "shared memory");
+    static_assert(!kQTmem || (kOCol + D <= kQCol && kQCol + kPieces * D / 4 <= 512), "tensor memory");
 };
 
 struct PagedDev {
@@ -726,6 +731,23 @@ __device__ __forceinline__ void split_pair(uint32_t x, float f, uint16_t& a, uin
     }
 }
 
+// The smallest e with top <= 448 * 2^e, 448 = 1.75 * 2^8, as far as the factor 2^-e is a plain number.
+__device__ __forceinline__ int row_exponent(float top) {
+    const uint32_t bits = __float_as_uint(top);
+    return min(max((int)(bits >> 23) - 135 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0), -119), 119);
+}
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// The largest magnitude of 16-bit values, two at a time.
+template <bool F16>
+__device__ __forceinline__ void take_max(uint32_t& top, uint32_t x) {
+    const uint32_t mag = x & 0x7fff7fffu;
+    if constexpr (F16)
+        asm("max.f16x2 %0, %0, %1;" : "+r"(top) : "r"(mag));  // a NaN does not count
+    else
+        asm("max.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(mag));
+}
+
 // Splits a thread's row of Q (NULL: a row that nobody reads) into the pieces of its tile, in tensor memory at `tmem` or
 // in shared memory at `tile` as row r of K-major tiles, and returns the row's factor 2^e.
 template <int D, bool F16, bool TMEM>
@@ -739,18 +761,10 @@ __device__ __forceinline__ float split_row(const uint16_t* src, uint32_t tmem, u
     }
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < D / 2; ++i) {
-        const uint32_t mag = x[i] & 0x7fff7fffu;
-        if constexpr (F16)
-            asm("max.f16x2 %0, %0, %1;" : "+r"(top) : "r"(mag));  // a NaN does not count
-        else
-            asm("max.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(mag));
-    }
+    for (int i = 0; i < D / 2; ++i) take_max<F16>(top, x[i]);
     const float2 t2 = unpack_h16<F16>(top);
-    // the smallest e with max <= 448 * 2^e, 448 = 1.75 * 2^8
-    const uint32_t bits = __float_as_uint(fmaxf(t2.x, t2.y));
-    const int e = min(max((int)(bits >> 23) - 135 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0), -119), 119);
-    const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+    const int e = row_exponent(fmaxf(t2.x, t2.y));
+    const float f = pow2f(-e);
 #pragma unroll
     for (int c0 = 0; c0 < D / 4; c0 += 16) {  // 64 columns at a time
         uint32_t out[kPieces][16];
@@ -783,7 +797,48 @@ __device__ __forceinline__ float split_row(const uint16_t* src, uint32_t tmem, u
     } else {
         fence_proxy_async_smem();
     }
-    return __uint_as_float((uint32_t)(127 + e) << 23);
+    return pow2f(e);
+}
+
+// The same by a warp for the first rows of a unit, pieces and factors in shared memory at `slot`: lanes side by side
+// hold four columns of a row.
+template <int D, bool F16, int PITCH>
+__device__ __forceinline__ void split_unit(const PagedDev& p, const Unit& w, uint8_t* slot, int lane) {
+    constexpr int kPieces = F16 ? 3 : 2, kLanes = D / 4, kAtOnce = 32 / kLanes;
+    float* factors = reinterpret_cast<float*>(slot + 32 * kPieces * PITCH);
+    const int rows = w.ntok * p.G, col = lane % kLanes;
+    for (int r0 = 0; r0 < rows; r0 += 4 * kAtOnce) {
+        uint2 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + i * kAtOnce + lane / kLanes;
+            x[i] = make_uint2(0, 0);
+            if (r < rows)
+                x[i] = *reinterpret_cast<const uint2*>(p.q + (w.row0 + r / p.G) * p.q_sr + (w.h * p.G + r % p.G) * p.q_sh + col * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + i * kAtOnce + lane / kLanes;
+            uint32_t top = 0;
+            take_max<F16>(top, x[i].x);
+            take_max<F16>(top, x[i].y);
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1) take_max<F16>(top, __shfl_xor_sync(kFull, top, o));
+            const float2 t2 = unpack_h16<F16>(top);
+            const int e = row_exponent(fmaxf(t2.x, t2.y));
+            const float f = pow2f(-e);
+            uint16_t a[2], b[2], c[2] = {0, 0};
+            split_pair<F16>(x[i].x, f, a[0], b[0], c[0]);
+            split_pair<F16>(x[i].y, f, a[1], b[1], c[1]);
+            if (r < rows) {
+                uint8_t* dst = slot + r * PITCH + col * 4;
+                *reinterpret_cast<uint32_t*>(dst) = a[0] | (uint32_t)a[1] << 16;
+                *reinterpret_cast<uint32_t*>(dst + 32 * PITCH) = b[0] | (uint32_t)b[1] << 16;
+                if constexpr (F16) *reinterpret_cast<uint32_t*>(dst + 64 * PITCH) = c[0] | (uint32_t)c[1] << 16;
+                if (col == 0) factors[r] = pow2f(e);
+            }
+        }
+    }
 }
 
 // Descriptor of a K-major tile of codes: rows of 128 bytes with the 128-byte swizzle, or of 64 with the 64-byte one
@@ -810,12 +865,14 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
     using E = Cfg8<D, F16, NT, KERNEL>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const WaitCtl wc{p.err, &bar.abort_flag, p.timeout_ns};
-    const uint32_t tmem = bar.tmem_base;
+    // Broadcast, so that the compiler knows what is the same in all lanes: an issuer's operands then stay in the registers
+    // that its instructions take them from.
+    const uint32_t tmem = __shfl_sync(kFull, bar.tmem_base, 0);
     Walk<NT, KERNEL, kBytes> walk(p, bar);
     Unit w;
     constexpr int kConvert = C::kProducer + 4;
-    // Scores of tile t with the keys of stage s: the sum over Q's pieces.
-    auto issue_s = [&](int t, uint32_t s) {
+    // Scores of tile t with the keys of stage s, into the columns from `to` on: the sum over Q's pieces.
+    auto issue_s = [&](int t, uint32_t to, uint32_t s) {
         constexpr uint32_t kIdesc = ptx_f8::idesc_e4m3(BM, BN, false, false);
         const uint64_t kd = codes_desc<D>(smem_u32(smem + E::kKeyOff + s * E::kTileBytes));
 #pragma unroll
@@ -826,22 +883,22 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
             for (int kk = 0; kk < D / 32; ++kk) {
                 const uint32_t more = piece > 0 || kk > 0 ? 1u : 0u;
                 if constexpr (E::kQTmem)
-                    ptx_f8::mma_f8_ts(tmem + t * BN, tmem + E::kQCol + piece * (D / 4) + kk * 8, step_desc(kd, kk * 2), idesc, more);
+                    ptx_f8::mma_f8_ts(tmem + to, tmem + E::kQCol + piece * (D / 4) + kk * 8, step_desc(kd, kk * 2), idesc, more);
                 else
-                    ptx_f8::mma_f8_ss(tmem + t * BN, step_desc(qd, kk * 2), step_desc(kd, kk * 2), idesc, more);
+                    ptx_f8::mma_f8_ss(tmem + to, step_desc(qd, kk * 2), step_desc(kd, kk * 2), idesc, more);
             }
         }
     };
     constexpr uint32_t kIdescO = idesc_h16(BM, D, false, true, F16);
-    auto issue_pv = [&](int t, uint32_t s, bool first) {
+    auto issue_pv = [&](uint32_t to, uint32_t from, uint32_t s, bool first) {
         const uint64_t vd = vmajor_desc(smem_u32(smem + E::kWideOff + s * 2 * E::kTileBytes));
 #pragma unroll kIssueUnroll
         for (int kk = 0; kk < BN / 16; ++kk)
-            mma_ts(tmem + C::o_col(t), tmem + C::p_col(t) + kk * 8, vmajor_step(vd, kk), kIdescO, !first || kk > 0 ? 1u : 0u);
+            mma_ts(tmem + to, tmem + from + kk * 8, vmajor_step(vd, kk), kIdescO, !first || kk > 0 ? 1u : 0u);
     };
     if (warp == C::kProducer || (C::kVProducer && warp == C::kFourth)) {
         // ------------------------------------------------ producers: as those of 16 bits, with a copy of scales a page
-        const bool two = C::kVProducer && p.page_size < 64;
+        const bool two = C::kVProducer;
         const int first = C::kVProducer && warp == C::kFourth ? 1 : 0;  // 0: K, 1: V
         const int end = two || first == 1 ? first + 1 : 2;
         const int box_rows = min(p.page_size, BN);
@@ -891,15 +948,28 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
             if (end == 2 && (two || first == 0)) bar.issued[1] = issued[1];
         }
     } else if (warp == C::kTail) {
-        // ------------------------------------------------ the CTA's slots
+        // ------------------------------------------------ the CTA's slots, and Q of small units
+        const bool small = NT == 1 && bar.sm_warps == 1;
+        uint32_t units = 0;
+        bool ok = true;
         int4 slot0 = make_int4(kNone, 0, 0, 0), slot1 = slot0;
         while (walk.next(w)) {
-            if (w.first && w.last) continue;
-            const int4 m = make_int4(w.last ? kLast : kPart, w.row0, w.ntok, w.h);
-            if (w.first)
-                slot1 = m;
-            else
-                slot0 = m;
+            if (!(w.first && w.last)) {
+                const int4 m = make_int4(w.last ? kLast : kPart, w.row0, w.ntok, w.h);
+                if (w.first)
+                    slot1 = m;
+                else
+                    slot0 = m;
+            }
+            if (!small || w.cnt_max == 0 || !ok) continue;  // the slots are written whatever happens
+            const uint32_t at = units % E::kQSlots;
+            ok = mbar_wait_warp(&bar.q_empty[1 + at], ((units / E::kQSlots) & 1) ^ 1, wc);
+            if (!ok) continue;
+            split_unit<D, F16, E::kQPitch>(p, w, smem + E::kQSlotOff + at * E::kQSlot, lane);
+            __syncwarp();
+            if (elect_one()) mbar_arrive(&bar.q_full[1 + at]);
+            __syncwarp();
+            ++units;
         }
         if (lane < 2) p.meta[blockIdx.x * 2 + lane] = lane == 0 ? slot0 : slot1;
     } else if (warp >= kConvert) {
@@ -938,7 +1008,56 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
                 __syncwarp();
             }
         }
-    } else if (!C::kOneIssuer && (warp == C::kIssuer || (NT == 2 && warp == C::kFourth))) {
+    } else if (NT == 1 && warp == C::kIssuer) {
+        // ------------------------------------------------ issuer of one tile: scores are two tiles ahead of P V
+        uint32_t nk = 0, nv = 0, units = 0;  // tiles of keys, of values
+        bool ok = true;
+        auto next_s = [&]() {
+            const uint32_t s = nk % E::kKeys;
+            ok = mbar_wait_warp(&bar.k_ready[s], (nk / E::kKeys) & 1, wc);
+            if (!ok) return;
+            tc_fence_after();
+            if (elect_one()) {
+                issue_s(0, (nk & 1) * BN, s);
+                mma_commit(&bar.s_full[nk & 1]);
+                mma_commit(&bar.k_empty[s]);
+            }
+            __syncwarp();
+            ++nk;
+        };
+        while (ok && walk.next(w)) {
+            const int cnt = __shfl_sync(kFull, w.cnt_max, 0);
+            if (cnt == 0) continue;
+            ok = mbar_wait_warp(&bar.q_full[0], units++ & 1, wc);
+            if (!ok) break;
+            // Two tiles of scores: what they write over was read by products issued before (P) and by the softmax
+            // before it made that P.
+            next_s();
+            if (ok && cnt > 1) next_s();
+            for (int j = 0; j < cnt && ok; ++j) {
+                const uint32_t s = nv % E::kWide, v_phase = (nv / E::kWide) & 1, b = nv & 1, p_phase = (nv >> 1) & 1;
+                const unsigned ready = look(&bar.kv_full[s], v_phase, &bar.p_full[b], p_phase, &bar.kv_full[s], v_phase,
+                                            &bar.p_full[b], p_phase);
+                ok = ((ready & 1) || mbar_wait_warp(&bar.kv_full[s], v_phase, wc)) &&
+                     ((ready & 2) || mbar_wait_warp(&bar.p_full[b], p_phase, wc));
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    issue_pv(E::kOCol, b * BN, s, j == 0);
+                    mma_commit(&bar.pv_done[b]);
+                    mma_commit(&bar.kv_empty[s]);
+                }
+                __syncwarp();
+                ++nv;
+                if (j + 2 < cnt) next_s();
+            }
+        }
+        if (elect_one()) {
+            mma_commit(&bar.drain[0]);
+            drain_wait(&bar.drain[0], 0, p.timeout_ns);
+        }
+        __syncwarp();
+    } else if (NT == 2 && !C::kOneIssuer && (warp == C::kIssuer || warp == C::kFourth)) {
         // ------------------------------------------------ issuers, one per query tile: as those of 16 bits with P in
         // columns of its own
         const int t = warp == C::kIssuer ? 0 : 1;
@@ -964,7 +1083,7 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
                     tc_fence_after();
                     if (elect_one()) {
                         if (j < cnt) {
-                            issue_s(t, sK);
+                            issue_s(t, t * BN, sK);
                             mma_commit(&bar.s_full[t]);
                         }
                         mma_commit(&bar.k_empty[sK]);
@@ -982,7 +1101,7 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
                     tc_fence_after();
                     if (elect_one()) {
                         if (j <= cnt) {
-                            issue_pv(t, sV, j == 1);
+                            issue_pv(C::o_col(t), C::p_col(t), sV, j == 1);
                             mma_commit(&bar.pv_done[t]);
                         }
                         mma_commit(&bar.kv_empty[sV]);
@@ -997,7 +1116,7 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
             drain_wait(&bar.drain[t], 0, p.timeout_ns);
         }
         __syncwarp();
-    } else if (C::kOneIssuer && warp == C::kIssuer) {
+    } else if (NT == 2 && C::kOneIssuer && warp == C::kIssuer) {
         // ------------------------------------------------ the one issuer of two tiles with P over S: as that of 16 bits
         uint32_t n = 0, pcnt0 = 0, pcnt1 = 0, units0 = 0, units1 = 0;
         bool ok = true;
@@ -1012,7 +1131,7 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
                 ok = mbar_wait_warp(&bar.q_full[t], units++ & 1, wc);
                 tc_fence_after();
                 if (ok && elect_one()) {
-                    issue_s(t, sK);
+                    issue_s(t, t * BN, sK);
                     mma_commit(&bar.s_full[t]);
                 }
                 __syncwarp();
@@ -1046,10 +1165,10 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
                     ++pcnt;
                     tc_fence_after();
                     if (elect_one()) {
-                        issue_pv(t, sV, j == 1);
+                        issue_pv(C::o_col(t), C::p_col(t), sV, j == 1);
                         if (j == w.cnt(t)) mma_commit(&bar.o_full[t]);  // last product of this tile
                         if (j < w.cnt(t)) {
-                            issue_s(t, sK);
+                            issue_s(t, t * BN, sK);
                             mma_commit(&bar.s_full[t]);
                         }
                     }
@@ -1068,52 +1187,132 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
     }
 }
 
-// The softmax of one-tile units of up to 32 rows. A row has a lane of tensor memory in each of the four warps: every
-// warp has a copy of Q's rows, so S too, and takes 32 of a tile's 128 keys. The copies' P are 0 at the other keys, so
-// that their O add up to the row's, each with a running maximum of its own; they are merged at the unit's end like the
-// parts of a unit that was cut. With all keys of a row in one thread a tile takes some 2000 cycles beside the
-// converters (64 sequences of 8192 keys 240 us), and its keys arrive every 1400.
-template <int D, bool F16, int KERNEL>
-__device__ __forceinline__ void softmax_copies(const PagedDev& p, uint8_t* smem, Shared& bar) {
+// Writes what a thread has of its row r of tile t at a unit's end: O and LSE of a whole unit, or the part's state.
+// All lanes of a warp.
+template <int D, bool F16, int TILES>
+__device__ __forceinline__ void finish_row(const PagedDev& p, const int4& u, int t, int r, int my_tok, int my_head, int rows, int cnt,
+                                           uint32_t tO, float m_ref, float m_row, float l) {
+                    const bool held = r < rows && my_tok < u.y, first = u.w & 1, last = u.w & 2;
+                    const float den = o_divisor<F16>(l, m_row, m_ref);
+                    if (first && last) {
+                        const float inv = den > 0.f ? 1.f / den : 0.f;
+                        // a row without keys is 0, though its products of 0 and a value may be NaN
+                        const uint32_t keep = l == 0.f ? 0u : ~0u;
+                        const long long row = u.x + my_tok, head = u.z * p.G + my_head;
+                        uint16_t* orow = reinterpret_cast<uint16_t*>(p.o) + row * p.o_sr + head * p.o_sh;
+    #pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 64) {
+                            uint32_t ov[64];
+                            if (cnt > 0) {
+                                tmem_ld32_at<0>(tO + c0, ov);
+                                tmem_ld32_at<32>(tO + c0 + 32, ov);
+                                tmem_wait_ld();
+                            } else {
+    #pragma unroll
+                                for (int i = 0; i < 64; ++i) ov[i] = 0;
+                            }
+    #pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const float2 x = fmul2(make_float2(__uint_as_float(ov[2 * i]), __uint_as_float(ov[2 * i + 1])),
+                                                       make_float2(inv, inv));
+                                ov[i] = pack_h16<F16>(x.x, x.y) & keep;
+                            }
+                            if (held) {
+                                if (p.o_wide) {
+    #pragma unroll
+                                    for (int q = 0; q < 4; ++q) store32(orow + c0 + 16 * q, &ov[8 * q]);
+                                } else {
+    #pragma unroll
+                                    for (int q = 0; q < 8; ++q)
+                                        *reinterpret_cast<uint4*>(orow + c0 + 8 * q) =
+                                            make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
+                                }
+                            }
+                        }
+                        if (held) p.lse[head * p.T + row] = row_lse(m_ref, l);
+                    } else {
+                        // the part's state of this row; a row without keys in it is m = -inf, and its o is not read. NaN
+                        // scores leave m_ref at -inf and l NaN: such a row has keys, and its m is any other number.
+                        float4* rec = record(p.part, blockIdx.x * 2 + (first ? 1 : 0), TILES, t, rows, D);
+                        if (held) rec[r] = make_float4(l == 0.f ? -INFINITY : fmaxf(m_ref, -FLT_MAX), l, den, 0.f);
+                        if (cnt > 0) {
+    #pragma unroll 1
+                            for (int c0 = 0; c0 < D; c0 += 32) {
+                                uint32_t ov[32];
+                                tmem_ld32(tO + c0, ov);
+                                tmem_wait_ld();
+                                if (held) {
+                                    float4* dst = rec + (1 + c0 / 4) * rows + r;
+    #pragma unroll
+                                    for (int q = 0; q < 8; ++q)
+                                        dst[q * rows] = make_float4(__uint_as_float(ov[4 * q]), __uint_as_float(ov[4 * q + 1]),
+                                                                    __uint_as_float(ov[4 * q + 2]), __uint_as_float(ov[4 * q + 3]));
+                                }
+                            }
+                        }
+                    }
+}
+
+// The softmax of units of one tile. Scores come in two columns of tiles in turn, and P is written over the scores it
+// is made of, so a tile waits for no product but that of its scores (and, where the reference maximum moves, for the
+// one before).
+//
+// With COLS = 128 a thread has a row. Units of up to 32 rows have COLS = 32: a row has a lane of tensor memory in each
+// of the four warps, every warp has a copy of Q's rows, so S too, and takes 32 of a tile's 128 keys. The copies' P are
+// 0 at the other keys, so that their O add up to the row's, each with a running maximum of its own; they are merged at
+// the unit's end like the parts of a unit that was cut. 64 sequences of 8192 keys take 240 us with a row in one thread
+// and one tile of scores, 187 with copies.
+template <int D, bool F16, int KERNEL, int COLS>
+__device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Shared& bar) {
     using C = Cfg<D, 1, KERNEL, kBytes>;
     using E = Cfg8<D, F16, 1, KERNEL>;
+    constexpr bool kCopies = COLS == 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const WaitCtl wc{p.err, &bar.abort_flag, p.timeout_ns};
     const int rows = p.tok_tile * p.G;
-    const int my_tok = lane / p.G, my_head = lane % p.G;
-    const uint32_t lane_off = bar.tmem_base + ((uint32_t)(warp * 32) << 16);
-    const uint32_t tS = lane_off + warp * 32, tO = lane_off + C::o_col(0), tP = lane_off + C::p_col(0);
-    // merging: rows of a round, and as many columns as the area holds of them
-    const int span = bar.most_rows <= 8 ? 8 : bar.most_rows <= 16 ? 16 : 32;
-    const int most = 32 * 32 / span, cols = min(D, most), pitch = most + 4;
-    float4* states = reinterpret_cast<float4*>(smem + E::kStateOff);
-    float* area = reinterpret_cast<float*>(smem + E::kMergeOff);
-    uint32_t scnt = 0, ocnt = 0, mcnt = 0;
+    const int r = kCopies ? lane : threadIdx.x;
+    const int my_tok = r / p.G, my_head = r % p.G, col0 = kCopies ? warp * 32 : 0;
+    const uint32_t tmem = bar.tmem_base + ((uint32_t)(warp * 32) << 16);
+    const uint32_t tO = tmem + E::kOCol;
+    uint32_t scnt = 0, mcnt = 0, units = 0;
     bool ok = true;
-    {
-        uint32_t zero[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) zero[i] = 0;
-        tmem_st32(tP, zero);
-        tmem_st32(tP + 32, zero);
-        tmem_wait_st();
-    }
     Walk<1, KERNEL, kBytes> walk(p, bar);
     Unit w;
     bool more = walk.next(w);
     float row_c = p.c;
     int factors = 0;
     auto take_q = [&]() {
-        const uint16_t* src = nullptr;
-        if (lane < rows && my_tok < w.ntok) src = p.q + (w.row0 + my_tok) * p.q_sr + (w.h * p.G + my_head) * p.q_sh;
-        __syncwarp();
-        row_c = p.c * split_row<D, F16, true>(src, lane_off + E::kQCol, nullptr, lane);
+        if constexpr (kCopies) {
+            const uint32_t at = units % E::kQSlots;
+            ok = mbar_wait_warp(&bar.q_full[1 + at], (units / E::kQSlots) & 1, wc);
+            ++units;
+            const uint8_t* slot = smem + E::kQSlotOff + at * E::kQSlot;
+            // lanes without a row have whatever lies there; they must not move a maximum
+            row_c = lane < rows && my_tok < w.ntok ? p.c * reinterpret_cast<const float*>(slot + 32 * E::kPieces * E::kQPitch)[lane] : 0.f;
+#pragma unroll
+            for (int k = 0; k < E::kPieces; ++k)
+#pragma unroll
+                for (int c = 0; c < D; c += 64) {
+                    uint32_t x[16];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(slot + (k * 32 + lane) * E::kQPitch + c + i * 16);
+                        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+                    }
+                    tmem_st16(tmem + E::kQCol + (k * D + c) / 4, x);
+                }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (elect_one()) mbar_arrive(&bar.q_empty[1 + at]);
+            __syncwarp();
+        } else {
+            const uint16_t* src = nullptr;
+            if (r < rows && my_tok < w.ntok) src = p.q + (w.row0 + my_tok) * p.q_sr + (w.h * p.G + my_head) * p.q_sh;
+            __syncwarp();
+            row_c = p.c * split_row<D, F16, true>(src, tmem + E::kQCol, nullptr, r);
+        }
         mbar_arrive(&bar.q_full[0]);
-    };
-    auto meet = [&]() {
-        mbar_arrive(&bar.merged);
-        ok = __all_sync(kFull, mbar_wait(&bar.merged, mcnt & 1, wc));
-        ++mcnt;
     };
     if (more && w.cnt0 > 0) take_q();
     while (ok && more) {
@@ -1125,122 +1324,151 @@ __device__ __forceinline__ void softmax_copies(const PagedDev& p, uint8_t* smem,
         float m_ref = -INFINITY, m_row = -INFINITY, l = 0.f;
         bool s_ready = false;
         for (int j = 0; j < cnt; ++j) {
-            ok = s_ready || mbar_wait(&bar.s_full[0], scnt & 1, wc);
+            const uint32_t b = scnt & 1, tS = tmem + b * BN;
+            ok = s_ready || mbar_wait(&bar.s_full[b], (scnt >> 1) & 1, wc);
             ok = __all_sync(kFull, ok);
             if (!ok) break;
-            ++scnt;
             tc_fence_after();
-            uint32_t su[32];
-            tmem_ld32(tS, su);
-            const float4* f = reinterpret_cast<const float4*>(smem + E::kFactorOff) + factors * (BN / 4) + warp * 8;
+            uint32_t su[COLS];
+            tmem_ld32_at<0>(tS + col0, su);
+            if constexpr (!kCopies) {
+                tmem_ld32_at<32>(tS + 32, su);
+                tmem_ld32_at<64>(tS + 64, su);
+                tmem_ld32_at<96>(tS + 96, su);
+            }
+            const float4* f = reinterpret_cast<const float4*>(smem + E::kFactorOff) + factors * (BN / 4) + col0 / 4;
             float4 f4[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) f4[i] = f[i];
-            factors = factors + 1 == E::kFactors ? 0 : factors + 1;
             tmem_wait_ld();
+            // the scores after this tile's may have come by now
+            s_ready = j + 1 < cnt && mbar_test(&bar.s_full[b ^ 1], ((scnt + 1) >> 1) & 1);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 a = fmul2(make_float2(__uint_as_float(su[4 * i]), __uint_as_float(su[4 * i + 1])),
-                                       make_float2(f4[i].x, f4[i].y));
-                const float2 b = fmul2(make_float2(__uint_as_float(su[4 * i + 2]), __uint_as_float(su[4 * i + 3])),
-                                       make_float2(f4[i].z, f4[i].w));
+            for (int i = 0; i < COLS / 4; ++i) {
+                const float4 x = i < 8 ? f4[i % 8] : f[i];
+                const float2 a = fmul2(make_float2(__uint_as_float(su[4 * i]), __uint_as_float(su[4 * i + 1])), make_float2(x.x, x.y));
+                const float2 c = fmul2(make_float2(__uint_as_float(su[4 * i + 2]), __uint_as_float(su[4 * i + 3])),
+                                       make_float2(x.z, x.w));
                 su[4 * i] = __float_as_uint(a.x), su[4 * i + 1] = __float_as_uint(a.y);
-                su[4 * i + 2] = __float_as_uint(b.x), su[4 * i + 3] = __float_as_uint(b.y);
+                su[4 * i + 2] = __float_as_uint(c.x), su[4 * i + 3] = __float_as_uint(c.y);
             }
-            tc_fence_before();
-            mbar_arrive(&bar.s_free[0]);
-            const int key0 = (k0 + j) * BN + warp * 32;
-            if (key0 > ctx - 32) {
-                uint32_t bits[1];
-                tree_bits(p, lane < rows && my_tok < w.ntok ? p.tree + (w.row0 + my_tok) * p.tree_stride : nullptr, key0, ctx,
-                          w.len, bits);
+            factors = factors + 1 == E::kFactors ? 0 : factors + 1;
+            const int key0 = (k0 + j) * BN + col0;
+            if (key0 > ctx - COLS) {
+                uint32_t bits[COLS / 32];
+                tree_bits(p, r < rows && my_tok < w.ntok ? p.tree + (w.row0 + my_tok) * p.tree_stride : nullptr, key0, ctx, w.len,
+                          bits);
 #pragma unroll
-                for (int col = 0; col < 32; ++col)
-                    if (!(bits[0] >> col & 1)) su[col] = __float_as_uint(-INFINITY);
-            } else if (key0 + 32 > lim_first) {
+                for (int col = 0; col < COLS; ++col)
+                    if (!(bits[col / 32] >> (col & 31) & 1)) su[col] = __float_as_uint(-INFINITY);
+            } else if (key0 + COLS > lim_first) {
                 const int out = lim - key0;
 #pragma unroll
-                for (int col = 0; col < 32; ++col)
+                for (int col = 0; col < COLS; ++col)
                     if (col >= out) su[col] = __float_as_uint(-INFINITY);
             }
-            float mx[2];
+            float mx[COLS / 16];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < COLS / 16; ++c) {
                 mx[c] = fmaxf(__uint_as_float(su[16 * c]), __uint_as_float(su[16 * c + 1]));
 #pragma unroll
                 for (int e = 2; e < 16; e += 2)
                     mx[c] = fmax3(mx[c], __uint_as_float(su[16 * c + e]), __uint_as_float(su[16 * c + e + 1]));
             }
-            const float m_tile = fmaxf(mx[0], mx[1]) * row_c;
+            float m_tile = mx[0];
+#pragma unroll
+            for (int c = 1; c < COLS / 16; ++c) m_tile = fmaxf(m_tile, mx[c]);
+            m_tile *= row_c;
             m_row = fmaxf(m_row, m_tile);
             float m_new = m_ref;
             if (m_tile > m_ref + kRescaleThreshold) m_new = m_tile;
             const bool moved = m_new != m_ref;
             const float alpha = moved ? ex2(m_ref - m_new) : 1.f;  // 0 when m_ref = -inf
-            const bool rescale = j > 0 && __any_sync(kFull, moved && m_ref != -INFINITY);
+            if (j > 0 && __any_sync(kFull, moved && m_ref != -INFINITY)) {
+                // the product of the tile before has written O (the one before that had when this tile's scores came)
+                ok = mbar_wait(&bar.pv_done[b ^ 1], ((scnt - 1) >> 1) & 1, wc);
+                ok = __all_sync(kFull, ok);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t ov[32];
+                    tmem_ld32(tO + c0, ov);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                    tmem_st32(tO + c0, ov);
+                }
+            }
             m_ref = m_new;
             const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
             const float2 cc2 = make_float2(row_c, row_c), nm2 = make_float2(neg_m, neg_m);
             float2 suma = make_float2(0.f, 0.f), sumb = make_float2(0.f, 0.f);
-            const bool o_ready = j > 0 && mbar_test(&bar.pv_done[0], ocnt & 1);
-            uint32_t pk[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float2 x = ffma2(make_float2(__uint_as_float(su[2 * i]), __uint_as_float(su[2 * i + 1])), cc2, nm2);
-                const float2 pp = make_float2(ex2(x.x), ex2(x.y));
-                if (i & 1)
-                    sumb = fadd2(sumb, pp);
-                else
-                    suma = fadd2(suma, pp);
-                pk[i] = pack_h16<F16>(pp.x, pp.y);
-            }
-            if (j > 0) {  // the product of tile j-1 has read P and written O
-                ok = o_ready || mbar_wait(&bar.pv_done[0], ocnt & 1, wc);
-                ok = __all_sync(kFull, ok);
-                if (!ok) break;
-                ++ocnt;
-                tc_fence_after();
-                if (rescale) {
-#pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 32) {
-                        uint32_t ov[32];
-                        tmem_ld32(tO + c0, ov);
-                        tmem_wait_ld();
+            for (int c0 = 0; c0 < COLS; c0 += 32) {
+                uint32_t pk[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-                        tmem_st32(tO + c0, ov);
-                    }
+                for (int i = 0; i < 16; ++i) {
+                    const float2 x =
+                        ffma2(make_float2(__uint_as_float(su[c0 + 2 * i]), __uint_as_float(su[c0 + 2 * i + 1])), cc2, nm2);
+                    const float2 pp = make_float2(ex2(x.x), ex2(x.y));
+                    if (i & 1)
+                        sumb = fadd2(sumb, pp);
+                    else
+                        suma = fadd2(suma, pp);
+                    pk[i] = pack_h16<F16>(pp.x, pp.y);
                 }
+                tmem_st16(tS + (col0 + c0) / 2, pk);
             }
-            tmem_st16(tP + warp * 16, pk);
-            s_ready = j + 1 < cnt && mbar_test(&bar.s_full[0], scnt & 1);
+            if constexpr (kCopies) {  // the other copies' keys
+                uint32_t zero[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) zero[i] = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k != warp) tmem_st16(tS + 16 * k, zero);
+            }
             l = l * alpha + ((suma.x + suma.y) + (sumb.x + sumb.y));
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&bar.p_full[0]);
+            mbar_arrive(&bar.p_full[b]);
+            ++scnt;
         }
         if (!ok) break;
         more = walk.next(w);  // while the last product runs
         if (more && w.cnt0 > 0) take_q();  // every product with this unit's has been waited for
+        if (!ok) break;
         const bool first = u.w & 1, last = u.w & 2;
-        if (cnt > 0) {
-            ok = mbar_wait(&bar.pv_done[0], ocnt & 1, wc);
+        if (cnt > 0) {  // the last product, and so those before it
+            ok = mbar_wait(&bar.pv_done[(scnt - 1) & 1], ((scnt - 1) >> 1) & 1, wc);
             ok = __all_sync(kFull, ok);
             if (!ok) break;
-            ++ocnt;
             tc_fence_after();
-            // The copy's state, as that of a part of a unit. Every warp is done with the unit before, or there would be
-            // no P for the product above.
-            if (lane < span)
-                states[warp * span + lane] =
-                    make_float4(l == 0.f ? -INFINITY : fmaxf(m_ref, -FLT_MAX), l, o_divisor<F16>(l, m_row, m_ref), 0.f);
         }
-        const int r = threadIdx.x % span, group = threadIdx.x / span;  // merges 8 columns of row r
-        const int tok = r / p.G;
-        const bool held = r < rows && tok < u.y && group * 8 < cols;
-        const long long row = u.x + tok, head = u.z * p.G + r % p.G;
+        if constexpr (!kCopies) {
+            finish_row<D, F16, C::Kernel::kTiles>(p, u, 0, r, my_tok, my_head, rows, cnt, tO, m_ref, m_row, l);
+            tc_fence_before();
+            continue;
+        }
+        // Merging, rows and columns in rounds that the area holds: `span` rows of `cols` columns, a thread 8 columns of row rr.
+        const int span = bar.most_rows <= 8 ? 8 : bar.most_rows <= 16 ? 16 : 32;
+        const int most = 32 * 32 / span, cols = min(D, most), pitch = most + 4;
+        float4* states = reinterpret_cast<float4*>(smem + E::kStateOff);
+        float* area = reinterpret_cast<float*>(smem + E::kMergeOff);
+        auto meet = [&]() {
+            mbar_arrive(&bar.merged);
+            ok = __all_sync(kFull, mbar_wait(&bar.merged, mcnt & 1, wc));
+            ++mcnt;
+        };
+        // The copy's state, as that of a part of a unit. Every warp is done with the unit before, or there would be no P
+        // for the products above.
+        if (cnt > 0 && lane < span)
+            states[warp * span + lane] = make_float4(l == 0.f ? -INFINITY : fmaxf(m_ref, -FLT_MAX), l, o_divisor<F16>(l, m_row, m_ref), 0.f);
+        const int rr = threadIdx.x % span, group = threadIdx.x / span, tok = rr / p.G;
+        const bool held = rr < rows && tok < u.y && group * 8 < cols;
+        const long long row = u.x + tok, head = u.z * p.G + rr % p.G;
         uint16_t* orow = reinterpret_cast<uint16_t*>(p.o) + row * p.o_sr + head * p.o_sh;
-        float4* rec = record(p.part, blockIdx.x * 2 + (first ? 1 : 0), C::Kernel::kTiles, 0, rows, D) + r;
+        float4* rec = record(p.part, blockIdx.x * 2 + (first ? 1 : 0), C::Kernel::kTiles, 0, rows, D) + rr;
 #pragma unroll 1
         for (int c0 = 0; c0 < D && ok; c0 += cols) {
             if (cnt > 0) {
@@ -1266,7 +1494,7 @@ __device__ __forceinline__ void softmax_copies(const PagedDev& p, uint8_t* smem,
             float4 st[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                st[k] = cnt > 0 ? states[k * span + r] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+                st[k] = cnt > 0 ? states[k * span + rr] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
                 m = fmaxf(m, st[k].x);
             }
 #pragma unroll
@@ -1277,11 +1505,11 @@ __device__ __forceinline__ void softmax_copies(const PagedDev& p, uint8_t* smem,
                 const float f = ex2(st[k].x - m);
                 sum = fmaf(f, st[k].y, sum);
                 den = fmaf(f, st[k].z, den);
-                const float4* src = reinterpret_cast<const float4*>(area + (k * span + r) * pitch + group * 8);
-                const float4 a = src[0], b = src[1];
+                const float4* src = reinterpret_cast<const float4*>(area + (k * span + rr) * pitch + group * 8);
+                const float4 a = src[0], c = src[1];
                 out[0] = fmaf(f, a.x, out[0]), out[1] = fmaf(f, a.y, out[1]), out[2] = fmaf(f, a.z, out[2]);
-                out[3] = fmaf(f, a.w, out[3]), out[4] = fmaf(f, b.x, out[4]), out[5] = fmaf(f, b.y, out[5]);
-                out[6] = fmaf(f, b.z, out[6]), out[7] = fmaf(f, b.w, out[7]);
+                out[3] = fmaf(f, a.w, out[3]), out[4] = fmaf(f, c.x, out[4]), out[5] = fmaf(f, c.y, out[5]);
+                out[6] = fmaf(f, c.z, out[6]), out[7] = fmaf(f, c.w, out[7]);
             }
             if (!held) continue;
             if (first && last) {
@@ -1313,8 +1541,9 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
     if (threadIdx.x == 0) {
         const uint32_t rows = copies ? 128u : 32u * (uint32_t)bar.sm_warps;  // softmax threads of a tile
         for (int i = 0; i < 4; ++i) {
-            mbar_init(&bar.q_full[i], VAR == kBytes ? rows : 1);
-            mbar_init(&bar.q_empty[i], 1);
+            const bool slot = VAR == kBytes && NT == 1 && i > 0;  // of small units' pieces
+            mbar_init(&bar.q_full[i], VAR == kBytes && !slot ? rows : 1);
+            mbar_init(&bar.q_empty[i], slot ? 4 : 1);
         }
         if constexpr (VAR == kBytes) {
             using E = Cfg8<D, F16, NT, KERNEL>;
@@ -1339,15 +1568,15 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 mbar_init(&bar.v_tail[s], 1);
             }
         }
-        for (int t = 0; t < NT; ++t) {
+        for (int t = 0; t < (VAR == kBytes ? 2 : NT); ++t) {
             mbar_init(&bar.s_full[t], 1);
             mbar_init(&bar.p_full[t], rows);
             mbar_init(&bar.o_full[t], 1);
             mbar_init(&bar.s_free[t], rows);
             mbar_init(&bar.pv_done[t], 1);
             mbar_init(&bar.drain[t], 1);
-            if (VAR == kBytes && NT == 1) mbar_init(&bar.merged, 128);
         }
+        if (VAR == kBytes) mbar_init(&bar.merged, 128);
         fence_mbar_init();
     }
     __syncthreads();
@@ -1673,12 +1902,14 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
         if constexpr (C::Kernel::kRebalance) regs_increase<C::Kernel::kSoftmaxRegs>();
         // ------------------------------------------------ softmax (thread = query row)
         const int t = NT == 2 ? warp >> 2 : 0;
-        bool whole_rows = true;
         if constexpr (VAR == kBytes && NT == 1) {
-            whole_rows = !copies;
-            if (copies && warp < 4) softmax_copies<D, F16, KERNEL>(p, smem, bar);
-        }
-        if (whole_rows && warp < 4 * NT && (warp & 3) < bar.sm_warps) {
+            if (warp < 4) {
+                if (copies)
+                    softmax_one<D, F16, KERNEL, 32>(p, smem, bar);
+                else if (warp < bar.sm_warps)
+                    softmax_one<D, F16, KERNEL, 128>(p, smem, bar);
+            }
+        } else if (warp < 4 * NT && (warp & 3) < bar.sm_warps) {
             const int r = (warp & 3) * 32 + lane;
             const int rows = p.tok_tile * p.G;
             const int my_tok = t * p.tok_tile + r / p.G, my_head = r % p.G;
@@ -1865,65 +2096,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 }
                 __syncwarp();
                 const int4 u = bar.unit[warp];
-                const bool held = r < rows && my_tok < u.y, first = u.w & 1, last = u.w & 2;
-                const float den = o_divisor<F16>(l, m_row, m_ref);
-                if (first && last) {
-                    const float inv = den > 0.f ? 1.f / den : 0.f;
-                    // a row without keys is 0, though its products of 0 and a value may be NaN
-                    const uint32_t keep = l == 0.f ? 0u : ~0u;
-                    const long long row = u.x + my_tok, head = u.z * p.G + my_head;
-                    uint16_t* orow = reinterpret_cast<uint16_t*>(p.o) + row * p.o_sr + head * p.o_sh;
-#pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 64) {
-                        uint32_t ov[64];
-                        if (cnt > 0) {
-                            tmem_ld32_at<0>(tO + c0, ov);
-                            tmem_ld32_at<32>(tO + c0 + 32, ov);
-                            tmem_wait_ld();
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 64; ++i) ov[i] = 0;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float2 x = fmul2(make_float2(__uint_as_float(ov[2 * i]), __uint_as_float(ov[2 * i + 1])),
-                                                   make_float2(inv, inv));
-                            ov[i] = pack_h16<F16>(x.x, x.y) & keep;
-                        }
-                        if (held) {
-                            if (p.o_wide) {
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) store32(orow + c0 + 16 * q, &ov[8 * q]);
-                            } else {
-#pragma unroll
-                                for (int q = 0; q < 8; ++q)
-                                    *reinterpret_cast<uint4*>(orow + c0 + 8 * q) =
-                                        make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
-                            }
-                        }
-                    }
-                    if (held) p.lse[head * p.T + row] = row_lse(m_ref, l);
-                } else {
-                    // the part's state of this row; a row without keys in it is m = -inf, and its o is not read. NaN
-                    // scores leave m_ref at -inf and l NaN: such a row has keys, and its m is any other number.
-                    float4* rec = record(p.part, blockIdx.x * 2 + (first ? 1 : 0), C::Kernel::kTiles, t, rows, D);
-                    if (held) rec[r] = make_float4(l == 0.f ? -INFINITY : fmaxf(m_ref, -FLT_MAX), l, den, 0.f);
-                    if (cnt > 0) {
-#pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            uint32_t ov[32];
-                            tmem_ld32(tO + c0, ov);
-                            tmem_wait_ld();
-                            if (held) {
-                                float4* dst = rec + (1 + c0 / 4) * rows + r;
-#pragma unroll
-                                for (int q = 0; q < 8; ++q)
-                                    dst[q * rows] = make_float4(__uint_as_float(ov[4 * q]), __uint_as_float(ov[4 * q + 1]),
-                                                                __uint_as_float(ov[4 * q + 2]), __uint_as_float(ov[4 * q + 3]));
-                            }
-                        }
-                    }
-                }
+                finish_row<D, F16, C::Kernel::kTiles>(p, u, t, r, my_tok, my_head, rows, cnt, tO, m_ref, m_row, l);
                 tc_fence_before();
             }
         }
