@@ -82,6 +82,7 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -174,48 +175,52 @@ struct Cfg {
     static constexpr bool kVProducer = kIssuers == 1;
 };
 
-// A CTA of the kBytes variant that works on units of NT tiles.
+// A CTA of the kBytes variant that works on units of NT tiles; SMALL: one-tile units of up to 32 rows.
 //
 // Keys go to the tensor cores as the codes they are, since a product of E4M3 codes is exact in fp32: Q is split
-// into kPieces 8-bit numbers whose sum it is (split_pair), and S is the sum of their products with the codes,
-// times the key's scale and the row's. Values are widened to 16 bits by a group of converter warps, scales
-// included: P in 8 bits would not do, since pieces of it would lose the many small probabilities of a long row.
+// into kPieces 8-bit numbers whose sum it is (split_half2), and S is the sum of their products with the codes,
+// times the key's scale and the row's. Values are widened to 16 bits by converter warps, scales included; for small
+// units to fp16 without them, since the scale can go into P there (softmax_one). P in 8-bit pieces, which would
+// need no converters, is slower: the splitting comes on top of the softmax, which a tile then waits for.
 //
-// Widening the keys too, with Q as it is, takes 335 us for 64 sequences of 8192 keys: the converters' integer
+// Widening keys and values, with Q as it is, takes 335 us for 64 sequences of 8192 keys: the converters' integer
 // instructions issue at 64 lanes a cycle.
-template <int D, bool F16, int NT, int KERNEL>
+template <int D, bool F16, int NT, int KERNEL, bool SMALL>
 struct Cfg8 {
     using Kernel = Shape<D, KERNEL, kBytes>;
     static constexpr int kTileBytes = BN * D;      // of codes
     static constexpr int kPieces = F16 ? 3 : 2;    // of 4, 4 and 3 bits of Q's 11 or 8
-    // Tensor memory of units of one tile: two tiles of scores, P over the scores it is made of, O, and Q's pieces (a
-    // product then reads keys alone from shared memory). Two tiles leave no room for Q there.
+    static constexpr bool kWideF16 = F16 || SMALL; // type of the widened values and of P
+    // Tensor memory of units of one tile: scores from 0 on, Q's pieces (a product then reads keys alone from shared
+    // memory), O, and P of two tiles in turn. Units of two tiles have no room for Q there.
     static constexpr bool kQTmem = NT == 1;
-    static constexpr int kOCol = 256, kQCol = 384;
+    static constexpr int kQCol = 128, kOCol = 256, kPCol = 384;
     static constexpr int kQBytes = kQTmem ? 0 : NT * kPieces * kTileBytes;
-    // widened values, then rings of codes and of their scales, and the keys' scales as floats
+    // widened values, then rings of codes and of their scales, and the keys' factors as floats
     static constexpr int kWide = D == 128 ? 2 : 3;
     static constexpr int kWideOff = kQBytes, kKeyOff = kWideOff + kWide * 2 * kTileBytes;
-    // For units of up to 32 rows: pieces of Q and factors of its rows for two units, and where copies of rows are
-    // merged (softmax_one).
+    // small units: pieces of Q and factors of its rows for two units, and where copies of rows are merged
     static constexpr int kQSlots = 2, kQPitch = D + 16, kQSlot = 32 * kPieces * kQPitch + 32 * 4;
     static constexpr int kStateBytes = 4 * 32 * 16, kMergeBytes = 4 * 32 * 36 * 4;
-    static constexpr int kExtraBytes = NT == 1 ? kQSlots * kQSlot + kStateBytes + kMergeBytes : 0;
+    static constexpr int kExtraBytes = SMALL ? kQSlots * kQSlot + kStateBytes + kMergeBytes : 0;
     static constexpr int kRoom = Kernel::kTilesBytes - kKeyOff - kExtraBytes;
-    static constexpr int kFit = (kRoom - 3 * BN * 4) / (kTileBytes + BN + BN * 2);
+    // Factors of a tile: the keys' scales, and for small units the exponents of the values' scales and the scales'
+    // inverses. Two stages more than keys have: a tile of keys arrives when the products with the one kKeys before
+    // it are done, and by then the softmax has read the factors of what came two before that (a thread reads a
+    // tile's factors before it takes the next one's scores).
+    static constexpr int kFactorBytes = (SMALL ? 3 : 1) * BN * 4;
+    static constexpr int kFit = (kRoom - 3 * kFactorBytes) / (kTileBytes + BN + kFactorBytes / 2);
     static constexpr int kBoth = kFit < 16 ? kFit : 16;
     static constexpr int kKeys = (kBoth + 1) / 2, kValues = kBoth / 2;  // stages
     static constexpr int kValueOff = kKeyOff + kKeys * kTileBytes;
     static constexpr int kKeyScaleOff = kValueOff + kValues * kTileBytes, kValueScaleOff = kKeyScaleOff + kKeys * BN;
-    // Two stages more than keys have: a tile of keys arrives when the products with the one kKeys before it are done,
-    // and by then the softmax has read what came two before that (an issuer releases a tile of keys at most one
-    // tile ahead of the softmax's last read).
     static constexpr int kFactors = kKeys + 2;
     static constexpr int kFactorOff = kValueScaleOff + kValues * BN;
-    static constexpr int kQSlotOff = kFactorOff + kFactors * BN * 4;
+    static constexpr int kQSlotOff = kFactorOff + kFactors * kFactorBytes;
     static constexpr int kStateOff = kQSlotOff + kQSlots * kQSlot, kMergeOff = kStateOff + kStateBytes;
     static_assert(kValues >= 1 && kQSlotOff + kExtraBytes <= Kernel::kTilesBytes, "shared memory");
-    static_assert(!kQTmem || (kOCol + D <= kQCol && kQCol + kPieces * D / 4 <= 512), "tensor memory");
+    static_assert(kQCol + kPieces * D / 4 <= kOCol && kOCol + D <= kPCol, "tensor memory");
+    static constexpr int kMakers = 4;  // converter warps
 };
 
 struct PagedDev {
@@ -628,6 +633,14 @@ __device__ __forceinline__ uint32_t mad(uint32_t a, uint32_t b, uint32_t c) {
     return d;
 }
 
+// 16 codes as fp16 numbers.
+__device__ __forceinline__ void codes16(uint4 v, uint32_t (&out)[8]) {
+    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(out[k]) : "h"((uint16_t)(in[k / 2] >> (16 * (k & 1)))));
+}
+
 // 16 codes times the scale 2^(s - 127). fp16 has an instruction that widens codes. For bf16, the seven bits below
 // a code's sign are moved to where bf16 has exponent and fraction, which makes a number 2^120 too small
 // (subnormal codes become subnormal numbers, to the same factor), and the factor goes into the multiplication
@@ -660,13 +673,13 @@ __device__ __forceinline__ void widen16(uint4 v, int s, uint32_t (&out)[8]) {
     }
 }
 
-// Makes the share of warp c of W of a 16-bit tile from a tile of codes: rows of 128 bytes per 64 columns, 16-byte
+// Makes the share of warp c of W of a 16-bit tile from a tile of codes (CODES: in fp16, without scales): rows of 128 bytes per 64 columns, 16-byte
 // chunks swizzled by the row as TMA does. Rows from `left` on become 0.
 // A lane has 16 codes of a row at a time, and the same row of every 8 and the same columns in all of its turns,
 // so that its addresses differ by constants. Eight lanes that access memory together read and write all
 // banks: at d = 128 (codes swizzled like the tile) four lanes on the first columns of a row and four on those of
 // the row that differs in bits 0 and 2, at d = 64 four on each of two rows.
-template <int D, bool F16, int W>
+template <int D, bool F16, int W, bool CODES>
 __device__ __forceinline__ void widen_tile(const uint8_t* raw, const uint8_t* scale, uint8_t* tile, int left, int c, int lane) {
     constexpr int kTurns = D == 128 ? 2 : 1;  // for 8 rows
     constexpr int kRows = BN / W, kEach = kRows / 8;
@@ -674,7 +687,7 @@ __device__ __forceinline__ void widen_tile(const uint8_t* raw, const uint8_t* sc
     const int r0 = D == 128 ? (lane >> 4) ^ (lane & 4 ? 5 : 0) : lane >> 2;
     // scales that take a second multiplication are looked for once a tile
     const uint32_t s4 = *reinterpret_cast<const uint32_t*>(scale + lane * 4);
-    const bool plain = (F16 || !__any_sync(kFull, __vcmpgtu4(s4, 0x86868686u) != 0)) && left >= BN;
+    const bool plain = (F16 || CODES || !__any_sync(kFull, __vcmpgtu4(s4, 0x86868686u) != 0)) && left >= BN;
 #pragma unroll
     for (int turn = 0; turn < kTurns; ++turn) {
         const int row7 = r0 ^ (turn * 2), row = c * kRows + row7;  // and every 8th row behind it
@@ -687,12 +700,15 @@ __device__ __forceinline__ void widen_tile(const uint8_t* raw, const uint8_t* sc
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
                 v[i] = *reinterpret_cast<const uint4*>(from + i * 8 * D);
-                s[i] = scale[row + i * 8];
+                s[i] = CODES ? 0 : scale[row + i * 8];
             }
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
                 uint32_t out[8];
-                widen16<F16, true>(v[i], s[i], out);
+                if constexpr (CODES)
+                    codes16(v[i], out);
+                else
+                    widen16<F16, true>(v[i], s[i], out);
                 *reinterpret_cast<uint4*>(to + i * 1024 + a0) = make_uint4(out[0], out[1], out[2], out[3]);
                 *reinterpret_cast<uint4*>(to + i * 1024 + a1) = make_uint4(out[4], out[5], out[6], out[7]);
             }
@@ -700,7 +716,11 @@ __device__ __forceinline__ void widen_tile(const uint8_t* raw, const uint8_t* sc
 #pragma unroll 1
             for (int i = 0; i < kEach; ++i) {
                 uint32_t out[8];
-                widen16<F16, false>(*reinterpret_cast<const uint4*>(from + i * 8 * D), scale[row + i * 8], out);
+                const uint4 v = *reinterpret_cast<const uint4*>(from + i * 8 * D);
+                if constexpr (CODES)
+                    codes16(v, out);
+                else
+                    widen16<F16, false>(v, scale[row + i * 8], out);
                 if (row + i * 8 >= left) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) out[k] = 0;
@@ -857,12 +877,90 @@ __device__ __noinline__ void drain_codes(Shared& bar, uint32_t keys, uint32_t va
         drain_wait(&bar.v_full[s], ((bar.issued[1] - 1 - s) / values) & 1, timeout_ns);
 }
 
+// The factors of one-tile units' keys, by a warp of its own: the products with keys do not wait for values to be widened
+// then.
+template <int D, bool F16, int KERNEL, bool SMALL>
+__device__ __forceinline__ void make_factors(const PagedDev& p, uint8_t* smem, Shared& bar) {
+    using E = Cfg8<D, F16, 1, KERNEL, SMALL>;
+    const int lane = threadIdx.x & 31;
+    const WaitCtl wc{p.err, &bar.abort_flag, p.timeout_ns};
+    Walk<1, KERNEL, kBytes> walk(p, bar);
+    Unit w;
+    uint32_t n = 0;
+    bool ok = true;
+    while (ok && walk.next(w)) {
+        for (int j = 0; j < w.cnt_max && ok; ++j, ++n) {
+            const uint32_t s = n % E::kKeys, sv = n % E::kValues;
+            ok = mbar_wait_warp(&bar.k_full[s], (n / E::kKeys) & 1, wc);
+            if (SMALL && ok) ok = mbar_wait_warp(&bar.v_full[sv], (n / E::kValues) & 1, wc);
+            if (!ok) break;
+            uint4* factors = reinterpret_cast<uint4*>(smem + E::kFactorOff + n % E::kFactors * E::kFactorBytes);
+            const uint32_t b4 = *reinterpret_cast<const uint32_t*>(smem + E::kKeyScaleOff + s * BN + lane * 4);
+            factors[lane] = make_uint4((b4 & 0xff) << 23, (b4 & 0xff00) << 15, (b4 & 0xff0000) << 7, b4 >> 1 & 0x7f800000);
+            if constexpr (SMALL) {
+                // A value's scale below 2^-90 counts as that (its row's values are below 2^-81), so that no sum of weights
+                // overflows; bytes beyond the sequence may be anything, and these stay finite.
+                const uint32_t v4 = *reinterpret_cast<const uint32_t*>(smem + E::kValueScaleOff + sv * BN + lane * 4);
+                uint32_t v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = min(max(v4 >> (8 * i) & 0xff, 37u), 253u);
+                reinterpret_cast<float4*>(factors)[BN / 4 + lane] =
+                    make_float4((float)v[0] - 127.f, (float)v[1] - 127.f, (float)v[2] - 127.f, (float)v[3] - 127.f);
+                factors[BN / 2 + lane] =
+                    make_uint4((254u - v[0]) << 23, (254u - v[1]) << 23, (254u - v[2]) << 23, (254u - v[3]) << 23);
+            }
+            __syncwarp();
+            if (elect_one()) {
+                mbar_arrive(&bar.k_ready[s]);
+                if (SMALL) mbar_arrive(&bar.v_empty[sv]);
+            }
+            __syncwarp();
+        }
+    }
+}
+
+// The products P V of one-tile units, by a warp of its own: one that issues the scores' too would come to either late (64
+// sequences of 8192 keys 172 us). Nothing orders the two but their barriers: scores, P and O have columns of their own.
+template <int D, bool F16, int KERNEL, bool SMALL>
+__device__ __forceinline__ void issue_values(const PagedDev& p, uint8_t* smem, Shared& bar) {
+    using E = Cfg8<D, F16, 1, KERNEL, SMALL>;
+    constexpr uint32_t kIdesc = idesc_h16(BM, D, false, true, E::kWideF16);
+    const WaitCtl wc{p.err, &bar.abort_flag, p.timeout_ns};
+    const uint32_t tmem = __shfl_sync(kFull, bar.tmem_base, 0);
+    Walk<1, KERNEL, kBytes> walk(p, bar);
+    Unit w;
+    uint32_t n = 0;
+    bool ok = true;
+    while (ok && walk.next(w)) {
+        for (int j = 0; j < w.cnt_max && ok; ++j, ++n) {
+            const uint32_t s = n % E::kWide, b = n & 1;
+            ok = mbar_wait_warp(&bar.kv_full[s], (n / E::kWide) & 1, wc) && mbar_wait_warp(&bar.p_full[b], (n >> 1) & 1, wc);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t vd = vmajor_desc(smem_u32(smem + E::kWideOff + s * 2 * E::kTileBytes));
+#pragma unroll
+                for (int kk = 0; kk < BN / 16; ++kk)
+                    mma_ts(tmem + E::kOCol, tmem + E::kPCol + b * 64 + kk * 8, vmajor_step(vd, kk), kIdesc, j > 0 || kk > 0 ? 1u : 0u);
+                mma_commit(&bar.pv_done[b]);
+                mma_commit(&bar.kv_empty[s]);
+            }
+            __syncwarp();
+        }
+    }
+    if (elect_one()) {
+        mma_commit(&bar.drain[1]);
+        drain_wait(&bar.drain[1], 0, p.timeout_ns);
+    }
+    __syncwarp();
+}
+
 // The roles of kBytes but the softmax's.
-template <int D, bool F16, int NT, int KERNEL>
+template <int D, bool F16, int NT, int KERNEL, bool SMALL>
 __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedDev& p, uint8_t* smem,
                                        Shared& bar) {
     using C = Cfg<D, NT, KERNEL, kBytes>;
-    using E = Cfg8<D, F16, NT, KERNEL>;
+    using E = Cfg8<D, F16, NT, KERNEL, SMALL>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const WaitCtl wc{p.err, &bar.abort_flag, p.timeout_ns};
     // Broadcast, so that the compiler knows what is the same in all lanes: an issuer's operands then stay in the registers
@@ -949,7 +1047,6 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
         }
     } else if (warp == C::kTail) {
         // ------------------------------------------------ the CTA's slots, and Q of small units
-        const bool small = NT == 1 && bar.sm_warps == 1;
         uint32_t units = 0;
         bool ok = true;
         int4 slot0 = make_int4(kNone, 0, 0, 0), slot1 = slot0;
@@ -961,7 +1058,7 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
                 else
                     slot0 = m;
             }
-            if (!small || w.cnt_max == 0 || !ok) continue;  // the slots are written whatever happens
+            if (!SMALL || w.cnt_max == 0 || !ok) continue;  // the slots are written whatever happens
             const uint32_t at = units % E::kQSlots;
             ok = mbar_wait_warp(&bar.q_empty[1 + at], ((units / E::kQSlots) & 1) ^ 1, wc);
             if (!ok) continue;
@@ -976,18 +1073,23 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
         // ------------------------------------------------ converters: the keys' factors, the values in 16 bits
         // All on every tile, in order: a wait tells the phases of a stage apart only while no use of it is passed
         // over, and none can pass while the wait stands.
-        constexpr int W = E::Kernel::kConverters;
+        constexpr int W = E::kMakers;
         const int c = warp - kConvert;
+        if constexpr (NT == 1 && KERNEL == kOne)
+            {
+                if (c == W) make_factors<D, F16, KERNEL, SMALL>(p, smem, bar);
+                if (c == W + 1) issue_values<D, F16, KERNEL, SMALL>(p, smem, bar);
+            }
         uint32_t n = 0;
-        bool ok = true;
+        bool ok = c < W;
         while (ok && walk.next(w)) {
             for (int j = 0; j < w.cnt_max && ok; ++j, ++n) {
                 const uint32_t sk = n % E::kKeys, sv = n % E::kValues, so = n % E::kWide;
                 const uint32_t pk = (n / E::kKeys) & 1, pv = (n / E::kValues) & 1, po = ((n / E::kWide) & 1) ^ 1;
                 const unsigned ready = look(&bar.k_full[sk], pk, &bar.v_full[sv], pv, &bar.kv_empty[so], po, &bar.k_full[sk], pk);
-                ok = (ready & 1) || mbar_wait_warp(&bar.k_full[sk], pk, wc);
-                if (!ok) break;
-                if (c < BN / 32) {
+                if constexpr (NT == 2) {
+                    ok = (ready & 1) || mbar_wait_warp(&bar.k_full[sk], pk, wc);
+                    if (!ok) break;
                     const int at = c * 32 + lane;
                     reinterpret_cast<uint32_t*>(smem + E::kFactorOff)[n % E::kFactors * BN + at] =
                         (uint32_t)smem[E::kKeyScaleOff + sk * BN + at] << 23;
@@ -997,7 +1099,7 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
                 ok = ((ready & 2) || mbar_wait_warp(&bar.v_full[sv], pv, wc)) &&
                      ((ready & 4) || mbar_wait_warp(&bar.kv_empty[so], po, wc));
                 if (!ok) break;
-                widen_tile<D, F16, W>(smem + E::kValueOff + sv * E::kTileBytes, smem + E::kValueScaleOff + sv * BN,
+                widen_tile<D, F16, W, SMALL>(smem + E::kValueOff + sv * E::kTileBytes, smem + E::kValueScaleOff + sv * BN,
                                       smem + E::kWideOff + so * 2 * E::kTileBytes, w.len - (w.k0 + j) * BN, c, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -1009,47 +1111,23 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
             }
         }
     } else if (NT == 1 && warp == C::kIssuer) {
-        // ------------------------------------------------ issuer of one tile: scores are two tiles ahead of P V
-        uint32_t nk = 0, nv = 0, units = 0;  // tiles of keys, of values
+        // ------------------------------------------------ issuer of one tile's scores
+        uint32_t n = 0, units = 0;
         bool ok = true;
-        auto next_s = [&]() {
-            const uint32_t s = nk % E::kKeys;
-            ok = mbar_wait_warp(&bar.k_ready[s], (nk / E::kKeys) & 1, wc);
-            if (!ok) return;
-            tc_fence_after();
-            if (elect_one()) {
-                issue_s(0, (nk & 1) * BN, s);
-                mma_commit(&bar.s_full[nk & 1]);
-                mma_commit(&bar.k_empty[s]);
-            }
-            __syncwarp();
-            ++nk;
-        };
         while (ok && walk.next(w)) {
-            const int cnt = __shfl_sync(kFull, w.cnt_max, 0);
-            if (cnt == 0) continue;
+            if (w.cnt_max == 0) continue;
             ok = mbar_wait_warp(&bar.q_full[0], units++ & 1, wc);
-            if (!ok) break;
-            // Two tiles of scores: what they write over was read by products issued before (P) and by the softmax
-            // before it made that P.
-            next_s();
-            if (ok && cnt > 1) next_s();
-            for (int j = 0; j < cnt && ok; ++j) {
-                const uint32_t s = nv % E::kWide, v_phase = (nv / E::kWide) & 1, b = nv & 1, p_phase = (nv >> 1) & 1;
-                const unsigned ready = look(&bar.kv_full[s], v_phase, &bar.p_full[b], p_phase, &bar.kv_full[s], v_phase,
-                                            &bar.p_full[b], p_phase);
-                ok = ((ready & 1) || mbar_wait_warp(&bar.kv_full[s], v_phase, wc)) &&
-                     ((ready & 2) || mbar_wait_warp(&bar.p_full[b], p_phase, wc));
+            for (int j = 0; j < w.cnt_max && ok; ++j, ++n) {
+                const uint32_t s = n % E::kKeys;
+                ok = mbar_wait_warp(&bar.k_ready[s], (n / E::kKeys) & 1, wc) && mbar_wait_warp(&bar.s_free[0], (n & 1) ^ 1, wc);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    issue_pv(E::kOCol, b * BN, s, j == 0);
-                    mma_commit(&bar.pv_done[b]);
-                    mma_commit(&bar.kv_empty[s]);
+                    issue_s(0, 0, s);
+                    mma_commit(&bar.s_full[0]);
+                    mma_commit(&bar.k_empty[s]);
                 }
                 __syncwarp();
-                ++nv;
-                if (j + 2 < cnt) next_s();
             }
         }
         if (elect_one()) {
@@ -1253,29 +1331,39 @@ __device__ __forceinline__ void finish_row(const PagedDev& p, const int4& u, int
                     }
 }
 
-// The softmax of units of one tile. Scores come in two columns of tiles in turn, and P is written over the scores it
-// is made of, so a tile waits for no product but that of its scores (and, where the reference maximum moves, for the
-// one before).
+// The softmax of units of one tile.
 //
-// With COLS = 128 a thread has a row. Units of up to 32 rows have COLS = 32: a row has a lane of tensor memory in each
-// of the four warps, every warp has a copy of Q's rows, so S too, and takes 32 of a tile's 128 keys. The copies' P are
-// 0 at the other keys, so that their O add up to the row's, each with a running maximum of its own; they are merged at
-// the unit's end like the parts of a unit that was cut. 64 sequences of 8192 keys take 240 us with a row in one thread
-// and one tile of scores, 187 with copies.
-template <int D, bool F16, int KERNEL, int COLS>
+// A thread has a row, but in small units a row has a lane of tensor memory in each of the four warps: every warp has a
+// copy of Q's rows, so S too, and takes 32 of a tile's 128 keys. The copies' P are 0 at the other keys, so that their O
+// add up to the row's, each with a running maximum of its own; they are merged at the unit's end like the parts of a
+// unit that was cut (64 sequences of 8192 keys 240 us with a row in one thread, 187 with copies).
+//
+// Small units' values are codes v of scale 2^e: O = sum p 2^e v, so P is taken with the scale, y = 2^(s + e - m) with m a
+// reference maximum of s + e, and the sum of weights from y 2^-e. y is at most 2^8 and rounded to fp16, that is to 2^-25
+// where it is small.
+template <int D, bool F16, int KERNEL, bool SMALL>
 __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Shared& bar) {
     using C = Cfg<D, 1, KERNEL, kBytes>;
-    using E = Cfg8<D, F16, 1, KERNEL>;
-    constexpr bool kCopies = COLS == 32;
+    using E = Cfg8<D, F16, 1, KERNEL, SMALL>;
+    constexpr bool kCopies = SMALL;
+    constexpr int COLS = SMALL ? 32 : 128;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const WaitCtl wc{p.err, &bar.abort_flag, p.timeout_ns};
     const int rows = p.tok_tile * p.G;
     const int r = kCopies ? lane : threadIdx.x;
     const int my_tok = r / p.G, my_head = r % p.G, col0 = kCopies ? warp * 32 : 0;
     const uint32_t tmem = bar.tmem_base + ((uint32_t)(warp * 32) << 16);
-    const uint32_t tO = tmem + E::kOCol;
-    uint32_t scnt = 0, mcnt = 0, units = 0;
+    const uint32_t tO = tmem + E::kOCol, tP = tmem + E::kPCol;
+    uint32_t scnt = 0, mcnt = 0, units = 0;  // scnt: tiles before this one
     bool ok = true;
+    if constexpr (kCopies) {  // P at the other copies' keys
+        uint32_t zero[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) zero[i] = 0;
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) tmem_st32(tP + c, zero);
+        tmem_wait_st();
+    }
     Walk<1, KERNEL, kBytes> walk(p, bar);
     Unit w;
     bool more = walk.next(w);
@@ -1324,31 +1412,37 @@ __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Sh
         float m_ref = -INFINITY, m_row = -INFINITY, l = 0.f;
         bool s_ready = false;
         for (int j = 0; j < cnt; ++j) {
-            const uint32_t b = scnt & 1, tS = tmem + b * BN;
-            ok = s_ready || mbar_wait(&bar.s_full[b], (scnt >> 1) & 1, wc);
+            const uint32_t b = scnt & 1;
+            ok = s_ready || mbar_wait(&bar.s_full[0], scnt & 1, wc);
             ok = __all_sync(kFull, ok);
             if (!ok) break;
             tc_fence_after();
             uint32_t su[COLS];
-            tmem_ld32_at<0>(tS + col0, su);
+            tmem_ld32_at<0>(tmem + col0, su);
             if constexpr (!kCopies) {
-                tmem_ld32_at<32>(tS + 32, su);
-                tmem_ld32_at<64>(tS + 64, su);
-                tmem_ld32_at<96>(tS + 96, su);
+                tmem_ld32_at<32>(tmem + 32, su);
+                tmem_ld32_at<64>(tmem + 64, su);
+                tmem_ld32_at<96>(tmem + 96, su);
             }
-            const float4* f = reinterpret_cast<const float4*>(smem + E::kFactorOff) + factors * (BN / 4) + col0 / 4;
-            float4 f4[8];
+            const float4* f = reinterpret_cast<const float4*>(smem + E::kFactorOff + factors * E::kFactorBytes) + col0 / 4;
+            float4 f4[8], e4[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f4[i] = f[i];
+            for (int i = 0; i < 8; ++i) {
+                f4[i] = f[i];
+                if constexpr (SMALL) e4[i] = f[BN / 4 + i];
+            }
             tmem_wait_ld();
-            // the scores after this tile's may have come by now
-            s_ready = j + 1 < cnt && mbar_test(&bar.s_full[b ^ 1], ((scnt + 1) >> 1) & 1);
+            tc_fence_before();
+            mbar_arrive(&bar.s_free[0]);  // the scores are in registers
 #pragma unroll
             for (int i = 0; i < COLS / 4; ++i) {
                 const float4 x = i < 8 ? f4[i % 8] : f[i];
-                const float2 a = fmul2(make_float2(__uint_as_float(su[4 * i]), __uint_as_float(su[4 * i + 1])), make_float2(x.x, x.y));
-                const float2 c = fmul2(make_float2(__uint_as_float(su[4 * i + 2]), __uint_as_float(su[4 * i + 3])),
-                                       make_float2(x.z, x.w));
+                float2 a = fmul2(make_float2(__uint_as_float(su[4 * i]), __uint_as_float(su[4 * i + 1])), make_float2(x.x, x.y));
+                float2 c = fmul2(make_float2(__uint_as_float(su[4 * i + 2]), __uint_as_float(su[4 * i + 3])), make_float2(x.z, x.w));
+                if constexpr (SMALL) {  // s + e
+                    a = ffma2(a, make_float2(row_c, row_c), make_float2(e4[i].x, e4[i].y));
+                    c = ffma2(c, make_float2(row_c, row_c), make_float2(e4[i].z, e4[i].w));
+                }
                 su[4 * i] = __float_as_uint(a.x), su[4 * i + 1] = __float_as_uint(a.y);
                 su[4 * i + 2] = __float_as_uint(c.x), su[4 * i + 3] = __float_as_uint(c.y);
             }
@@ -1378,14 +1472,37 @@ __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Sh
             float m_tile = mx[0];
 #pragma unroll
             for (int c = 1; c < COLS / 16; ++c) m_tile = fmaxf(m_tile, mx[c]);
-            m_tile *= row_c;
+            if constexpr (!SMALL) m_tile *= row_c;
             m_row = fmaxf(m_row, m_tile);
             float m_new = m_ref;
             if (m_tile > m_ref + kRescaleThreshold) m_new = m_tile;
             const bool moved = m_new != m_ref;
             const float alpha = moved ? ex2(m_ref - m_new) : 1.f;  // 0 when m_ref = -inf
-            if (j > 0 && __any_sync(kFull, moved && m_ref != -INFINITY)) {
-                // the product of the tile before has written O (the one before that had when this tile's scores came)
+            const bool rescale = j > 0 && __any_sync(kFull, moved && m_ref != -INFINITY);
+            m_ref = m_new;
+            const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
+            const float2 cc2 = make_float2(row_c, row_c), nm2 = make_float2(neg_m, neg_m);
+            float2 suma = make_float2(0.f, 0.f), sumb = make_float2(0.f, 0.f);
+            // The product of the tile before the last has read this P: looked at beside other work.
+            const bool p_free = scnt < 2 || mbar_test(&bar.pv_done[b], ((scnt >> 1) & 1) ^ 1);
+#pragma unroll
+            for (int i = 0; i < COLS / 2; ++i) {
+                float2 x = make_float2(__uint_as_float(su[2 * i]), __uint_as_float(su[2 * i + 1]));
+                x = SMALL ? fadd2(x, nm2) : ffma2(x, cc2, nm2);
+                const float2 pp = make_float2(ex2(x.x), ex2(x.y));
+                float2& sum = i & 1 ? sumb : suma;
+                if constexpr (SMALL) {
+                    const float2 g = reinterpret_cast<const float2*>(f + BN / 2)[i];
+                    sum = ffma2(pp, g, sum);
+                } else {
+                    sum = fadd2(sum, pp);
+                }
+                su[i] = pack_h16<E::kWideF16>(pp.x, pp.y);
+            }
+            ok = p_free || mbar_wait(&bar.pv_done[b], ((scnt >> 1) & 1) ^ 1, wc);
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            if (rescale) {  // the tile before has written O
                 ok = mbar_wait(&bar.pv_done[b ^ 1], ((scnt - 1) >> 1) & 1, wc);
                 ok = __all_sync(kFull, ok);
                 if (!ok) break;
@@ -1400,46 +1517,29 @@ __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Sh
                     tmem_st32(tO + c0, ov);
                 }
             }
-            m_ref = m_new;
-            const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
-            const float2 cc2 = make_float2(row_c, row_c), nm2 = make_float2(neg_m, neg_m);
-            float2 suma = make_float2(0.f, 0.f), sumb = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int c0 = 0; c0 < COLS; c0 += 32) {
+            tc_fence_after();
+            if constexpr (kCopies) {
                 uint32_t pk[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float2 x =
-                        ffma2(make_float2(__uint_as_float(su[c0 + 2 * i]), __uint_as_float(su[c0 + 2 * i + 1])), cc2, nm2);
-                    const float2 pp = make_float2(ex2(x.x), ex2(x.y));
-                    if (i & 1)
-                        sumb = fadd2(sumb, pp);
-                    else
-                        suma = fadd2(suma, pp);
-                    pk[i] = pack_h16<F16>(pp.x, pp.y);
-                }
-                tmem_st16(tS + (col0 + c0) / 2, pk);
+                for (int i = 0; i < 16; ++i) pk[i] = su[i];
+                tmem_st16(tP + b * 64 + warp * 16, pk);
+            } else {
+                tmem_st32_at<0>(tP + b * 64, su);
+                tmem_st32_at<32>(tP + b * 64 + 32, su);
             }
-            if constexpr (kCopies) {  // the other copies' keys
-                uint32_t zero[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) zero[i] = 0;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k != warp) tmem_st16(tS + 16 * k, zero);
-            }
+            ++scnt;
+            s_ready = j + 1 < cnt && mbar_test(&bar.s_full[0], scnt & 1);
             l = l * alpha + ((suma.x + suma.y) + (sumb.x + sumb.y));
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&bar.p_full[b]);
-            ++scnt;
         }
         if (!ok) break;
         more = walk.next(w);  // while the last product runs
         if (more && w.cnt0 > 0) take_q();  // every product with this unit's has been waited for
         if (!ok) break;
         const bool first = u.w & 1, last = u.w & 2;
-        if (cnt > 0) {  // the last product, and so those before it
+        if (cnt > 0) {
             ok = mbar_wait(&bar.pv_done[(scnt - 1) & 1], ((scnt - 1) >> 1) & 1, wc);
             ok = __all_sync(kFull, ok);
             if (!ok) break;
@@ -1463,7 +1563,7 @@ __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Sh
         // The copy's state, as that of a part of a unit. Every warp is done with the unit before, or there would be no P
         // for the products above.
         if (cnt > 0 && lane < span)
-            states[warp * span + lane] = make_float4(l == 0.f ? -INFINITY : fmaxf(m_ref, -FLT_MAX), l, o_divisor<F16>(l, m_row, m_ref), 0.f);
+            states[warp * span + lane] = make_float4(l == 0.f ? -INFINITY : fmaxf(m_ref, -FLT_MAX), l, l, 0.f);
         const int rr = threadIdx.x % span, group = threadIdx.x / span, tok = rr / p.G;
         const bool held = rr < rows && tok < u.y && group * 8 < cols;
         const long long row = u.x + tok, head = u.z * p.G + rr % p.G;
@@ -1546,16 +1646,14 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             mbar_init(&bar.q_empty[i], slot ? 4 : 1);
         }
         if constexpr (VAR == kBytes) {
-            using E = Cfg8<D, F16, NT, KERNEL>;
-            constexpr uint32_t kConverters = E::Kernel::kConverters;
-            for (int s = 0; s < E::kKeys; ++s) {
+            using E = Cfg8<D, F16, NT, KERNEL, false>;
+            constexpr uint32_t kConverters = E::kMakers;
+            for (int s = 0; s < 8; ++s) {
                 mbar_init(&bar.k_full[s], 1);
-                mbar_init(&bar.k_ready[s], BN / 32);
+                mbar_init(&bar.k_ready[s], NT == 1 ? 1 : kConverters);
                 mbar_init(&bar.k_empty[s], C::kIssuers);
-            }
-            for (int s = 0; s < E::kValues; ++s) {
                 mbar_init(&bar.v_full[s], 1);
-                mbar_init(&bar.v_empty[s], kConverters);
+                mbar_init(&bar.v_empty[s], copies ? kConverters + 1 : kConverters);  // and the factors' warp
             }
             for (int s = 0; s < E::kWide; ++s) {
                 mbar_init(&bar.kv_full[s], kConverters);
@@ -1593,7 +1691,10 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
     if (warp >= C::kProducer) {
         if constexpr (C::Kernel::kRebalance) regs_decrease<C::Kernel::kOtherRegs>();
         if constexpr (VAR == kBytes) {
-            roles8<D, F16, NT, KERNEL>(tm_k, tm_v, p, smem, bar);
+            if (NT == 1 && copies)
+                roles8<D, F16, NT, KERNEL, NT == 1>(tm_k, tm_v, p, smem, bar);
+            else
+                roles8<D, F16, NT, KERNEL, false>(tm_k, tm_v, p, smem, bar);
         } else {
         Walk<NT, KERNEL, VAR> walk(p, bar);
         Unit w;
@@ -1903,12 +2004,19 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
         // ------------------------------------------------ softmax (thread = query row)
         const int t = NT == 2 ? warp >> 2 : 0;
         if constexpr (VAR == kBytes && NT == 1) {
-            if (warp < 4) {
-                if (copies)
-                    softmax_one<D, F16, KERNEL, 32>(p, smem, bar);
-                else if (warp < bar.sm_warps)
-                    softmax_one<D, F16, KERNEL, 128>(p, smem, bar);
-            }
+            auto go = [&](auto small) {
+                constexpr bool kSmall = decltype(small)::value;
+                if (warp < (kSmall ? 4 : bar.sm_warps))
+                    softmax_one<D, F16, KERNEL, kSmall>(p, smem, bar);
+                else if (KERNEL == kMixed && warp == 4)  // softmax warps of two-tile units
+                    make_factors<D, F16, KERNEL, kSmall>(p, smem, bar);
+                else if (KERNEL == kMixed && warp == 5)
+                    issue_values<D, F16, KERNEL, kSmall>(p, smem, bar);
+            };
+            if (copies)
+                go(std::true_type{});
+            else
+                go(std::false_type{});
         } else if (warp < 4 * NT && (warp & 3) < bar.sm_warps) {
             const int r = (warp & 3) * 32 + lane;
             const int rows = p.tok_tile * p.G;
@@ -1926,7 +2034,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
             int factors = 0;
             auto take_q = [&]() {
                 if constexpr (VAR == kBytes) {
-                    using E = Cfg8<D, F16, NT, KERNEL>;
+                    using E = Cfg8<D, F16, NT, KERNEL, false>;
                     const uint16_t* src = nullptr;
                     if (r < rows && my_tok < w.ntok) src = p.q + (w.row0 + my_tok) * p.q_sr + (w.h * p.G + my_head) * p.q_sh;
                     __syncwarp();
@@ -1961,7 +2069,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                     tmem_ld32_at<96>(tS + 96, su);
                     tmem_wait_ld();
                     if constexpr (VAR == kBytes) {
-                        using E = Cfg8<D, F16, NT, KERNEL>;
+                        using E = Cfg8<D, F16, NT, KERNEL, false>;
                         const float4* f = reinterpret_cast<const float4*>(smem + E::kFactorOff) + factors * (BN / 4);
 #pragma unroll
                         for (int i = 0; i < BN / 4; ++i) {
@@ -2084,7 +2192,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 }
                 if (!ok) break;
                 if constexpr (VAR == kBytes)
-                    factors = (factors + w.cnt_max - cnt) % Cfg8<D, F16, NT, KERNEL>::kFactors;  // of tiles that only the other saw
+                    factors = (factors + w.cnt_max - cnt) % Cfg8<D, F16, NT, KERNEL, false>::kFactors;  // of tiles that only the other saw
                 more = walk.next(w);  // while the last product runs
                 if (more && w.cnt(t) > 0) take_q();  // every product with this unit's has been waited for
                 if (cnt > 0) {
@@ -2107,8 +2215,9 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
     // Every copy issued must land before the CTA exits. The issuers have waited for each, unless a wait ran out.
     if (threadIdx.x == 0 && bar.abort_flag != 0) {
         if constexpr (VAR == kBytes) {
-            using E = Cfg8<D, F16, NT, KERNEL>;
-            drain_codes(bar, E::kKeys, E::kValues, p.timeout_ns);
+            using E = Cfg8<D, F16, NT, KERNEL, false>;
+            using S = Cfg8<D, F16, NT, KERNEL, NT == 1>;
+            drain_codes(bar, copies ? S::kKeys : E::kKeys, copies ? S::kValues : E::kValues, p.timeout_ns);
         } else {
             drain_ring(bar, C::kStages, p.timeout_ns);
         }
