@@ -104,36 +104,46 @@ def _check_cache(k_cache, v_cache, k_scale, v_scale) -> None:
 
 # ---------------------------------------------------------------- writes and reads
 def _pages_call(entry, k, v, slots, k_cache, v_cache, k_scale, v_scale, stream) -> None:
-    dtype = k.dtype
-    if not (dtype in _TYPES and k.dim() == 3 and k.stride()[2] == 1 and v.dtype is dtype and v.shape == k.shape and v.stride()[2] == 1
-            and _is_cache(k_cache, v_cache, k_scale, v_scale) and k_cache.shape[1] == k.shape[1] and k_cache.shape[3] == k.shape[2]
-            and slots.dtype is _INT32 and slots.shape == (k.shape[0],) and slots.is_contiguous()):
+    # shapes and strides are read once, for the checks and for the struct
+    dtype, shape, pages = k.dtype, k.shape, k_cache.shape
+    good = len(shape) == 3 and len(pages) == 4 and v.shape == shape and v_cache.shape == pages
+    if good:
+        rows, heads, d = shape
+        num_pages, _, page_size, _ = pages
+        kr, kh, ke = k.stride()
+        vr, vh, ve = v.stride()
+        kp, kch, ks, kce = k_cache.stride()
+        vp, vch, vs, vce = v_cache.stride()
+        good = (dtype in _TYPES and v.dtype is dtype and k_cache.dtype in _CODES and v_cache.dtype in _CODES
+                and k_scale.dtype in _SCALE_BYTES and v_scale.dtype in _SCALE_BYTES and slots.dtype is _INT32
+                and ke == 1 and ve == 1 and kce == 1 and vce == 1 and pages[1] == heads and pages[3] == d
+                and k_scale.shape == pages[:3] and v_scale.shape == pages[:3] and slots.shape == shape[:1] and slots.is_contiguous())
+        if good:
+            ksp, ksh, kse = k_scale.stride()
+            vsp, vsh, vse = v_scale.stride()
+            good = kse == 1 and vse == 1
+    if not good:
         _type_code("k", k)
         _need_dims("k", k, 3)
         _need_dims("k_cache", k_cache, 4)
-        (rows, heads, d), (pages, _, page_size, _) = k.shape, k_cache.shape
+        (rows, heads, d), (num_pages, _, page_size, _) = k.shape, k_cache.shape
         for name, t in (("k", k), ("v", v)):
             if not _is_rows(t, dtype, (rows, heads, d)):
                 _refuse(name, t, dtype, (rows, heads, d))
         for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-            _check_codes(name, t, (pages, heads, page_size, d))
+            _check_codes(name, t, (num_pages, heads, page_size, d))
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            _check_scale(name, t, (pages, heads, page_size))
+            _check_scale(name, t, (num_pages, heads, page_size))
         if not _is_ints(slots, (rows,)):
             _refuse("slots", slots, _INT32, (rows,))
+        # empty rows, or strides over an extent of 1, which the conditions above are too strict for
+        (kr, kh, _), (vr, vh, _), (kp, kch, ks, _), (vp, vch, vs, _) = k.stride(), v.stride(), k_cache.stride(), v_cache.stride()
+        (ksp, ksh, _), (vsp, vsh, _) = k_scale.stride(), v_scale.stride()
     dev = k.get_device()
     if not (dev >= 0 and v.get_device() == dev and slots.get_device() == dev and k_cache.get_device() == dev
             and v_cache.get_device() == dev and k_scale.get_device() == dev and v_scale.get_device() == dev):
         _refuse_devices(k, v, slots, k_cache, v_cache, k_scale, v_scale)
-    rows, heads, d = k.shape
-    pages, _, page_size, _ = k_cache.shape
-    kr, kh, _ = k.stride()
-    vr, vh, _ = v.stride()
-    kp, kch, ks, _ = k_cache.stride()
-    vp, vch, vs, _ = v_cache.stride()
-    ksp, ksh, _ = k_scale.stride()
-    vsp, vsh, _ = v_scale.stride()
-    packed = _PAGES_FP8.pack(rows, heads, d, pages, page_size, _TYPES[dtype], 0, 0, k.data_ptr(), v.data_ptr(), slots.data_ptr(),
+    packed = _PAGES_FP8.pack(rows, heads, d, num_pages, page_size, _TYPES[dtype], 0, 0, k.data_ptr(), v.data_ptr(), slots.data_ptr(),
                              k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), kr, kh, vr, vh, kp, kch, ks,
                              vp, vch, vs, ksp, ksh, vsp, vsh)
     guard = _guard(dev, stream)
@@ -158,9 +168,9 @@ def attn_pages_read_fp8(slots: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
                         v: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The keys and values of the given slots [rows] as 16-bit rows (k, v) [rows, Hkv, d], of the type of a given k
     or v, or `dtype`. Rows with a negative slot are left as they are (zeros in tensors allocated here)."""
-    _need_dims("k_cache", k_cache, 4)
-    _need_dims("slots", slots, 1)
     if k is None or v is None:
+        _need_dims("k_cache", k_cache, 4)
+        _need_dims("slots", slots, 1)
         like = k if k is not None else v
         dtype = dtype if like is None else like.dtype
         if dtype not in _TYPES:
@@ -195,40 +205,40 @@ def attn_tree_plan(parents: torch.Tensor, cu_q: torch.Tensor, kv_len: torch.Tens
     if not 1 <= max_nodes <= 1024 or int(max_nodes) != max_nodes:
         raise ValueError(f"max_nodes must be 1 to 1024, got {max_nodes}")
     words = (int(max_nodes) + 31) // 32
-    dev = parents.get_device()
-    if not (parents.dtype is _INT32 and parents.dim() == 1 and parents.is_contiguous()
-            and cu_q.dtype is _INT32 and cu_q.dim() == 1 and cu_q.is_contiguous()
-            and kv_len.dtype is _INT32 and kv_len.dim() == 1 and kv_len.is_contiguous() and cu_q.shape[0] == kv_len.shape[0] + 1
+    dev, shape, seqs = parents.get_device(), parents.shape, kv_len.shape
+    if not (parents.dtype is _INT32 and cu_q.dtype is _INT32 and kv_len.dtype is _INT32 and len(shape) == 1 and len(seqs) == 1
+            and cu_q.shape == (seqs[0] + 1,) and parents.is_contiguous() and cu_q.is_contiguous() and kv_len.is_contiguous()
             and dev >= 0 and cu_q.get_device() == dev and kv_len.get_device() == dev):
         _need_dims("parents", parents, 1)
         _need_dims("kv_len", kv_len, 1)
-        n = kv_len.shape[0]
-        for name, t, shape in (("parents", parents, parents.shape), ("cu_q", cu_q, (n + 1,)), ("kv_len", kv_len, (n,))):
-            if not _is_ints(t, shape):
-                _refuse(name, t, _INT32, shape)
-        _refuse_devices(parents, cu_q, kv_len)
-    rows = parents.shape[0]
+        n = seqs[0]
+        for name, t, want in (("parents", parents, shape), ("cu_q", cu_q, (n + 1,)), ("kv_len", kv_len, (n,))):
+            if not _is_ints(t, want):
+                _refuse(name, t, _INT32, want)
+        if dev < 0 or cu_q.get_device() != dev or kv_len.get_device() != dev:
+            _refuse_devices(parents, cu_q, kv_len)
     guard = _guard(dev, stream)
-    if guard is not None:
-        guard.__enter__()
-    try:
-        if mask is None:
-            mask = torch.empty((rows, words), dtype=_INT32, device=parents.device)
-        else:
-            if not _is_ints(mask, (rows, words)):
-                _refuse("mask", mask, _INT32, (rows, words))
-            if mask.get_device() != dev:
-                _refuse_devices(parents, mask)
-        if positions is None:
-            positions = torch.empty(rows, dtype=_INT32, device=parents.device)
-        else:
-            positions = _given("positions", positions, rows, parents)
-        _launch(lib.attn_tree_plan, dev, _TREE_PLAN.pack(
-            kv_len.shape[0], rows, words, 0, parents.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), mask.data_ptr(),
-            mask.stride()[0] if rows > 1 else words, positions.data_ptr()))
-    finally:
-        if guard is not None:
-            guard.__exit__(None, None, None)
+    if guard is None:
+        return _tree_call(dev, shape[0], seqs[0], words, parents, cu_q, kv_len, mask, positions)
+    with guard:
+        return _tree_call(dev, shape[0], seqs[0], words, parents, cu_q, kv_len, mask, positions)
+
+
+def _tree_call(dev, rows, seqs, words, parents, cu_q, kv_len, mask, positions):
+    stride = words
+    if mask is None:
+        mask = torch.empty((rows, words), dtype=_INT32, device=parents.device)
+    else:
+        if not _is_ints(mask, (rows, words)):
+            _refuse("mask", mask, _INT32, (rows, words))
+        if mask.get_device() != dev:
+            _refuse_devices(parents, mask)
+        if rows > 1:
+            stride = mask.stride()[0]
+    positions = (torch.empty(rows, dtype=_INT32, device=parents.device) if positions is None
+                 else _given("positions", positions, rows, parents))
+    _launch(lib.attn_tree_plan, dev, _TREE_PLAN.pack(seqs, rows, words, 0, parents.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(),
+                                                     mask.data_ptr(), stride, positions.data_ptr()))
     return mask, positions
 
 

@@ -59,10 +59,12 @@ def rotary_frequencies(rotary_dim: int, *, base: float = 10000.0, linear: float 
     return freq.to(device=device, dtype=torch.float32)
 
 
-def _call(entry, q, k, positions, inv_freq, interleaved, magnitude, q_out, k_out, stream):
-    if k is None and k_out is not None:
-        raise ValueError("k_out given without k")
-    dtype, dims, dev = q.dtype, q.dim(), q.get_device()
+_F32 = torch.float32
+
+
+def _check_call(q, k, positions, inv_freq, q_out, k_out) -> None:
+    """Says what is wrong with the tensors of a call, if anything is."""
+    dtype, dims = q.dtype, q.dim()
     if dtype not in _TYPES:
         raise TypeError(f"q must be bfloat16, float16 or float32, got {dtype}")
     if dims not in (3, 4):
@@ -79,41 +81,71 @@ def _call(entry, q, k, positions, inv_freq, interleaved, magnitude, q_out, k_out
     for name, t in (("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out)):
         if t is not None and t.stride()[-1] != 1 and t.numel() > 0:
             raise ValueError(f"{name} must be contiguous along its last dimension")
-    if dims == 4:
-        B, _, N, d = q.shape
-    else:
-        (N, _, d), B = q.shape, 1
     if positions.dtype is not _INT32:
         raise TypeError(f"positions must be {_INT32}, got {positions.dtype}")
-    if positions.shape == (N,):
-        pb, pn = 0, positions.stride()[0]
-    elif dims == 4 and positions.shape == (B, N):
-        pb, pn = positions.stride()
-    else:
-        raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {(N,)}" + (f" or {(B, N)}" if dims == 4 else ""))
-    if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        _refuse("inv_freq", inv_freq, torch.float32, (inv_freq.numel(),))
-    if dev < 0 or any(t is not None and t.get_device() != dev for t in (k, positions, inv_freq, q_out, k_out)):
+    n = q.shape[0] if dims == 3 else q.shape[2]
+    if positions.shape != (n,) and (dims == 3 or positions.shape != (q.shape[0], n)):
+        raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {(n,)}" +
+                         (f" or {(q.shape[0], n)}" if dims == 4 else ""))
+    if inv_freq.dtype is not _F32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        _refuse("inv_freq", inv_freq, _F32, (inv_freq.numel(),))
+
+
+def _strides(t, dims):
+    if t is None:
+        return 0, 0, 0
+    s = t.stride()
+    return s[:3] if dims == 4 else (0, s[1], s[0])
+
+
+def _call(entry, q, k, positions, inv_freq, interleaved, magnitude, q_out, k_out, stream):
+    if k is None and k_out is not None:
+        raise ValueError("k_out given without k")
+    # one condition over plain reads for a ragged batch's rows, as serving has them; what it does not hold for is looked at
+    dtype, shape, at, freq = q.dtype, q.shape, positions.shape, inv_freq.shape
+    good = len(shape) == 3 and k is not None and q_out is not None and k_out is not None and len(k.shape) == 3 and len(freq) == 1
+    if good:
+        N, heads, d = shape
+        kshape, sq, sk, so, sp = k.shape, q.stride(), k.stride(), q_out.stride(), k_out.stride()
+        good = (dtype in _TYPES and k.dtype is dtype and q_out.dtype is dtype and k_out.dtype is dtype and positions.dtype is _INT32
+                and inv_freq.dtype is _F32 and kshape[0] == N and kshape[2] == d and q_out.shape == shape and k_out.shape == kshape
+                and at == (N,) and sq[2] == 1 and sk[2] == 1 and so[2] == 1 and sp[2] == 1 and inv_freq.is_contiguous())
+    if not good:
+        _check_call(q, k, positions, inv_freq, q_out, k_out)
+    dev = q.get_device()
+    if not (dev >= 0 and positions.get_device() == dev and inv_freq.get_device() == dev and (k is None or k.get_device() == dev)
+            and (q_out is None or q_out.get_device() == dev) and (k_out is None or k_out.get_device() == dev)):
         _refuse_devices(q, positions, inv_freq, *(t for t in (k, q_out, k_out) if t is not None))
+    if good:
+        packed = _ROTARY.pack(1, N, heads, kshape[1], d, 2 * freq[0], _TYPES[dtype], 1 if interleaved else 0, magnitude, 0,
+                              positions.data_ptr(), 0, positions.stride()[0], inv_freq.data_ptr(), q.data_ptr(), k.data_ptr(),
+                              q_out.data_ptr(), k_out.data_ptr(), 0, sq[1], sq[0], 0, sk[1], sk[0], 0, so[1], so[0], 0, sp[1], sp[0])
+        guard = _guard(dev, stream)
+        if guard is None:
+            _launch(entry, dev, packed)
+        else:
+            with guard:
+                _launch(entry, dev, packed)
+        return q_out, k_out
+    dims = len(shape)
+    if dims == 4:
+        B, _, N, d = shape
+    else:
+        (N, _, d), B = shape, 1
+    pb, pn = positions.stride() if len(at) == 2 else (0, positions.stride()[0])
     guard = _guard(dev, stream)
     if guard is not None:
         guard.__enter__()
     try:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+            q_out = torch.empty(shape, dtype=dtype, device=q.device)
         if k_out is None and k is not None:
             k_out = torch.empty(k.shape, dtype=dtype, device=q.device)
-
-        def strides(t):
-            if t is None:
-                return 0, 0, 0
-            s = t.stride()
-            return (s[0], s[1], s[2]) if dims == 4 else (0, s[1], s[0])
-
         _launch(entry, dev, _ROTARY.pack(
-            B, N, q.shape[1], 0 if k is None else k.shape[1], d, 2 * inv_freq.shape[0], _TYPES[dtype], 1 if interleaved else 0,
+            B, N, shape[1], 0 if k is None else k.shape[1], d, 2 * freq[0], _TYPES[dtype], 1 if interleaved else 0,
             magnitude, 0, positions.data_ptr(), pb, pn, inv_freq.data_ptr(), q.data_ptr(), 0 if k is None else k.data_ptr(),
-            q_out.data_ptr(), 0 if k is None else k_out.data_ptr(), *strides(q), *strides(k), *strides(q_out), *strides(k_out)))
+            q_out.data_ptr(), 0 if k is None else k_out.data_ptr(), *_strides(q, dims), *_strides(k, dims), *_strides(q_out, dims),
+            *_strides(k_out, dims)))
     finally:
         if guard is not None:
             guard.__exit__(None, None, None)

@@ -6,8 +6,9 @@
 // even, so a code carries one rounding.
 //
 // What bounds it: a row is read and its codes written once (or the other way), so HBM; a decode step's few
-// rows take a launch's latency. A lane handles 16 values of a key row and the same ones of the value row:
-// two 16-byte loads and one 16-byte store of each, 8 lanes (4 at d = 64) a row.
+// rows take a launch's latency. A lane handles 16 values of a key row and the same ones of the value row, in one
+// access of 32 bytes and one of 16 each, 8 lanes (4 at d = 64) a row. Where a 16-bit row is not aligned to 32 bytes its
+// access is two of 16, which touch every sector twice.
 #include <cstdint>
 
 #include "internal.h"
@@ -24,8 +25,22 @@ constexpr int kLeast = -119, kMost = 119;  // exponents of the scales
 struct PagesF8Args {
     attn_pages_write_fp8_params p;
     int shift;  // log2(page_size)
+    int wide;   // rows of k and v are 32-byte aligned
     int* err;
 };
+
+// (row, head) of a thread. The division is by far the dearest instruction here, in 64 bits more so.
+template <int LANES>
+__device__ __forceinline__ void row_head(const PagesF8Args& a, long long& row, long long& h) {
+    const long long at = ((long long)blockIdx.x * (kThreads / LANES)) + threadIdx.x / LANES;
+    if (at < (1ll << 32)) {
+        row = (uint32_t)at / (uint32_t)a.p.num_kv_heads;
+        h = (uint32_t)at % (uint32_t)a.p.num_kv_heads;
+    } else {
+        row = at / a.p.num_kv_heads;
+        h = at % a.p.num_kv_heads;
+    }
+}
 
 // Slot of a row, or -1: a row to be skipped, or a slot that the cache does not have.
 __device__ __forceinline__ int slot_of(const PagesF8Args& a, long long row) {
@@ -49,9 +64,16 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)
 template <bool F16>
 struct Row16 {
     uint4 v[2];
-    __device__ __forceinline__ void load(const uint16_t* src) {
-        v[0] = *reinterpret_cast<const uint4*>(src);
-        v[1] = *reinterpret_cast<const uint4*>(src + 8);
+    __device__ __forceinline__ void load(const uint16_t* src, bool wide) {
+        if (wide) {
+            asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                         : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y), "=r"(v[1].z), "=r"(v[1].w)
+                         : "l"(src)
+                         : "memory");
+        } else {
+            v[0] = *reinterpret_cast<const uint4*>(src);
+            v[1] = *reinterpret_cast<const uint4*>(src + 8);
+        }
     }
     __device__ __forceinline__ void get(float (&x)[16]) const {
         const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
@@ -86,14 +108,14 @@ __global__ void __launch_bounds__(kThreads) pages_write_fp8_kernel(const PagesF8
     ptx::grid_dep_wait();
     constexpr int kLanes = D / 16;
     const attn_pages_write_fp8_params& p = a.p;
-    const long long at = ((long long)blockIdx.x * kThreads + threadIdx.x) / kLanes;  // (row, head)
-    const long long row = at / p.num_kv_heads, h = at % p.num_kv_heads;
+    long long row, h;
+    row_head<kLanes>(a, row, h);
     const int c = (threadIdx.x % kLanes) * 16;
     const int slot = row < p.rows ? slot_of(a, row) : -1;
     Row16<F16> k{}, v{};
     if (slot >= 0) {
-        k.load(static_cast<const uint16_t*>(p.k) + row * p.k_row_stride[0] + h * p.k_row_stride[1] + c);
-        v.load(static_cast<const uint16_t*>(p.v) + row * p.v_row_stride[0] + h * p.v_row_stride[1] + c);
+        k.load(static_cast<const uint16_t*>(p.k) + row * p.k_row_stride[0] + h * p.k_row_stride[1] + c, a.wide);
+        v.load(static_cast<const uint16_t*>(p.v) + row * p.v_row_stride[0] + h * p.v_row_stride[1] + c, a.wide);
     }
     float x[16];
     int ek, ev;
@@ -113,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) pages_write_fp8_kernel(const PagesF8
 
 // 16 codes times the scale of byte s, as 16-bit values.
 template <bool F16>
-__device__ __forceinline__ void restore(uint16_t* dst, uint4 codes, uint32_t s) {
+__device__ __forceinline__ void restore(uint16_t* dst, uint4 codes, uint32_t s, bool wide) {
     const float f = __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7fc00000u : s << 23);  // E8M0: 2^-127, NaN
     const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
     uint32_t out[8];
@@ -124,8 +146,14 @@ __device__ __forceinline__ void restore(uint16_t* dst, uint4 codes, uint32_t s) 
         const float2 x = ptx::unpack_h16<true>(h);
         out[i] = ptx::pack_h16<F16>(x.x * f, x.y * f);
     }
-    *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
-    *reinterpret_cast<uint4*>(dst + 8) = make_uint4(out[4], out[5], out[6], out[7]);
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(out[0]), "r"(out[1]), "r"(out[2]),
+                     "r"(out[3]), "r"(out[4]), "r"(out[5]), "r"(out[6]), "r"(out[7])
+                     : "memory");
+    } else {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+        *reinterpret_cast<uint4*>(dst + 8) = make_uint4(out[4], out[5], out[6], out[7]);
+    }
 }
 
 template <int D, bool F16>
@@ -134,8 +162,8 @@ __global__ void __launch_bounds__(kThreads) pages_read_fp8_kernel(const PagesF8A
     ptx::grid_dep_wait();
     constexpr int kLanes = D / 16;
     const attn_pages_write_fp8_params& p = a.p;
-    const long long at = ((long long)blockIdx.x * kThreads + threadIdx.x) / kLanes;  // (row, head)
-    const long long row = at / p.num_kv_heads, h = at % p.num_kv_heads;
+    long long row, h;
+    row_head<kLanes>(a, row, h);
     const int c = (threadIdx.x % kLanes) * 16;
     const int slot = row < p.rows ? slot_of(a, row) : -1;
     if (slot < 0) return;
@@ -149,8 +177,8 @@ __global__ void __launch_bounds__(kThreads) pages_read_fp8_kernel(const PagesF8A
     // the rows are this call's output
     uint16_t* k = static_cast<uint16_t*>(const_cast<void*>(p.k)) + row * p.k_row_stride[0] + h * p.k_row_stride[1] + c;
     uint16_t* v = static_cast<uint16_t*>(const_cast<void*>(p.v)) + row * p.v_row_stride[0] + h * p.v_row_stride[1] + c;
-    restore<F16>(k, kc, ks);
-    restore<F16>(v, vc, vs);
+    restore<F16>(k, kc, ks, a.wide);
+    restore<F16>(v, vc, vs, a.wide);
 }
 
 }  // namespace
@@ -160,6 +188,10 @@ cudaError_t launch_pages_fp8(const attn_pages_write_fp8_params& p, bool read, co
     a.p = p;
     while ((1 << a.shift) < p.page_size) ++a.shift;
     a.err = lc.err;
+    auto bits = [&](const void* base, const int64_t* st) {  // of the rows' addresses
+        return reinterpret_cast<uintptr_t>(base) | (uintptr_t)(p.rows > 1 ? st[0] * 2 : 0) | (uintptr_t)(p.num_kv_heads > 1 ? st[1] * 2 : 0);
+    };
+    a.wide = ((bits(p.k, p.k_row_stride) | bits(p.v, p.v_row_stride)) & 31) == 0;
     const long long threads = (long long)p.rows * p.num_kv_heads * (p.d / 16);
     const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads));
     const bool f16 = p.dtype == ATTN_F16;
