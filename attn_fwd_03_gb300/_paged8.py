@@ -235,8 +235,7 @@ def _tree_call(dev, rows, seqs, words, parents, cu_q, kv_len, mask, positions):
             _refuse_devices(parents, mask)
         if rows > 1:
             stride = mask.stride()[0]
-    positions = (torch.empty(rows, dtype=_INT32, device=parents.device) if positions is None
-                 else _given("positions", positions, rows, parents))
+    positions = torch.empty_like(parents) if positions is None else _given("positions", positions, rows, parents)
     _launch(lib.attn_tree_plan, dev, _TREE_PLAN.pack(seqs, rows, words, 0, parents.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(),
                                                      mask.data_ptr(), stride, positions.data_ptr()))
     return mask, positions
