@@ -102,6 +102,7 @@ constexpr int kUnitCost = 384;
 // A key tile of a two-tile unit against one of a one-tile unit: the mixed step takes 68.5 us (1.2: 72.3, 2.0:
 // 70.0), at d = 64 51.7 us (54.6, 57.0).
 constexpr float kPairCost = 1.5f;
+constexpr float kPairCostSmall = 2.7f, kPairCostCodes = 1.4f;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kIssueUnroll = 4;  // k-steps of a product in a row: 2 and 8 are within 2 %, 1 is 13 % slower
 
@@ -140,6 +141,9 @@ struct Shape {
     static constexpr int kLaunchRegs = kThreads * kPerSm == 384 ? 168 : 128;
     static constexpr int kSoftmaxRegs = KERNEL != kMixed ? (kF8 ? 240 : 184) : D == 64 || kF8 ? 192 : 200;
     static constexpr int kOtherRegs = KERNEL != kMixed ? (kF8 ? 88 : 72) : kF8 ? 64 : D == 64 ? 120 : 104;
+    // of kBytes, in a CTA on one-tile units: of four warps, where in kMixed the second tile's stay at the launch's
+    static constexpr int kOneTileRegs = 240;
+    static_assert(!kF8 || KERNEL != kMixed || 4 * kOneTileRegs + 4 * kLaunchRegs + 8 * kOtherRegs <= 16 * kLaunchRegs, "register split");
     static_assert(!kRebalance || 4 * kTiles * kSoftmaxRegs + (kThreads / 32 - 4 * kTiles) * kOtherRegs <= kThreads / 32 * kLaunchRegs,
                   "register split");
 };
@@ -393,9 +397,13 @@ __device__ __forceinline__ void locate(const PagedDev& p, Shared& sh) {
     int i = blockIdx.x, n = gridDim.x;
     bool pair = false;
     if (NT == 2) {
-        const float c0 = (float)done[0], c1 = (float)done[1] * kPairCost;
+        const float pair_cost = VAR != kBytes ? kPairCost : rows <= 32 ? kPairCostSmall : kPairCostCodes;
+        const float c0 = (float)done[0], c1 = (float)done[1] * pair_cost;
         int n0 = done[0] == 0 ? 0 : max(1, (int)(n * (c0 / (c0 + c1)) + 0.5f));
         if (done[1] > 0) n0 = min(n0, n - 1);
+        // an even number of kBytes' CTAs: two SMs side by side share a cache of instructions that the loops of one kind fill
+        // (a pair of both kinds took a quarter longer than the others)
+        if (VAR == kBytes && n0 > 1) n0 &= ~1;
         pair = i >= n0;
         i = pair ? i - n0 : i;
         n = pair ? n - n0 : n0;
@@ -1426,17 +1434,19 @@ __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Sh
             }
             const float4* f = reinterpret_cast<const float4*>(smem + E::kFactorOff + factors * E::kFactorBytes) + col0 / 4;
             float4 f4[8], e4[8];
+            if constexpr (SMALL) {  // beside the scores
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                f4[i] = f[i];
-                if constexpr (SMALL) e4[i] = f[BN / 4 + i];
+                for (int i = 0; i < 8; ++i) {
+                    f4[i] = f[i];
+                    e4[i] = f[BN / 4 + i];
+                }
             }
             tmem_wait_ld();
             tc_fence_before();
             mbar_arrive(&bar.s_free[0]);  // the scores are in registers
 #pragma unroll
             for (int i = 0; i < COLS / 4; ++i) {
-                const float4 x = i < 8 ? f4[i % 8] : f[i];
+                const float4 x = SMALL ? f4[i % 8] : f[i];
                 float2 a = fmul2(make_float2(__uint_as_float(su[4 * i]), __uint_as_float(su[4 * i + 1])), make_float2(x.x, x.y));
                 float2 c = fmul2(make_float2(__uint_as_float(su[4 * i + 2]), __uint_as_float(su[4 * i + 3])), make_float2(x.z, x.w));
                 if constexpr (SMALL) {  // s + e
@@ -2000,24 +2010,29 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
         }
         }
     } else {
-        if constexpr (C::Kernel::kRebalance) regs_increase<C::Kernel::kSoftmaxRegs>();
         // ------------------------------------------------ softmax (thread = query row)
         const int t = NT == 2 ? warp >> 2 : 0;
         if constexpr (VAR == kBytes && NT == 1) {
-            auto go = [&](auto small) {
-                constexpr bool kSmall = decltype(small)::value;
-                if (warp < (kSmall ? 4 : bar.sm_warps))
-                    softmax_one<D, F16, KERNEL, kSmall>(p, smem, bar);
-                else if (KERNEL == kMixed && warp == 4)  // softmax warps of two-tile units
-                    make_factors<D, F16, KERNEL, kSmall>(p, smem, bar);
-                else if (KERNEL == kMixed && warp == 5)
-                    issue_values<D, F16, KERNEL, kSmall>(p, smem, bar);
-            };
-            if (copies)
-                go(std::true_type{});
-            else
-                go(std::false_type{});
-        } else if (warp < 4 * NT && (warp & 3) < bar.sm_warps) {
+            if (warp < 4) {
+                regs_increase<C::Kernel::kOneTileRegs>();
+                if (copies)
+                    softmax_one<D, F16, KERNEL, true>(p, smem, bar);
+                else if (warp < bar.sm_warps)
+                    softmax_one<D, F16, KERNEL, false>(p, smem, bar);
+            } else if (KERNEL == kMixed && warp == 4) {  // softmax warps of two-tile units
+                if (copies)
+                    make_factors<D, F16, KERNEL, true>(p, smem, bar);
+                else
+                    make_factors<D, F16, KERNEL, false>(p, smem, bar);
+            } else if (KERNEL == kMixed && warp == 5) {
+                if (copies)
+                    issue_values<D, F16, KERNEL, true>(p, smem, bar);
+                else
+                    issue_values<D, F16, KERNEL, false>(p, smem, bar);
+            }
+        } else {
+        if constexpr (C::Kernel::kRebalance) regs_increase<C::Kernel::kSoftmaxRegs>();
+        if (warp < 4 * NT && (warp & 3) < bar.sm_warps) {
             const int r = (warp & 3) * 32 + lane;
             const int rows = p.tok_tile * p.G;
             const int my_tok = t * p.tok_tile + r / p.G, my_head = r % p.G;
@@ -2207,6 +2222,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 finish_row<D, F16, C::Kernel::kTiles>(p, u, t, r, my_tok, my_head, rows, cnt, tO, m_ref, m_row, l);
                 tc_fence_before();
             }
+        }
         }
     }
     tc_fence_before();
@@ -2486,8 +2502,10 @@ cudaError_t launch_tc(const CUtensorMap (&maps)[3], const PagedDev& p, int grid,
     const cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D, F16, KERNEL, VAR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                Kernel::kSmemBytes);
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_tc_kernel<D, F16, KERNEL, VAR>, dim3(grid), dim3(Kernel::kThreads), Kernel::kSmemBytes, s, maps[0],
-                      maps[1], maps[2], p);
+    // kMixed of kBytes starts when every SM is free, so that its CTAs come to lie in their order (locate): started early, one
+    // by one as SMs fall free, both kinds end up side by side (24 trees over an 8-bit cache 326 us, 181 in order).
+    return launch_chained(!(VAR == kBytes && KERNEL == kMixed), paged_tc_kernel<D, F16, KERNEL, VAR>, dim3(grid),
+                          dim3(Kernel::kThreads), Kernel::kSmemBytes, s, maps[0], maps[1], maps[2], p);
 }
 
 template <int D, bool F16, int VAR>

@@ -33,9 +33,10 @@ void note_launch(const void* kernel);
 // griddepcontrol.wait before its first global memory access, which returns once the previous
 // kernel has completed and its writes are visible; a kernel that follows a non-kernel
 // operation is serialised as usual.
+// `early` = false serialises it behind that kernel like any launch.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                       const Args&... args) {
+cudaError_t launch_chained(bool early, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                           const Args&... args) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -45,10 +46,15 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = early ? 1 : 0;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     if (e == cudaSuccess) note_launch(reinterpret_cast<const void*>(kernel));
     return e;
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                       const Args&... args) {
+    return launch_chained(true, kernel, grid, block, smem, s, args...);
 }
 
 // Tensor maps for the tcgen05 forward (built by the host API).
