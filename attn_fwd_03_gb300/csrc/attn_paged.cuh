@@ -102,6 +102,9 @@ constexpr int kUnitCost = 384;
 // A key tile of a two-tile unit against one of a one-tile unit: the mixed step takes 68.5 us (1.2: 72.3, 2.0:
 // 70.0), at d = 64 51.7 us (54.6, 57.0).
 constexpr float kPairCost = 1.5f;
+// The same for kBytes, where the batch's one-tile units are small (their values are not scaled) and where they are
+// not: a mixed step of 64 decoding sequences and a chunk takes 90 us with 2.7 (2.0: 100, 3.5: 91), 24 trees of 8 to 64
+// tokens 181 us with 1.4 (1.1: 189, 1.7: 186).
 constexpr float kPairCostSmall = 2.7f, kPairCostCodes = 1.4f;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kIssueUnroll = 4;  // k-steps of a product in a row: 2 and 8 are within 2 %, 1 is 13 % slower
@@ -129,7 +132,9 @@ struct Shape {
     static constexpr int kTiles = KERNEL == kMixed ? 2 : 1;  // of a unit, at most
     static constexpr int kPerSm = !kF8 && (KERNEL == kFew || (KERNEL == kOne && D == 64)) ? 2 : 1;
     static constexpr int kFirst = 4 * kTiles;  // the first warp behind the softmax warps
-    static constexpr int kConverters = !kF8 ? 0 : KERNEL == kMixed ? 4 : 8;  // warps
+    // warps of kBytes behind those: four converters, and in kOne the factors' and P V's (in kMixed those are softmax warps
+    // that a CTA on one-tile units has left) up to a whole warpgroup
+    static constexpr int kConverters = !kF8 ? 0 : KERNEL == kMixed ? 4 : 8;
     static constexpr int kThreads = (KERNEL == kMixed ? 384 : 256) + 32 * kConverters;
     // shared memory for Q, K and V tiles
     static constexpr int kTilesBytes = (KERNEL == kFew ? 104 : kPerSm == 2 ? 96 : 224) * 1024;
@@ -182,7 +187,7 @@ struct Cfg {
 // A CTA of the kBytes variant that works on units of NT tiles; SMALL: one-tile units of up to 32 rows.
 //
 // Keys go to the tensor cores as the codes they are, since a product of E4M3 codes is exact in fp32: Q is split
-// into kPieces 8-bit numbers whose sum it is (split_half2), and S is the sum of their products with the codes,
+// into kPieces 8-bit numbers whose sum it is (split_pair), and S is the sum of their products with the codes,
 // times the key's scale and the row's. Values are widened to 16 bits by converter warps, scales included; for small
 // units to fp16 without them, since the scale can go into P there (softmax_one). P in 8-bit pieces, which would
 // need no converters, is slower: the splitting comes on top of the softmax, which a tile then waits for.
@@ -653,20 +658,24 @@ __device__ __forceinline__ void codes16(uint4 v, uint32_t (&out)[8]) {
 // a code's sign are moved to where bf16 has exponent and fraction, which makes a number 2^120 too small
 // (subnormal codes become subnormal numbers, to the same factor), and the factor goes into the multiplication
 // by the scale; byte * 16 + sign * 240 moves the sign, too. Multiply-adds issue at 128 lanes a cycle, shifts and
-// logic at 64. Scales beyond 2^7 (not FAST) take a second multiplication.
+// logic at 64. Scales that the type does not hold as a factor (beyond 2^7 in bf16, below 2^-24 in fp16) take a
+// second multiplication (not FAST).
 template <bool F16, bool FAST>
 __device__ __forceinline__ void widen16(uint4 v, int s, uint32_t (&out)[8]) {
-    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
     if constexpr (F16) {
-        const float scale = __uint_as_float((uint32_t)s << 23);
+        const float scale = __uint_as_float((uint32_t)(FAST ? s : max(s, 113)) << 23);
         const uint32_t f = pack_f16(scale, scale);
+        codes16(v, out);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            uint32_t h;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(in[k / 2] >> (16 * (k & 1)))));
-            out[k] = mul2<true>(h, f);
+        for (int k = 0; k < 8; ++k) out[k] = mul2<true>(out[k], f);
+        if constexpr (!FAST) {
+            const float rest = __uint_as_float((uint32_t)(127 + min(s - 113, 0)) << 23);
+            const uint32_t more = pack_f16(rest, rest);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) out[k] = mul2<true>(out[k], more);
         }
     } else {
+        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
         const uint32_t f = (uint32_t)((FAST ? s : min(s, 134)) + 120) * 0x800080u;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -681,8 +690,8 @@ __device__ __forceinline__ void widen16(uint4 v, int s, uint32_t (&out)[8]) {
     }
 }
 
-// Makes the share of warp c of W of a 16-bit tile from a tile of codes (CODES: in fp16, without scales): rows of 128 bytes per 64 columns, 16-byte
-// chunks swizzled by the row as TMA does. Rows from `left` on become 0.
+// Makes the share of warp c of W of a 16-bit tile from a tile of codes (CODES: in fp16, without scales): rows of 128
+// bytes per 64 columns, 16-byte chunks swizzled by the row as TMA does. Rows from `left` on become 0.
 // A lane has 16 codes of a row at a time, and the same row of every 8 and the same columns in all of its turns,
 // so that its addresses differ by constants. Eight lanes that access memory together read and write all
 // banks: at d = 128 (codes swizzled like the tile) four lanes on the first columns of a row and four on those of
@@ -695,7 +704,8 @@ __device__ __forceinline__ void widen_tile(const uint8_t* raw, const uint8_t* sc
     const int r0 = D == 128 ? (lane >> 4) ^ (lane & 4 ? 5 : 0) : lane >> 2;
     // scales that take a second multiplication are looked for once a tile
     const uint32_t s4 = *reinterpret_cast<const uint32_t*>(scale + lane * 4);
-    const bool plain = (F16 || CODES || !__any_sync(kFull, __vcmpgtu4(s4, 0x86868686u) != 0)) && left >= BN;
+    const bool other = !CODES && (F16 ? __vcmpltu4(s4, 0x67676767u) : __vcmpgtu4(s4, 0x86868686u)) != 0;
+    const bool plain = !__any_sync(kFull, other) && left >= BN;
 #pragma unroll
     for (int turn = 0; turn < kTurns; ++turn) {
         const int row7 = r0 ^ (turn * 2), row = c * kRows + row7;  // and every 8th row behind it
@@ -897,6 +907,7 @@ __device__ __forceinline__ void make_factors(const PagedDev& p, uint8_t* smem, S
     uint32_t n = 0;
     bool ok = true;
     while (ok && walk.next(w)) {
+        uint32_t largest = 0;  // values' scale so far in the unit
         for (int j = 0; j < w.cnt_max && ok; ++j, ++n) {
             const uint32_t s = n % E::kKeys, sv = n % E::kValues;
             ok = mbar_wait_warp(&bar.k_full[s], (n / E::kKeys) & 1, wc);
@@ -906,12 +917,19 @@ __device__ __forceinline__ void make_factors(const PagedDev& p, uint8_t* smem, S
             const uint32_t b4 = *reinterpret_cast<const uint32_t*>(smem + E::kKeyScaleOff + s * BN + lane * 4);
             factors[lane] = make_uint4((b4 & 0xff) << 23, (b4 & 0xff00) << 15, (b4 & 0xff0000) << 7, b4 >> 1 & 0x7f800000);
             if constexpr (SMALL) {
-                // A value's scale below 2^-90 counts as that (its row's values are below 2^-81), so that no sum of weights
-                // overflows; bytes beyond the sequence may be anything, and these stay finite.
-                const uint32_t v4 = *reinterpret_cast<const uint32_t*>(smem + E::kValueScaleOff + sv * BN + lane * 4);
+                // A scale below 2^-90 counts as that (its values are below 2^-81), so that no sum of weights overflows,
+                // and one below 2^-80 of the largest so far as that, so that no weight that counts is lost: with m the
+                // maximum of s + e over keys b, e_b at most the largest E, y = 2^(s + e - m) >= 2^(s - s_b - 80) is 0 in
+                // fp32 only beside a key b of 2^46 times the weight. Bytes beyond the sequence may be anything.
+                uint32_t v4 = *reinterpret_cast<const uint32_t*>(smem + E::kValueScaleOff + sv * BN + lane * 4);
+                const int left = w.len - (w.k0 + j) * BN - lane * 4;
+                if (left < 4) v4 = left > 0 ? v4 & (1u << 8 * left) - 1 : 0;
+                const uint32_t m4 = __vmaxu4(v4, v4 >> 16);
+                largest = max(largest, __reduce_max_sync(kFull, max(m4 & 0xff, m4 >> 8 & 0xff)));
+                const uint32_t least = max(37, (int)largest - 80);
                 uint32_t v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = min(max(v4 >> (8 * i) & 0xff, 37u), 253u);
+                for (int i = 0; i < 4; ++i) v[i] = min(max(v4 >> (8 * i) & 0xff, least), 253u);
                 reinterpret_cast<float4*>(factors)[BN / 4 + lane] =
                     make_float4((float)v[0] - 127.f, (float)v[1] - 127.f, (float)v[2] - 127.f, (float)v[3] - 127.f);
                 factors[BN / 2 + lane] =
@@ -927,8 +945,8 @@ __device__ __forceinline__ void make_factors(const PagedDev& p, uint8_t* smem, S
     }
 }
 
-// The products P V of one-tile units, by a warp of its own: one that issues the scores' too would come to either late (64
-// sequences of 8192 keys 172 us). Nothing orders the two but their barriers: scores, P and O have columns of their own.
+// The products P V of one-tile units, by a warp of its own: one that issues the scores' too comes to either late.
+// Nothing orders the two but their barriers: scores, P and O have columns of their own.
 template <int D, bool F16, int KERNEL, bool SMALL>
 __device__ __forceinline__ void issue_values(const PagedDev& p, uint8_t* smem, Shared& bar) {
     using E = Cfg8<D, F16, 1, KERNEL, SMALL>;
@@ -1083,11 +1101,10 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
         // over, and none can pass while the wait stands.
         constexpr int W = E::kMakers;
         const int c = warp - kConvert;
-        if constexpr (NT == 1 && KERNEL == kOne)
-            {
-                if (c == W) make_factors<D, F16, KERNEL, SMALL>(p, smem, bar);
-                if (c == W + 1) issue_values<D, F16, KERNEL, SMALL>(p, smem, bar);
-            }
+        if constexpr (NT == 1 && KERNEL == kOne) {
+            if (c == W) make_factors<D, F16, KERNEL, SMALL>(p, smem, bar);
+            if (c == W + 1) issue_values<D, F16, KERNEL, SMALL>(p, smem, bar);
+        }
         uint32_t n = 0;
         bool ok = c < W;
         while (ok && walk.next(w)) {
@@ -1278,65 +1295,65 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
 template <int D, bool F16, int TILES>
 __device__ __forceinline__ void finish_row(const PagedDev& p, const int4& u, int t, int r, int my_tok, int my_head, int rows, int cnt,
                                            uint32_t tO, float m_ref, float m_row, float l) {
-                    const bool held = r < rows && my_tok < u.y, first = u.w & 1, last = u.w & 2;
-                    const float den = o_divisor<F16>(l, m_row, m_ref);
-                    if (first && last) {
-                        const float inv = den > 0.f ? 1.f / den : 0.f;
-                        // a row without keys is 0, though its products of 0 and a value may be NaN
-                        const uint32_t keep = l == 0.f ? 0u : ~0u;
-                        const long long row = u.x + my_tok, head = u.z * p.G + my_head;
-                        uint16_t* orow = reinterpret_cast<uint16_t*>(p.o) + row * p.o_sr + head * p.o_sh;
-    #pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 64) {
-                            uint32_t ov[64];
-                            if (cnt > 0) {
-                                tmem_ld32_at<0>(tO + c0, ov);
-                                tmem_ld32_at<32>(tO + c0 + 32, ov);
-                                tmem_wait_ld();
-                            } else {
-    #pragma unroll
-                                for (int i = 0; i < 64; ++i) ov[i] = 0;
-                            }
-    #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const float2 x = fmul2(make_float2(__uint_as_float(ov[2 * i]), __uint_as_float(ov[2 * i + 1])),
-                                                       make_float2(inv, inv));
-                                ov[i] = pack_h16<F16>(x.x, x.y) & keep;
-                            }
-                            if (held) {
-                                if (p.o_wide) {
-    #pragma unroll
-                                    for (int q = 0; q < 4; ++q) store32(orow + c0 + 16 * q, &ov[8 * q]);
-                                } else {
-    #pragma unroll
-                                    for (int q = 0; q < 8; ++q)
-                                        *reinterpret_cast<uint4*>(orow + c0 + 8 * q) =
-                                            make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
-                                }
-                            }
-                        }
-                        if (held) p.lse[head * p.T + row] = row_lse(m_ref, l);
-                    } else {
-                        // the part's state of this row; a row without keys in it is m = -inf, and its o is not read. NaN
-                        // scores leave m_ref at -inf and l NaN: such a row has keys, and its m is any other number.
-                        float4* rec = record(p.part, blockIdx.x * 2 + (first ? 1 : 0), TILES, t, rows, D);
-                        if (held) rec[r] = make_float4(l == 0.f ? -INFINITY : fmaxf(m_ref, -FLT_MAX), l, den, 0.f);
-                        if (cnt > 0) {
-    #pragma unroll 1
-                            for (int c0 = 0; c0 < D; c0 += 32) {
-                                uint32_t ov[32];
-                                tmem_ld32(tO + c0, ov);
-                                tmem_wait_ld();
-                                if (held) {
-                                    float4* dst = rec + (1 + c0 / 4) * rows + r;
-    #pragma unroll
-                                    for (int q = 0; q < 8; ++q)
-                                        dst[q * rows] = make_float4(__uint_as_float(ov[4 * q]), __uint_as_float(ov[4 * q + 1]),
-                                                                    __uint_as_float(ov[4 * q + 2]), __uint_as_float(ov[4 * q + 3]));
-                                }
-                            }
-                        }
-                    }
+    const bool held = r < rows && my_tok < u.y, first = u.w & 1, last = u.w & 2;
+    const float den = o_divisor<F16>(l, m_row, m_ref);
+    if (first && last) {
+        const float inv = den > 0.f ? 1.f / den : 0.f;
+        // a row without keys is 0, though its products of 0 and a value may be NaN
+        const uint32_t keep = l == 0.f ? 0u : ~0u;
+        const long long row = u.x + my_tok, head = u.z * p.G + my_head;
+        uint16_t* orow = reinterpret_cast<uint16_t*>(p.o) + row * p.o_sr + head * p.o_sh;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 64) {
+            uint32_t ov[64];
+            if (cnt > 0) {
+                tmem_ld32_at<0>(tO + c0, ov);
+                tmem_ld32_at<32>(tO + c0 + 32, ov);
+                tmem_wait_ld();
+            } else {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) ov[i] = 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float2 x = fmul2(make_float2(__uint_as_float(ov[2 * i]), __uint_as_float(ov[2 * i + 1])),
+                                       make_float2(inv, inv));
+                ov[i] = pack_h16<F16>(x.x, x.y) & keep;
+            }
+            if (held) {
+                if (p.o_wide) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) store32(orow + c0 + 16 * q, &ov[8 * q]);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        *reinterpret_cast<uint4*>(orow + c0 + 8 * q) =
+                            make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
+                }
+            }
+        }
+        if (held) p.lse[head * p.T + row] = row_lse(m_ref, l);
+    } else {
+        // the part's state of this row; a row without keys in it is m = -inf, and its o is not read. NaN
+        // scores leave m_ref at -inf and l NaN: such a row has keys, and its m is any other number.
+        float4* rec = record(p.part, blockIdx.x * 2 + (first ? 1 : 0), TILES, t, rows, D);
+        if (held) rec[r] = make_float4(l == 0.f ? -INFINITY : fmaxf(m_ref, -FLT_MAX), l, den, 0.f);
+        if (cnt > 0) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t ov[32];
+                tmem_ld32(tO + c0, ov);
+                tmem_wait_ld();
+                if (held) {
+                    float4* dst = rec + (1 + c0 / 4) * rows + r;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        dst[q * rows] = make_float4(__uint_as_float(ov[4 * q]), __uint_as_float(ov[4 * q + 1]),
+                                                    __uint_as_float(ov[4 * q + 2]), __uint_as_float(ov[4 * q + 3]));
+                }
+            }
+        }
+    }
 }
 
 // The softmax of units of one tile.
@@ -1487,7 +1504,10 @@ __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Sh
             float m_new = m_ref;
             if (m_tile > m_ref + kRescaleThreshold) m_new = m_tile;
             const bool moved = m_new != m_ref;
-            const float alpha = moved ? ex2(m_ref - m_new) : 1.f;  // 0 when m_ref = -inf
+            // 0 when m_ref = -inf. In small units m has the scales in it, and l, which has not, may take a factor below
+            // fp32's range: in two halves.
+            const float half = moved ? ex2((SMALL ? 0.5f : 1.f) * (m_ref - m_new)) : 1.f;
+            const float alpha = SMALL ? half * half : half;
             const bool rescale = j > 0 && __any_sync(kFull, moved && m_ref != -INFINITY);
             m_ref = m_new;
             const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
@@ -1539,7 +1559,7 @@ __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Sh
             }
             ++scnt;
             s_ready = j + 1 < cnt && mbar_test(&bar.s_full[0], scnt & 1);
-            l = l * alpha + ((suma.x + suma.y) + (sumb.x + sumb.y));
+            l = (SMALL ? l * half * half : l * alpha) + ((suma.x + suma.y) + (sumb.x + sumb.y));
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&bar.p_full[b]);
@@ -1570,8 +1590,16 @@ __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Sh
             ok = __all_sync(kFull, mbar_wait(&bar.merged, mcnt & 1, wc));
             ++mcnt;
         };
-        // The copy's state, as that of a part of a unit. Every warp is done with the unit before, or there would be no P
-        // for the products above.
+        // The copy's state, as that of a part of a unit, but that one with an l far from 1 (scales far from 1) takes l's
+        // exponent into m, so that states meet by their weights and not by their scales. Every warp is done with the unit
+        // before, or there would be no P for the products above.
+        const int l_exp = (int)(__float_as_uint(l) >> 23 & 0xff) - 126;
+        float to_unit = 1.f;
+        if (l != 0.f && abs(l_exp) > 40 && l_exp < 129) {  // not NaN
+            to_unit = pow2f(-l_exp);
+            m_ref += (float)l_exp;
+            l *= to_unit;
+        }
         if (cnt > 0 && lane < span)
             states[warp * span + lane] = make_float4(l == 0.f ? -INFINITY : fmaxf(m_ref, -FLT_MAX), l, l, 0.f);
         const int rr = threadIdx.x % span, group = threadIdx.x / span, tok = rr / p.G;
@@ -1592,8 +1620,9 @@ __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Sh
                         float4* dst = reinterpret_cast<float4*>(area + (warp * span + lane) * pitch + c1);
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
-                            dst[q] = make_float4(__uint_as_float(ov[4 * q]), __uint_as_float(ov[4 * q + 1]),
-                                                 __uint_as_float(ov[4 * q + 2]), __uint_as_float(ov[4 * q + 3]));
+                            dst[q] = make_float4(__uint_as_float(ov[4 * q]) * to_unit, __uint_as_float(ov[4 * q + 1]) * to_unit,
+                                                 __uint_as_float(ov[4 * q + 2]) * to_unit,
+                                                 __uint_as_float(ov[4 * q + 3]) * to_unit);
                     }
                 }
                 tc_fence_before();

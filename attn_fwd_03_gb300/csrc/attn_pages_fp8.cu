@@ -189,7 +189,8 @@ cudaError_t launch_pages_fp8(const attn_pages_write_fp8_params& p, bool read, co
     while ((1 << a.shift) < p.page_size) ++a.shift;
     a.err = lc.err;
     auto bits = [&](const void* base, const int64_t* st) {  // of the rows' addresses
-        return reinterpret_cast<uintptr_t>(base) | (uintptr_t)(p.rows > 1 ? st[0] * 2 : 0) | (uintptr_t)(p.num_kv_heads > 1 ? st[1] * 2 : 0);
+        return reinterpret_cast<uintptr_t>(base) | (uintptr_t)(p.rows > 1 ? st[0] * 2 : 0) |
+               (uintptr_t)(p.num_kv_heads > 1 ? st[1] * 2 : 0);
     };
     a.wide = ((bits(p.k, p.k_row_stride) | bits(p.v, p.v_row_stride)) & 31) == 0;
     const long long threads = (long long)p.rows * p.num_kv_heads * (p.d / 16);

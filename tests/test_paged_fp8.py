@@ -220,10 +220,10 @@ def test_max_q_is_only_a_hint(A, max_q):
 
 
 @pytest.mark.parametrize("dtype,mult", [(torch.bfloat16, 2.0 ** 40), (torch.bfloat16, 2.0 ** -60), (torch.float16, 300.0),
-                                        (torch.float16, 2.0 ** -9)])
+                                        (torch.float16, 2.0 ** -9), (torch.float16, 2.0 ** -17)])
 @pytest.mark.parametrize("n", [2, 70])
 def test_large_and_small_values(A, n, dtype, mult):
-    # scales beyond 2^7 take a second multiplication on chip; O is compared over the largest value
+    # scales beyond 2^7 in bf16 and below 2^-24 in fp16 take a second multiplication on chip; O is compared over its largest
     c = Case([n, 1], [300, 5], 2, 2, 64, 16, dtype, 51, mult=mult)
     o, lse = A.attn_paged_fp8(*c.args(), causal=True, max_q=n)
     _ok(A)
@@ -233,6 +233,29 @@ def test_large_and_small_values(A, n, dtype, mult):
     top = np.abs(O).max()
     assert np.all(np.abs(to64(o) - O) <= (4e-3 if dtype == torch.float16 else 2e-2) * top + tiny)
     assert_lse(lse, L)
+
+
+@pytest.mark.parametrize("n", [1, 6, 70])
+@pytest.mark.parametrize("kv", [70, 300, 5000])
+@pytest.mark.parametrize("order", [(-200, 0, 40), (40, -200, 0), (0, 100, -60)])
+def test_values_of_very_different_size(A, order, kv, n):
+    # a third of the keys each with values of 2^order, below 2^-128 zeros: a weight counts whatever its value
+    c = Case([n, 2], [kv, 40], 2, 2, 64, 16, torch.bfloat16, 55)
+    for b, length in enumerate(c.kv):
+        for j in range(length):
+            at, e = (c.table[b, j // 16], slice(None), j % 16), order[3 * j // length]
+            if e < -128:
+                c.codes[1][at], c.exps[1][at] = 0, 8
+            else:
+                c.exps[1][at] += np.uint8(e) if e >= 0 else np.uint8(256 + e)
+    c.values[1] = serving.restore(c.codes[1], np.where(c.exps[1] == 255, 127, c.exps[1]))
+    o, lse = A.attn_paged_fp8(*c.args(), causal=True)
+    _ok(A)
+    O, L = paged.paged_forward(to64(c.q), *c.values, c.table, c.cu, c.kv, 0.125, True)
+    assert_lse(lse, L)
+    # a weight and the output are each rounded by at most 2^-8 of themselves, the scores by less than 1e-3
+    size, _ = paged.paged_forward(to64(c.q), c.values[0], np.abs(c.values[1]), c.table, c.cu, c.kv, 0.125, True)
+    assert np.all(np.abs(to64(o) - O) <= (2.0 ** -7 + 1e-3) * size + 2.0 ** -70 * np.abs(c.values[1]).max())
 
 
 def test_large_queries_and_keys(A):
