@@ -8,7 +8,9 @@
 // What bounds it: a row is read and its codes written once (or the other way), so HBM; a decode step's few
 // rows take a launch's latency. A lane handles 16 values of a key row and the same ones of the value row, in one
 // access of 32 bytes and one of 16 each, 8 lanes (4 at d = 64) a row. Where a 16-bit row is not aligned to 32 bytes its
-// access is two of 16, which touch every sector twice.
+// access is two of 16, which touch every sector twice. 16301 rows of 8 heads with d = 128 are written in 13.8 us
+// (what is written stays in L2), 65021 read back in 60.6 us (6.6 TB/s, 97 % of the measured copy rate; 67.2 with
+// 16-byte accesses), a decode step's 64 rows written in 1.9 us.
 #include <cstdint>
 
 #include "internal.h"
