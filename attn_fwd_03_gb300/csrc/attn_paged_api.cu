@@ -144,11 +144,11 @@ attn_status_t check_tree(const attn_paged_tree_params* p, bool* empty, int es = 
 attn_status_t check_fp8(const attn_paged_fp8_params* p, bool* empty) {
     if (!p) return report_error(ATTN_ERR_INVALID, "params is NULL");
     attn_status_t st;
-    if (p->t.mask) {
+    if (p->t.mask || p->t.words != 0) {  // the mask of a batch without rows may be NULL
         if ((st = check_tree(&p->t, empty, 1)) != ATTN_OK) return st;
     } else {
-        if (p->t.words != 0 || p->t.mask_stride != 0 || p->t.reserved1 != 0)
-            return report_error(ATTN_ERR_INVALID, "words, mask_stride and reserved1 must be 0 without a mask");
+        if (p->t.mask_stride != 0 || p->t.reserved1 != 0)
+            return report_error(ATTN_ERR_INVALID, "mask_stride and reserved1 must be 0 without a mask");
         if ((st = check_paged(&p->t.f, empty, 1)) != ATTN_OK) return st;
     }
     if (*empty) return ATTN_OK;

@@ -377,3 +377,15 @@ def test_binding_refusals(A):
         A.attn_rotary(_t(3, 64), None, _t(3, dtype=I32), freq)
     with pytest.raises(TypeError, match="k and v must be"):
         A.attn_pages_read_fp8(_t(3, dtype=I32), *_cache(), dtype=torch.float32)
+
+
+# ---------------------------------------------------------------- batches without rows
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("size", [dict(total_q=0), dict(num_seqs=0)])
+@pytest.mark.parametrize("stride", [0, 2])
+def test_a_tree_call_without_rows_needs_no_mask(A, stride, size, f8):
+    p = _attend(A, True, f8, mask=0, mask_stride=stride, **size)
+    _run(A, "attn_paged_fp8" if f8 else "attn_paged_tree", p, "ATTN_OK")
+    if f8:
+        assert A.lib.attn_paged_fp8_workspace_size(ctypes.byref(p)) == 0
+    _run(A, "attn_paged_fp8" if f8 else "attn_paged_tree", _attend(A, True, f8, mask=0, mask_stride=stride), "ATTN_ERR_INVALID")
