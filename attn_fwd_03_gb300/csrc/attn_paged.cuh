@@ -188,9 +188,9 @@ struct Cfg {
 //
 // Keys go to the tensor cores as the codes they are, since a product of E4M3 codes is exact in fp32: Q is split
 // into kPieces 8-bit numbers whose sum it is (split_pair), and S is the sum of their products with the codes,
-// times the key's scale and the row's. Values are widened to 16 bits by converter warps, scales included; for small
-// units to fp16 without them, since the scale can go into P there (softmax_one). P in 8-bit pieces, which would
-// need no converters, is slower: the splitting comes on top of the softmax, which a tile then waits for.
+// times the key's scale and the row's. Values are widened to 16 bits by converter warps, scales included. P in 8-bit
+// pieces, which would need no converters, is slower: the splitting comes on top of the softmax, which a tile then waits
+// for.
 //
 // Widening keys and values, with Q as it is, takes 335 us for 64 sequences of 8192 keys: the converters' integer
 // instructions issue at 64 lanes a cycle.
@@ -199,7 +199,6 @@ struct Cfg8 {
     using Kernel = Shape<D, KERNEL, kBytes>;
     static constexpr int kTileBytes = BN * D;      // of codes
     static constexpr int kPieces = F16 ? 3 : 2;    // of 4, 4 and 3 bits of Q's 11 or 8
-    static constexpr bool kWideF16 = F16 || SMALL; // type of the widened values and of P
     // Tensor memory of units of one tile: scores from 0 on, Q's pieces (a product then reads keys alone from shared
     // memory), O, and P of two tiles in turn. Units of two tiles have no room for Q there.
     static constexpr bool kQTmem = NT == 1;
@@ -213,11 +212,10 @@ struct Cfg8 {
     static constexpr int kStateBytes = 4 * 32 * 16, kMergeBytes = 4 * 32 * 36 * 4;
     static constexpr int kExtraBytes = SMALL ? kQSlots * kQSlot + kStateBytes + kMergeBytes : 0;
     static constexpr int kRoom = Kernel::kTilesBytes - kKeyOff - kExtraBytes;
-    // Factors of a tile: the keys' scales, and for small units the exponents of the values' scales and the scales'
-    // inverses. Two stages more than keys have: a tile of keys arrives when the products with the one kKeys before
-    // it are done, and by then the softmax has read the factors of what came two before that (a thread reads a
-    // tile's factors before it takes the next one's scores).
-    static constexpr int kFactorBytes = (SMALL ? 3 : 1) * BN * 4;
+    // Factors of a tile: the keys' scales. Two stages more than keys have: a tile of keys arrives when the products
+    // with the one kKeys before it are done, and by then the softmax has read the factors of what came two before that
+    // (a thread reads a tile's factors before it takes the next one's scores).
+    static constexpr int kFactorBytes = BN * 4;
     static constexpr int kFit = (kRoom - 3 * kFactorBytes) / (kTileBytes + BN + kFactorBytes / 2);
     static constexpr int kBoth = kFit < 16 ? kFit : 16;
     static constexpr int kKeys = (kBoth + 1) / 2, kValues = kBoth / 2;  // stages
@@ -646,6 +644,14 @@ __device__ __forceinline__ uint32_t mad(uint32_t a, uint32_t b, uint32_t c) {
     return d;
 }
 
+// Two bytes of x as 16-bit numbers with their signs; the selector names each byte and, with 8 added, its sign.
+template <int SELECT>
+__device__ __forceinline__ uint32_t spread_signed(uint32_t x) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(d) : "r"(x), "n"(SELECT));
+    return d;
+}
+
 // 16 codes as fp16 numbers.
 __device__ __forceinline__ void codes16(uint4 v, uint32_t (&out)[8]) {
     const uint32_t in[4] = {v.x, v.y, v.z, v.w};
@@ -654,12 +660,13 @@ __device__ __forceinline__ void codes16(uint4 v, uint32_t (&out)[8]) {
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(out[k]) : "h"((uint16_t)(in[k / 2] >> (16 * (k & 1)))));
 }
 
-// 16 codes times the scale 2^(s - 127). fp16 has an instruction that widens codes. For bf16, the seven bits below
-// a code's sign are moved to where bf16 has exponent and fraction, which makes a number 2^120 too small
-// (subnormal codes become subnormal numbers, to the same factor), and the factor goes into the multiplication
-// by the scale; byte * 16 + sign * 240 moves the sign, too. Multiply-adds issue at 128 lanes a cycle, shifts and
-// logic at 64. Scales that the type does not hold as a factor (beyond 2^7 in bf16, below 2^-24 in fp16) take a
-// second multiplication (not FAST).
+// 16 codes times the scale 2^(s - 127). fp16 has an instruction that widens codes. For bf16, a byte is spread over 16
+// bits with its sign repeated in the upper ones (a byte permutation does that), moved to where bf16 has exponent and
+// fraction, and the sign's repetitions are cleared, which makes a number 2^120 too small (subnormal codes become
+// subnormal numbers, to the same factor); the factor goes into the multiplication by the scale. Decode of 64 sequences of
+// 8192 keys takes 162 us with these four instructions for two codes, 183 with five (sign and rest moved apart), 178 through
+// fp16 and fp32. Scales that the type does not hold as a factor (beyond 2^7 in bf16, below 2^-24 in fp16) take a second
+// multiplication (not FAST).
 template <bool F16, bool FAST>
 __device__ __forceinline__ void widen16(uint4 v, int s, uint32_t (&out)[8]) {
     if constexpr (F16) {
@@ -679,8 +686,8 @@ __device__ __forceinline__ void widen16(uint4 v, int s, uint32_t (&out)[8]) {
         const uint32_t f = (uint32_t)((FAST ? s : min(s, 134)) + 120) * 0x800080u;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const uint32_t b = __byte_perm(in[k / 2], 0, k & 1 ? 0x4342 : 0x4140);
-            out[k] = mul2<false>(mad(b & 0x00800080u, 240, mad(b, 16, 0)), f);
+            const uint32_t b = k & 1 ? spread_signed<0xb3a2>(in[k / 2]) : spread_signed<0x9180>(in[k / 2]);
+            out[k] = mul2<false>(mad(b, 16, 0) & 0x87f087f0u, f);
         }
         if constexpr (!FAST) {
             const uint32_t more = (uint32_t)(max(s - 134, 0) + 127) * 0x800080u;
@@ -690,13 +697,13 @@ __device__ __forceinline__ void widen16(uint4 v, int s, uint32_t (&out)[8]) {
     }
 }
 
-// Makes the share of warp c of W of a 16-bit tile from a tile of codes (CODES: in fp16, without scales): rows of 128
-// bytes per 64 columns, 16-byte chunks swizzled by the row as TMA does. Rows from `left` on become 0.
+// Makes the share of warp c of W of a 16-bit tile from a tile of codes: rows of 128 bytes per 64 columns, 16-byte
+// chunks swizzled by the row as TMA does. Rows from `left` on become 0.
 // A lane has 16 codes of a row at a time, and the same row of every 8 and the same columns in all of its turns,
 // so that its addresses differ by constants. Eight lanes that access memory together read and write all
 // banks: at d = 128 (codes swizzled like the tile) four lanes on the first columns of a row and four on those of
 // the row that differs in bits 0 and 2, at d = 64 four on each of two rows.
-template <int D, bool F16, int W, bool CODES>
+template <int D, bool F16, int W>
 __device__ __forceinline__ void widen_tile(const uint8_t* raw, const uint8_t* scale, uint8_t* tile, int left, int c, int lane) {
     constexpr int kTurns = D == 128 ? 2 : 1;  // for 8 rows
     constexpr int kRows = BN / W, kEach = kRows / 8;
@@ -704,7 +711,7 @@ __device__ __forceinline__ void widen_tile(const uint8_t* raw, const uint8_t* sc
     const int r0 = D == 128 ? (lane >> 4) ^ (lane & 4 ? 5 : 0) : lane >> 2;
     // scales that take a second multiplication are looked for once a tile
     const uint32_t s4 = *reinterpret_cast<const uint32_t*>(scale + lane * 4);
-    const bool other = !CODES && (F16 ? __vcmpltu4(s4, 0x67676767u) : __vcmpgtu4(s4, 0x86868686u)) != 0;
+    const bool other = (F16 ? __vcmpltu4(s4, 0x67676767u) : __vcmpgtu4(s4, 0x86868686u)) != 0;
     const bool plain = !__any_sync(kFull, other) && left >= BN;
 #pragma unroll
     for (int turn = 0; turn < kTurns; ++turn) {
@@ -718,15 +725,12 @@ __device__ __forceinline__ void widen_tile(const uint8_t* raw, const uint8_t* sc
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
                 v[i] = *reinterpret_cast<const uint4*>(from + i * 8 * D);
-                s[i] = CODES ? 0 : scale[row + i * 8];
+                s[i] = scale[row + i * 8];
             }
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
                 uint32_t out[8];
-                if constexpr (CODES)
-                    codes16(v[i], out);
-                else
-                    widen16<F16, true>(v[i], s[i], out);
+                widen16<F16, true>(v[i], s[i], out);
                 *reinterpret_cast<uint4*>(to + i * 1024 + a0) = make_uint4(out[0], out[1], out[2], out[3]);
                 *reinterpret_cast<uint4*>(to + i * 1024 + a1) = make_uint4(out[4], out[5], out[6], out[7]);
             }
@@ -735,10 +739,7 @@ __device__ __forceinline__ void widen_tile(const uint8_t* raw, const uint8_t* sc
             for (int i = 0; i < kEach; ++i) {
                 uint32_t out[8];
                 const uint4 v = *reinterpret_cast<const uint4*>(from + i * 8 * D);
-                if constexpr (CODES)
-                    codes16(v, out);
-                else
-                    widen16<F16, false>(v, scale[row + i * 8], out);
+                widen16<F16, false>(v, scale[row + i * 8], out);
                 if (row + i * 8 >= left) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) out[k] = 0;
@@ -907,39 +908,15 @@ __device__ __forceinline__ void make_factors(const PagedDev& p, uint8_t* smem, S
     uint32_t n = 0;
     bool ok = true;
     while (ok && walk.next(w)) {
-        uint32_t largest = 0;  // values' scale so far in the unit
         for (int j = 0; j < w.cnt_max && ok; ++j, ++n) {
-            const uint32_t s = n % E::kKeys, sv = n % E::kValues;
+            const uint32_t s = n % E::kKeys;
             ok = mbar_wait_warp(&bar.k_full[s], (n / E::kKeys) & 1, wc);
-            if (SMALL && ok) ok = mbar_wait_warp(&bar.v_full[sv], (n / E::kValues) & 1, wc);
             if (!ok) break;
             uint4* factors = reinterpret_cast<uint4*>(smem + E::kFactorOff + n % E::kFactors * E::kFactorBytes);
             const uint32_t b4 = *reinterpret_cast<const uint32_t*>(smem + E::kKeyScaleOff + s * BN + lane * 4);
             factors[lane] = make_uint4((b4 & 0xff) << 23, (b4 & 0xff00) << 15, (b4 & 0xff0000) << 7, b4 >> 1 & 0x7f800000);
-            if constexpr (SMALL) {
-                // A scale below 2^-90 counts as that (its values are below 2^-81), so that no sum of weights overflows,
-                // and one below 2^-80 of the largest so far as that, so that no weight that counts is lost: with m the
-                // maximum of s + e over keys b, e_b at most the largest E, y = 2^(s + e - m) >= 2^(s - s_b - 80) is 0 in
-                // fp32 only beside a key b of 2^46 times the weight. Bytes beyond the sequence may be anything.
-                uint32_t v4 = *reinterpret_cast<const uint32_t*>(smem + E::kValueScaleOff + sv * BN + lane * 4);
-                const int left = w.len - (w.k0 + j) * BN - lane * 4;
-                if (left < 4) v4 = left > 0 ? v4 & (1u << 8 * left) - 1 : 0;
-                const uint32_t m4 = __vmaxu4(v4, v4 >> 16);
-                largest = max(largest, __reduce_max_sync(kFull, max(m4 & 0xff, m4 >> 8 & 0xff)));
-                const uint32_t least = max(37, (int)largest - 80);
-                uint32_t v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = min(max(v4 >> (8 * i) & 0xff, least), 253u);
-                reinterpret_cast<float4*>(factors)[BN / 4 + lane] =
-                    make_float4((float)v[0] - 127.f, (float)v[1] - 127.f, (float)v[2] - 127.f, (float)v[3] - 127.f);
-                factors[BN / 2 + lane] =
-                    make_uint4((254u - v[0]) << 23, (254u - v[1]) << 23, (254u - v[2]) << 23, (254u - v[3]) << 23);
-            }
             __syncwarp();
-            if (elect_one()) {
-                mbar_arrive(&bar.k_ready[s]);
-                if (SMALL) mbar_arrive(&bar.v_empty[sv]);
-            }
+            if (elect_one()) mbar_arrive(&bar.k_ready[s]);
             __syncwarp();
         }
     }
@@ -950,7 +927,7 @@ __device__ __forceinline__ void make_factors(const PagedDev& p, uint8_t* smem, S
 template <int D, bool F16, int KERNEL, bool SMALL>
 __device__ __forceinline__ void issue_values(const PagedDev& p, uint8_t* smem, Shared& bar) {
     using E = Cfg8<D, F16, 1, KERNEL, SMALL>;
-    constexpr uint32_t kIdesc = idesc_h16(BM, D, false, true, E::kWideF16);
+    constexpr uint32_t kIdesc = idesc_h16(BM, D, false, true, F16);
     const WaitCtl wc{p.err, &bar.abort_flag, p.timeout_ns};
     const uint32_t tmem = __shfl_sync(kFull, bar.tmem_base, 0);
     Walk<1, KERNEL, kBytes> walk(p, bar);
@@ -1124,7 +1101,7 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
                 ok = ((ready & 2) || mbar_wait_warp(&bar.v_full[sv], pv, wc)) &&
                      ((ready & 4) || mbar_wait_warp(&bar.kv_empty[so], po, wc));
                 if (!ok) break;
-                widen_tile<D, F16, W, SMALL>(smem + E::kValueOff + sv * E::kTileBytes, smem + E::kValueScaleOff + sv * BN,
+                widen_tile<D, F16, W>(smem + E::kValueOff + sv * E::kTileBytes, smem + E::kValueScaleOff + sv * BN,
                                       smem + E::kWideOff + so * 2 * E::kTileBytes, w.len - (w.k0 + j) * BN, c, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -1362,10 +1339,6 @@ __device__ __forceinline__ void finish_row(const PagedDev& p, const int4& u, int
 // copy of Q's rows, so S too, and takes 32 of a tile's 128 keys. The copies' P are 0 at the other keys, so that their O
 // add up to the row's, each with a running maximum of its own; they are merged at the unit's end like the parts of a
 // unit that was cut (64 sequences of 8192 keys 240 us with a row in one thread, 187 with copies).
-//
-// Small units' values are codes v of scale 2^e: O = sum p 2^e v, so P is taken with the scale, y = 2^(s + e - m) with m a
-// reference maximum of s + e, and the sum of weights from y 2^-e. y is at most 2^8 and rounded to fp16, that is to 2^-25
-// where it is small.
 template <int D, bool F16, int KERNEL, bool SMALL>
 __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Shared& bar) {
     using C = Cfg<D, 1, KERNEL, kBytes>;
@@ -1450,13 +1423,10 @@ __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Sh
                 tmem_ld32_at<96>(tmem + 96, su);
             }
             const float4* f = reinterpret_cast<const float4*>(smem + E::kFactorOff + factors * E::kFactorBytes) + col0 / 4;
-            float4 f4[8], e4[8];
+            float4 f4[8];
             if constexpr (SMALL) {  // beside the scores
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    f4[i] = f[i];
-                    e4[i] = f[BN / 4 + i];
-                }
+                for (int i = 0; i < 8; ++i) f4[i] = f[i];
             }
             tmem_wait_ld();
             tc_fence_before();
@@ -1464,12 +1434,8 @@ __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Sh
 #pragma unroll
             for (int i = 0; i < COLS / 4; ++i) {
                 const float4 x = SMALL ? f4[i % 8] : f[i];
-                float2 a = fmul2(make_float2(__uint_as_float(su[4 * i]), __uint_as_float(su[4 * i + 1])), make_float2(x.x, x.y));
-                float2 c = fmul2(make_float2(__uint_as_float(su[4 * i + 2]), __uint_as_float(su[4 * i + 3])), make_float2(x.z, x.w));
-                if constexpr (SMALL) {  // s + e
-                    a = ffma2(a, make_float2(row_c, row_c), make_float2(e4[i].x, e4[i].y));
-                    c = ffma2(c, make_float2(row_c, row_c), make_float2(e4[i].z, e4[i].w));
-                }
+                const float2 a = fmul2(make_float2(__uint_as_float(su[4 * i]), __uint_as_float(su[4 * i + 1])), make_float2(x.x, x.y));
+                const float2 c = fmul2(make_float2(__uint_as_float(su[4 * i + 2]), __uint_as_float(su[4 * i + 3])), make_float2(x.z, x.w));
                 su[4 * i] = __float_as_uint(a.x), su[4 * i + 1] = __float_as_uint(a.y);
                 su[4 * i + 2] = __float_as_uint(c.x), su[4 * i + 3] = __float_as_uint(c.y);
             }
@@ -1499,15 +1465,12 @@ __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Sh
             float m_tile = mx[0];
 #pragma unroll
             for (int c = 1; c < COLS / 16; ++c) m_tile = fmaxf(m_tile, mx[c]);
-            if constexpr (!SMALL) m_tile *= row_c;
+            m_tile *= row_c;
             m_row = fmaxf(m_row, m_tile);
             float m_new = m_ref;
             if (m_tile > m_ref + kRescaleThreshold) m_new = m_tile;
             const bool moved = m_new != m_ref;
-            // 0 when m_ref = -inf. In small units m has the scales in it, and l, which has not, may take a factor below
-            // fp32's range: in two halves.
-            const float half = moved ? ex2((SMALL ? 0.5f : 1.f) * (m_ref - m_new)) : 1.f;
-            const float alpha = SMALL ? half * half : half;
+            const float alpha = moved ? ex2(m_ref - m_new) : 1.f;  // 0 when m_ref = -inf
             const bool rescale = j > 0 && __any_sync(kFull, moved && m_ref != -INFINITY);
             m_ref = m_new;
             const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
@@ -1517,17 +1480,11 @@ __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Sh
             const bool p_free = scnt < 2 || mbar_test(&bar.pv_done[b], ((scnt >> 1) & 1) ^ 1);
 #pragma unroll
             for (int i = 0; i < COLS / 2; ++i) {
-                float2 x = make_float2(__uint_as_float(su[2 * i]), __uint_as_float(su[2 * i + 1]));
-                x = SMALL ? fadd2(x, nm2) : ffma2(x, cc2, nm2);
+                const float2 x = ffma2(make_float2(__uint_as_float(su[2 * i]), __uint_as_float(su[2 * i + 1])), cc2, nm2);
                 const float2 pp = make_float2(ex2(x.x), ex2(x.y));
                 float2& sum = i & 1 ? sumb : suma;
-                if constexpr (SMALL) {
-                    const float2 g = reinterpret_cast<const float2*>(f + BN / 2)[i];
-                    sum = ffma2(pp, g, sum);
-                } else {
-                    sum = fadd2(sum, pp);
-                }
-                su[i] = pack_h16<E::kWideF16>(pp.x, pp.y);
+                sum = fadd2(sum, pp);
+                su[i] = pack_h16<F16>(pp.x, pp.y);
             }
             ok = p_free || mbar_wait(&bar.pv_done[b], ((scnt >> 1) & 1) ^ 1, wc);
             ok = __all_sync(kFull, ok);
@@ -1559,7 +1516,7 @@ __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Sh
             }
             ++scnt;
             s_ready = j + 1 < cnt && mbar_test(&bar.s_full[0], scnt & 1);
-            l = (SMALL ? l * half * half : l * alpha) + ((suma.x + suma.y) + (sumb.x + sumb.y));
+            l = l * alpha + ((suma.x + suma.y) + (sumb.x + sumb.y));
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&bar.p_full[b]);
@@ -1590,16 +1547,8 @@ __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Sh
             ok = __all_sync(kFull, mbar_wait(&bar.merged, mcnt & 1, wc));
             ++mcnt;
         };
-        // The copy's state, as that of a part of a unit, but that one with an l far from 1 (scales far from 1) takes l's
-        // exponent into m, so that states meet by their weights and not by their scales. Every warp is done with the unit
-        // before, or there would be no P for the products above.
-        const int l_exp = (int)(__float_as_uint(l) >> 23 & 0xff) - 126;
-        float to_unit = 1.f;
-        if (l != 0.f && abs(l_exp) > 40 && l_exp < 129) {  // not NaN
-            to_unit = pow2f(-l_exp);
-            m_ref += (float)l_exp;
-            l *= to_unit;
-        }
+        // The copy's state, as that of a part of a unit. Every warp is done with the unit before, or there would be no P for
+        // the products above.
         if (cnt > 0 && lane < span)
             states[warp * span + lane] = make_float4(l == 0.f ? -INFINITY : fmaxf(m_ref, -FLT_MAX), l, l, 0.f);
         const int rr = threadIdx.x % span, group = threadIdx.x / span, tok = rr / p.G;
@@ -1620,9 +1569,8 @@ __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Sh
                         float4* dst = reinterpret_cast<float4*>(area + (warp * span + lane) * pitch + c1);
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
-                            dst[q] = make_float4(__uint_as_float(ov[4 * q]) * to_unit, __uint_as_float(ov[4 * q + 1]) * to_unit,
-                                                 __uint_as_float(ov[4 * q + 2]) * to_unit,
-                                                 __uint_as_float(ov[4 * q + 3]) * to_unit);
+                            dst[q] = make_float4(__uint_as_float(ov[4 * q]), __uint_as_float(ov[4 * q + 1]),
+                                                 __uint_as_float(ov[4 * q + 2]), __uint_as_float(ov[4 * q + 3]));
                     }
                 }
                 tc_fence_before();
@@ -1692,7 +1640,7 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 mbar_init(&bar.k_ready[s], NT == 1 ? 1 : kConverters);
                 mbar_init(&bar.k_empty[s], C::kIssuers);
                 mbar_init(&bar.v_full[s], 1);
-                mbar_init(&bar.v_empty[s], copies ? kConverters + 1 : kConverters);  // and the factors' warp
+                mbar_init(&bar.v_empty[s], kConverters);
             }
             for (int s = 0; s < E::kWide; ++s) {
                 mbar_init(&bar.kv_full[s], kConverters);

@@ -514,13 +514,12 @@ ATTN_API attn_status_t attn_paged_tree(const attn_paged_tree_params *p, void *st
 
 /*
  * Attention over a paged cache in 8 bits, of a run of tokens (t.mask NULL; t.words, t.mask_stride
- * 0) or of trees (t.mask and t.words given; a batch without rows or sequences needs no mask). t.f as for attn_paged, with f.dtype the type of q and o, the
- * caches E4M3 codes and k_stride, v_stride in bytes. Keys and values are code * scale, with the
- * scales of attn_pages_write_fp8, 2^-119 to 2^119. Values are taken in f.dtype: exact in bf16; in fp16
- * they have to be within its range, and are rounded below 2^-14. The products, the softmax and
- * their accuracy are attn_paged's, but that values below 2^-81, or below 2^-71 of the largest of
- * the sequence and head, count with an error of up to that. Slots beyond a sequence's length may
- * hold any codes and scales.
+ * 0) or of trees (t.mask and t.words given; a batch without rows or sequences needs no mask). t.f as
+ * for attn_paged, with f.dtype the type of q and o, the caches E4M3 codes and k_stride, v_stride in
+ * bytes. Keys and values are code * scale, with the scales of attn_pages_write_fp8, 2^-119 to 2^119.
+ * Values are taken in f.dtype: exact in bf16; in fp16 they have to be within its range, and are
+ * rounded below 2^-14. The products, the softmax and their accuracy are attn_paged's. Slots beyond a
+ * sequence's length may hold any codes and scales.
  */
 typedef struct attn_paged_fp8_params {
     attn_paged_tree_params t;

@@ -53,3 +53,50 @@ def test_a_batch_without_rows(A, bits, seqs):
     assert o.shape == (0, 2, 64) and lse.shape == (2, 0)
 
 
+# ---------------------------------------------------------------- weights
+def _check_columns(c, o, lse, causal, scale):
+    """Every column by the sizes of what it sums: a weight and the output are each rounded by at most half a step, values in
+    fp16 by half of 2^-24 where they are below 2^-14 (and O, too), the scores by less than 1e-3."""
+    O, L = _forward(c, causal, scale)
+    size, _ = _forward(c, causal, scale, (c.values[0], np.abs(c.values[1])))
+    eps, tiny = torch.finfo(c.dtype).eps, 2.0 ** -24 if c.dtype == F16 else 0.0
+    assert_lse(lse, L)
+    assert np.all(np.abs(to64(o) - O) <= (eps + 1e-3) * size + tiny)
+
+
+@pytest.mark.parametrize("dtype,low", [(BF16, -30), (BF16, -100), (F16, -19)])
+@pytest.mark.parametrize("kv", [60, 300, 3000])
+@pytest.mark.parametrize("n", [1, 6, 40, 150])
+def test_columns_of_small_values_beside_rows_of_large_ones(A, n, kv, dtype, low):
+    # every other key has values 2^-low times larger, in the first half of the columns only; weights are much alike
+    c = Case([n, 2], [kv + n, 40], 2, 2, 64, 16, dtype, 90)
+    for b, length in enumerate(c.kv):
+        for j in range(length):
+            at = (c.table[b, j // 16], slice(None), j % 16)
+            if j % 2:
+                c.codes[1][at + (slice(32, None),)] = 0
+                c.exps[1][at] = 127 - (5 if dtype == F16 else 0)  # within fp16's range
+            else:
+                c.exps[1][at] = 127 - 5 + low if dtype == F16 else 127 + low
+    _restored(c)
+    o, lse = A.attn_paged_fp8(*c.args(), causal=True, scale=0.02, max_q=n)
+    _ok(A)
+    _check_columns(c, o, lse, True, 0.02)
+
+
+@pytest.mark.parametrize("n", [1, 7, 40, 150])
+@pytest.mark.parametrize("kv", [300, 5000])
+def test_light_keys_beside_a_heavy_one(A, n, kv):
+    # one key of weight 1, zero in half of the columns, among keys of weight 2^-26: a bf16 weight like any other
+    c = Case([n], [kv], 1, 2, 64, 16, BF16, 91)
+    c.q[:] = 0
+    c.q[:, :, 0] = 16.0
+    for j in range(kv):
+        _set(c, 0, 0, j, np.eye(1, 64) * (9.0 if j == 70 else 0.0), 0)
+        _set(c, 1, 0, j, np.where(np.arange(64) < 32, 1.0, 0.0 if j == 70 else 1.0 + (j % 8) / 8)[None], 0)
+    _restored(c)
+    o, lse = A.attn_paged_fp8(*c.args(), max_q=n)
+    _ok(A)
+    _check_columns(c, o, lse, False, 0.125)
+
+
