@@ -1550,7 +1550,8 @@ __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Sh
         // The copy's state, as that of a part of a unit. Every warp is done with the unit before, or there would be no P for
         // the products above.
         if (cnt > 0 && lane < span)
-            states[warp * span + lane] = make_float4(l == 0.f ? -INFINITY : fmaxf(m_ref, -FLT_MAX), l, l, 0.f);
+            states[warp * span + lane] =
+                make_float4(l == 0.f ? -INFINITY : fmaxf(m_ref, -FLT_MAX), l, o_divisor<F16>(l, m_row, m_ref), 0.f);
         const int rr = threadIdx.x % span, group = threadIdx.x / span, tok = rr / p.G;
         const bool held = rr < rows && tok < u.y && group * 8 < cols;
         const long long row = u.x + tok, head = u.z * p.G + rr % p.G;

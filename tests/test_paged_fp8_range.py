@@ -100,3 +100,24 @@ def test_light_keys_beside_a_heavy_one(A, n, kv):
     _check_columns(c, o, lse, False, 0.125)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("group", [16, 40])
+def test_the_largest_weight_is_divided_by_what_it_was_rounded_to(A, group, dtype):
+    # Scores whose maximum lags behind: key 9 sets it, key 137 is 2^3 to 2^7.9 times heavier, the others have no weight. With
+    # w = 2^x that of key 137 and 1 that of key 9, both of the same values v, O = v whatever w is rounded to. 100 sequences over the
+    # same pages, so that most are not cut between two tiles.
+    c = Case([1], [256], 8, group, 64, 16, dtype, 92)
+    for j in range(256):
+        _set(c, 0, 0, j, np.eye(1, 64) * {9: 0.0, 137: 1.0}.get(j, 0.0) - np.eye(1, 64, 1) * (0.0 if j in (9, 137) else 448.0), 0)
+        _set(c, 1, 0, j, np.full((1, 64), 1.875), 0)
+    x = torch.linspace(3.0, 7.9, group)
+    c.q = torch.zeros(100, 8, group, 64, dtype=dtype)
+    c.q[..., 0], c.q[..., 1] = x, 1.0
+    c.q = c.q.view(100, 8 * group, 64)
+    c.table, c.kv, c.cu = np.repeat(c.table, 100, 0), [256] * 100, np.arange(101)
+    _restored(c)
+    o, _ = A.attn_paged_fp8(*c.args(), scale=math.log(2.0), max_q=1)
+    _ok(A)
+    assert torch.all(o == 1.875)
+
+
