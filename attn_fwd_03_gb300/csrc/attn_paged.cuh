@@ -629,26 +629,18 @@ __device__ __forceinline__ void tree_bits(const PagedDev& p, const uint32_t* row
 }
 
 // ---------------------------------------------------------------- 8-bit caches
-template <bool F16>
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     uint32_t d;
-    if constexpr (F16)
-        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    else
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-__device__ __forceinline__ uint32_t mad(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t d;
-    asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
 
-// Two bytes of x as 16-bit numbers with their signs; the selector names each byte and, with 8 added, its sign.
-template <int SELECT>
-__device__ __forceinline__ uint32_t spread_signed(uint32_t x) {
-    uint32_t d;
-    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(d) : "r"(x), "n"(SELECT));
+// The two fp16 numbers of x times that in the lower half of y, in fp32.
+__device__ __forceinline__ float2 widen2(uint32_t x, uint32_t y) {
+    float2 d;
+    asm("{\n\t.reg .b16 lo, hi, f, g;\n\tmov.b32 {lo, hi}, %2;\n\tmov.b32 {f, g}, %3;\n\t"
+        "fma.rn.f32.f16 %0, lo, f, 0f00000000;\n\tfma.rn.f32.f16 %1, hi, f, 0f00000000;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "r"(x), "r"(y));
     return d;
 }
 
@@ -660,39 +652,43 @@ __device__ __forceinline__ void codes16(uint4 v, uint32_t (&out)[8]) {
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(out[k]) : "h"((uint16_t)(in[k / 2] >> (16 * (k & 1)))));
 }
 
-// 16 codes times the scale 2^(s - 127). fp16 has an instruction that widens codes. For bf16, a byte is spread over 16
-// bits with its sign repeated in the upper ones (a byte permutation does that), moved to where bf16 has exponent and
-// fraction, and the sign's repetitions are cleared, which makes a number 2^120 too small (subnormal codes become
-// subnormal numbers, to the same factor); the factor goes into the multiplication by the scale. Decode of 64 sequences of
-// 8192 keys takes 162 us with these four instructions for two codes, 183 with five (sign and rest moved apart), 178 through
-// fp16 and fp32. Scales that the type does not hold as a factor (beyond 2^7 in bf16, below 2^-24 in fp16) take a second
-// multiplication (not FAST).
-template <bool F16, bool FAST>
+// 16 codes times the scale 2^(s - 127), which fp16 has to hold (2^-24 to 2^15): the codes as fp16 numbers, times the
+// scale in fp16, or for bf16 in fp32, exact, by multiply-adds of fp16 numbers into fp32. NaN stays NaN on the way.
+// Moving a code's bits to where bf16 has them takes as many instructions (a byte permutation that repeats the sign, a
+// move, a mask, a multiplication), but turns NaN into 480: decode of 64 sequences of 8192 keys takes 165 us, 162 in
+// that way, 186 with a look for NaN codes on top; 178 with conversions to fp32 and the multiplication apart.
+template <bool F16>
 __device__ __forceinline__ void widen16(uint4 v, int s, uint32_t (&out)[8]) {
-    if constexpr (F16) {
-        const float scale = __uint_as_float((uint32_t)(FAST ? s : max(s, 113)) << 23);
-        const uint32_t f = pack_f16(scale, scale);
-        codes16(v, out);
+    const float scale = __uint_as_float((uint32_t)s << 23);
+    const uint32_t f = pack_f16(scale, scale);
+    codes16(v, out);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) out[k] = mul2<true>(out[k], f);
-        if constexpr (!FAST) {
-            const float rest = __uint_as_float((uint32_t)(127 + min(s - 113, 0)) << 23);
-            const uint32_t more = pack_f16(rest, rest);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) out[k] = mul2<true>(out[k], more);
+    for (int k = 0; k < 8; ++k) {
+        if constexpr (F16) {
+            out[k] = mul2(out[k], f);
+        } else {
+            const float2 x = widen2(out[k], f);
+            out[k] = pack_bf16(x.x, x.y);
         }
+    }
+}
+
+// The same for any scale (in bf16, bytes 0 and 255 are 2^-127 and NaN; in fp16, up to 2^15): in two multiplications where
+// fp16 has to hold the factors.
+template <bool F16>
+__device__ __forceinline__ void widen16_any(uint4 v, int s, uint32_t (&out)[8]) {
+    codes16(v, out);
+    if constexpr (F16) {
+        const float scale = __uint_as_float((uint32_t)max(s, 113) << 23), rest = __uint_as_float((uint32_t)(127 + min(s - 113, 0)) << 23);
+        const uint32_t f = pack_f16(scale, scale), more = pack_f16(rest, rest);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) out[k] = mul2(mul2(out[k], f), more);
     } else {
-        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-        const uint32_t f = (uint32_t)((FAST ? s : min(s, 134)) + 120) * 0x800080u;
+        const float scale = __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7fc00000u : (uint32_t)s << 23);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const uint32_t b = k & 1 ? spread_signed<0xb3a2>(in[k / 2]) : spread_signed<0x9180>(in[k / 2]);
-            out[k] = mul2<false>(mad(b, 16, 0) & 0x87f087f0u, f);
-        }
-        if constexpr (!FAST) {
-            const uint32_t more = (uint32_t)(max(s - 134, 0) + 127) * 0x800080u;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) out[k] = mul2<false>(out[k], more);
+            const float2 x = unpack_h16<true>(out[k]);
+            out[k] = pack_bf16(x.x * scale, x.y * scale);
         }
     }
 }
@@ -709,9 +705,9 @@ __device__ __forceinline__ void widen_tile(const uint8_t* raw, const uint8_t* sc
     constexpr int kRows = BN / W, kEach = kRows / 8;
     const int ch = D == 128 ? (lane & 3) | (lane & 8) >> 1 : lane & 3;
     const int r0 = D == 128 ? (lane >> 4) ^ (lane & 4 ? 5 : 0) : lane >> 2;
-    // scales that take a second multiplication are looked for once a tile
+    // scales that widen16 does not take are looked for once a tile
     const uint32_t s4 = *reinterpret_cast<const uint32_t*>(scale + lane * 4);
-    const bool other = (F16 ? __vcmpltu4(s4, 0x67676767u) : __vcmpgtu4(s4, 0x86868686u)) != 0;
+    const bool other = (__vcmpltu4(s4, 0x67676767u) | (F16 ? 0 : __vcmpgtu4(s4, 0x8e8e8e8eu))) != 0;
     const bool plain = !__any_sync(kFull, other) && left >= BN;
 #pragma unroll
     for (int turn = 0; turn < kTurns; ++turn) {
@@ -730,7 +726,7 @@ __device__ __forceinline__ void widen_tile(const uint8_t* raw, const uint8_t* sc
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
                 uint32_t out[8];
-                widen16<F16, true>(v[i], s[i], out);
+                widen16<F16>(v[i], s[i], out);
                 *reinterpret_cast<uint4*>(to + i * 1024 + a0) = make_uint4(out[0], out[1], out[2], out[3]);
                 *reinterpret_cast<uint4*>(to + i * 1024 + a1) = make_uint4(out[4], out[5], out[6], out[7]);
             }
@@ -739,7 +735,7 @@ __device__ __forceinline__ void widen_tile(const uint8_t* raw, const uint8_t* sc
             for (int i = 0; i < kEach; ++i) {
                 uint32_t out[8];
                 const uint4 v = *reinterpret_cast<const uint4*>(from + i * 8 * D);
-                widen16<F16, false>(v, scale[row + i * 8], out);
+                widen16_any<F16>(v, scale[row + i * 8], out);
                 if (row + i * 8 >= left) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) out[k] = 0;

@@ -121,3 +121,18 @@ def test_the_largest_weight_is_divided_by_what_it_was_rounded_to(A, group, dtype
     assert torch.all(o == 1.875)
 
 
+# ---------------------------------------------------------------- NaN and infinities
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("n", [1, 6, 50, 200])
+@pytest.mark.parametrize("code", [127, 255])
+def test_nan_among_the_values_shows(A, n, code, dtype):
+    c = Case([n, n], [200 + n, 130 + n], 1, 2, 64, 16, dtype, 93)
+    c.codes[1][c.table[0, 3], 0, 2, 5] = code  # a value of sequence 0 that every row sees
+    o, lse = A.attn_paged_fp8(*c.args(), causal=True, max_q=n)
+    _ok(A)
+    assert torch.isnan(o[:n, :, 5]).all() and torch.isfinite(o[:n, :, :5]).all() and torch.isfinite(o[:n, :, 6:]).all()
+    assert torch.isfinite(o[n:]).all() and torch.isfinite(lse).all()
+    k, _ = A.attn_pages_read_fp8(_i32([int(c.table[0, 3]) * 16 + 2]), *reversed(c.cache()[:2]), *reversed(c.cache()[2:]), dtype=dtype)
+    assert torch.isnan(k[0, 0, 5])
+
+
