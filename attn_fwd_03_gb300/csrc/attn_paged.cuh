@@ -772,6 +772,9 @@ __device__ __forceinline__ int row_exponent(float top) {
     return min(max((int)(bits >> 23) - 135 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0), -119), 119);
 }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// What a row whose largest magnitude is `top` is multiplied by before it is split, with e = row_exponent(top). The 8-bit
+// formats saturate: a row with an infinity becomes NaN instead, so that it shows in O and LSE.
+__device__ __forceinline__ float split_factor(float top, int e) { return top < INFINITY ? pow2f(-e) : NAN; }
 
 // The largest magnitude of 16-bit values, two at a time.
 template <bool F16>
@@ -798,8 +801,9 @@ __device__ __forceinline__ float split_row(const uint16_t* src, uint32_t tmem, u
 #pragma unroll
     for (int i = 0; i < D / 2; ++i) take_max<F16>(top, x[i]);
     const float2 t2 = unpack_h16<F16>(top);
-    const int e = row_exponent(fmaxf(t2.x, t2.y));
-    const float f = pow2f(-e);
+    const float largest = fmaxf(t2.x, t2.y);
+    const int e = row_exponent(largest);
+    const float f = split_factor(largest, e);
 #pragma unroll
     for (int c0 = 0; c0 < D / 4; c0 += 16) {  // 64 columns at a time
         uint32_t out[kPieces][16];
@@ -860,8 +864,9 @@ __device__ __forceinline__ void split_unit(const PagedDev& p, const Unit& w, uin
 #pragma unroll
             for (int o = 1; o < kLanes; o <<= 1) take_max<F16>(top, __shfl_xor_sync(kFull, top, o));
             const float2 t2 = unpack_h16<F16>(top);
-            const int e = row_exponent(fmaxf(t2.x, t2.y));
-            const float f = pow2f(-e);
+            const float largest = fmaxf(t2.x, t2.y);
+            const int e = row_exponent(largest);
+            const float f = split_factor(largest, e);
             uint16_t a[2], b[2], c[2] = {0, 0};
             split_pair<F16>(x[i].x, f, a[0], b[0], c[0]);
             split_pair<F16>(x[i].y, f, a[1], b[1], c[1]);

@@ -518,8 +518,9 @@ ATTN_API attn_status_t attn_paged_tree(const attn_paged_tree_params *p, void *st
  * for attn_paged, with f.dtype the type of q and o, the caches E4M3 codes and k_stride, v_stride in
  * bytes. Keys and values are code * scale, with the scales of attn_pages_write_fp8, 2^-119 to 2^119.
  * Values are taken in f.dtype: exact in bf16; in fp16 they have to be within its range, and are
- * rounded below 2^-14. The products, the softmax and their accuracy are attn_paged's. Slots beyond a
- * sequence's length may hold any codes and scales.
+ * rounded below 2^-14. The products, the softmax and their accuracy are attn_paged's. A row of q with
+ * an infinity gets NaN in O and LSE, if it sees a key. Slots beyond a sequence's length may hold any
+ * codes and scales.
  */
 typedef struct attn_paged_fp8_params {
     attn_paged_tree_params t;

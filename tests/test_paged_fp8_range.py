@@ -136,3 +136,27 @@ def test_nan_among_the_values_shows(A, n, code, dtype):
     assert torch.isnan(k[0, 0, 5])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("n", [1, 6, 50, 200])
+@pytest.mark.parametrize("what", [math.inf, -math.inf, math.nan])
+def test_queries_that_are_not_finite_show(A, n, what, dtype):
+    c = Case([n, n], [200 + n, 130 + n], 1, 2, 64, 16, dtype, 94)
+    c.q[n // 2, 1, 7] = what
+    o, lse = A.attn_paged_fp8(*c.args(), causal=True, max_q=n)
+    _ok(A)
+    bad = torch.zeros(2 * n, 2, dtype=torch.bool)
+    bad[n // 2, 1] = True
+    assert torch.isnan(o.cpu()).all(-1).equal(bad) and torch.isnan(lse.t().cpu()).equal(bad)
+    assert torch.isfinite(o.cpu()[~bad]).all() and torch.isfinite(lse.t().cpu()[~bad]).all()
+
+
+@pytest.mark.parametrize("n", [6, 40, 200])
+def test_rows_without_keys_whatever_the_query(A, n):
+    # more rows than keys: the first see none
+    c = Case([n], [2], 1, 2, 64, 16, BF16, 95)
+    c.q[0, 0, 3], c.q[1, 1, 5], c.q[2] = math.inf, math.nan, 0.0
+    o, lse = A.attn_paged_fp8(*c.args(), causal=True, max_q=n)
+    _ok(A)
+    assert torch.all(o[:n - 2] == 0) and torch.isneginf(lse[:, :n - 2]).all() and torch.isfinite(lse[:, n - 2:]).all()
+
+
