@@ -77,6 +77,7 @@
 #pragma once
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -212,7 +213,7 @@ struct Cfg8 {
     static constexpr int kStateBytes = 4 * 32 * 16, kMergeBytes = 4 * 32 * 36 * 4;
     static constexpr int kExtraBytes = SMALL ? kQSlots * kQSlot + kStateBytes + kMergeBytes : 0;
     static constexpr int kRoom = Kernel::kTilesBytes - kKeyOff - kExtraBytes;
-    // Factors of a tile: the keys' scales. Two stages more than keys have: a tile of keys arrives when the products
+    // Factors of a tile: the keys' scales, times 2^-bias. Two stages more than keys have: a tile of keys arrives when the products
     // with the one kKeys before it are done, and by then the softmax has read the factors of what came two before that
     // (a thread reads a tile's factors before it takes the next one's scores).
     static constexpr int kFactorBytes = BN * 4;
@@ -235,7 +236,7 @@ struct PagedDev {
     int tok_tile;     // tokens of a tile: its rows are tok_tile * G
     int num_pages, page_size, shift, max_pages;
     int causal;
-    float c;          // scale * log2(e)
+    float c;          // scale * log2(e); of kBytes times 2^bias
     const int32_t *cu_q, *kv_len, *table;
     long long table_stride;
     uint8_t* o;
@@ -252,6 +253,7 @@ struct PagedDev {
     const uint32_t* tree;
     long long tree_stride;
     int tree_words, tree_nodes;
+    float key_bias;   // kBytes: 2^-bias, which goes onto the keys' scales (key_bias_of)
     // kBytes: scales of keys and values, and their strides over (page, head)
     const uint8_t *k_scale, *v_scale;
     long long ks_page, ks_head, vs_page, vs_head;
@@ -881,6 +883,9 @@ __device__ __forceinline__ void split_unit(const PagedDev& p, const Unit& w, uin
     }
 }
 
+// What a row's scores are multiplied by behind their keys' factors: c * 2^e. Above 0, so that masked scores stay -inf.
+__device__ __forceinline__ float row_factor(float c, float f) { return fmaxf(c * f, FLT_MIN); }
+
 // Descriptor of a K-major tile of codes: rows of 128 bytes with the 128-byte swizzle, or of 64 with the 64-byte one
 // (layout 4). A product's k-step is 32 codes.
 template <int D>
@@ -913,9 +918,11 @@ __device__ __forceinline__ void make_factors(const PagedDev& p, uint8_t* smem, S
             const uint32_t s = n % E::kKeys;
             ok = mbar_wait_warp(&bar.k_full[s], (n / E::kKeys) & 1, wc);
             if (!ok) break;
-            uint4* factors = reinterpret_cast<uint4*>(smem + E::kFactorOff + n % E::kFactors * E::kFactorBytes);
+            float4* factors = reinterpret_cast<float4*>(smem + E::kFactorOff + n % E::kFactors * E::kFactorBytes);
             const uint32_t b4 = *reinterpret_cast<const uint32_t*>(smem + E::kKeyScaleOff + s * BN + lane * 4);
-            factors[lane] = make_uint4((b4 & 0xff) << 23, (b4 & 0xff00) << 15, (b4 & 0xff0000) << 7, b4 >> 1 & 0x7f800000);
+            factors[lane] =
+                make_float4(__uint_as_float((b4 & 0xff) << 23) * p.key_bias, __uint_as_float((b4 & 0xff00) << 15) * p.key_bias,
+                            __uint_as_float((b4 & 0xff0000) << 7) * p.key_bias, __uint_as_float(b4 >> 1 & 0x7f800000) * p.key_bias);
             __syncwarp();
             if (elect_one()) mbar_arrive(&bar.k_ready[s]);
             __syncwarp();
@@ -1094,8 +1101,8 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
                     ok = (ready & 1) || mbar_wait_warp(&bar.k_full[sk], pk, wc);
                     if (!ok) break;
                     const int at = c * 32 + lane;
-                    reinterpret_cast<uint32_t*>(smem + E::kFactorOff)[n % E::kFactors * BN + at] =
-                        (uint32_t)smem[E::kKeyScaleOff + sk * BN + at] << 23;
+                    reinterpret_cast<float*>(smem + E::kFactorOff)[n % E::kFactors * BN + at] =
+                        __uint_as_float((uint32_t)smem[E::kKeyScaleOff + sk * BN + at] << 23) * p.key_bias;
                     __syncwarp();
                     if (elect_one()) mbar_arrive(&bar.k_ready[sk]);
                 }
@@ -1375,7 +1382,8 @@ __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Sh
             ++units;
             const uint8_t* slot = smem + E::kQSlotOff + at * E::kQSlot;
             // lanes without a row have whatever lies there; they must not move a maximum
-            row_c = lane < rows && my_tok < w.ntok ? p.c * reinterpret_cast<const float*>(slot + 32 * E::kPieces * E::kQPitch)[lane] : 0.f;
+            const float f = lane < rows && my_tok < w.ntok ? reinterpret_cast<const float*>(slot + 32 * E::kPieces * E::kQPitch)[lane] : 0.f;
+            row_c = row_factor(p.c, f);
 #pragma unroll
             for (int k = 0; k < E::kPieces; ++k)
 #pragma unroll
@@ -1397,7 +1405,7 @@ __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Sh
             const uint16_t* src = nullptr;
             if (r < rows && my_tok < w.ntok) src = p.q + (w.row0 + my_tok) * p.q_sr + (w.h * p.G + my_head) * p.q_sh;
             __syncwarp();
-            row_c = p.c * split_row<D, F16, true>(src, tmem + E::kQCol, nullptr, r);
+            row_c = row_factor(p.c, split_row<D, F16, true>(src, tmem + E::kQCol, nullptr, r));
         }
         mbar_arrive(&bar.q_full[0]);
     };
@@ -2032,8 +2040,8 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                     const uint16_t* src = nullptr;
                     if (r < rows && my_tok < w.ntok) src = p.q + (w.row0 + my_tok) * p.q_sr + (w.h * p.G + my_head) * p.q_sh;
                     __syncwarp();
-                    row_c = p.c * split_row<D, F16, E::kQTmem>(src, tmem + lane_off + E::kQCol,
-                                                           smem + t * E::kPieces * E::kTileBytes, r);
+                    row_c = row_factor(p.c, split_row<D, F16, E::kQTmem>(src, tmem + lane_off + E::kQCol,
+                                                                         smem + t * E::kPieces * E::kTileBytes, r));
                     mbar_arrive(&bar.q_full[t]);
                 }
             };
@@ -2445,6 +2453,12 @@ Plan plan_of(const attn_paged_params& p, int num_sms, int var) {
     return pl;
 }
 
+// kBytes: a score is (sum of products of pieces of Q and codes) * (key's scale 2^k) * (row's 2^e) * c in this order, and the sum
+// may reach 2^25 where k reaches 119. So 2^-bias of the latter two goes onto the keys' scales, as much as leaves c * 2^bias * 2^e
+// finite for every e up to 119, and no more than is needed. The product with a key's factor then stays within fp32 for k up to
+// 102 + bias: up to 112 for a scale of 1 / 8 and less, 109 for 1.
+int key_bias_of(float c) { return std::min(17, std::max(0, (int)std::floor(8.f - std::log2(c)))); }
+
 // 4-D map of 16-bit elements over the given extents, dimension 0 contiguous, 64-column boxes.
 // Rows of 64 columns that do not follow one another (pages that hold [slot, head, d]) are fetched in
 // 128-byte pieces, or half of every fetch would be another head's row: 64 sequences of 4096 keys at d = 64 took
@@ -2569,7 +2583,9 @@ attn_status_t launch_variant(const attn_paged_params& p, const Extra& x, const L
     while ((1 << a.shift) < p.page_size) ++a.shift;
     a.max_pages = p.max_pages;
     a.causal = p.causal;
-    a.c = p.scale * kLog2e;
+    const int bias = VAR == kBytes ? key_bias_of(p.scale * kLog2e) : 0;
+    a.c = std::ldexp(p.scale * kLog2e, bias);
+    a.key_bias = std::ldexp(1.f, -bias);
     a.cu_q = p.cu_q;
     a.kv_len = p.kv_len;
     a.table = p.block_table;

@@ -160,3 +160,42 @@ def test_rows_without_keys_whatever_the_query(A, n):
     assert torch.all(o[:n - 2] == 0) and torch.isneginf(lse[:, :n - 2]).all() and torch.isfinite(lse[:, n - 2:]).all()
 
 
+# ---------------------------------------------------------------- scales of the keys
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 6, 50, 200])
+@pytest.mark.parametrize("up,down", [(118, 12), (110, 12), (105, 0), (-100, 0), (-112, 12)])
+def test_keys_at_the_ends_of_the_scales(A, n, up, down, d):
+    # keys 2^up times as large, queries as much smaller but for 2^down, which is in the scale: ordinary scores
+    c = Case([n, 3], [300 + n, 9], 2, 2, d, 16, BF16, 96)
+    c.exps[0][c.exps[0] != 255] = np.clip(c.exps[0][c.exps[0] != 255].astype(int) + up, 8, 246)
+    c.q = (c.q.float() * 2.0 ** (down - up)).to(BF16)
+    _restored(c)
+    scale = 2.0 ** -down / math.sqrt(d)
+    o, lse = A.attn_paged_fp8(*c.args(), causal=True, scale=scale, max_q=n)
+    _ok(A)
+    c.check(o, lse, True, scale=scale)
+
+
+@pytest.mark.parametrize("n", [1, 6, 50, 200])
+def test_large_keys_beside_ordinary_ones(A, n):
+    # ordinary keys and queries, but that one token's keys reach 2^126 in columns where the queries are 0: its scores are 0
+    c = Case([n], [200 + n], 2, 2, 64, 16, BF16, 97)
+    c.q[:, :, 32:] = 0
+    _set(c, 0, 0, 5, np.where(np.arange(64) < 32, 0.0, 448.0)[None], 118)
+    _restored(c)
+    o, lse = A.attn_paged_fp8(*c.args(), causal=True, max_q=n)
+    _ok(A)
+    c.check(o, lse, True)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("n", [1, 6, 50, 200])
+def test_small_scale_and_rows_of_zeros(A, n, dtype):
+    # scores of almost 0 everywhere: each row averages the values that it sees
+    c = Case([n], [200 + n], 1, 2, 64, 16, dtype, 98)
+    c.q[::2] = 0
+    o, lse = A.attn_paged_fp8(*c.args(), causal=True, scale=1e-30, max_q=n)
+    _ok(A)
+    c.check(o, lse, True, scale=1e-30)
+
+
