@@ -199,7 +199,7 @@ template <int D, bool F16, int NT, int KERNEL, bool SMALL>
 struct Cfg8 {
     using Kernel = Shape<D, KERNEL, kBytes>;
     static constexpr int kTileBytes = BN * D;      // of codes
-    static constexpr int kPieces = F16 ? 3 : 2;    // of 4, 4 and 3 bits of Q's 11 or 8
+    static constexpr int kPieces = F16 ? 3 : 2;    // of 4, 3 and 3 bits of Q's 11 or 8 (split_pair)
     // Tensor memory of units of one tile: scores from 0 on, Q's pieces (a product then reads keys alone from shared
     // memory), O, and P of two tiles in turn. Units of two tiles have no room for Q there.
     static constexpr bool kQTmem = NT == 1;
@@ -711,7 +711,7 @@ __device__ __forceinline__ void widen_tile(const uint8_t* raw, const uint8_t* sc
     const uint32_t s4 = *reinterpret_cast<const uint32_t*>(scale + lane * 4);
     const bool other = (__vcmpltu4(s4, 0x67676767u) | (F16 ? 0 : __vcmpgtu4(s4, 0x8e8e8e8eu))) != 0;
     const bool plain = !__any_sync(kFull, other) && left >= BN;
-#pragma unroll
+#pragma unroll 1  // the roles of a CTA share its instruction cache: a mixed step of 64 sequences and a chunk 150 us, 181 unrolled
     for (int turn = 0; turn < kTurns; ++turn) {
         const int row7 = r0 ^ (turn * 2), row = c * kRows + row7;  // and every 8th row behind it
         const uint8_t* from = raw + row * D + (D == 128 ? (ch ^ row7) * 16 : ch * 16);
@@ -749,29 +749,37 @@ __device__ __forceinline__ void widen_tile(const uint8_t* raw, const uint8_t* sc
     }
 }
 
-// Two values of Q over the row's factor (at most 448) as sums of 8-bit numbers. The nearest E4M3 number leaves a
-// remainder of 4 bits less, whose nearest E4M3 number leaves nothing of a bf16 value; of an fp16 value it leaves
-// 3 bits, which E5M2 holds. All exact while the value is above 2^-2 (2^-6 in fp16), else to 2^-10 (2^-17): of a row's
-// largest value 2^-18 or less, where the row's fp32 sums end at 2^-24 of their largest term.
+// Two values of Q over the row's factor (at most 3584) as sums of 8-bit numbers: an E4M3 number (4 bits, up to 448) and one
+// (bf16) or two (fp16) E5M2 numbers (3 bits). Up to 448 the nearest E4M3 number leaves at most 8 units of a bf16 value's 8
+// bits, which 3 bits hold; of an fp16 value's 11 bits it leaves up to 64 units, of which an E5M2 number leaves up to 4.
+// Beyond 448 the nearest E5M2 number comes first and leaves at most 256, 16 (fp16: 128) units, of which an E4M3 number leaves
+// none (4). All exact from 2^-6 on, E4M3's least normal number; below, it leaves up to 2^-10, and the error is at most 2^-14
+// (fp16: 2^-17), which is 2^-24 (2^-27) of the row's largest value.
 template <bool F16>
 __device__ __forceinline__ void split_pair(uint32_t x, float f, uint16_t& a, uint16_t& b, uint16_t& c) {
     const float2 y2 = fmul2(unpack_h16<F16>(x), make_float2(f, f));
-    uint32_t y = pack_f16(y2.x, y2.y), back;
+    uint32_t y = pack_f16(y2.x, y2.y), large, back;
+    asm("{\n\t.reg .b32 m;\n\tabs.f16x2 m, %1;\n\tset.gt.u32.f16x2 %0, m, %2;\n\t}" : "=r"(large) : "r"(y), "r"(0x5f005f00u));
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(b) : "r"(y));
+    asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(back) : "h"(b));
+    const uint32_t first = back & large;
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(y) : "r"(first));
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(a) : "r"(y));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(a));
     asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(y) : "r"(back));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b) : "r"(y));
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(b) : "r"(first | (y & ~large)));
     if constexpr (F16) {
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(b));
-        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(y) : "r"(back));
+        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(back) : "h"(b));
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(y) : "r"(back & ~large));
         asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(c) : "r"(y));
     }
 }
 
-// The smallest e with top <= 448 * 2^e, 448 = 1.75 * 2^8, as far as the factor 2^-e is a plain number.
+// The smallest e with top <= 3584 * 2^e, 3584 = 1.75 * 2^11, as far as the factor 2^-e is a plain number.
+constexpr int kMostRowExponent = 116;
 __device__ __forceinline__ int row_exponent(float top) {
     const uint32_t bits = __float_as_uint(top);
-    return min(max((int)(bits >> 23) - 135 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0), -119), 119);
+    return min(max((int)(bits >> 23) - 138 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0), -119), kMostRowExponent);
 }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 // What a row whose largest magnitude is `top` is multiplied by before it is split, with e = row_exponent(top). The 8-bit
@@ -789,45 +797,49 @@ __device__ __forceinline__ void take_max(uint32_t& top, uint32_t x) {
 }
 
 // Splits a thread's row of Q (NULL: a row that nobody reads) into the pieces of its tile, in tensor memory at `tmem` or
-// in shared memory at `tile` as row r of K-major tiles, and returns the row's factor 2^e.
+// in shared memory at `tile` as row r of K-major tiles, and returns the row's factor 2^e. Reads the row twice, and splits 32
+// columns at a time in a loop: the roles of a CTA share its instruction cache, and a row in registers costs spills.
 template <int D, bool F16, bool TMEM>
 __device__ __forceinline__ float split_row(const uint16_t* src, uint32_t tmem, uint8_t* tile, int r) {
     constexpr int kPieces = F16 ? 3 : 2;
-    uint32_t x[D / 2];
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-        const uint4 v = src ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
-        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-    }
+    const uint4* words = reinterpret_cast<const uint4*>(src);
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < D / 2; ++i) take_max<F16>(top, x[i]);
+    for (int i = 0; i < D / 8; ++i) {
+        const uint4 v = src ? words[i] : make_uint4(0, 0, 0, 0);
+        take_max<F16>(top, v.x), take_max<F16>(top, v.y), take_max<F16>(top, v.z), take_max<F16>(top, v.w);
+    }
     const float2 t2 = unpack_h16<F16>(top);
     const float largest = fmaxf(t2.x, t2.y);
     const int e = row_exponent(largest);
     const float f = split_factor(largest, e);
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t out[kPieces][8];
 #pragma unroll
-    for (int c0 = 0; c0 < D / 4; c0 += 16) {  // 64 columns at a time
-        uint32_t out[kPieces][16];
+        for (int i = 0; i < 4; ++i) {
+            const uint4 v = src ? words[c0 / 8 + i] : make_uint4(0, 0, 0, 0);
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            uint16_t a[2], b[2], c[2] = {0, 0};
+            for (int j = 0; j < 2; ++j) {
+                uint16_t a[2], b[2], c[2] = {0, 0};
 #pragma unroll
-            for (int k = 0; k < 2; ++k) split_pair<F16>(x[2 * (c0 + i) + k], f, a[k], b[k], c[k]);
-            out[0][i] = a[0] | (uint32_t)a[1] << 16;
-            out[1][i] = b[0] | (uint32_t)b[1] << 16;
-            if constexpr (F16) out[kPieces - 1][i] = c[0] | (uint32_t)c[1] << 16;
+                for (int k = 0; k < 2; ++k) split_pair<F16>(x[2 * j + k], f, a[k], b[k], c[k]);
+                out[0][2 * i + j] = a[0] | (uint32_t)a[1] << 16;
+                out[1][2 * i + j] = b[0] | (uint32_t)b[1] << 16;
+                if constexpr (F16) out[kPieces - 1][2 * i + j] = c[0] | (uint32_t)c[1] << 16;
+            }
         }
 #pragma unroll
         for (int k = 0; k < kPieces; ++k) {
             if constexpr (TMEM) {
-                tmem_st16(tmem + k * (D / 4) + c0, out[k]);
+                tmem_st8(tmem + (k * D + c0) / 4, out[k]);
             } else {
                 uint8_t* dst = tile + k * BM * D + r * D;
                 const int sw = D == 128 ? r & 7 : (r >> 1) & 3;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<uint4*>(dst + (((c0 / 4 + i) ^ sw) << 4)) =
+                for (int i = 0; i < 2; ++i)
+                    *reinterpret_cast<uint4*>(dst + (((c0 / 16 + i) ^ sw) << 4)) =
                         make_uint4(out[k][4 * i], out[k][4 * i + 1], out[k][4 * i + 2], out[k][4 * i + 3]);
             }
         }
@@ -986,7 +998,7 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
         const uint64_t kd = codes_desc<D>(smem_u32(smem + E::kKeyOff + s * E::kTileBytes));
 #pragma unroll
         for (int piece = 0; piece < E::kPieces; ++piece) {
-            const uint32_t idesc = piece == 2 ? kIdesc | 1u << 7 : kIdesc;  // A in E5M2
+            const uint32_t idesc = piece > 0 ? kIdesc | 1u << 7 : kIdesc;  // A in E5M2
             const uint64_t qd = codes_desc<D>(smem_u32(smem + (t * E::kPieces + piece) * E::kTileBytes));
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk) {
@@ -2454,10 +2466,10 @@ Plan plan_of(const attn_paged_params& p, int num_sms, int var) {
 }
 
 // kBytes: a score is (sum of products of pieces of Q and codes) * (key's scale 2^k) * (row's 2^e) * c in this order, and the sum
-// may reach 2^25 where k reaches 119. So 2^-bias of the latter two goes onto the keys' scales, as much as leaves c * 2^bias * 2^e
-// finite for every e up to 119, and no more than is needed. The product with a key's factor then stays within fp32 for k up to
-// 102 + bias: up to 112 for a scale of 1 / 8 and less, 109 for 1.
-int key_bias_of(float c) { return std::min(17, std::max(0, (int)std::floor(8.f - std::log2(c)))); }
+// may reach 2^28 where k reaches 119. So 2^-bias of the latter two goes onto the keys' scales, as much as leaves c * 2^bias * 2^e
+// finite for every e, and no more than is needed. The product with a key's factor then stays within fp32 for k up to 100 +
+// bias: up to 113 for a scale of 1 / 8 and less, 110 for 1.
+int key_bias_of(float c) { return std::min(19, std::max(0, (int)std::floor(127.f - kMostRowExponent - std::log2(c)))); }
 
 // 4-D map of 16-bit elements over the given extents, dimension 0 contiguous, 64-column boxes.
 // Rows of 64 columns that do not follow one another (pages that hold [slot, head, d]) are fetched in

@@ -518,7 +518,8 @@ ATTN_API attn_status_t attn_paged_tree(const attn_paged_tree_params *p, void *st
  * for attn_paged, with f.dtype the type of q and o, the caches E4M3 codes and k_stride, v_stride in
  * bytes. Keys and values are code * scale, with the scales of attn_pages_write_fp8, 2^-119 to 2^119.
  * Values are taken in f.dtype: exact in bf16; in fp16 they have to be within its range, and are
- * rounded below 2^-14. The products, the softmax and their accuracy are attn_paged's. A row of q with
+ * rounded below 2^-14. The products, the softmax and their accuracy are attn_paged's, but that entries of
+ * a row of q below 2^-16 of its largest are rounded, by at most 2^-24 of that (fp16: 2^-27). A row of q with
  * an infinity gets NaN in O and LSE, if it sees a key. Scores that q's rows leave ordinary may overflow,
  * to NaN, where keys reach 2^120 (with a scale above 1/8, 2^117; above 1, 2^117 / scale). Slots beyond a
  * sequence's length may hold any codes and scales.

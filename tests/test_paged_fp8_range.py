@@ -199,3 +199,26 @@ def test_small_scale_and_rows_of_zeros(A, n, dtype):
     c.check(o, lse, True, scale=1e-30)
 
 
+# ---------------------------------------------------------------- entries of a query
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 6, 50, 200])
+@pytest.mark.parametrize("ratio", [256, 1024, 2048])
+def test_one_large_entry_in_a_query(A, ratio, n, d, dtype):
+    # one entry of up to `ratio` times the largest of the others, 4, its keys as much smaller: ordinary scores, to which every entry
+    # counts. Entries below 2^-16 of the row's largest, 4 * ratio, are off by 2^-24 of it, 2^-22 * ratio, at most: 2^-11 for 2048,
+    # where they are below 2^-3. A tenth of normal entries with a largest of 4 are; with keys of up to 8 and either sign some 10
+    # such errors of half that size on the average make 10^0.5 * 2^-12 * 8 / 64^0.5 = 8e-4 of a score's unit at most, of
+    # LSE's 1e-3
+    c = Case([n], [1000 + n], 1, 2, d, 16, dtype, 99)
+    c.q = (c.q.float() * 4.0 / c.q.float().abs().amax()).to(dtype)
+    c.q[:, :, 11] *= ratio
+    codes = torch.from_numpy(c.codes[0]).view(torch.float8_e4m3fn).float()
+    codes[..., 11] /= ratio
+    c.codes[0] = codes.to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    _restored(c)
+    o, lse = A.attn_paged_fp8(*c.args(), causal=True, max_q=n)
+    _ok(A)
+    c.check(o, lse, True)
+
+
