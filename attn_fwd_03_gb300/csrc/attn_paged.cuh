@@ -675,13 +675,14 @@ __device__ __forceinline__ void widen16(uint4 v, int s, uint32_t (&out)[8]) {
     }
 }
 
-// The same for any scale (in bf16, bytes 0 and 255 are 2^-127 and NaN; in fp16, up to 2^15): in two multiplications where
-// fp16 has to hold the factors.
+// The same for any scale (in bf16, bytes 0 and 255 are 2^-127 and NaN): in two multiplications where fp16 has to hold the
+// factors. Whatever is left of a scale beyond 2^30 would only come upon values beyond fp16's range.
 template <bool F16>
 __device__ __forceinline__ void widen16_any(uint4 v, int s, uint32_t (&out)[8]) {
     codes16(v, out);
     if constexpr (F16) {
-        const float scale = __uint_as_float((uint32_t)max(s, 113) << 23), rest = __uint_as_float((uint32_t)(127 + min(s - 113, 0)) << 23);
+        const int s0 = min(max(s, 113), 142), s1 = min(127 + s - s0, 142);
+        const float scale = __uint_as_float((uint32_t)s0 << 23), rest = __uint_as_float((uint32_t)s1 << 23);
         const uint32_t f = pack_f16(scale, scale), more = pack_f16(rest, rest);
 #pragma unroll
         for (int k = 0; k < 8; ++k) out[k] = mul2(mul2(out[k], f), more);
@@ -709,7 +710,7 @@ __device__ __forceinline__ void widen_tile(const uint8_t* raw, const uint8_t* sc
     const int r0 = D == 128 ? (lane >> 4) ^ (lane & 4 ? 5 : 0) : lane >> 2;
     // scales that widen16 does not take are looked for once a tile
     const uint32_t s4 = *reinterpret_cast<const uint32_t*>(scale + lane * 4);
-    const bool other = (__vcmpltu4(s4, 0x67676767u) | (F16 ? 0 : __vcmpgtu4(s4, 0x8e8e8e8eu))) != 0;
+    const bool other = (__vcmpltu4(s4, 0x67676767u) | __vcmpgtu4(s4, 0x8e8e8e8eu)) != 0;
     const bool plain = !__any_sync(kFull, other) && left >= BN;
 #pragma unroll 1  // the roles of a CTA share its instruction cache: a mixed step of 64 sequences and a chunk 150 us, 181 unrolled
     for (int turn = 0; turn < kTurns; ++turn) {

@@ -222,3 +222,18 @@ def test_one_large_entry_in_a_query(A, ratio, n, d, dtype):
     c.check(o, lse, True)
 
 
+# ---------------------------------------------------------------- scales of the values
+@pytest.mark.parametrize("n", [1, 6, 50, 200])
+def test_fp16_values_whose_scale_is_beyond_its_range(A, n):
+    # codes of up to 2^-3 times 2^17, and rows of zeros with any scale: values that fp16 holds
+    c = Case([n], [200 + n], 1, 2, 64, 16, F16, 100)
+    g = np.random.default_rng(100)
+    for j in range(200 + n):
+        _set(c, 1, 0, j, g.integers(-7, 8, (1, 64)) * 2.0 ** -(6 + j % 3) if j % 5 else np.zeros((1, 64)), 17 if j % 5 else 100)
+    _restored(c)
+    o, lse = A.attn_paged_fp8(*c.args(), causal=True, max_q=n)
+    _ok(A)
+    O, L = _forward(c, True, 0.125)
+    # parity_util's bounds over the largest O, which is some 2^14 here
+    assert_lse(lse, L)
+    assert np.all(np.abs(to64(o) - O) <= 4e-3 * np.abs(O).max())
