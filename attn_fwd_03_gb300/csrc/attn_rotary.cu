@@ -3,7 +3,8 @@
 // Mathematics: pair i of a row at position x is turned by t = x * f_i. In turns that is x * f_i / (2 pi)
 // modulo 1, and only the fraction matters, so each frequency becomes a 64-bit integer F_i = f_i / (2 pi) *
 // 2^64 (mod 2^64) and the angle x * F_i, a product that wraps where whole turns end. It is exact to 2^-32 of
-// a turn at any 32-bit position, where fp32 angles lose 2^-24 of a position that may be a million; the
+// a turn at any 32-bit position, where fp32 angles lose 2^-24 of a position that may be a million. fp32 holds 24 of
+// those 32 bits: cosine and sine are those of the upper 24, turned by the lower 8 to first order. The
 // backward pass is the same turn with the sine's sign changed.
 //
 // What bounds it: every row is read and written once and needs 6 operations a pair, so HBM (gradients of q and k of
@@ -124,9 +125,13 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
         float c = 0.f, s = 0.f;
         if (n < p.N) {
             const int x = p.positions[b * p.position_stride[0] + n * p.position_stride[1]];
-            // the fraction of a turn in units of half a turn, -1 to 1
-            const long long t = (long long)((uint64_t)(long long)x * turns_of(p.inv_freq[f]));
-            sincospif(__ll2float_rn(t) * 0x1p-63f, &s, &c);
+            // the fraction of a turn in units of 2^-32, rounded; in units of half a turn -1 to 1
+            const int t = (int)(((uint64_t)(long long)x * turns_of(p.inv_freq[f]) + 0x80000000u) >> 32);
+            float s0, c0;
+            sincospif((float)(t & ~0xff) * 0x1p-31f, &s0, &c0);
+            const float rest = (float)(t & 0xff) * (0x1p-31f * 3.14159265f);  // radians
+            c = fmaf(-s0, rest, c0);
+            s = fmaf(c0, rest, s0);
         }
         float* plane = reinterpret_cast<float*>(&s_turn[r][(f >> 2) & 1][f >> 3]) + (f & 3);
         plane[0] = c * p.magnitude;

@@ -161,3 +161,17 @@ def test_nothing_to_turn(A):
     q, k = A.attn_rotary(torch.zeros(0, 4, 64, device="cuda"), torch.zeros(0, 2, 64, device="cuda"), none, freq)
     assert q.shape == (0, 4, 64) and k.shape == (0, 2, 64)
     assert A.attn_rotary(torch.zeros(2, 0, 3, 64, device="cuda"), None, torch.zeros(3, dtype=torch.int32, device="cuda"), freq)[0].numel() == 0
+
+
+def test_angles_near_half_a_turn(A):
+    # fp32 holds an angle near half a turn to 2^-25 of that only, and the sine there is the distance to it: positions whose angle
+    # is within 2^-9 of a turn of it, the sine read off as y0 of (0, -1) and y1 of (1, 0). Bound: the angle to 2^-32 of a turn,
+    # 2^-29.3, and the sine's own rounding and the product's, 2^-22 of it together
+    pos = [p for p in range(1, 40000) if abs(serving.turn_of(p, 1.0) - 0.5) < 2.0 ** -9]
+    freq = torch.ones(8, device="cuda")
+    x = torch.zeros(len(pos), 1, 16, device="cuda")
+    x[..., :8] = 1.0
+    got, _ = A.attn_rotary(x, None, torch.tensor(pos, dtype=torch.int32, device="cuda"), freq)
+    want = serving.rotate(to64(x).transpose(1, 0, 2), pos, freq.tolist(), False).transpose(1, 0, 2)
+    off = np.abs(to64(got) - want)[..., 8:]
+    assert len(pos) > 100 and np.all(off <= 2.0 ** -29 + 2.0 ** -22 * np.abs(want[..., 8:]))
