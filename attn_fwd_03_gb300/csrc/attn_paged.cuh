@@ -2064,8 +2064,9 @@ __device__ __forceinline__ void work(const CUtensorMap& tm_q, const CUtensorMap&
                 if (lane == 0) bar.unit[warp] = make_int4(w.row0, w.ntok, w.h, (w.first ? 1 : 0) + (w.last ? 2 : 0));
                 const int cnt = w.cnt(t), k0 = w.k0;
                 // keys this row sees, and those that the tile's first row sees
-                const int lim = w.causal ? min(w.len, w.base + my_tok + 1) : w.len;
-                const int lim_first = w.causal ? min(w.len, w.base + t * p.tok_tile + 1) : w.len;
+                const bool causal = VAR == kRun ? p.causal : w.causal;
+                const int lim = causal ? min(w.len, w.base + my_tok + 1) : w.len;
+                const int lim_first = causal ? min(w.len, w.base + t * p.tok_tile + 1) : w.len;
                 // where a tree's keys begin
                 const int ctx = VAR != kRun && !w.causal && p.tree != nullptr ? w.ctx : INT_MAX;
                 float m_ref = -INFINITY, m_row = -INFINITY, l = 0.f;
