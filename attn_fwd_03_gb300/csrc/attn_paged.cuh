@@ -103,9 +103,11 @@ constexpr int kUnitCost = 384;
 // A key tile of a two-tile unit against one of a one-tile unit: the mixed step takes 68.5 us (1.2: 72.3, 2.0:
 // 70.0), at d = 64 51.7 us (54.6, 57.0).
 constexpr float kPairCost = 1.5f;
-// The same for kBytes, where the batch's one-tile units are small (their values are not scaled) and where they are
-// not: a mixed step of 64 decoding sequences and a chunk takes 90 us with 2.7 (2.0: 100, 3.5: 91), 24 trees of 8 to 64
-// tokens 181 us with 1.4 (1.1: 189, 1.7: 186).
+// The same for kBytes, where the batch's one-tile units are small and where they are not. At d = 128 a mixed step of 64
+// decoding sequences and a 512-row chunk (up to 4096 keys each) takes 154 us with 2.7 (2.0: 170, 2.4: 165, 3.0: 158, 3.5: 168;
+// in fp16 160, 182, 174, 164, 174), 24 trees of 22 to 61 tokens (40 query and 8 key/value heads, up to 8192 keys) in fp16 174 us
+// with 1.4 (1.2: 185, 1.3: 180, 1.6: 181), in bf16 182 (173, 175, 195). At d = 64 less would do: 157 and 148 us with 2.7 and 2.0, 144
+// and 137 in fp16, 171 and 161 with 1.4 and 1.2, 168 and 158 in fp16.
 constexpr float kPairCostSmall = 2.7f, kPairCostCodes = 1.4f;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kIssueUnroll = 4;  // k-steps of a product in a row: 2 and 8 are within 2 %, 1 is 13 % slower
@@ -193,7 +195,7 @@ struct Cfg {
 // pieces, which would need no converters, is slower: the splitting comes on top of the softmax, which a tile then waits
 // for.
 //
-// Widening keys and values, with Q as it is, takes 335 us for 64 sequences of 8192 keys: the converters' integer
+// Widening keys and values, with Q as it is, took 335 us for 64 sequences of 8192 keys: the converters' integer
 // instructions issue at 64 lanes a cycle.
 template <int D, bool F16, int NT, int KERNEL, bool SMALL>
 struct Cfg8 {
@@ -406,8 +408,9 @@ __device__ __forceinline__ void locate(const PagedDev& p, Shared& sh) {
         const float c0 = (float)done[0], c1 = (float)done[1] * pair_cost;
         int n0 = done[0] == 0 ? 0 : max(1, (int)(n * (c0 / (c0 + c1)) + 0.5f));
         if (done[1] > 0) n0 = min(n0, n - 1);
-        // an even number of kBytes' CTAs: two SMs side by side share a cache of instructions that the loops of one kind fill
-        // (a pair of both kinds took a quarter longer than the others)
+        // An even number of kBytes' CTAs, as far as one may judge by times: pairs of CTAs seem to share a cache of instructions
+        // that the loops of one kind fill, so that a pair of both kinds falls behind (24 trees 174 us, 190 with any number; a mixed
+        // step 154 and 185). Which SM a CTA comes to is not promised; nothing but time depends on it.
         if (VAR == kBytes && n0 > 1) n0 &= ~1;
         pair = i >= n0;
         i = pair ? i - n0 : i;
@@ -657,8 +660,8 @@ __device__ __forceinline__ void codes16(uint4 v, uint32_t (&out)[8]) {
 // 16 codes times the scale 2^(s - 127), which fp16 has to hold (2^-24 to 2^15): the codes as fp16 numbers, times the
 // scale in fp16, or for bf16 in fp32, exact, by multiply-adds of fp16 numbers into fp32. NaN stays NaN on the way.
 // Moving a code's bits to where bf16 has them takes as many instructions (a byte permutation that repeats the sign, a
-// move, a mask, a multiplication), but turns NaN into 480: decode of 64 sequences of 8192 keys takes 165 us, 162 in
-// that way, 186 with a look for NaN codes on top; 178 with conversions to fp32 and the multiplication apart.
+// move, a mask, a multiplication), but turns NaN into 480, and is hardly faster: decode of 64 sequences of 8192 keys takes
+// 160 us, 161 in that way, 187 with a look for NaN codes on top.
 template <bool F16>
 __device__ __forceinline__ void widen16(uint4 v, int s, uint32_t (&out)[8]) {
     const float scale = __uint_as_float((uint32_t)s << 23);
@@ -697,54 +700,58 @@ __device__ __forceinline__ void widen16_any(uint4 v, int s, uint32_t (&out)[8]) 
 }
 
 // Makes the share of warp c of W of a 16-bit tile from a tile of codes: rows of 128 bytes per 64 columns, 16-byte
-// chunks swizzled by the row as TMA does. Rows from `left` on become 0.
-// A lane has 16 codes of a row at a time, and the same row of every 8 and the same columns in all of its turns,
+// chunks swizzled by the row as TMA does. Rows from `left` on become 0. A warp takes every W-th group of 8 rows.
+// A lane has 16 codes of a row at a time, and the same row of every group and the same columns in all of its turns,
 // so that its addresses differ by constants. Eight lanes that access memory together read and write all
 // banks: at d = 128 (codes swizzled like the tile) four lanes on the first columns of a row and four on those of
 // the row that differs in bits 0 and 2, at d = 64 four on each of two rows.
-template <int D, bool F16, int W>
+// The roles of a CTA share its instruction cache. LOOP: the two turns in a loop, for the kernel that has both kinds of unit (a
+// mixed step of 64 sequences and a chunk 154 us, 183 unrolled); where units are of one tile, both at once (64 sequences of 8192
+// keys 160 us, 169 in a loop; 2000 of 300 keys 251 and 241).
+template <int D, bool F16, int W, bool LOOP>
 __device__ __forceinline__ void widen_tile(const uint8_t* raw, const uint8_t* scale, uint8_t* tile, int left, int c, int lane) {
     constexpr int kTurns = D == 128 ? 2 : 1;  // for 8 rows
-    constexpr int kRows = BN / W, kEach = kRows / 8;
+    constexpr int kEach = BN / 8 / W;         // groups of a warp
+    static_assert(kEach * 8 * W == BN, "groups");
     const int ch = D == 128 ? (lane & 3) | (lane & 8) >> 1 : lane & 3;
     const int r0 = D == 128 ? (lane >> 4) ^ (lane & 4 ? 5 : 0) : lane >> 2;
     // scales that widen16 does not take are looked for once a tile
     const uint32_t s4 = *reinterpret_cast<const uint32_t*>(scale + lane * 4);
     const bool other = (__vcmpltu4(s4, 0x67676767u) | __vcmpgtu4(s4, 0x8e8e8e8eu)) != 0;
-    const bool plain = !__any_sync(kFull, other) && left >= BN;
-#pragma unroll 1  // the roles of a CTA share its instruction cache: a mixed step of 64 sequences and a chunk 150 us, 181 unrolled
-    for (int turn = 0; turn < kTurns; ++turn) {
-        const int row7 = r0 ^ (turn * 2), row = c * kRows + row7;  // and every 8th row behind it
-        const uint8_t* from = raw + row * D + (D == 128 ? (ch ^ row7) * 16 : ch * 16);
-        uint8_t* to = tile + (ch >> 2) * BN * 128 + row * 128;
-        const int a0 = (((ch & 3) * 2) ^ row7) * 16, a1 = (((ch & 3) * 2 + 1) ^ row7) * 16;
-        if (plain) {
+    // a turn's first row, and of a row: where its codes are, and where the two chunks go
+    auto row_of = [&](int turn) { return c * 8 + (r0 ^ (turn * 2)); };
+    auto codes_of = [&](int row) { return raw + row * D + (D == 128 ? (ch ^ (row & 7)) * 16 : ch * 16); };
+    auto chunk_of = [&](int row, int k) { return tile + (ch >> 2) * BN * 128 + row * 128 + (((ch & 3) * 2 + k) ^ (row & 7)) * 16; };
+    if (!__any_sync(kFull, other) && left >= BN) {
+#pragma unroll LOOP ? 1 : kTurns
+        for (int turn = 0; turn < kTurns; ++turn) {
+            const int row = row_of(turn);
+            const uint8_t* from = codes_of(row);
+            uint8_t *to0 = chunk_of(row, 0), *to1 = chunk_of(row, 1);
             uint4 v[kEach];
             int s[kEach];
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
-                v[i] = *reinterpret_cast<const uint4*>(from + i * 8 * D);
-                s[i] = scale[row + i * 8];
+                v[i] = *reinterpret_cast<const uint4*>(from + i * W * 8 * D);
+                s[i] = scale[row + i * W * 8];
             }
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
                 uint32_t out[8];
                 widen16<F16>(v[i], s[i], out);
-                *reinterpret_cast<uint4*>(to + i * 1024 + a0) = make_uint4(out[0], out[1], out[2], out[3]);
-                *reinterpret_cast<uint4*>(to + i * 1024 + a1) = make_uint4(out[4], out[5], out[6], out[7]);
+                *reinterpret_cast<uint4*>(to0 + i * W * 1024) = make_uint4(out[0], out[1], out[2], out[3]);
+                *reinterpret_cast<uint4*>(to1 + i * W * 1024) = make_uint4(out[4], out[5], out[6], out[7]);
             }
-        } else {
+        }
+    } else {
 #pragma unroll 1
-            for (int i = 0; i < kEach; ++i) {
-                uint32_t out[8];
-                const uint4 v = *reinterpret_cast<const uint4*>(from + i * 8 * D);
-                widen16_any<F16>(v, scale[row + i * 8], out);
-                if (row + i * 8 >= left) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) out[k] = 0;
-                }
-                *reinterpret_cast<uint4*>(to + i * 1024 + a0) = make_uint4(out[0], out[1], out[2], out[3]);
-                *reinterpret_cast<uint4*>(to + i * 1024 + a1) = make_uint4(out[4], out[5], out[6], out[7]);
+        for (int turn = 0; turn < kTurns; ++turn) {
+#pragma unroll 1
+            for (int row = row_of(turn); row < BN; row += W * 8) {
+                uint32_t out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (row < left) widen16_any<F16>(*reinterpret_cast<const uint4*>(codes_of(row)), scale[row], out);
+                *reinterpret_cast<uint4*>(chunk_of(row, 0)) = make_uint4(out[0], out[1], out[2], out[3]);
+                *reinterpret_cast<uint4*>(chunk_of(row, 1)) = make_uint4(out[4], out[5], out[6], out[7]);
             }
         }
     }
@@ -1122,7 +1129,7 @@ __device__ __forceinline__ void roles8(const CUtensorMap& tm_k, const CUtensorMa
                 ok = ((ready & 2) || mbar_wait_warp(&bar.v_full[sv], pv, wc)) &&
                      ((ready & 4) || mbar_wait_warp(&bar.kv_empty[so], po, wc));
                 if (!ok) break;
-                widen_tile<D, F16, W>(smem + E::kValueOff + sv * E::kTileBytes, smem + E::kValueScaleOff + sv * BN,
+                widen_tile<D, F16, W, KERNEL == kMixed>(smem + E::kValueOff + sv * E::kTileBytes, smem + E::kValueScaleOff + sv * BN,
                                       smem + E::kWideOff + so * 2 * E::kTileBytes, w.len - (w.k0 + j) * BN, c, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -1359,7 +1366,8 @@ __device__ __forceinline__ void finish_row(const PagedDev& p, const int4& u, int
 // A thread has a row, but in small units a row has a lane of tensor memory in each of the four warps: every warp has a
 // copy of Q's rows, so S too, and takes 32 of a tile's 128 keys. The copies' P are 0 at the other keys, so that their O
 // add up to the row's, each with a running maximum of its own; they are merged at the unit's end like the parts of a
-// unit that was cut (64 sequences of 8192 keys 240 us with a row in one thread, 187 with copies).
+// unit that was cut (64 sequences of 8192 keys 314 us with a row in one thread, 160 with copies; 512 of 128 keys 158 and 143, one
+// of 517 keys 17 to 19 either way).
 template <int D, bool F16, int KERNEL, bool SMALL>
 __device__ __forceinline__ void softmax_one(const PagedDev& p, uint8_t* smem, Shared& bar) {
     using C = Cfg<D, 1, KERNEL, kBytes>;
@@ -2471,7 +2479,7 @@ Plan plan_of(const attn_paged_params& p, int num_sms, int var) {
 // may reach 2^28 where k reaches 119. So 2^-bias of the latter two goes onto the keys' scales, as much as leaves c * 2^bias * 2^e
 // finite for every e, and no more than is needed. The product with a key's factor then stays within fp32 for k up to 100 +
 // bias: up to 113 for a scale of 1 / 8 and less, 110 for 1.
-int key_bias_of(float c) { return std::min(19, std::max(0, (int)std::floor(127.f - kMostRowExponent - std::log2(c)))); }
+int key_bias_of(float c) { return (int)std::min(19.f, std::max(0.f, std::floor(127.f - kMostRowExponent - std::log2(c)))); }
 
 // 4-D map of 16-bit elements over the given extents, dimension 0 contiguous, 64-column boxes.
 // Rows of 64 columns that do not follow one another (pages that hold [slot, head, d]) are fetched in
@@ -2509,8 +2517,8 @@ cudaError_t launch_tc(const CUtensorMap (&maps)[3], const PagedDev& p, int grid,
     const cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D, F16, KERNEL, VAR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                Kernel::kSmemBytes);
     if (e != cudaSuccess) return e;
-    // kMixed of kBytes starts when every SM is free, so that its CTAs come to lie in their order (locate): started early, one
-    // by one as SMs fall free, both kinds end up side by side (24 trees over an 8-bit cache 326 us, 181 in order).
+    // kMixed of kBytes starts when every SM is free, so that its CTAs mostly come to lie in their order (locate): started early,
+    // one by one as SMs fall free, both kinds end up side by side (24 trees over an 8-bit cache 304 us, 174 in order).
     return launch_chained(!(VAR == kBytes && KERNEL == kMixed), paged_tc_kernel<D, F16, KERNEL, VAR>, dim3(grid),
                           dim3(Kernel::kThreads), Kernel::kSmemBytes, s, maps[0], maps[1], maps[2], p);
 }

@@ -9,8 +9,8 @@ import numpy as np
 import pytest
 import torch
 
-from oracle import paged, serving
-from parity_util import assert_close_bf16, assert_lse, assert_masked_rows_zero, to64
+from oracle import paged, ref, serving
+from parity_util import assert_close_bf16, assert_lse, to64
 from test_paged_fp8 import A, Case, _i32, _ok  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -237,3 +237,46 @@ def test_fp16_values_whose_scale_is_beyond_its_range(A, n):
     # parity_util's bounds over the largest O, which is some 2^14 here
     assert_lse(lse, L)
     assert np.all(np.abs(to64(o) - O) <= 4e-3 * np.abs(O).max())
+
+
+# ---------------------------------------------------------------- large caches, and rows moved within one
+def test_cache_beyond_32_bit_offsets(A):
+    # more than 2^32 bytes of codes; the pages in use lie at both ends
+    hkv, page, d = 8, 256, 128
+    pages = (1 << 32) // (hkv * page * d) + 40
+    kv, table = [700, 300], np.array([[pages - 1, 3, pages - 2], [pages - 3, 0, 10 ** 6]])
+    cache = [torch.empty(pages, page, hkv, d, dtype=torch.uint8, device="cuda").transpose(1, 2) for _ in range(2)]
+    cache += [torch.empty(pages, hkv, page, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    slots = _i32([int(table[b, j // page]) * page + j % page for b in range(2) for j in range(kv[b])])
+    g = torch.Generator().manual_seed(102)
+    rows = [torch.randn(1000, hkv, d, generator=g).to(BF16) for _ in range(2)]
+    A.attn_pages_write_fp8(rows[0].cuda(), rows[1].cuda(), slots, *cache)
+    held = A.attn_pages_read_fp8(slots, *cache)
+    _ok(A)
+    for x, got in zip(rows, held):  # a code is off by 2^-4 of its value, or by 2^-10 of a scale, less than 2^-17 of the row's largest
+        x, got = to64(x), to64(got)
+        assert np.all(np.abs(got - x) <= 2.0 ** -4 * np.abs(x) + 2.0 ** -17 * np.abs(x).max(-1, keepdims=True))
+    q = torch.randn(4, hkv * 2, d, generator=g).to(BF16)
+    o, lse = A.attn_paged_fp8(q.cuda(), *cache, _i32(table), _i32([0, 1, 4]), _i32(kv), causal=True)
+    _ok(A)
+    ks, vs = (to64(x).transpose(1, 0, 2) for x in held)
+    for r0, r1, k0, k1 in ((0, 1, 0, 700), (1, 4, 700, 1000)):
+        O, L = ref.decode_forward(to64(q[r0:r1]).transpose(1, 0, 2)[None], np.repeat(ks[:, k0:k1], 2, 0)[None],
+                                  np.repeat(vs[:, k0:k1], 2, 0)[None], 1 / math.sqrt(d), True)
+        assert_close_bf16("O", o[r0:r1], O[0].transpose(1, 0, 2))
+        assert_lse(lse[:, r0:r1], L[0])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_rows_moved_to_other_slots_keep_their_values(A, dtype):
+    # the accepted nodes of a tree, read and written to consecutive slots: bf16 holds every value of a cache
+    c = Case([1], [90], 2, 1, 64, 16, dtype, 103)
+    cache = c.cache()
+    slot = lambda j: int(c.table[0, j // 16]) * 16 + j % 16  # noqa: E731
+    kept, to = [80, 83, 84, 88], [80, 81, 82, 83]
+    A.attn_pages_write_fp8(*A.attn_pages_read_fp8(_i32([slot(j) for j in kept]), *cache), _i32([slot(j) for j in to]), *cache)
+    k, v = A.attn_pages_read_fp8(_i32([slot(j) for j in to]), *cache)
+    _ok(A)
+    for got, x in ((k, c.values[0]), (v, c.values[1])):
+        for t, j in enumerate(kept):
+            assert np.array_equal(to64(got[t]), x[c.table[0, j // 16], :, j % 16])
