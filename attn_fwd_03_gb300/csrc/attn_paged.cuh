@@ -804,6 +804,13 @@ __device__ __forceinline__ void take_max(uint32_t& top, uint32_t x) {
         asm("max.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(mag));
 }
 
+// tmem_st16 for 8 columns.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // Splits a thread's row of Q (NULL: a row that nobody reads) into the pieces of its tile, in tensor memory at `tmem` or
 // in shared memory at `tile` as row r of K-major tiles, and returns the row's factor 2^e. Reads the row twice, and splits 32
 // columns at a time in a loop: the roles of a CTA share its instruction cache, and a row in registers costs spills.
