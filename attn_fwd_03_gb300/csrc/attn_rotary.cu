@@ -10,7 +10,7 @@
 // What bounds it: every row is read and written once and needs 6 operations a pair, so HBM (gradients of q and k of
 // 16 heads, 32768 rows and 128 columns, half of them turned side by side: 84.5 us, 6.35 TB/s, 93 % of the measured copy
 // rate; 32-byte accesses where the pieces lie side by side are no faster), or latency where a step brings few rows
-// (64 rows of 40 heads: 2.7 us a launch, one after another).
+// (64 rows of 40 heads: 2.9 us a launch, one after another).
 //
 // Split: a block takes kRows rows of one batch entry and a range of heads. Its threads first make the
 // block's cosines and sines (each serves every head of its row) in shared memory; a thread then keeps those

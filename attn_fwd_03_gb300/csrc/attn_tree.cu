@@ -4,7 +4,8 @@
 // from the highest down and ends after as many steps as the node is deep. A block takes a sequence (its
 // parents in shared memory, a thread per node); the block behind the last sequence takes the padding rows.
 // Bound by latency: a step's launch, two reads that depend on each other, and the deepest node's walk (one tree of 26
-// nodes 1.7 us, 300 trees of up to 64 nodes 3.5 us, device time in a captured graph).
+// nodes 1.8 us, 300 trees of up to 64 nodes 3.6 us, device time in a captured graph). Walks grow with a tree's depth, and a
+// thread has up to 8 of them: a chain of 64 nodes takes 8 us, of 256 53 us, of 1024 663 us.
 #include <cstdint>
 
 #include "internal.h"
